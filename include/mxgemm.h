@@ -440,6 +440,149 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
                                   size_t ws_bytes, uint32_t run_flags, void *stream);
 
 /*
+ * Row operators around the GEMM.  What a feed-forward block (dense or mixture of
+ * experts) does between its products, each in one pass over its rows: RMS norm
+ * with the residual's addition, the gated activation, and the routing of token
+ * rows to experts and back, with the gradients that training needs.  Where the
+ * next step is a product they write its MX operand (codes and scales) directly,
+ * by the recipe of mxgemm_quantize applied to the FP32 result.
+ *
+ * Common to them:
+ *  - in_dtype (MXGEMM_IN_F32 or MXGEMM_IN_BF16) is the element type of every
+ *    plain matrix of the call; sums and products are FP32, rounded once when
+ *    stored.  Row lengths (K, F, N) are multiples of 32.
+ *  - Input matrices are given with the number of elements from row to row
+ *    (`..._stride`, at least the row length; ignored for a single row).  Plain
+ *    matrices start on 32-byte boundaries and so does each of their rows.
+ *    Outputs are dense; codes and scales are 16-byte aligned.
+ *  - fmt 0 asks for no MX output (codes and scales NULL); MXGEMM_FMT_MXFP8_E4M3
+ *    and MXGEMM_FMT_MXFP4_E2M1 write codes [rows, K] bytes or [rows, K/2] bytes
+ *    and scales, row-major [rows, K/32] or, with MXGEMM_QUANT_SF_TILED (K a
+ *    multiple of 128), in the tile layout of mxgemm_relayout_scales with
+ *    mxgemm_sf_bytes(rows, K) bytes.
+ *  - Stream-ordered, no allocation, no host synchronisation; every result is the
+ *    same from run to run (no atomics).
+ *  - Errors: MXGEMM_ERR_ARG (a missing pointer, an unknown type, format, flag or
+ *    activation, nothing to write), MXGEMM_ERR_SHAPE, MXGEMM_ERR_ALIGN,
+ *    MXGEMM_ERR_UNSUPPORTED, MXGEMM_ERR_WORKSPACE, MXGEMM_ERR_ARCH,
+ *    MXGEMM_ERR_CUDA; all but the last before anything is launched.
+ */
+
+/*
+ * RMS norm:  h = x + residual (or x);  rstd = 1/sqrt(mean(h^2) + eps);
+ *            y = h * rstd * weight.
+ *   residual: NULL for none.   weight: K values of type weight_dtype.
+ *   h, y:     [rows, K] of type in_dtype, either may be NULL; h may be x or
+ *             residual itself where that is dense.  y is computed from the
+ *             unrounded h.
+ *   codes, scales: MX(y), see above.    rstd: [rows] FP32, or NULL.
+ * K up to 32768 (MXGEMM_ERR_UNSUPPORTED beyond: a row is held on chip).
+ */
+MXGEMM_API int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, const void *residual,
+                              int64_t residual_stride, const void *weight, int weight_dtype, float eps, int64_t rows,
+                              int64_t K, void *h, void *y, int fmt, void *codes, uint8_t *scales, float *rstd,
+                              uint32_t flags, void *stream);
+
+/*
+ * Its gradient.  h and rstd as the forward left them, dy the gradient of y, dh
+ * (or NULL) the gradient that reaches h past the norm:
+ *   p = dy * weight;  dx = rstd * p - h * rstd^3 * mean(p * h) + dh
+ *   dweight[k] = sum over rows of dy * h * rstd          (FP32, K values)
+ * dx is the gradient of x and of the residual alike.  dx may be dh itself where
+ * that is dense.  workspace: mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
+ * bytes (0 for sizes the call refuses), 32-byte aligned, holding nothing between
+ * calls.
+ */
+MXGEMM_API size_t mxgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t K);
+MXGEMM_API int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *h,
+                                       int64_t h_stride, const float *rstd, const void *weight, int weight_dtype,
+                                       const void *dh, int64_t dh_stride, int64_t rows, int64_t K, void *dx,
+                                       float *dweight, void *workspace, size_t ws_bytes, void *stream);
+
+/* Activations of mxgemm_glu. */
+#define MXGEMM_ACT_SILU             1          /* g / (1 + exp(-g))                   */
+#define MXGEMM_ACT_GELU_TANH        2          /* g (1 + tanh(sqrt(2/pi)(g + 0.044715 g^3))) / 2 */
+
+/*
+ * Gated activation  a = act(gate) * up.
+ *   gate, up: [rows, F] with one stride; a product's [rows, 2F] output is passed
+ *             as (p, p + F) with stride 2F.
+ *   y:        [rows, F] of type in_dtype, or NULL.   codes, scales: MX(a).
+ *   kept_codes, kept_scales: both or neither; an 8-bit checkpoint of the inputs
+ *             for mxgemm_glu_backward in 1.03 bytes a value: MXFP8 codes [rows, 2F]
+ *             (gate, then up) and row-major scales [rows, 2F/32].  The output is
+ *             computed from the inputs themselves.
+ */
+MXGEMM_API int mxgemm_glu(int act, int in_dtype, const void *gate, const void *up, int64_t stride, int64_t rows,
+                          int64_t F, void *y, int fmt, void *codes, uint8_t *scales, uint32_t flags,
+                          void *kept_codes, uint8_t *kept_scales, void *stream);
+
+/*
+ * Its gradient, given dy = the gradient of a:
+ *   dgate = dy * up * act'(gate),   dup = dy * act(gate)
+ * from gate and up, or (with those NULL) from the forward's checkpoint.
+ *   dgu:  [rows, 2F] of type in_dtype (dgate, then dup), or NULL.
+ *   codes, scales: MX of that [rows, 2F] matrix (its row length is 2F).
+ *   a:    [rows, F] of type in_dtype: the forward's output computed again, for
+ *         the gradient of the weight that follows; or NULL.
+ */
+MXGEMM_API int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_t dy_stride, const void *gate,
+                                   const void *up, int64_t stride, const void *kept_codes,
+                                   const uint8_t *kept_scales, int64_t rows, int64_t F, void *dgu, int fmt,
+                                   void *codes, uint8_t *scales, uint32_t flags, void *a, void *stream);
+
+/*
+ * Sort token slots by expert.  Token t has topk slots t*topk .. t*topk + topk-1;
+ * expert_ids[s] (int32 or int64, id_bytes 4 or 8) is the slot's expert.
+ *   offsets:     groups + 1 int64: expert e owns rows [offsets[e], offsets[e+1]),
+ *                as mxgemm_grouped_run reads them.
+ *   row_of_slot: the slot's row, slots of one expert in slot order.  A slot whose
+ *                id is outside 0..groups-1 (an expert's capacity was reached, or
+ *                padding) is dropped: its row lies past offsets[groups] and the
+ *                entry is -1 - row.
+ *   slot_of_row: the inverse (rows past offsets[groups] hold the dropped slots),
+ *                or NULL.
+ * slots 1 .. 2^31 - 1, groups 1 .. 512.
+ */
+MXGEMM_API int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t groups, int64_t *offsets,
+                               int32_t *row_of_slot, int32_t *slot_of_row, void *stream);
+
+/*
+ * Write each token's row to the rows of its slots: rows[row_of_slot[s]] = x[s / topk].
+ *   fmt MXGEMM_FMT_MXFP8_E4M3 / MXGEMM_FMT_MXFP4_E2M1: codes and row-major scales
+ *   [tokens*topk, K/32], the A and SA of mxgemm_grouped_run (each token is encoded
+ *   once); MXGEMM_FMT_BF16: BF16 rows, scales NULL.
+ * The rows of dropped slots are zero (scale code 127).  row_of_slot is
+ * mxgemm_moe_sort's; an entry that names no row of the table writes nothing.
+ * Its gradient is mxgemm_moe_combine without weights.
+ */
+MXGEMM_API int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride, int64_t tokens, int64_t topk,
+                                   int64_t K, const int32_t *row_of_slot, int fmt, void *rows, uint8_t *scales,
+                                   void *stream);
+
+/*
+ * Sum the experts' rows back to tokens:
+ *   out[t] = add[t] + sum_j weights[t*topk + j] * y[row_of_slot[t*topk + j]]
+ *   weights: FP32, or NULL for 1.   add: [tokens, N] (the residual stream), or
+ *   NULL; out may be add itself where that is dense.
+ * Dropped slots add nothing: neither their rows nor their weights are read (they
+ * may hold NaN); a token without slots gets add[t] or zero.
+ */
+MXGEMM_API int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride, int64_t tokens, int64_t topk,
+                                  int64_t N, const int32_t *row_of_slot, const float *weights, const void *add,
+                                  int64_t add_stride, void *out, void *stream);
+
+/*
+ * Its gradient:  dy[row_of_slot[s]] = weights[s] * dout[s / topk] (a dropped
+ * slot's row is zero) and dweights[s] = <dout[s / topk], y[row_of_slot[s]]> (FP32,
+ * zero for a dropped slot).
+ */
+MXGEMM_API int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64_t dout_stride, const void *y,
+                                           int64_t y_stride, int64_t tokens, int64_t topk, int64_t N,
+                                           const int32_t *row_of_slot, const float *weights, void *dy,
+                                           float *dweights, void *stream);
+
+/*
  * Scale-placement checker for MXFP4 dot products ("Deciding Scale Placement in
  * MXFP4 Dot Products with Integer Arithmetic", AI-compiler daily digest of
  * 2026-10-22, item 2): for each scale pair (sa[p], sb[p]) (E8M0 codes 0..254)

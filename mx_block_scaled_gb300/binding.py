@@ -1,7 +1,8 @@
 """Thin ctypes binding of libmxgemm.so (include/mxgemm.h), same names as the C ABI.
 
 Argument marshalling only: every step of the GEMM (scale relayout, the tcgen05
-GEMM, the split-K reduce) runs in the library's CUDA kernels.  PyTorch is used
+GEMM, the split-K reduce) and of the operators around it (RMS norm, gated
+activation, expert routing) runs in the library's CUDA kernels.  PyTorch is used
 for device memory and streams.  If the library is missing this module raises
 at import time; there is no fallback implementation.  With the environment
 variable MXGEMM_DEBUG=1 the module loads the debug build (libmxgemm_debug.so:
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 from .build import DEBUG_LIB_PATH, LIB_PATH
 
@@ -50,10 +52,13 @@ MXGEMM_RUN_B_STATIC = 1 << 3
 MXGEMM_IN_F32 = 1
 MXGEMM_IN_BF16 = 2
 MXGEMM_QUANT_SF_TILED = 1 << 0
+MXGEMM_ACT_SILU = 1
+MXGEMM_ACT_GELU_TANH = 2
 
 # (name, restype, argtypes) for every entry point declared in include/mxgemm.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_I = ctypes.c_int
 SIGNATURES = [
     ("mxgemm_plan_create", ctypes.c_int,
      [ctypes.POINTER(ctypes.c_void_p), _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_uint32]),
@@ -77,6 +82,20 @@ SIGNATURES = [
     ("mxgemm_grouped_workspace_bytes", ctypes.c_size_t, [_P]),
     ("mxgemm_grouped_plan_describe", ctypes.c_int, [_P, ctypes.c_char_p, ctypes.c_size_t]),
     ("mxgemm_grouped_run", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, ctypes.c_uint32, _P]),
+    ("mxgemm_rmsnorm", ctypes.c_int,
+     [_I, _P, _I64, _P, _I64, _P, _I, ctypes.c_float, _I64, _I64, _P, _P, _I, _P, _P, _P, ctypes.c_uint32, _P]),
+    ("mxgemm_rmsnorm_backward_workspace_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("mxgemm_rmsnorm_backward", ctypes.c_int,
+     [_I, _P, _I64, _P, _I64, _P, _P, _I, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("mxgemm_glu", ctypes.c_int,
+     [_I, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _P, ctypes.c_uint32, _P, _P, _P]),
+    ("mxgemm_glu_backward", ctypes.c_int,
+     [_I, _I, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _I, _P, _P, ctypes.c_uint32, _P, _P]),
+    ("mxgemm_moe_sort", ctypes.c_int, [_P, _I, _I64, _I64, _P, _P, _P, _P]),
+    ("mxgemm_moe_dispatch", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P]),
+    ("mxgemm_moe_combine", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
+    ("mxgemm_moe_combine_backward", ctypes.c_int,
+     [_I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     ("mxgemm_placement_scan", ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P]),
     ("mxgemm_probe_tensor_rate", ctypes.c_int,
      [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_double), _P]),
@@ -346,6 +365,326 @@ def quantize(x, fmt: int, tiled: bool = False, codes=None, scales=None, stream=N
     _check(mxgemm_quantize(fmt, in_dtype, x.data_ptr(), rows, K, codes.data_ptr(), scales.data_ptr(),
                            MXGEMM_QUANT_SF_TILED if tiled else 0, _stream_handle(stream)), "mxgemm_quantize")
     return codes, scales
+
+
+# ---- row operators around the GEMM ----------------------------------------------
+
+def mxgemm_rmsnorm_backward_workspace_bytes(rows: int, K: int) -> int:
+    return _lib.mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
+
+
+
+class RmsNorm(NamedTuple):
+    h: object
+    y: object
+    codes: object
+    scales: object
+    rstd: object
+
+
+class Glu(NamedTuple):
+    y: object
+    codes: object
+    scales: object
+    kept_codes: object
+    kept_scales: object
+
+
+class GluGrad(NamedTuple):
+    dgu: object
+    codes: object
+    scales: object
+    a: object
+
+
+_IN_DTYPE = {}  # torch dtype -> MXGEMM_IN_*, filled by the first call (torch is imported lazily)
+
+
+def _in_dtype(t, what: str) -> int:
+    if not _IN_DTYPE:
+        import torch
+        _IN_DTYPE.update({torch.float32: MXGEMM_IN_F32, torch.bfloat16: MXGEMM_IN_BF16})
+    d = _IN_DTYPE.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return d
+
+
+def _in_rows(t, like, shape, what: str):
+    """(pointer, row stride) of an input matrix whose rows are contiguous; None -> (0, 0)."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype is not like.dtype or t.device != like.device or t.stride(1) != 1:
+        raise ValueError(f"{what} must be a {tuple(shape)} {like.dtype} tensor on {like.device} with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _dense(t, shape, dtype, device, what: str) -> int:
+    """Pointer of a dense tensor of this shape and type; None -> 0."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _cuda_matrix(t, what: str):
+    if t.dim() != 2 or not t.is_cuda or t.stride(1) != 1:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor with contiguous rows")
+    return t.shape
+
+
+def _mx_out(fmt: int, tiled: bool, rows: int, K: int, codes, scales, device, what: str):
+    """Codes and scales of an MX output, made where they are missing, and their pointers."""
+    import torch
+    if fmt == 0:
+        if codes is not None or scales is not None or tiled:
+            raise ValueError(f"{what}: an MX output needs a format")
+        return None, None, 0, 0
+    kb = K if fmt == MXGEMM_FMT_MXFP8_E4M3 else K // 2
+    if codes is None:
+        codes = torch.empty((rows, kb), dtype=torch.uint8, device=device)
+    if scales is None:
+        scales = torch.empty((mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32), dtype=torch.uint8,
+                             device=device)
+    cp = _dense(codes, (rows, kb), torch.uint8, device, "codes")
+    sp = _dense(scales, (mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32), torch.uint8, device, "scales")
+    return codes, scales, cp, sp
+
+
+def _raw_stream(stream, device) -> int:
+    """Stream handle: `stream`, or torch's current stream on `device`."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def rmsnorm(x, weight, eps: float, residual=None, fmt: int = 0, tiled: bool = False, plain: bool = False, h=None,
+            y=None, codes=None, scales=None, rstd=None, stream=None) -> RmsNorm:
+    """h = x + residual, rstd = 1/sqrt(mean(h^2) + eps), y = h * rstd * weight.
+
+    ``x`` [rows, K] float32 or bfloat16 (rows contiguous, any row stride whose rows
+    stay 32-byte aligned), ``weight`` [K] of either type.  Returns what was asked
+    for: ``h`` (made when there is a residual; may be passed as ``residual`` itself),
+    ``y`` with ``plain=True``, MX ``codes`` and ``scales`` with ``fmt``, and ``rstd``
+    [rows] float32.  Outputs that are passed in are written in place.
+    """
+    import torch
+    rows, K = shape = _cuda_matrix(x, "x")
+    dt, dev = _in_dtype(x, "x"), x.device
+    rp, rs = _in_rows(residual, x, shape, "residual")
+    if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
+    if h is None and residual is not None:
+        h = torch.empty(shape, dtype=x.dtype, device=dev)
+    if y is None and plain:
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    if rstd is None:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, K, codes, scales, dev, "rmsnorm")
+    _check(_lib.mxgemm_rmsnorm(dt, x.data_ptr(), x.stride(0), rp, rs, weight.data_ptr(), _in_dtype(weight, "weight"),
+                               eps, rows, K, _dense(h, shape, x.dtype, dev, "h"), _dense(y, shape, x.dtype, dev, "y"),
+                               fmt, cp, sp, _dense(rstd, (rows,), torch.float32, dev, "rstd"),
+                               MXGEMM_QUANT_SF_TILED if tiled else 0, _raw_stream(stream, dev)), "mxgemm_rmsnorm")
+    return RmsNorm(h, y, codes, scales, rstd)
+
+
+def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of :func:`rmsnorm`: (dx [rows, K], dweight [K] float32).
+
+    ``h`` and ``rstd`` as the forward left them (``h`` is x where there was no
+    residual); ``dh`` is the gradient that reaches h past the norm.  dx is the
+    gradient of x and of the residual.
+    """
+    import torch
+    rows, K = shape = _cuda_matrix(dy, "dy")
+    dt, dev = _in_dtype(dy, "dy"), dy.device
+    hp, hs = _in_rows(h, dy, shape, "h")
+    gp, gs = _in_rows(dh, dy, shape, "dh")
+    if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+    if dweight is None:
+        dweight = torch.empty((K,), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty((mxgemm_rmsnorm_backward_workspace_bytes(rows, K),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _check(_lib.mxgemm_rmsnorm_backward(dt, dy.data_ptr(), dy.stride(0), hp, hs,
+                                        _dense(rstd, (rows,), torch.float32, dev, "rstd"), weight.data_ptr(),
+                                        _in_dtype(weight, "weight"), gp, gs, rows, K,
+                                        _dense(dx, shape, dy.dtype, dev, "dx"),
+                                        _dense(dweight, (K,), torch.float32, dev, "dweight"), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+           "mxgemm_rmsnorm_backward")
+    return dx, dweight
+
+
+def glu(gate, up, act: int, fmt: int = 0, tiled: bool = False, plain: bool = False, keep: bool = False, y=None,
+        codes=None, scales=None, kept_codes=None, kept_scales=None, stream=None) -> Glu:
+    """Gated activation a = act(gate) * up (``act``: MXGEMM_ACT_*).
+
+    ``gate`` and ``up`` [rows, F] with one row stride (the halves of a product's
+    [rows, 2F] output are passed as views).  ``plain=True`` returns a as ``y``,
+    ``fmt`` as MX codes and scales; ``keep=True`` also returns the inputs' 8-bit
+    checkpoint (codes [rows, 2F], scales [rows, 2F/32]) for :func:`glu_backward`.
+    """
+    import torch
+    rows, F = shape = _cuda_matrix(gate, "gate")
+    dt, dev = _in_dtype(gate, "gate"), gate.device
+    up_ptr, up_stride = _in_rows(up, gate, shape, "up")
+    if up_ptr == 0 or (rows > 1 and up_stride != gate.stride(0)):
+        raise ValueError("gate and up must have the same row stride")
+    if y is None and plain:
+        y = torch.empty(shape, dtype=gate.dtype, device=dev)
+    if keep or kept_codes is not None or kept_scales is not None:
+        kept_codes, kept_scales, kc, ks = _mx_out(MXGEMM_FMT_MXFP8_E4M3, False, rows, 2 * F, kept_codes, kept_scales,
+                                                  dev, "glu")
+    else:
+        kc = ks = 0
+    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, F, codes, scales, dev, "glu")
+    _check(_lib.mxgemm_glu(act, dt, gate.data_ptr(), up_ptr, gate.stride(0), rows, F,
+                           _dense(y, shape, gate.dtype, dev, "y"), fmt, cp, sp, MXGEMM_QUANT_SF_TILED if tiled else 0,
+                           kc, ks, _raw_stream(stream, dev)), "mxgemm_glu")
+    return Glu(y, codes, scales, kept_codes, kept_scales)
+
+
+def glu_backward(dy, act: int, gate=None, up=None, kept_codes=None, kept_scales=None, fmt: int = 0,
+                 tiled: bool = False, plain: bool = True, recompute: bool = False, dgu=None, codes=None, scales=None,
+                 a=None, stream=None) -> GluGrad:
+    """Gradient of :func:`glu` from ``gate`` and ``up``, or from its checkpoint.
+
+    Returns ``dgu`` [rows, 2F] (dgate, then dup; not with ``plain=False``), its MX
+    codes and scales with ``fmt`` (row length 2F), and with ``recompute=True`` the
+    forward's output ``a`` [rows, F] again.
+    """
+    import torch
+    rows, F = shape = _cuda_matrix(dy, "dy")
+    dt, dev = _in_dtype(dy, "dy"), dy.device
+    gp, gs = _in_rows(gate, dy, shape, "gate")
+    up_ptr, up_stride = _in_rows(up, dy, shape, "up")
+    if rows > 1 and up_stride != gs:
+        raise ValueError("gate and up must have the same row stride")
+    if dgu is None and plain:
+        dgu = torch.empty((rows, 2 * F), dtype=dy.dtype, device=dev)
+    if a is None and recompute:
+        a = torch.empty(shape, dtype=dy.dtype, device=dev)
+    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, 2 * F, codes, scales, dev, "glu_backward")
+    _check(_lib.mxgemm_glu_backward(act, dt, dy.data_ptr(), dy.stride(0), gp, up_ptr, gs,
+                                    _dense(kept_codes, (rows, 2 * F), torch.uint8, dev, "kept_codes"),
+                                    _dense(kept_scales, (rows, F // 16), torch.uint8, dev, "kept_scales"), rows, F,
+                                    _dense(dgu, (rows, 2 * F), dy.dtype, dev, "dgu"), fmt, cp, sp,
+                                    MXGEMM_QUANT_SF_TILED if tiled else 0, _dense(a, shape, dy.dtype, dev, "a"),
+                                    _raw_stream(stream, dev)), "mxgemm_glu_backward")
+    return GluGrad(dgu, codes, scales, a)
+
+
+def moe_sort(expert_ids, groups: int, offsets=None, row_of_slot=None, slot_of_row=None, stream=None):
+    """Sort token slots by expert: (offsets [groups + 1] int64, row_of_slot, slot_of_row int32 [slots]).
+
+    ``expert_ids``: contiguous CUDA int32 or int64, any shape ([tokens, topk] as a
+    router leaves them).  Ids outside 0..groups-1 drop their slot: its row lies past
+    offsets[groups] and its row_of_slot entry is -1 - row.
+    """
+    import torch
+    dev, n = expert_ids.device, expert_ids.numel()
+    if not expert_ids.is_cuda or not expert_ids.is_contiguous() or expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expert_ids must be a contiguous CUDA int32 or int64 tensor")
+    if offsets is None:
+        offsets = torch.empty((groups + 1,), dtype=torch.int64, device=dev)
+    if row_of_slot is None:
+        row_of_slot = torch.empty((n,), dtype=torch.int32, device=dev)
+    if slot_of_row is None:
+        slot_of_row = torch.empty((n,), dtype=torch.int32, device=dev)
+    _check(_lib.mxgemm_moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), n, groups,
+                                _dense(offsets, (groups + 1,), torch.int64, dev, "offsets"),
+                                _dense(row_of_slot, (n,), torch.int32, dev, "row_of_slot"),
+                                _dense(slot_of_row, (n,), torch.int32, dev, "slot_of_row"), _raw_stream(stream, dev)),
+           "mxgemm_moe_sort")
+    return offsets, row_of_slot, slot_of_row
+
+
+def _slots(row_of_slot, tokens: int, device) -> int:
+    """Slots per token of a row_of_slot table."""
+    n = row_of_slot.numel()
+    if tokens < 1 or n < tokens or n % tokens:
+        raise ValueError("row_of_slot must hold the same number of slots for every token")
+    return n // tokens
+
+
+def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None, stream=None):
+    """rows[row_of_slot[s]] = x[s // topk]: (rows, scales) in expert order.
+
+    ``fmt`` MXFP8 / MXFP4: each token encoded once, codes [slots, K] or [slots, K/2]
+    and row-major scales [slots, K/32], ready for :class:`GroupedPlan`;
+    MXGEMM_FMT_BF16: bfloat16 rows, scales None.  Rows of dropped slots are zero.
+    """
+    import torch
+    tokens, K = _cuda_matrix(x, "x")
+    dt, dev, n = _in_dtype(x, "x"), x.device, row_of_slot.numel()
+    topk = _slots(row_of_slot, tokens, dev)
+    index = _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot")
+    if fmt == MXGEMM_FMT_BF16:
+        if rows is None:
+            rows = torch.empty((n, K), dtype=torch.bfloat16, device=dev)
+        rp, sp = _dense(rows, (n, K), torch.bfloat16, dev, "rows"), 0
+        if scales is not None:
+            raise ValueError("BF16 rows have no scales")
+    else:
+        rows, scales, rp, sp = _mx_out(fmt, False, n, K, rows, scales, dev, "moe_dispatch")
+    _check(_lib.mxgemm_moe_dispatch(dt, x.data_ptr(), x.stride(0), tokens, topk, K, index, fmt, rp, sp,
+                                    _raw_stream(stream, dev)), "mxgemm_moe_dispatch")
+    return rows, scales
+
+
+def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None, stream=None):
+    """out[t] = add[t] + sum_j weights[t, j] * y[row_of_slot[t * topk + j]]  ([tokens, N], y's type).
+
+    Dropped slots add nothing, whatever their rows of ``y`` and their weights hold.
+    Without ``weights`` (all 1) this is the gradient of :func:`moe_dispatch`.
+    """
+    import torch
+    n, N = _cuda_matrix(y, "y")
+    dt, dev = _in_dtype(y, "y"), y.device
+    if topk < 1 or n % topk or row_of_slot.numel() != n:
+        raise ValueError("y must have one row for each of the tokens * topk slots")
+    tokens = n // topk
+    index = _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot")
+    ap, as_ = _in_rows(add, y, (tokens, N), "add")
+    if out is None:
+        out = torch.empty((tokens, N), dtype=y.dtype, device=dev)
+    wp = 0 if weights is None else _dense(weights.view(-1), (n,), torch.float32, dev, "weights")
+    _check(_lib.mxgemm_moe_combine(dt, y.data_ptr(), y.stride(0), tokens, topk, N, index, wp, ap, as_,
+                                   _dense(out, (tokens, N), y.dtype, dev, "out"), _raw_stream(stream, dev)),
+           "mxgemm_moe_combine")
+    return out
+
+
+def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None, stream=None):
+    """Gradients of :func:`moe_combine`: (dy [tokens * topk, N], dweights, shaped as ``weights``, float32).
+
+    A dropped slot's row of dy and its weight's gradient are zero.
+    """
+    import torch
+    tokens, N = _cuda_matrix(dout, "dout")
+    dt, dev, n = _in_dtype(dout, "dout"), dout.device, row_of_slot.numel()
+    topk = _slots(row_of_slot, tokens, dev)
+    yp, ys = _in_rows(y, dout, (n, N), "y")
+    if yp == 0:
+        raise ValueError("y is missing")
+    if dy is None:
+        dy = torch.empty((n, N), dtype=y.dtype, device=dev)
+    if dweights is None:
+        dweights = torch.empty(weights.shape, dtype=torch.float32, device=dev)
+    _check(_lib.mxgemm_moe_combine_backward(dt, dout.data_ptr(), dout.stride(0), yp, ys, tokens, topk, N,
+                                            _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot"),
+                                            _dense(weights.view(-1), (n,), torch.float32, dev, "weights"),
+                                            _dense(dy, (n, N), y.dtype, dev, "dy"),
+                                            _dense(dweights.view(-1), (n,), torch.float32, dev, "dweights"),
+                                            _raw_stream(stream, dev)), "mxgemm_moe_combine_backward")
+    return dy, dweights
 
 
 def mxgemm_placement_scan(k: int, sa_ptr: int, sb_ptr: int, npairs: int, counts_ptr: int, first_ptr: int,

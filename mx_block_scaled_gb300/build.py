@@ -1,12 +1,13 @@
 """Build libmxgemm.so and libmxgemm_debug.so in-tree with nvcc for sm_103a.
 
-Seven translation units (host API + relayout/reduce kernels, MXFP8 GEMM,
+Eleven translation units (host API + relayout/reduce kernels, MXFP8 GEMM,
 MXFP4 GEMM, BF16 GEMM, MX quantiser, scale-placement checker, tensor-pipe
-probe) are compiled in parallel and linked into
+probe, and the row operators: their host API, RMS norm, gated activation,
+expert routing) are compiled in parallel and linked into
 ``mx_block_scaled_gb300/lib/libmxgemm.so``.  The four that hold the GEMM
 kernels and their host code are compiled a second time with MXGEMM_DEBUG
 (bounds-checked loads and stores, NaN-filled C, synchronous status) and linked
-with the other three into ``lib/libmxgemm_debug.so``.
+with the others into ``lib/libmxgemm_debug.so``.
 """
 from __future__ import annotations
 
@@ -24,7 +25,8 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmxgemm.so")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libmxgemm_debug.so")
 
-SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu", "quantize.cu", "placement.cu", "probe.cu"]
+SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu", "quantize.cu", "placement.cu", "probe.cu",
+           "ops.cu", "norm.cu", "glu.cu", "moe.cu"]
 DEBUG_SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu"]  # the rest is shared
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1,0 +1,182 @@
+"""Gated activation with MX output and 8-bit checkpoint, and its gradient, on the
+GPU against the 64-bit definition (row_ops_ref.py), through the binding."""
+import numpy as np
+import pytest
+
+import row_ops_ref as ref
+from gpu_util import lib
+from test_rmsnorm_gpu import _dtype, _make, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    lib()
+
+
+def _scales(t, tiled, rows, K):
+    s = t.cpu().numpy()
+    return ref.untile(s, rows, K) if tiled else s
+
+
+@pytest.mark.parametrize("act", [ref.ACT_SILU, ref.ACT_GELU])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,tiled", [(0, False), (1, False), (1, True), (2, False), (2, True)])
+@pytest.mark.parametrize("rows,F,keep", [(1, 128, True), (5, 640, False), (131, 384, True), (2, 14336, True)])
+def test_forward(oracle_mod, act, dtype, fmt, tiled, rows, F, keep):
+    b = lib()
+    rng = np.random.default_rng([rows, F, fmt, act])
+    gu, gu64 = _make(rng, (rows, 2 * F), _dtype(dtype), 3.0)
+    plain = fmt == 0 or rows == 5
+    out = b.glu(gu[:, :F], gu[:, F:], act, fmt=fmt, tiled=tiled, plain=plain, keep=keep)
+    a, err = ref.glu(gu64[:, :F], gu64[:, F:], act)
+    if plain:
+        ref.assert_near(_np(out.y), a, err, dtype == "bf16", "a")
+    if fmt:
+        ref.assert_mx(out.codes.cpu().numpy(), _scales(out.scales, tiled, rows, F), a, err + ref.TINY_F32, fmt, "MX(a)")
+    if keep:  # the checkpoint is the quantiser on the inputs, bit for bit
+        codes, scales = oracle_mod.quantize(1, gu.float().cpu().numpy(), oracle_mod.IN_F32)
+        assert (out.kept_codes.cpu().numpy() == codes).all() and (out.kept_scales.cpu().numpy() == scales).all()
+
+
+@pytest.mark.parametrize("F", [32, 96, 160, 1568])
+def test_forward_without_whole_tiles(F):
+    b = lib()
+    rng = np.random.default_rng(F)
+    gu, gu64 = _make(rng, (19, 2 * F), _dtype("bf16"), 2.0)
+    for fmt in (1, 2):
+        out = b.glu(gu[:, :F], gu[:, F:], ref.ACT_SILU, fmt=fmt, keep=True)
+        a, err = ref.glu(gu64[:, :F], gu64[:, F:], ref.ACT_SILU)
+        ref.assert_mx(out.codes.cpu().numpy(), out.scales.cpu().numpy(), a, err, fmt, "MX(a)")
+
+
+@pytest.mark.parametrize("act", [ref.ACT_SILU, ref.ACT_GELU])
+def test_far_arguments(act):
+    """Gates far to both sides, where the exponential leaves FP32, and non-finite ones."""
+    import torch
+    b = lib()
+    g = np.zeros((2, 64), np.float32)
+    g[0] = np.concatenate([np.linspace(-120, 120, 56), [1e4, -1e4, 1e19, -1e19, 1e25, -1e25, -0.0, 0.0]])
+    g[1, :3] = [np.nan, np.inf, -np.inf]
+    u = np.ones((2, 64), np.float32)
+    gd, ud = torch.from_numpy(g).cuda(), torch.from_numpy(u).cuda()
+    out = b.glu(gd, ud, act, plain=True)
+    with np.errstate(all="ignore"):
+        a, err = ref.glu(g.astype(np.float64), u.astype(np.float64), act)
+    ref.assert_near(_np(out.y)[0], a[0], err[0], False, "a")
+    got = _np(out.y)[1]
+    assert np.isnan(got[0]) and got[1] == np.inf and (got[3:] == 0).all()  # -inf * 0 is NaN or -0
+    dgu = _np(b.glu_backward(ud, act, gate=gd, up=ud).dgu)
+    far = np.abs(g[0]) >= 1e4
+    assert np.array_equal(dgu[0, :64][far], (g[0][far] > 0).astype(float)), "slopes far out are 0 and 1"
+    with np.errstate(all="ignore"):
+        dg, e, du, ed = ref.glu_backward(u[:1].astype(np.float64), g[:1].astype(np.float64), u[:1].astype(np.float64),
+                                         act)
+    near = ~far
+    ref.assert_near(dgu[0, :64][near], dg[0][near], e[0][near], False, "dgate")
+    ref.assert_near(dgu[0, 64:][near], du[0][near], ed[0][near], False, "dup")
+
+
+@pytest.mark.parametrize("act", [ref.ACT_SILU, ref.ACT_GELU])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("fmt,tiled,rows,F", [
+    (0, False, 1, 32), (0, False, 7, 608), (1, False, 33, 96), (1, True, 130, 192), (1, True, 3, 1024),
+    (2, False, 6, 160), (2, True, 129, 64), (2, False, 5, 512),
+])
+def test_backward(act, dtype, kept, fmt, tiled, rows, F):
+    b = lib()
+    rng = np.random.default_rng([rows, F, fmt, act])
+    dt, bf16 = _dtype(dtype), dtype == "bf16"
+    gu, gu64 = _make(rng, (rows, 2 * F), dt, 2.0)
+    dy, dy64 = _make(rng, (rows, F), dt)
+    src = dict(gate=gu[:, :F], up=gu[:, F:])
+    if kept:
+        f = b.glu(gu[:, :F], gu[:, F:], act, keep=True)
+        src = dict(kept_codes=f.kept_codes, kept_scales=f.kept_scales)
+        sc = np.exp2(f.kept_scales.cpu().numpy().astype(np.float64) - 127)
+        gu64 = ref.decode_codes(f.kept_codes.cpu().numpy(), 1) * np.repeat(sc, 32, axis=1)
+    g64, u64 = gu64[:, :F], gu64[:, F:]
+    out = b.glu_backward(dy, act, fmt=fmt, tiled=tiled, recompute=True, **src)
+    dg, edg, du, edu = ref.glu_backward(dy64, g64, u64, act)
+    ref.assert_near(_np(out.dgu)[:, :F], dg, edg, bf16, "dgate")
+    ref.assert_near(_np(out.dgu)[:, F:], du, edu, bf16, "dup")
+    a, ea = ref.glu(g64, u64, act)
+    ref.assert_near(_np(out.a), a, ea, bf16, "a")
+    if fmt:
+        both, err = np.concatenate([dg, du], 1), np.concatenate([edg, edu], 1) + ref.TINY_F32
+        ref.assert_mx(out.codes.cpu().numpy(), _scales(out.scales, tiled, rows, 2 * F), both, err, fmt, "MX(dgu)")
+        only = b.glu_backward(dy, act, fmt=fmt, tiled=tiled, plain=False, **src)
+        assert only.dgu is None and (only.codes == out.codes).all() and (only.scales == out.scales).all()
+
+
+@pytest.mark.parametrize("act", [ref.ACT_SILU, ref.ACT_GELU])
+def test_gradient_against_differences(act):
+    b = lib()
+    rng = np.random.default_rng(act)
+    F = 96
+    gu, gu64 = _make(rng, (4, 2 * F), _dtype("f32"), 2.0)
+    dy, dy64 = _make(rng, (4, F), _dtype("f32"))
+    dgu = _np(b.glu_backward(dy, act, gate=gu[:, :F], up=gu[:, F:]).dgu)
+    v, e = rng.standard_normal((4, 2 * F)), 1e-5
+    loss = lambda z: (ref.glu(z[:, :F], z[:, F:], act)[0] * dy64).sum()  # noqa: E731
+    _, edg, _, edu = ref.glu_backward(dy64, gu64[:, :F], gu64[:, F:], act)
+    lim = (np.concatenate([edg, edu], 1) * np.abs(v)).sum() + ref.U * np.abs(dgu * v).sum() + 1e-8 * v.size
+    assert abs((loss(gu64 + e * v) - loss(gu64 - e * v)) / (2 * e) - (dgu * v).sum()) < lim
+
+
+def test_checkpoint_gradient_is_near_the_exact_one():
+    """E4M3 keeps each input to within half an ulp (2^-4 of its magnitude, or of its
+    block's largest where that is subnormal): the gradient moves by the slopes times that."""
+    b = lib()
+    rng = np.random.default_rng(12)
+    F = 512
+    gu, gu64 = _make(rng, (16, 2 * F), _dtype("bf16"))
+    dy, dy64 = _make(rng, (16, F), _dtype("bf16"))
+    f = b.glu(gu[:, :F], gu[:, F:], ref.ACT_SILU, keep=True)
+    got = _np(b.glu_backward(dy, ref.ACT_SILU, kept_codes=f.kept_codes, kept_scales=f.kept_scales).dgu)
+    dg, _, du, _ = ref.glu_backward(dy64, gu64[:, :F], gu64[:, F:], ref.ACT_SILU)
+    want = np.concatenate([dg, du], 1)
+    # |act'| <= 1.1, |act''| <= 0.5: relative to |dy| (|u| + |g|) an eighth of 2^-1
+    assert np.linalg.norm(got - want) < 2.0 ** -4 * 1.6 * np.linalg.norm(
+        np.concatenate([np.abs(dy64) * (np.abs(gu64[:, F:]) + np.abs(gu64[:, :F] * gu64[:, F:])),
+                        np.abs(dy64 * gu64[:, :F])], 1))
+
+
+def test_separate_tensors_strides_and_guards():
+    import torch
+    b = lib()
+    rng = np.random.default_rng(3)
+    rows, F = 11, 224
+    gw, gw64 = _make(rng, (rows, F + 160), _dtype("bf16"))
+    uw, uw64 = _make(rng, (rows, F + 160), _dtype("bf16"))
+    pad = 64
+    codes = torch.full((rows * F + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    kept = torch.full((rows * 2 * F + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = b.glu(gw[:, 32:32 + F], uw[:, 160:], ref.ACT_SILU, fmt=1, codes=codes[pad:-pad].view(rows, F), keep=True,
+                kept_codes=kept[pad:-pad].view(rows, 2 * F))
+    a, err = ref.glu(gw64[:, 32:32 + F], uw64[:, 160:], ref.ACT_SILU)
+    ref.assert_mx(out.codes.cpu().numpy(), out.scales.cpu().numpy(), a, err, 1, "MX(a)")
+    for t in (codes, kept):
+        assert (t[:pad] == 0xA5).all() and (t[-pad:] == 0xA5).all()
+    with pytest.raises(ValueError):
+        b.glu(gw[:, :F], uw[:, :F].contiguous(), ref.ACT_SILU, plain=True)     # two strides
+
+
+def test_offsets_past_32_bits():
+    import torch
+    b = lib()
+    rows, F = (1 << 31) // (2 * 14336) + 9, 14336
+    gu = torch.full((rows, 2 * F), 0.5, dtype=torch.bfloat16, device="cuda")
+    gu[-8:] = torch.randn((8, 2 * F), device="cuda").to(torch.bfloat16)
+    out = b.glu(gu[:, :F], gu[:, F:], ref.ACT_SILU, fmt=1, keep=True)
+    tail = b.glu(gu[-8:, :F], gu[-8:, F:], ref.ACT_SILU, fmt=1, keep=True)
+    for name in ("codes", "scales", "kept_codes", "kept_scales"):
+        assert torch.equal(getattr(out, name)[-8:], getattr(tail, name)), name
+    dy = torch.ones((rows, F), dtype=torch.bfloat16, device="cuda")
+    full = b.glu_backward(dy, ref.ACT_SILU, kept_codes=out.kept_codes, kept_scales=out.kept_scales)
+    part = b.glu_backward(dy[-8:], ref.ACT_SILU, kept_codes=tail.kept_codes, kept_scales=tail.kept_scales)
+    assert torch.equal(full.dgu[-8:], part.dgu)
