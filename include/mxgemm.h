@@ -542,10 +542,15 @@ MXGEMM_API int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_
  *                entry is -1 - row.
  *   slot_of_row: the inverse (rows past offsets[groups] hold the dropped slots),
  *                or NULL.
+ *   workspace:   mxgemm_moe_sort_workspace_bytes(slots, groups) bytes (0 for few
+ *                slots, and for sizes the call refuses; NULL then), 16-byte
+ *                aligned, holding nothing between calls.
  * slots 1 .. 2^31 - 1, groups 1 .. 512.
  */
+MXGEMM_API size_t mxgemm_moe_sort_workspace_bytes(int64_t slots, int64_t groups);
 MXGEMM_API int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t groups, int64_t *offsets,
-                               int32_t *row_of_slot, int32_t *slot_of_row, void *stream);
+                               int32_t *row_of_slot, int32_t *slot_of_row, void *workspace, size_t ws_bytes,
+                               void *stream);
 
 /*
  * Write each token's row to the rows of its slots: rows[row_of_slot[s]] = x[s / topk].

@@ -11,6 +11,7 @@ bounds-checked kernels, NaN-filled C, synchronous status) instead.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -91,7 +92,8 @@ SIGNATURES = [
      [_I, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _P, ctypes.c_uint32, _P, _P, _P]),
     ("mxgemm_glu_backward", ctypes.c_int,
      [_I, _I, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _I, _P, _P, ctypes.c_uint32, _P, _P]),
-    ("mxgemm_moe_sort", ctypes.c_int, [_P, _I, _I64, _I64, _P, _P, _P, _P]),
+    ("mxgemm_moe_sort_workspace_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("mxgemm_moe_sort", ctypes.c_int, [_P, _I, _I64, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("mxgemm_moe_dispatch", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P]),
     ("mxgemm_moe_combine", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
     ("mxgemm_moe_combine_backward", ctypes.c_int,
@@ -368,10 +370,17 @@ def quantize(x, fmt: int, tiled: bool = False, codes=None, scales=None, stream=N
 
 
 # ---- row operators around the GEMM ----------------------------------------------
+#
+# Outputs that are not passed in are made; everything runs on torch's current
+# stream, or on `stream=`.
 
 def mxgemm_rmsnorm_backward_workspace_bytes(rows: int, K: int) -> int:
     return _lib.mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
 
+
+
+def mxgemm_moe_sort_workspace_bytes(slots: int, groups: int) -> int:
+    return _lib.mxgemm_moe_sort_workspace_bytes(slots, groups)
 
 
 class RmsNorm(NamedTuple):
@@ -428,6 +437,27 @@ def _dense(t, shape, dtype, device, what: str) -> int:
     return t.data_ptr()
 
 
+def _flat(t, n: int, dtype, device, what: str) -> int:
+    """Pointer of a dense tensor of n elements, whatever its shape."""
+    if t.numel() != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _workspace(t, need: int, device):
+    """(pointer, bytes) of the caller's workspace, or of one made for this call.  Memory
+    that torch's allocator takes back is reused in stream order, so a workspace may be
+    let go once the call has enqueued its kernels on the current stream."""
+    if t is None:
+        if need == 0:
+            return 0, 0
+        import torch
+        t = torch.empty((need,), dtype=torch.uint8, device=device)
+    elif t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _cuda_matrix(t, what: str):
     if t.dim() != 2 or not t.is_cuda or t.stride(1) != 1:
         raise ValueError(f"{what} must be a 2-D CUDA tensor with contiguous rows")
@@ -441,27 +471,39 @@ def _mx_out(fmt: int, tiled: bool, rows: int, K: int, codes, scales, device, wha
         if codes is not None or scales is not None or tiled:
             raise ValueError(f"{what}: an MX output needs a format")
         return None, None, 0, 0
-    kb = K if fmt == MXGEMM_FMT_MXFP8_E4M3 else K // 2
+    u8 = torch.uint8
+    shape = (rows, K if fmt == MXGEMM_FMT_MXFP8_E4M3 else K // 2)
+    sf_shape = (mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32)
     if codes is None:
-        codes = torch.empty((rows, kb), dtype=torch.uint8, device=device)
+        codes = torch.empty(shape, dtype=u8, device=device)
     if scales is None:
-        scales = torch.empty((mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32), dtype=torch.uint8,
-                             device=device)
-    cp = _dense(codes, (rows, kb), torch.uint8, device, "codes")
-    sp = _dense(scales, (mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32), torch.uint8, device, "scales")
-    return codes, scales, cp, sp
+        scales = torch.empty(sf_shape, dtype=u8, device=device)
+    return codes, scales, _dense(codes, shape, u8, device, "codes"), _dense(scales, sf_shape, u8, device, "scales")
 
 
-def _raw_stream(stream, device) -> int:
-    """Stream handle: `stream`, or torch's current stream on `device`."""
-    if stream is not None:
-        return stream.cuda_stream
+def _raw_stream(device) -> int:
+    """Handle of torch's current stream on `device` (read without making a Stream
+    object: 0.1 us instead of 2)."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _on_stream(f):
+    """`stream=` runs the whole call, its allocations included, with that stream current:
+    memory that torch hands out belongs to the stream that the kernels run on."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        import torch
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
+
+
+@_on_stream
 def rmsnorm(x, weight, eps: float, residual=None, fmt: int = 0, tiled: bool = False, plain: bool = False, h=None,
-            y=None, codes=None, scales=None, rstd=None, stream=None) -> RmsNorm:
+            y=None, codes=None, scales=None, rstd=None) -> RmsNorm:
     """h = x + residual, rstd = 1/sqrt(mean(h^2) + eps), y = h * rstd * weight.
 
     ``x`` [rows, K] float32 or bfloat16 (rows contiguous, any row stride whose rows
@@ -486,11 +528,12 @@ def rmsnorm(x, weight, eps: float, residual=None, fmt: int = 0, tiled: bool = Fa
     _check(_lib.mxgemm_rmsnorm(dt, x.data_ptr(), x.stride(0), rp, rs, weight.data_ptr(), _in_dtype(weight, "weight"),
                                eps, rows, K, _dense(h, shape, x.dtype, dev, "h"), _dense(y, shape, x.dtype, dev, "y"),
                                fmt, cp, sp, _dense(rstd, (rows,), torch.float32, dev, "rstd"),
-                               MXGEMM_QUANT_SF_TILED if tiled else 0, _raw_stream(stream, dev)), "mxgemm_rmsnorm")
+                               MXGEMM_QUANT_SF_TILED if tiled else 0, _raw_stream(dev)), "mxgemm_rmsnorm")
     return RmsNorm(h, y, codes, scales, rstd)
 
 
-def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+@_on_stream
+def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None):
     """Gradients of :func:`rmsnorm`: (dx [rows, K], dweight [K] float32).
 
     ``h`` and ``rstd`` as the forward left them (``h`` is x where there was no
@@ -508,22 +551,19 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, worksp
         dx = torch.empty(shape, dtype=dy.dtype, device=dev)
     if dweight is None:
         dweight = torch.empty((K,), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty((mxgemm_rmsnorm_backward_workspace_bytes(rows, K),), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    wp, ws = _workspace(workspace, mxgemm_rmsnorm_backward_workspace_bytes(rows, K), dev)
     _check(_lib.mxgemm_rmsnorm_backward(dt, dy.data_ptr(), dy.stride(0), hp, hs,
                                         _dense(rstd, (rows,), torch.float32, dev, "rstd"), weight.data_ptr(),
                                         _in_dtype(weight, "weight"), gp, gs, rows, K,
                                         _dense(dx, shape, dy.dtype, dev, "dx"),
-                                        _dense(dweight, (K,), torch.float32, dev, "dweight"), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
-           "mxgemm_rmsnorm_backward")
+                                        _dense(dweight, (K,), torch.float32, dev, "dweight"), wp, ws,
+                                        _raw_stream(dev)), "mxgemm_rmsnorm_backward")
     return dx, dweight
 
 
+@_on_stream
 def glu(gate, up, act: int, fmt: int = 0, tiled: bool = False, plain: bool = False, keep: bool = False, y=None,
-        codes=None, scales=None, kept_codes=None, kept_scales=None, stream=None) -> Glu:
+        codes=None, scales=None, kept_codes=None, kept_scales=None) -> Glu:
     """Gated activation a = act(gate) * up (``act``: MXGEMM_ACT_*).
 
     ``gate`` and ``up`` [rows, F] with one row stride (the halves of a product's
@@ -547,13 +587,14 @@ def glu(gate, up, act: int, fmt: int = 0, tiled: bool = False, plain: bool = Fal
     codes, scales, cp, sp = _mx_out(fmt, tiled, rows, F, codes, scales, dev, "glu")
     _check(_lib.mxgemm_glu(act, dt, gate.data_ptr(), up_ptr, gate.stride(0), rows, F,
                            _dense(y, shape, gate.dtype, dev, "y"), fmt, cp, sp, MXGEMM_QUANT_SF_TILED if tiled else 0,
-                           kc, ks, _raw_stream(stream, dev)), "mxgemm_glu")
+                           kc, ks, _raw_stream(dev)), "mxgemm_glu")
     return Glu(y, codes, scales, kept_codes, kept_scales)
 
 
+@_on_stream
 def glu_backward(dy, act: int, gate=None, up=None, kept_codes=None, kept_scales=None, fmt: int = 0,
                  tiled: bool = False, plain: bool = True, recompute: bool = False, dgu=None, codes=None, scales=None,
-                 a=None, stream=None) -> GluGrad:
+                 a=None) -> GluGrad:
     """Gradient of :func:`glu` from ``gate`` and ``up``, or from its checkpoint.
 
     Returns ``dgu`` [rows, 2F] (dgate, then dup; not with ``plain=False``), its MX
@@ -577,11 +618,12 @@ def glu_backward(dy, act: int, gate=None, up=None, kept_codes=None, kept_scales=
                                     _dense(kept_scales, (rows, F // 16), torch.uint8, dev, "kept_scales"), rows, F,
                                     _dense(dgu, (rows, 2 * F), dy.dtype, dev, "dgu"), fmt, cp, sp,
                                     MXGEMM_QUANT_SF_TILED if tiled else 0, _dense(a, shape, dy.dtype, dev, "a"),
-                                    _raw_stream(stream, dev)), "mxgemm_glu_backward")
+                                    _raw_stream(dev)), "mxgemm_glu_backward")
     return GluGrad(dgu, codes, scales, a)
 
 
-def moe_sort(expert_ids, groups: int, offsets=None, row_of_slot=None, slot_of_row=None, stream=None):
+@_on_stream
+def moe_sort(expert_ids, groups: int, offsets=None, row_of_slot=None, slot_of_row=None, workspace=None):
     """Sort token slots by expert: (offsets [groups + 1] int64, row_of_slot, slot_of_row int32 [slots]).
 
     ``expert_ids``: contiguous CUDA int32 or int64, any shape ([tokens, topk] as a
@@ -598,15 +640,16 @@ def moe_sort(expert_ids, groups: int, offsets=None, row_of_slot=None, slot_of_ro
         row_of_slot = torch.empty((n,), dtype=torch.int32, device=dev)
     if slot_of_row is None:
         slot_of_row = torch.empty((n,), dtype=torch.int32, device=dev)
+    wp, ws = _workspace(workspace, mxgemm_moe_sort_workspace_bytes(n, groups), dev)
     _check(_lib.mxgemm_moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), n, groups,
                                 _dense(offsets, (groups + 1,), torch.int64, dev, "offsets"),
-                                _dense(row_of_slot, (n,), torch.int32, dev, "row_of_slot"),
-                                _dense(slot_of_row, (n,), torch.int32, dev, "slot_of_row"), _raw_stream(stream, dev)),
-           "mxgemm_moe_sort")
+                                _flat(row_of_slot, n, torch.int32, dev, "row_of_slot"),
+                                _flat(slot_of_row, n, torch.int32, dev, "slot_of_row"), wp, ws,
+                                _raw_stream(dev)), "mxgemm_moe_sort")
     return offsets, row_of_slot, slot_of_row
 
 
-def _slots(row_of_slot, tokens: int, device) -> int:
+def _slots(row_of_slot, tokens: int) -> int:
     """Slots per token of a row_of_slot table."""
     n = row_of_slot.numel()
     if tokens < 1 or n < tokens or n % tokens:
@@ -614,7 +657,8 @@ def _slots(row_of_slot, tokens: int, device) -> int:
     return n // tokens
 
 
-def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None, stream=None):
+@_on_stream
+def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None):
     """rows[row_of_slot[s]] = x[s // topk]: (rows, scales) in expert order.
 
     ``fmt`` MXFP8 / MXFP4: each token encoded once, codes [slots, K] or [slots, K/2]
@@ -624,8 +668,8 @@ def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None, stream=None):
     import torch
     tokens, K = _cuda_matrix(x, "x")
     dt, dev, n = _in_dtype(x, "x"), x.device, row_of_slot.numel()
-    topk = _slots(row_of_slot, tokens, dev)
-    index = _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot")
+    topk = _slots(row_of_slot, tokens)
+    index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
     if fmt == MXGEMM_FMT_BF16:
         if rows is None:
             rows = torch.empty((n, K), dtype=torch.bfloat16, device=dev)
@@ -635,11 +679,12 @@ def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None, stream=None):
     else:
         rows, scales, rp, sp = _mx_out(fmt, False, n, K, rows, scales, dev, "moe_dispatch")
     _check(_lib.mxgemm_moe_dispatch(dt, x.data_ptr(), x.stride(0), tokens, topk, K, index, fmt, rp, sp,
-                                    _raw_stream(stream, dev)), "mxgemm_moe_dispatch")
+                                    _raw_stream(dev)), "mxgemm_moe_dispatch")
     return rows, scales
 
 
-def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None, stream=None):
+@_on_stream
+def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None):
     """out[t] = add[t] + sum_j weights[t, j] * y[row_of_slot[t * topk + j]]  ([tokens, N], y's type).
 
     Dropped slots add nothing, whatever their rows of ``y`` and their weights hold.
@@ -651,18 +696,19 @@ def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None, str
     if topk < 1 or n % topk or row_of_slot.numel() != n:
         raise ValueError("y must have one row for each of the tokens * topk slots")
     tokens = n // topk
-    index = _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot")
+    index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
     ap, as_ = _in_rows(add, y, (tokens, N), "add")
     if out is None:
         out = torch.empty((tokens, N), dtype=y.dtype, device=dev)
-    wp = 0 if weights is None else _dense(weights.view(-1), (n,), torch.float32, dev, "weights")
+    wp = 0 if weights is None else _flat(weights, n, torch.float32, dev, "weights")
     _check(_lib.mxgemm_moe_combine(dt, y.data_ptr(), y.stride(0), tokens, topk, N, index, wp, ap, as_,
-                                   _dense(out, (tokens, N), y.dtype, dev, "out"), _raw_stream(stream, dev)),
+                                   _dense(out, (tokens, N), y.dtype, dev, "out"), _raw_stream(dev)),
            "mxgemm_moe_combine")
     return out
 
 
-def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None, stream=None):
+@_on_stream
+def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None):
     """Gradients of :func:`moe_combine`: (dy [tokens * topk, N], dweights, shaped as ``weights``, float32).
 
     A dropped slot's row of dy and its weight's gradient are zero.
@@ -670,7 +716,7 @@ def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None, 
     import torch
     tokens, N = _cuda_matrix(dout, "dout")
     dt, dev, n = _in_dtype(dout, "dout"), dout.device, row_of_slot.numel()
-    topk = _slots(row_of_slot, tokens, dev)
+    topk = _slots(row_of_slot, tokens)
     yp, ys = _in_rows(y, dout, (n, N), "y")
     if yp == 0:
         raise ValueError("y is missing")
@@ -679,11 +725,11 @@ def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None, 
     if dweights is None:
         dweights = torch.empty(weights.shape, dtype=torch.float32, device=dev)
     _check(_lib.mxgemm_moe_combine_backward(dt, dout.data_ptr(), dout.stride(0), yp, ys, tokens, topk, N,
-                                            _dense(row_of_slot.view(-1), (n,), torch.int32, dev, "row_of_slot"),
-                                            _dense(weights.view(-1), (n,), torch.float32, dev, "weights"),
+                                            _flat(row_of_slot, n, torch.int32, dev, "row_of_slot"),
+                                            _flat(weights, n, torch.float32, dev, "weights"),
                                             _dense(dy, (n, N), y.dtype, dev, "dy"),
-                                            _dense(dweights.view(-1), (n,), torch.float32, dev, "dweights"),
-                                            _raw_stream(stream, dev)), "mxgemm_moe_combine_backward")
+                                            _flat(dweights, n, torch.float32, dev, "dweights"),
+                                            _raw_stream(dev)), "mxgemm_moe_combine_backward")
     return dy, dweights
 
 

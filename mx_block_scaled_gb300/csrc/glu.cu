@@ -8,7 +8,12 @@
 //
 // Elementwise over rows apart from the scale blocks: a warp takes 512
 // consecutive values of a row, every byte of input is read once and every output
-// is written from the same registers.
+// is written from the same registers.  Bound by HBM: 8192 x 14336 BF16, forward
+// with the checkpoint 833 MB in 130 us (6.4 TB/s), without it 591 MB in 87 us (6.8),
+// backward from the checkpoint 1182 MB in 177 us (6.7).  To get there each value
+// must cost fewer than 38 instructions: packed FP32 products, three-input
+// magnitude maxima and the hardware's 2^x and 1/x (with expf and an IEEE division
+// the forward took 257 us).
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -19,42 +24,71 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// act(g) and its slope's parts share q; expf overflows to infinity for very
-// negative arguments, where q is then 0 and the products are the limits.
+// Blocks of a kernel on an SM; the grid is that times the SMs, each warp walks
+// the chunks.  Every warp keeps the next chunk's 2 KB (BF16) of loads in flight, so
+// two blocks of 16 KB cover HBM's latency: 8192 x 14336 BF16 with the checkpoint
+// 130 us at two blocks (<= 128 registers), 153 at three, 258 at four (spills).
+// Without the checkpoint a BF16 chunk fits 64 registers: 87 us at four blocks, 92
+// at three, 98 at two.
+template <int IN, bool KEEP>
+constexpr int kForwardBlocks = IN == kBf16 && !KEEP ? 4 : 2;
+constexpr int kBackwardBlocks = 2;  // 8192 x 14336 from the checkpoint: 177 us; three 181, four 252 (spills)
+
+// q of the activation's gate: the hardware's 2^x and 1/x, each within two ulps,
+// on an argument that carries the conversion to base 2 in its last constant.
+// 2^x overflows to infinity for far negative gates, where q is then 0, and the
+// reciprocal flushes below 2^-126.  `inner` is the argument's slope by g.
 template <int ACT>
 __device__ __forceinline__ float act_gate(float g, float &inner)
 {
-    float t = g;
+    constexpr float kLog2e = 1.4426950408889634f;
+    float t;
     inner = 1.0f;
     if (ACT == kActGeluTanh) {
-        const float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
-        t = c * fmaf(0.044715f * g * g, g, g);
+        constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
+        t = -c * kLog2e * fmaf(0.044715f * g * g, g, g);
         inner = c * fmaf(0.134145f * g, g, 1.0f);
+    } else {
+        t = -kLog2e * g;
     }
-    return 1.0f / (1.0f + expf(-t));
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    return q;
 }
 
 template <int ACT, int IN, int FMT, bool KEEP>
-__global__ void __launch_bounds__(kThreads) glu_kernel(const GluParams p)
+__global__ void __launch_bounds__(kThreads, kForwardBlocks<IN, KEEP>) glu_kernel(const GluParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t F = p.F, per_row = (F + kWarpVals - 1) / kWarpVals, units = p.rows * per_row;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t row = u / per_row, k0 = (u - row * per_row) * kWarpVals, k = k0 + lane * kLaneVals;
+    const int64_t F = p.F;
+    ChunkWalk at(F, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+                 static_cast<int64_t>(gridDim.x) * kWarps);
+    // the next chunk's loads are in flight while this one is computed
+    Raw16<IN> next_g, next_u;
+    auto fetch = [&]() {
+        const int64_t k = static_cast<int64_t>(at.chunk) * kWarpVals + lane * kLaneVals;
+        const bool inside = at.row < p.rows && k < F;
+        next_g.load(p.gate + at.row * p.stride + k * E, inside);
+        next_u.load(p.up + at.row * p.stride + k * E, inside);
+    };
+    fetch();
+    while (at.row < p.rows) {
+        const Raw16<IN> rg = next_g, ru = next_u;
+        const int64_t row = at.row, k0 = static_cast<int64_t>(at.chunk) * kWarpVals, k = k0 + lane * kLaneVals;
         const bool inside = k < F;
-        Raw16<IN> rg, ru;
-        rg.load(p.gate + row * p.stride + k * E, inside);
-        ru.load(p.up + row * p.stride + k * E, inside);
+        at.next();
+        fetch();
         float a[kLaneVals];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) {
-            float inner;
-            const float g = rg.at(i);
-            a[i] = g * act_gate<ACT>(g, inner) * ru.at(i);
+        for (int i = 0; i < kLaneVals; i += 2) {
+            float s0, s1;
+            const float q0 = act_gate<ACT>(rg.at(i), s0), q1 = act_gate<ACT>(rg.at(i + 1), s1);
+            mul2(a[i], a[i + 1], rg.at(i), rg.at(i + 1), q0, q1);
+            mul2(a[i], a[i + 1], a[i], a[i + 1], ru.at(i), ru.at(i + 1));
         }
         if (p.y && inside)
             store16<IN>(p.y + (row * F + k) * E, a);
@@ -65,19 +99,20 @@ __global__ void __launch_bounds__(kThreads) glu_kernel(const GluParams p)
             store_scales(p.mx.scales, p.mx.mode, row, k0, F, lane, q.scode);
         }
         if (KEEP) {
-            // gate in the first F columns, up in the last F; F is a multiple of 32, so a block never straddles
+            // a row of the checkpoint is two rows of F: the gate's, then the up's (F is a multiple of 32, so no block
+            // straddles them)
+            const int mode = F % 128 == 0 ? kScaleWords : kScaleBytes;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                const Raw16<IN> &x = half ? ru : rg;
                 float v[kLaneVals];
 #pragma unroll
                 for (int i = 0; i < kLaneVals; ++i)
-                    v[i] = half ? ru.at(i) : rg.at(i);
-                const auto q = mx_encode<kMxfp8>(v);
-                if (inside) {
+                    v[i] = x.at(i);
+                const auto q = mx_encode<kMxfp8>(v, amax_bits(x));
+                if (inside)
                     store_codes(p.kept_codes + (2 * row + half) * F, k, q);
-                    if ((lane & 1) == 0)
-                        p.kept_scales[((2 * row + half) * F + k) >> 5] = static_cast<uint8_t>(q.scode);
-                }
+                store_scales(p.kept_scales, mode, 2 * row + half, k0, F, lane, q.scode);
             }
         }
     }
@@ -86,51 +121,74 @@ __global__ void __launch_bounds__(kThreads) glu_kernel(const GluParams p)
                          static_cast<int64_t>(gridDim.x) * kThreads);
 }
 
+// What a chunk of the backward pass reads.
+template <int IN, bool KEPT>
+struct BackIn {
+    Raw16<IN> dy;
+    Raw16<IN> g, u;        // !KEPT
+    uint4 qg, qu;          // KEPT
+    uint32_t sg, su;
+
+    __device__ __forceinline__ void load(const GluBackParams &p, int64_t row, int64_t k)
+    {
+        constexpr int E = ElemBytes<IN>::value;
+        const bool inside = row < p.rows && k < p.F;
+        dy.load(p.dy + row * p.dy_stride + k * E, inside);
+        if (KEPT) {
+            qg = qu = make_uint4(0, 0, 0, 0);
+            sg = su = 127;
+            if (inside) {
+                const int64_t at = 2 * row * p.F + k;
+                qg = __ldcs(reinterpret_cast<const uint4 *>(p.kept_codes + at));
+                qu = __ldcs(reinterpret_cast<const uint4 *>(p.kept_codes + at + p.F));
+                sg = p.kept_scales[at >> 5];
+                su = p.kept_scales[(at + p.F) >> 5];
+            }
+        } else {
+            g.load(p.gate + row * p.stride + k * E, inside);
+            u.load(p.up + row * p.stride + k * E, inside);
+        }
+    }
+};
+
 template <int ACT, int IN, int FMT, bool KEPT>
-__global__ void __launch_bounds__(kThreads) glu_backward_kernel(const GluBackParams p)
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks) glu_backward_kernel(const GluBackParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t F = p.F, per_row = (F + kWarpVals - 1) / kWarpVals, units = p.rows * per_row;
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); n < units;
-         n += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t row = n / per_row, k0 = (n - row * per_row) * kWarpVals, k = k0 + lane * kLaneVals;
+    const int64_t F = p.F;
+    ChunkWalk at(F, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+                 static_cast<int64_t>(gridDim.x) * kWarps);
+    BackIn<IN, KEPT> next;
+    next.load(p, at.row, static_cast<int64_t>(at.chunk) * kWarpVals + lane * kLaneVals);
+    while (at.row < p.rows) {
+        const BackIn<IN, KEPT> in = next;
+        const int64_t row = at.row, k0 = static_cast<int64_t>(at.chunk) * kWarpVals, k = k0 + lane * kLaneVals;
         const bool inside = k < F;
-        Raw16<IN> rdy;
-        rdy.load(p.dy + row * p.dy_stride + k * E, inside);
+        at.next();
+        next.load(p, at.row, static_cast<int64_t>(at.chunk) * kWarpVals + lane * kLaneVals);
         float g[kLaneVals], u[kLaneVals];
         if (KEPT) {
-            uint4 qg = make_uint4(0, 0, 0, 0), qu = qg;
-            uint32_t sg = 127, su = 127;
-            if (inside) {
-                const int64_t at = 2 * row * F + k;
-                qg = __ldcs(reinterpret_cast<const uint4 *>(p.kept_codes + at));
-                qu = __ldcs(reinterpret_cast<const uint4 *>(p.kept_codes + at + F));
-                sg = p.kept_scales[at >> 5];
-                su = p.kept_scales[(at + F) >> 5];
-            }
-            decode_e4m3(qg, sg, g);
-            decode_e4m3(qu, su, u);
+            decode_e4m3(in.qg, in.sg, g);
+            decode_e4m3(in.qu, in.su, u);
         } else {
-            Raw16<IN> rg, ru;
-            rg.load(p.gate + row * p.stride + k * E, inside);
-            ru.load(p.up + row * p.stride + k * E, inside);
 #pragma unroll
             for (int i = 0; i < kLaneVals; ++i) {
-                g[i] = rg.at(i);
-                u[i] = ru.at(i);
+                g[i] = in.g.at(i);
+                u[i] = in.u.at(i);
             }
         }
         float dg[kLaneVals], du[kLaneVals], a[kLaneVals];
 #pragma unroll
         for (int i = 0; i < kLaneVals; ++i) {
             float inner;
-            const float q = act_gate<ACT>(g[i], inner), dy = rdy.at(i), f = g[i] * q;
+            const float q = act_gate<ACT>(g[i], inner), dy = in.dy.at(i), f = g[i] * q;
             // where q has reached 0 or 1 the slope is q, also where `inner` has overflowed
             const float m = f * (1.0f - q);
-            dg[i] = dy * u[i] * (m == 0.0f ? q : fmaf(m, inner, q));
+            const float slope = ACT == kActSilu ? m + q : m == 0.0f ? q : fmaf(m, inner, q);
+            dg[i] = dy * u[i] * slope;
             du[i] = dy * f;
             a[i] = f * u[i];
         }
@@ -154,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) glu_backward_kernel(const GluBackPar
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int64_t kk = k + half * F;
-                    const int64_t at = p.mx.mode == kScaleTiled
+                    const int64_t to = p.mx.mode == kScaleTiled
                                            ? tile_scale_offset(row, kk >> 7, F >> 6) + ((kk >> 5) & 3)
                                            : (2 * row * F + half * F + k) >> 5;
-                    p.mx.scales[at] = static_cast<uint8_t>(half ? qu.scode : qg.scode);
+                    p.mx.scales[to] = static_cast<uint8_t>(half ? qu.scode : qg.scode);
                 }
             }
         }
@@ -167,35 +225,41 @@ __global__ void __launch_bounds__(kThreads) glu_backward_kernel(const GluBackPar
                          static_cast<int64_t>(gridDim.x) * kThreads);
 }
 
-unsigned row_grid(int64_t rows, int64_t F, int num_sms)
+unsigned row_grid(int64_t rows, int64_t F, int64_t most)
 {
-    const int64_t units = rows * ((F + kWarpVals - 1) / kWarpVals);
-    const int64_t blocks = (units + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 8;
-    return static_cast<unsigned>(blocks < cap ? blocks : cap);
+    const int64_t chunks = rows * ((F + kWarpVals - 1) / kWarpVals), blocks = (chunks + kWarps - 1) / kWarps;
+    return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
-template <int ACT, int IN, int FMT>
+template <int ACT, int IN, int FMT, bool KEEP>
 cudaError_t launch_glu_one(const GluParams &p, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(row_grid(p.rows, p.F, num_sms), kThreads, 0, s, attr);
-    return p.kept_codes ? cudaLaunchKernelEx(&cfg, glu_kernel<ACT, IN, FMT, true>, p)
-                        : cudaLaunchKernelEx(&cfg, glu_kernel<ACT, IN, FMT, false>, p);
+    const cudaLaunchConfig_t cfg =
+        row_launch(row_grid(p.rows, p.F, num_sms * kForwardBlocks<IN, KEEP>), kThreads, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, glu_kernel<ACT, IN, FMT, KEEP>, p);
+}
+
+template <int ACT, int IN, int FMT>
+cudaError_t launch_glu_keep(const GluParams &p, int num_sms, cudaStream_t s)
+{
+    return p.kept_codes ? launch_glu_one<ACT, IN, FMT, true>(p, num_sms, s)
+                        : launch_glu_one<ACT, IN, FMT, false>(p, num_sms, s);
 }
 
 template <int ACT, int IN>
 cudaError_t launch_glu_fmt(const GluParams &p, int num_sms, cudaStream_t s)
 {
-    return p.mx.fmt == kMxfp8   ? launch_glu_one<ACT, IN, kMxfp8>(p, num_sms, s)
-           : p.mx.fmt == kMxfp4 ? launch_glu_one<ACT, IN, kMxfp4>(p, num_sms, s)
-                                : launch_glu_one<ACT, IN, kNoFmt>(p, num_sms, s);
+    return p.mx.fmt == kMxfp8   ? launch_glu_keep<ACT, IN, kMxfp8>(p, num_sms, s)
+           : p.mx.fmt == kMxfp4 ? launch_glu_keep<ACT, IN, kMxfp4>(p, num_sms, s)
+                                : launch_glu_keep<ACT, IN, kNoFmt>(p, num_sms, s);
 }
 
 template <int ACT, int IN, int FMT>
 cudaError_t launch_back_one(const GluBackParams &p, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(row_grid(p.rows, p.F, num_sms), kThreads, 0, s, attr);
+    const cudaLaunchConfig_t cfg = row_launch(row_grid(p.rows, p.F, num_sms * kBackwardBlocks), kThreads, 0, s, attr);
     return p.kept_codes ? cudaLaunchKernelEx(&cfg, glu_backward_kernel<ACT, IN, FMT, true>, p)
                         : cudaLaunchKernelEx(&cfg, glu_backward_kernel<ACT, IN, FMT, false>, p);
 }

@@ -14,84 +14,136 @@ namespace mxg {
 namespace {
 
 // --------------------------------------------------------------------- sort --
-// A stable counting sort by one cluster.  Every warp owns a contiguous run of
-// slots.  (1) Each warp counts its run by expert in its own row of shared memory
-// (lanes with the same expert find each other with match.any); (2) columns are
-// summed over the block's warps, over the cluster's blocks (distributed shared
-// memory) and over the experts, which gives each (expert, block, warp) its first
-// row; (3) each warp walks its run again and hands out rows in slot order.
-constexpr int kSortThreads = 1024;
+// A stable counting sort.  Every block owns a contiguous tile of slots and every
+// warp of it a contiguous run.  (1) With more than one tile, a first kernel counts
+// each tile's slots by expert.  (2) Each warp of the second kernel counts its run by
+// expert in its own row of shared memory (lanes with the same expert find each other
+// with match.any) and the columns are scanned over the warps; this does not need the
+// first kernel's counts and runs beside it.  (3) Each block adds up the counts: over
+// all tiles, which after a scan over the experts gives an expert's first row, and
+// over the tiles before its own.  (4) Each warp walks its run again and hands out
+// rows in slot order.
+//
+// Latency-bound: 131072 slots are 2 MB of traffic.  What counts is that no SM gets
+// many slots, since match.any and the scattered stores of the inverse map go
+// through one SM slowly: 131072 slots on 8 SMs (one cluster) took 28 us.
+constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
+constexpr int kSortAhead = 4;
 
-__device__ __forceinline__ void cluster_barrier()
+template <typename ID>
+__device__ __forceinline__ int expert_key(ID id, int groups)
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return id >= 0 && id < static_cast<ID>(groups) ? static_cast<int>(id) : groups;
 }
 
-__device__ __forceinline__ int ld_cluster(const int *p, int rank)
+// counts[tile][key]: the tile's slots of an expert (key `groups`: dropped).
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads)
+    moe_count_kernel(const ID *ids, int64_t slots, int groups, int64_t tile, int *counts)
 {
-    uint32_t a;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+    __shared__ int total[kMaxSortGroups + 1];
+    griddep_wait();
+    // only now: the sort kernel reads the ids before it waits for this kernel, so what wrote them must be complete
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, keys = groups + 1;
+    for (int e = tid; e < keys; e += kSortThreads)
+        total[e] = 0;
+    __syncthreads();
+    const int64_t s0 = blockIdx.x * tile, s1 = s0 + tile < slots ? s0 + tile : slots;
+#pragma unroll 4
+    for (int64_t s = s0 + tid; s < s1; s += kSortThreads)
+        atomicAdd(&total[expert_key(ids[s], groups)], 1);  // counts only: the order does not matter
+    __syncthreads();
+    for (int e = tid; e < keys; e += kSortThreads)
+        counts[static_cast<int64_t>(blockIdx.x) * keys + e] = total[e];
 }
 
 template <typename ID>
 __global__ void __launch_bounds__(kSortThreads)
-    moe_sort_kernel(const ID *ids, int64_t slots, int groups, int64_t run, int64_t *offsets, int32_t *row_of_slot,
-                    int32_t *slot_of_row)
+    moe_sort_kernel(const ID *ids, int64_t slots, int groups, int64_t run, const int *counts, int64_t *offsets,
+                    int32_t *row_of_slot, int32_t *slot_of_row)
 {
     extern __shared__ int hist[];  // [kSortWarps][groups + 1]
-    __shared__ int total[kMaxSortGroups + 1];  // this block's slots of an expert (the last entry: dropped)
-    __shared__ int first[kMaxSortGroups + 1];  // this block's first row of an expert
+    __shared__ int all[kMaxSortGroups + 1];    // slots of an expert (the last entry: dropped)
+    __shared__ int first[kMaxSortGroups + 1];  // slots of it in earlier tiles; then this tile's first row
     __shared__ int warp_part[kSortWarps];
-    griddep_launch_dependents();
-    griddep_wait();
+    if (!counts)
+        griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, keys = groups + 1;
-    const int rank = static_cast<int>(blockIdx.x), blocks = static_cast<int>(gridDim.x);
+    const int tile = static_cast<int>(blockIdx.x), tiles = static_cast<int>(gridDim.x);
     int *mine = hist + warp * keys;
+    const int64_t s0 = (static_cast<int64_t>(tile) * kSortWarps + warp) * run;
+    const int64_t s1 = s0 + run < slots ? s0 + run : slots;
 
+    // four steps' ids are loaded together: one memory latency for 128 slots of a warp
+    int key[kSortAhead];
+    auto load_keys = [&](int64_t b) {
+        ID id[kSortAhead];
+#pragma unroll
+        for (int i = 0; i < kSortAhead; ++i)
+            id[i] = b + 32 * i + lane < s1 ? ids[b + 32 * i + lane] : 0;
+#pragma unroll
+        for (int i = 0; i < kSortAhead; ++i)
+            key[i] = b + 32 * i + lane < s1 ? expert_key(id[i], groups) : -1;
+    };
+    load_keys(s0);
     for (int i = lane; i < keys; i += 32)
         mine[i] = 0;
+    for (int e = tid; e < keys; e += kSortThreads)
+        all[e] = first[e] = 0;
     __syncwarp();
-    const int64_t s0 = (static_cast<int64_t>(rank) * kSortWarps + warp) * run;
-    const int64_t s1 = s0 + run < slots ? s0 + run : slots;
-    auto key_of = [&](int64_t s) -> int {
-        if (s >= s1)
-            return -1;
-        const ID id = ids[s];
-        return id >= 0 && id < static_cast<ID>(groups) ? static_cast<int>(id) : groups;
-    };
-    for (int64_t b = s0; b < s1; b += 32) {
-        const int key = key_of(b + lane);
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
-        if (key >= 0 && lane == __ffs(peers) - 1)
-            mine[key] += __popc(peers);
-        __syncwarp();
+    for (int64_t b = s0; b < s1; b += 32 * kSortAhead) {
+        if (b > s0)
+            load_keys(b);
+#pragma unroll
+        for (int i = 0; i < kSortAhead; ++i) {
+            if (b + 32 * i >= s1)
+                break;  // warp-uniform
+            const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key[i]);
+            if (key[i] >= 0 && lane == __ffs(peers) - 1)
+                mine[key[i]] += __popc(peers);
+            __syncwarp();
+        }
     }
     __syncthreads();
+    // warps of this block that have a run
+    const int64_t runs = (slots - static_cast<int64_t>(tile) * kSortWarps * run + run - 1) / run;
+    const int busy = runs < kSortWarps ? static_cast<int>(runs > 0 ? runs : 0) : kSortWarps;
     for (int e = tid; e < keys; e += kSortThreads) {
         int sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = hist[w * keys + e];
-            hist[w * keys + e] = sum;
-            sum += c;
-        }
-        total[e] = sum;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w)
+            if (w < busy) {
+                const int c = hist[w * keys + e];
+                hist[w * keys + e] = sum;
+                sum += c;
+            }
+        if (!counts)
+            all[e] = sum;
     }
-    cluster_barrier();
-    // keys <= 513 < kSortThreads: one thread per expert
-    int before = 0, all = 0;
-    if (tid < keys)
-        for (int r = 0; r < blocks; ++r) {
-            const int c = ld_cluster(&total[tid], r);
-            before += r < rank ? c : 0;
-            all += c;
+    if (counts) {
+        griddep_wait();
+        // a strip of tiles per group of `keys` threads; integer sums, so their order does not matter
+        const int strips = kSortThreads > keys ? kSortThreads / keys : 1;
+        for (int at = tid; at < strips * keys; at += kSortThreads) {
+            const int strip = at / keys, e = at - strip * keys;
+            int sum = 0, before = 0;
+#pragma unroll 8
+            for (int c = strip; c < tiles; c += strips) {
+                const int n = counts[static_cast<int64_t>(c) * keys + e];
+                sum += n;
+                before += c < tile ? n : 0;
+            }
+            atomicAdd(&all[e], sum);
+            atomicAdd(&first[e], before);
         }
-    int incl = all;
+    }
+    griddep_launch_dependents();
+    __syncthreads();
+    // scan over the keys, two to a thread (keys <= 513)
+    const int e0 = 2 * tid, n0 = e0 < keys ? all[e0] : 0, n1 = e0 + 1 < keys ? all[e0 + 1] : 0;
+    int incl = n0 + n1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
@@ -100,39 +152,57 @@ __global__ void __launch_bounds__(kSortThreads)
     if (lane == 31)
         warp_part[warp] = incl;
     __syncthreads();
-    int carry = 0;
-    for (int w = 0; w < warp; ++w)
-        carry += warp_part[w];
-    const int start = carry + incl - all;
-    if (tid < keys) {
-        first[tid] = start + before;
-        if (rank == 0)
-            offsets[tid] = start;  // the dropped slots' start is the last group's end
+    if (e0 < keys) {
+        int start = incl - n0 - n1;
+        for (int w = 0; w < warp; ++w)
+            start += warp_part[w];
+        first[e0] += start;
+        if (e0 + 1 < keys)
+            first[e0 + 1] += start + n0;
+        if (tile == 0) {  // the dropped slots' start is the last group's end
+            offsets[e0] = start;
+            if (e0 + 1 < keys)
+                offsets[e0 + 1] = start + n0;
+        }
     }
     __syncthreads();
-    for (int64_t b = s0; b < s1; b += 32) {
-        const int key = key_of(b + lane);
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
-        const int at = key >= 0 ? mine[key] : 0;
-        __syncwarp();
-        if (key >= 0) {
-            if (lane == __ffs(peers) - 1)
-                mine[key] = at + __popc(peers);
-            const int row = first[key] + at + __popc(peers & ((1u << lane) - 1u));
-            row_of_slot[b + lane] = key < groups ? row : -1 - row;
-            if (slot_of_row)
-                slot_of_row[row] = static_cast<int32_t>(b + lane);
+    for (int64_t b = s0; b < s1; b += 32 * kSortAhead) {
+        if (run > 32 * kSortAhead)
+            load_keys(b);
+#pragma unroll
+        for (int i = 0; i < kSortAhead; ++i) {
+            if (b + 32 * i >= s1)
+                break;  // warp-uniform
+            const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key[i]);
+            const int at = key[i] >= 0 ? mine[key[i]] : 0;
+            __syncwarp();
+            if (key[i] >= 0) {
+                if (lane == __ffs(peers) - 1)
+                    mine[key[i]] = at + __popc(peers);
+                const int64_t s = b + 32 * i + lane;
+                const int row = first[key[i]] + at + __popc(peers & ((1u << lane) - 1u));
+                row_of_slot[s] = key[i] < groups ? row : -1 - row;
+                if (slot_of_row)
+                    slot_of_row[row] = static_cast<int32_t>(s);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
-    cluster_barrier();  // no block leaves while another may still read its totals
 }
 
 // ----------------------------------------------------------------- dispatch --
-// A warp reads 512 values of a token once, encodes them once and writes them to
-// the rows of all the token's slots.
+// A warp reads 512 or 1024 values of a token once, encodes them once and writes
+// them to the rows of all the token's slots.  One unit of work per warp and a block
+// for every eight: with persistent warps on four blocks an SM the writes of 16384
+// tokens x 2048 to 8 of 64 experts (346 MB) took 71 us, so they take 52 us (6.6
+// TB/s).  Two chunks a warp keep more bytes in flight where there are warps enough
+// (4099 x 4096, top 2, MXFP4: 10.1 us against 11.9); with few, one chunk is faster
+// (32 x 2048, top 8: 2.0 us against 2.3).
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+
+// Warps below which a call is latency-bound: sixteen a multiprocessor.
+constexpr int64_t kFewWarps = 16;
 
 // The row of a slot and whether it is dropped; an entry outside the table gives row -1.
 __device__ __forceinline__ int slot_row(int r, int64_t slots, bool &dropped)
@@ -142,100 +212,137 @@ __device__ __forceinline__ int slot_row(int r, int64_t slots, bool &dropped)
     return row < slots ? row : -1;
 }
 
-template <int IN, int FMT>
-__global__ void __launch_bounds__(kThreads) moe_dispatch_kernel(const DispatchParams p)
+template <int IN, int FMT, int CHUNKS>
+__global__ void __launch_bounds__(kThreads, 4) moe_dispatch_kernel(const DispatchParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t K = p.K, per_row = (K + kWarpVals - 1) / kWarpVals, units = p.tokens * per_row;
-    const int64_t slots = p.tokens * p.topk;
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); n < units;
-         n += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t t = n / per_row, k0 = (n - t * per_row) * kWarpVals, k = k0 + lane * kLaneVals;
-        const bool inside = k < K;
-        Raw16<IN> x;
-        x.load(p.x + t * p.x_stride + k * E, inside);
-        int r = lane < p.topk ? p.row_of_slot[t * p.topk + lane] : 0;
-        float v[kLaneVals];
+    const int topk = static_cast<int>(p.topk);
+    const uint32_t per_row = static_cast<uint32_t>((p.K + CHUNKS * kWarpVals - 1) / (CHUNKS * kWarpVals));
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = unit / per_row;
+    if (token >= p.tokens)
+        return;
+    const int64_t K = p.K, t = token, slots = p.tokens * topk;
+    const int64_t k0 = static_cast<int64_t>(unit - token * per_row) * (CHUNKS * kWarpVals) + lane * kLaneVals;
+    Raw16<IN> x[CHUNKS];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            v[i] = x.at(i);
-        Codes16<FMT == kMxfp4 ? kMxfp4 : kMxfp8> q, zero;
-        if (FMT != kRowsBf16) {
-            q = mx_encode<FMT == kMxfp4 ? kMxfp4 : kMxfp8>(v);
-            zero = q;
+    for (int c = 0; c < CHUNKS; ++c)
+        x[c].load(p.x + t * p.x_stride + (k0 + c * kWarpVals) * E, k0 + c * kWarpVals < K);
+    const int32_t *entry = p.row_of_slot + t * topk;
+    int r = lane < topk ? entry[lane] : 0;
+    constexpr int kWords = FMT == kRowsBf16 ? 8 : FMT == kMxfp8 ? 4 : 2;
+    uint32_t w[CHUNKS][kWords], scode[CHUNKS], word[CHUNKS];
 #pragma unroll
-            for (uint32_t &w : zero.w)
-                w = 0;
-            zero.scode = 127;
+    for (int c = 0; c < CHUNKS; ++c) {
+        if constexpr (FMT == kRowsBf16) {  // a BF16 token is copied bit for bit
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[c][i] = IN == kBf16 ? x[c].r[0][i] : pack_bf16(x[c].at(2 * i), x[c].at(2 * i + 1));
+        } else {
+            float v[kLaneVals];
+#pragma unroll
+            for (int i = 0; i < kLaneVals; ++i)
+                v[i] = x[c].at(i);
+            const Codes16<FMT> q = mx_encode<FMT>(v, amax_bits(x[c]));
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[c][i] = q.w[i];
+            scode[c] = q.scode;
+            word[c] = tile_scale_word(q.scode, lane);
         }
-        for (int64_t j = 0; j < p.topk; ++j) {
-            if (j > 0 && (j & 31) == 0)
-                r = j + lane < p.topk ? p.row_of_slot[t * p.topk + j + lane] : 0;
-            bool dropped;
-            const int64_t row = slot_row(__shfl_sync(0xFFFFFFFFu, r, static_cast<int>(j & 31)), slots, dropped);
-            if (row < 0)
-                continue;  // warp-uniform
-            if (FMT == kRowsBf16) {
-                uint32_t d[8];  // a BF16 token is copied bit for bit
+    }
+    for (int j = 0; j < topk; ++j) {
+        if (j > 0 && (j & 31) == 0)
+            r = j + lane < topk ? entry[j + lane] : 0;
+        bool dropped;
+        const int64_t row = slot_row(__shfl_sync(0xFFFFFFFFu, r, j & 31), slots, dropped);
+        if (row < 0)
+            continue;  // warp-uniform
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    d[i] = dropped ? 0u : IN == kBf16 ? x.r[0][i] : pack_bf16(v[2 * i], v[2 * i + 1]);
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t k = k0 + c * kWarpVals;
+            const bool inside = k < K;
+            uint32_t o[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                o[i] = dropped ? 0u : w[c][i];
+            if constexpr (FMT == kRowsBf16) {
                 if (inside)
-                    st_row32(p.rows + (row * K + k) * 2, d);
+                    st_row32(p.rows + (row * K + k) * 2, o);
             } else {
-                const auto &o = dropped ? zero : q;
-                if (inside)
-                    store_codes(p.rows + row * (FMT == kMxfp8 ? K : K >> 1), k, o);
-                store_scales(p.scales, p.mode, row, k0, K, lane, o.scode);
+                if (inside && FMT == kMxfp8)
+                    *reinterpret_cast<uint4 *>(p.rows + row * K + k) = make_uint4(o[0], o[1], o[2], o[kWords - 1]);
+                if (inside && FMT == kMxfp4)
+                    *reinterpret_cast<uint2 *>(p.rows + ((row * K + k) >> 1)) = make_uint2(o[0], o[1]);
+                uint8_t *scales = p.scales + ((row * K + k) >> 5);
+                if (p.mode == kScaleWords) {
+                    if (inside && (lane & 7) == 0)
+                        *reinterpret_cast<uint32_t *>(scales) = dropped ? 0x7F7F7F7Fu : word[c];
+                } else if (inside && (lane & 1) == 0) {
+                    *scales = static_cast<uint8_t>(dropped ? 127u : scode[c]);
+                }
             }
         }
     }
 }
 
 // ------------------------------------------------------------------ combine --
-// A warp sums 512 values of a token over its slots, in slot order.
-template <int IN>
-__global__ void __launch_bounds__(kThreads) moe_combine_kernel(const CombineParams p)
+// A warp sums 512 values of a token over its slots, in slot order; the rows of
+// AHEAD slots are loaded before the first is added.  Neighbouring warps read
+// neighbouring parts of the same rows.  Two slots ahead fit 64 registers, and four
+// blocks an SM then keep HBM busy: 8192 x 4096, top 2, with residual (269 MB) 42.5
+// us (6.3 TB/s), 8192 x 2048, top 8 (336 MB) 51.5 us (6.5); four ahead on three
+// blocks 54.9.  With few warps the latency of a batch counts: 32 x 2048, top 8, takes
+// 2.2 us eight ahead, 2.9 two ahead.
+template <int IN, int AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 4 : 2) moe_combine_kernel(const CombineParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t N = p.N, per_row = (N + kWarpVals - 1) / kWarpVals, units = p.tokens * per_row;
-    const int64_t slots = p.tokens * p.topk;
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); n < units;
-         n += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t t = n / per_row, k = (n - t * per_row) * kWarpVals + lane * kLaneVals;
-        const bool inside = k < N;
-        float acc[kLaneVals];
+    const int lane = threadIdx.x & 31, topk = static_cast<int>(p.topk);
+    const uint32_t per_row = static_cast<uint32_t>((p.N + kWarpVals - 1) / kWarpVals);
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = unit / per_row;
+    if (token >= p.tokens)
+        return;
+    const int64_t t = token, slots = p.tokens * topk;
+    const int64_t k = static_cast<int64_t>(unit - token * per_row) * kWarpVals + lane * kLaneVals;
+    const bool inside = k < p.N;
+    const int32_t *entry = p.row_of_slot + t * topk;
+    const char *y0 = p.y + k * E;
+    Raw16<IN> add;
+    add.load(p.add + t * p.add_stride + k * E, inside && p.add != nullptr);
+    float acc[kLaneVals];
+    for (int j0 = 0; j0 < topk; j0 += AHEAD) {
+        int r[AHEAD];
+        float w[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            acc[i] = 0.0f;
-        for (int64_t j = 0; j < p.topk; ++j) {
-            bool dropped;
-            const int64_t row = slot_row(p.row_of_slot[t * p.topk + j], slots, dropped);
-            if (dropped || row < 0)
-                continue;  // warp-uniform: a dropped row is never read
-            const float w = p.weights ? p.weights[t * p.topk + j] : 1.0f;
-            Raw16<IN> y;
-            y.load(p.y + row * p.y_stride + k * E, inside);
-#pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
-                acc[i] = fmaf(w, y.at(i), acc[i]);
+        for (int i = 0; i < AHEAD; ++i) {
+            r[i] = j0 + i < topk ? entry[j0 + i] : -1;
+            w[i] = p.weights && j0 + i < topk ? p.weights[t * topk + j0 + i] : 1.0f;
         }
-        if (p.add) {
-            Raw16<IN> a;
-            a.load(p.add + t * p.add_stride + k * E, inside);
+        Raw16<IN> y[AHEAD];
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
-                acc[i] += a.at(i);
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool live = r[i] >= 0 && r[i] < slots;  // a dropped row is never read
+            w[i] = live ? w[i] : 0.0f;
+            y[i].load(y0 + r[i] * p.y_stride, inside && live);
         }
-        if (inside)
-            store16<IN>(p.out + (t * N + k) * E, acc);
+        if (j0 == 0) {
+#pragma unroll
+            for (int n = 0; n < kLaneVals; ++n)
+                acc[n] = add.at(n);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int n = 0; n < kLaneVals; ++n)
+                acc[n] = fmaf(w[i], y[i].at(n), acc[n]);
     }
+    if (inside)
+        store16<IN>(p.out + (t * p.N + k) * E, acc);
 }
 
 // A warp per slot: dy[row] = w * dout[t] and dw = <dout[t], y[row]>.
@@ -275,21 +382,34 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(const Co
     }
 }
 
-unsigned grid_for(int64_t warps, int num_sms)
+unsigned strided_blocks(int64_t warps, int num_sms, int per_sm)
 {
-    const int64_t blocks = (warps + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * 8;
+    const int64_t blocks = (warps + kWarps - 1) / kWarps, cap = static_cast<int64_t>(num_sms) * per_sm;
     return static_cast<unsigned>(blocks < cap ? blocks : cap);
 }
 
-template <int IN>
+unsigned warp_blocks(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
+
+template <int IN, int FMT>
 cudaError_t launch_dispatch(const DispatchParams &p, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        row_launch(grid_for(p.tokens * ((p.K + kWarpVals - 1) / kWarpVals), num_sms), kThreads, 0, s, attr);
-    return p.fmt == kMxfp8   ? cudaLaunchKernelEx(&cfg, moe_dispatch_kernel<IN, kMxfp8>, p)
-           : p.fmt == kMxfp4 ? cudaLaunchKernelEx(&cfg, moe_dispatch_kernel<IN, kMxfp4>, p)
-                             : cudaLaunchKernelEx(&cfg, moe_dispatch_kernel<IN, kRowsBf16>, p);
+    const int64_t units = p.tokens * ((p.K + kWarpVals - 1) / kWarpVals);
+    if (units <= kFewWarps * num_sms) {
+        const cudaLaunchConfig_t cfg = row_launch(warp_blocks(units), kThreads, 0, s, attr);
+        return cudaLaunchKernelEx(&cfg, moe_dispatch_kernel<IN, FMT, 1>, p);
+    }
+    const int64_t pairs = p.tokens * ((p.K + 2 * kWarpVals - 1) / (2 * kWarpVals));
+    const cudaLaunchConfig_t cfg = row_launch(warp_blocks(pairs), kThreads, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_dispatch_kernel<IN, FMT, 2>, p);
+}
+
+template <int IN>
+cudaError_t launch_dispatch_fmt(const DispatchParams &p, int num_sms, cudaStream_t s)
+{
+    return p.fmt == kMxfp8   ? launch_dispatch<IN, kMxfp8>(p, num_sms, s)
+           : p.fmt == kMxfp4 ? launch_dispatch<IN, kMxfp4>(p, num_sms, s)
+                             : launch_dispatch<IN, kRowsBf16>(p, num_sms, s);
 }
 
 }  // namespace
@@ -304,48 +424,79 @@ cudaError_t prepare_moe()
                : cudaFuncSetAttribute(moe_sort_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
-cudaError_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int groups, int64_t *offsets,
-                            int32_t *row_of_slot, int32_t *slot_of_row, cudaStream_t s)
+namespace {
+
+template <typename ID>
+cudaError_t launch_sort(const ID *ids, int64_t slots, int groups, int64_t *offsets, int32_t *row_of_slot,
+                        int32_t *slot_of_row, int *counts, cudaStream_t s)
 {
-    // a run of whole 32-slot steps per warp; one block while that gives each warp at most four steps
-    const int blocks = slots <= 4 * kSortThreads ? 1 : kSortCluster;
-    const int64_t warps = static_cast<int64_t>(blocks) * kSortWarps;
+    const int64_t tiles = sort_tiles(slots, groups), warps = tiles * kSortWarps;
     const int64_t run = ((slots + warps - 1) / warps + 31) / 32 * 32;
+    cudaLaunchAttribute attr[1];
+    if (tiles == 1) {
+        counts = nullptr;
+    } else {
+        const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, 0, s, attr);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_count_kernel<ID>, ids, slots, groups, run * kSortWarps, counts);
+        if (e != cudaSuccess)
+            return e;
+    }
     const size_t smem = static_cast<size_t>(kSortWarps) * (groups + 1) * sizeof(int);
-    cudaLaunchAttribute attr[2];
-    cudaLaunchAttribute one[1];
-    cudaLaunchConfig_t cfg = row_launch(blocks, kSortThreads, smem, s, one);
-    attr[0] = one[0];
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = blocks;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return ids64 ? cudaLaunchKernelEx(&cfg, moe_sort_kernel<long long>, static_cast<const long long *>(ids), slots,
-                                      groups, run, offsets, row_of_slot, slot_of_row)
-                 : cudaLaunchKernelEx(&cfg, moe_sort_kernel<int>, static_cast<const int *>(ids), slots, groups, run,
-                                      offsets, row_of_slot, slot_of_row);
+    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<ID>, ids, slots, groups, run, static_cast<const int *>(counts),
+                              offsets, row_of_slot, slot_of_row);
+}
+
+}  // namespace
+
+// Tiles of a sort.  One block (and one launch) while its warps have at most four
+// steps; from there 1024 slots a tile, up to 128 tiles, and fewer where many
+// experts make the tables of counts long (each tile reads them all).
+int64_t sort_tiles(int64_t slots, int64_t groups)
+{
+    if (slots <= 4 * kSortThreads)
+        return 1;
+    const int64_t most = groups > 128 ? 64 : 128, tiles = (slots + 1023) / 1024;
+    return tiles < most ? tiles : most;
+}
+
+cudaError_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int groups, int64_t *offsets,
+                            int32_t *row_of_slot, int32_t *slot_of_row, int *counts, cudaStream_t s)
+{
+    return ids64 ? launch_sort(static_cast<const long long *>(ids), slots, groups, offsets, row_of_slot, slot_of_row,
+                               counts, s)
+                 : launch_sort(static_cast<const int *>(ids), slots, groups, offsets, row_of_slot, slot_of_row, counts,
+                               s);
 }
 
 cudaError_t launch_moe_dispatch(const DispatchParams &p, int in_dtype, int num_sms, cudaStream_t s)
 {
-    return in_dtype == kBf16 ? launch_dispatch<kBf16>(p, num_sms, s) : launch_dispatch<kF32>(p, num_sms, s);
+    return in_dtype == kBf16 ? launch_dispatch_fmt<kBf16>(p, num_sms, s) : launch_dispatch_fmt<kF32>(p, num_sms, s);
 }
+
+namespace {
+
+template <int IN>
+cudaError_t launch_combine(const CombineParams &p, int num_sms, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const int64_t units = p.tokens * ((p.N + kWarpVals - 1) / kWarpVals);
+    const cudaLaunchConfig_t cfg = row_launch(warp_blocks(units), kThreads, 0, s, attr);
+    return units <= kFewWarps * num_sms ? cudaLaunchKernelEx(&cfg, moe_combine_kernel<IN, 8>, p)
+                                        : cudaLaunchKernelEx(&cfg, moe_combine_kernel<IN, 2>, p);
+}
+
+}  // namespace
 
 cudaError_t launch_moe_combine(const CombineParams &p, int in_dtype, int num_sms, cudaStream_t s)
 {
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        row_launch(grid_for(p.tokens * ((p.N + kWarpVals - 1) / kWarpVals), num_sms), kThreads, 0, s, attr);
-    return in_dtype == kBf16 ? cudaLaunchKernelEx(&cfg, moe_combine_kernel<kBf16>, p)
-                             : cudaLaunchKernelEx(&cfg, moe_combine_kernel<kF32>, p);
+    return in_dtype == kBf16 ? launch_combine<kBf16>(p, num_sms, s) : launch_combine<kF32>(p, num_sms, s);
 }
 
 cudaError_t launch_moe_combine_backward(const CombineBackParams &p, int in_dtype, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(grid_for(p.tokens * p.topk, num_sms), kThreads, 0, s, attr);
+    const cudaLaunchConfig_t cfg = row_launch(strided_blocks(p.tokens * p.topk, num_sms, 8), kThreads, 0, s, attr);
     return in_dtype == kBf16 ? cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kBf16>, p)
                              : cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kF32>, p);
 }

@@ -108,6 +108,82 @@ __device__ __forceinline__ void store16(char *p, const float (&v)[kLaneVals])
     }
 }
 
+// Two FP32 products in one instruction (the packed form has twice the scalar rate).
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Pairs of FP32 values in one 64-bit register: the packed product and
+// multiply-add round each half as the scalar ones do.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_split(F2 v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// A word of two BF16 values as an FP32 pair.
+__device__ __forceinline__ F2 f2_bf16(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+// max(|a|, |b|, |c|); a NaN among them gives NaN.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Bit pattern of the largest magnitude of a lane's sixteen values.  Patterns of
+// magnitudes order like the values, and a NaN's is above the infinity's.
+__device__ __forceinline__ uint32_t amax_bits(const float (&v)[kLaneVals])
+{
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i + 1 < kLaneVals; i += 2)
+        m = max_abs3(m, v[i], v[i + 1]);
+    return __float_as_uint(max_abs3(m, v[kLaneVals - 1], v[kLaneVals - 1]));
+}
+
+// The same from the values as loaded; BF16 pairs are compared two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_bits(const Raw16<DT> &x)
+{
+    if constexpr (DT == kBf16) {
+        uint32_t m = x.r[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.r[0][i]));
+        m &= 0x7FFF7FFFu;
+        return max(m << 16, m & 0xFFFF0000u);
+    } else {
+        float v[kLaneVals];
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            v[i] = x.at(i);
+        return amax_bits(v);
+    }
+}
+
 // Two FP32 values -> two E4M3 codes (lo in the low byte), nearest-even, saturating.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi)
 {
@@ -141,39 +217,40 @@ struct Codes16 {
     uint32_t scode;  // scale code of this lane's block
 };
 
-// Encode a warp's chunk (every lane of the warp calls it; lanes outside the row
-// hold zeros).
+// Encode a warp's chunk whose lanes' largest magnitudes are `amax` (every lane of
+// the warp calls it; lanes outside the row hold zeros).
 template <int FMT>
-__device__ __forceinline__ Codes16<FMT> mx_encode(const float (&v)[kLaneVals])
+__device__ __forceinline__ Codes16<FMT> mx_encode(const float (&v)[kLaneVals], uint32_t amax)
 {
     constexpr int kEMax = FMT == kMxfp8 ? 8 : 2;
     Codes16<FMT> c;
-    // absolute bit patterns order like the values; any pattern from the infinity's on is an infinity or a NaN
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < kLaneVals; ++i)
-        amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     const bool nonfinite = amax >= 0x7F800000u;
     const int scode = amax == 0 ? 127 : max(static_cast<int>(amax >> 23) - kEMax, 0);
     const float mul = __uint_as_float(static_cast<uint32_t>(254 - scode) << 23);  // 2^(127 - scode), exact products
     c.scode = nonfinite ? 255u : static_cast<uint32_t>(scode);
+    float t[kLaneVals];
+#pragma unroll
+    for (int i = 0; i < kLaneVals; i += 2)
+        mul2(t[i], t[i + 1], v[i], v[i + 1], mul, mul);
     if (FMT == kMxfp8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = e4m3_pair(v[4 * i] * mul, v[4 * i + 1] * mul);
-            const uint32_t hi = e4m3_pair(v[4 * i + 2] * mul, v[4 * i + 3] * mul);
+            const uint32_t lo = e4m3_pair(t[4 * i], t[4 * i + 1]);
+            const uint32_t hi = e4m3_pair(t[4 * i + 2], t[4 * i + 3]);
             c.w[i] = nonfinite ? 0u : (lo | (hi << 16));
         }
     } else {
-        float t[kLaneVals];
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            t[i] = v[i] * mul;
         c.w[0] = nonfinite ? 0u : e2m1_word(t);
         c.w[Codes16<FMT>::kWords - 1] = nonfinite ? 0u : e2m1_word(t + 8);
     }
     return c;
+}
+
+template <int FMT>
+__device__ __forceinline__ Codes16<FMT> mx_encode(const float (&v)[kLaneVals])
+{
+    return mx_encode<FMT>(v, amax_bits(v));
 }
 
 // The four scale codes of this lane's K-tile in one word (block c in byte c).
@@ -256,6 +333,33 @@ __device__ __forceinline__ void decode_e4m3(const uint4 q, uint32_t scode, float
         v[2 * i + 1] = hi * s;
     }
 }
+
+// A warp's walk over chunks of a matrix's rows (512 values, or `len`), every
+// `step`-th chunk from `first` on: one division at the start, additions from then on.
+struct ChunkWalk {
+    int64_t row;
+    int chunk, per_row;
+    int64_t row_step;
+    int chunk_step;
+
+    __device__ __forceinline__ ChunkWalk(int64_t row_len, int64_t first, int64_t step, int64_t len = kWarpVals)
+    {
+        per_row = static_cast<int>((row_len + len - 1) / len);
+        row = first / per_row;
+        chunk = static_cast<int>(first - row * per_row);
+        row_step = step / per_row;
+        chunk_step = static_cast<int>(step - row_step * per_row);
+    }
+    __device__ __forceinline__ void next()
+    {
+        row += row_step;
+        chunk += chunk_step;
+        if (chunk >= per_row) {
+            chunk -= per_row;
+            ++row;
+        }
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v)
 {

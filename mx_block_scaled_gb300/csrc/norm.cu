@@ -4,9 +4,13 @@
 //   h = x + r;  rstd = 1/sqrt(mean(h^2) + eps);  y = h * rstd * w
 //   p = dy * w;  dx = rstd * p - h * rstd^3 * mean(p * h) + dh;  dw = sum_rows dy * h * rstd
 //
-// Both are one pass over rows that never leave the registers between their
-// reduction and their use: the forward reads x (and r) once and writes h, y,
-// codes and scales from the same registers, in FP32 until the final rounding.
+// Both are one pass over the rows, bound by HBM.  The forward keeps a row in the
+// registers of one block between its reduction and its use and writes h, y, codes
+// and scales from them, in FP32 until the final rounding; blocks on the same SM
+// cover each other's reductions: 16384 x 8192 BF16 with residual and tiled MXFP8
+// (944 MB) 137 us, 6.9 TB/s.  The backward also sums over rows, so its blocks stay
+// and hide the reduction in a pipeline instead: 16384 x 8192 BF16 (1074 MB) 175 us,
+// 6.1 TB/s, 8192 x 4096 (268 MB) 51 us, of which 4 are the second launch.
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -154,24 +158,231 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_kernel(const Nor
     }
 }
 
-// dw[k] = sum of partial[b][k] over the blocks, in block order within each of
-// eight slices and then over the slices: the same sum every run.
-__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float *partial, int blocks, int64_t K, float *dw)
+// The same for rows of at most 8192 values (16 a thread), as a pipeline.  Each
+// thread copies its own values of dy, h and dh of the coming rows to its own places
+// in a ring in shared memory (cp.async) and reads them back itself, so the ring needs
+// no barrier.  Between two barriers a block forms the dot product's partial sums of
+// one row and finishes the row before it, whose sums the last barrier made visible:
+// the reduction's latency is covered by work instead of being waited out.
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
-    __shared__ float part[8][32];
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// A thread's values come in 16-byte pieces `threads` pieces apart, so that a warp's
+// copies are 512 consecutive bytes (two 16-byte halves of a 32-byte run per thread
+// would fetch every sector twice).
+template <int IN, int WT, int DEPTH>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(const NormBackParams p)
+{
+    constexpr int E = ElemBytes<IN>::value;
+    constexpr int kPer = 16 / E;                 // values of a piece
+    constexpr int kPieces = kLaneVals / kPer;    // pieces of a thread
+    constexpr int kPairs = kPer / 2;             // FP32 pairs of a piece
+    extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][dy, h, dh][piece][thread]
+    __shared__ __align__(16) float part[2][kMaxThreads / 32];
+    __shared__ float row_rstd[2];  // by thread 0, a row ahead; each iteration's barrier shows it to the others
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t K = p.K, step = gridDim.x;
+    const bool with_dh = p.dh != nullptr;
+    const uint32_t plane = threads * 16;                                   // bytes of one piece of all threads
+    const uint32_t stage_bytes = (with_dh ? 3 : 2) * kPieces * plane;
+    const uint32_t ring0 = smem_addr(ring) + tid * 16, ring_end = ring0 + DEPTH * stage_bytes;
+    bool inside[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+        inside[i] = (i * threads + tid) * kPer < K;
+
+    // the row that is fetched next, and where to
+    int64_t ahead_row = blockIdx.x;
+    const char *src_dy = p.dy + ahead_row * p.dy_stride + tid * 16, *src_h = p.h + ahead_row * p.h_stride + tid * 16,
+               *src_dh = p.dh + ahead_row * p.dh_stride + tid * 16;
+    uint32_t to = ring0;
+    auto fetch = [&]() {
+        if (ahead_row < p.rows) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                if (inside[i]) {
+                    cp_async16(to + i * plane, src_dy + i * plane);
+                    cp_async16(to + (kPieces + i) * plane, src_h + i * plane);
+                    if (with_dh)
+                        cp_async16(to + (2 * kPieces + i) * plane, src_dh + i * plane);
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ahead_row += step;
+        src_dy += step * p.dy_stride;
+        src_h += step * p.h_stride;
+        src_dh += step * p.dh_stride;
+        to += stage_bytes;
+        to = to == ring_end ? ring0 : to;
+    };
+    if (tid < 2 * (kMaxThreads / 32))
+        part[tid / (kMaxThreads / 32)][tid % (kMaxThreads / 32)] = 0.0f;  // for warps that there are not
+    auto take = [&](uint32_t at, int i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (inside[i])
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(at)
+                         : "memory");
+        return v;
+    };
+    auto pair = [](const uint4 &v, int n) -> F2 {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (IN == kBf16)
+            return f2_bf16(w[n]);
+        else
+            return f2(__uint_as_float(w[2 * n]), __uint_as_float(w[2 * n + 1]));
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d)
+        fetch();
+    F2 w[kPieces][kPairs], dw[kPieces][kPairs];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+        for (int n = 0; n < kPairs; ++n) {
+            const uint32_t k = (i * threads + tid) * kPer + 2 * n;
+            w[i][n] = f2(0.0f, 0.0f);
+            if (inside[i]) {
+                if constexpr (WT == kBf16) {
+                    w[i][n] = f2_bf16(reinterpret_cast<const uint32_t *>(p.weight)[k / 2]);
+                } else {
+                    const float2 v = reinterpret_cast<const float2 *>(p.weight)[k / 2];
+                    w[i][n] = f2(v.x, v.y);
+                }
+            }
+            dw[i][n] = f2(0.0f, 0.0f);
+        }
+    uint4 next_dy[kPieces], next_h[kPieces];
+    // partial sums of p * h of a row that has landed; its dy and h stay in registers for its turn
+    auto dot_row = [&](uint32_t from, int buf) {
+        F2 dot = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            next_dy[i] = take(from + i * plane, i);
+            next_h[i] = take(from + (kPieces + i) * plane, i);
+#pragma unroll
+            for (int n = 0; n < kPairs; ++n)
+                dot = f2_fma(f2_mul(pair(next_dy[i], n), w[i][n]), pair(next_h[i], n), dot);
+        }
+        float lo, hi;
+        f2_split(dot, lo, hi);
+        lo = warp_sum(lo + hi);
+        if (lane == 0)
+            part[buf][warp] = lo;
+    };
+    int64_t row = blockIdx.x;
+    char *dx = p.dx + row * K * E + tid * 16;
+    float next_rstd = 0.0f;
+    if (tid == 0 && row < p.rows) {
+        row_rstd[0] = p.rstd[row];
+        next_rstd = row + step < p.rows ? p.rstd[row + step] : 0.0f;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+    __syncthreads();
+    dot_row(ring0, 0);
+    __syncthreads();
+    const float inv_k = 1.0f / static_cast<float>(K);
+    uint32_t stage = ring0;
+    int buf = 0;
+    for (; row < p.rows; row += step, buf ^= 1) {
+        uint32_t following = stage + stage_bytes;
+        following = following == ring_end ? ring0 : following;
+        fetch();  // into the stage that the last row left
+        const float rstd = row_rstd[buf];
+        if (tid == 0) {
+            row_rstd[buf ^ 1] = next_rstd;
+            next_rstd = row + 2 * step < p.rows ? p.rstd[row + 2 * step] : 0.0f;
+        }
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kMaxThreads / 128; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(part[buf])[i];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const float sum = (s.x + s.y) + (s.z + s.w);
+        uint4 dy[kPieces], h[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            dy[i] = next_dy[i];
+            h[i] = next_h[i];
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+        if (row + step < p.rows)
+            dot_row(following, buf ^ 1);
+        const float coef = -(rstd * rstd * rstd * (sum * inv_k));
+        const F2 coef2 = f2(coef, coef), rstd2 = f2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            uint4 dh = make_uint4(0, 0, 0, 0);
+            if (with_dh)
+                dh = take(stage + (2 * kPieces + i) * plane, i);
+            float d[kPer];
+#pragma unroll
+            for (int n = 0; n < kPairs; ++n) {
+                const F2 g = pair(dy[i], n), v = pair(h[i], n);
+                const F2 o = f2_fma(v, coef2, f2_fma(f2_mul(g, w[i][n]), rstd2, pair(dh, n)));
+                f2_split(o, d[2 * n], d[2 * n + 1]);
+                dw[i][n] = f2_fma(g, f2_mul(v, rstd2), dw[i][n]);
+            }
+            if (inside[i]) {
+                uint4 o;
+                if constexpr (IN == kBf16)
+                    o = make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]),
+                                   pack_bf16(d[6], d[7]));
+                else
+                    o = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]),
+                                   __float_as_uint(d[3]));
+                *reinterpret_cast<uint4 *>(dx + i * plane) = o;
+            }
+        }
+        dx += step * K * E;
+        stage = following;
+        __syncthreads();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+        if (inside[i]) {
+            float *out = p.partial + blockIdx.x * K + (i * threads + tid) * kPer;
+#pragma unroll
+            for (int n = 0; n < kPairs; n += 2) {
+                float4 o;
+                f2_split(dw[i][n], o.x, o.y);
+                f2_split(dw[i][n + 1], o.z, o.w);
+                *reinterpret_cast<float4 *>(out + 2 * n) = o;
+            }
+        }
+}
+
+// dw[k] = sum of partial[b][k] over the blocks, in block order within each of 32
+// slices and then over the slices: the same sum every run.
+constexpr int kSlices = 32;
+
+__global__ void __launch_bounds__(32 * kSlices)
+    rmsnorm_dweight_kernel(const float *partial, int blocks, int64_t K, float *dw)
+{
+    __shared__ float part[kSlices][32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float v = 0.0f;
-#pragma unroll 4
-    for (int b = slice; b < blocks; b += 8)
+#pragma unroll 10
+    for (int b = slice; b < blocks; b += kSlices)
         v += partial[b * K + k];
     part[slice][lane] = v;
     __syncthreads();
     if (slice == 0) {
 #pragma unroll
-        for (int s = 1; s < 8; ++s)
+        for (int s = 1; s < kSlices; ++s)
             v += part[s][lane];
         dw[k] = v;
     }
@@ -188,6 +399,13 @@ Shape pick_shape(int64_t K)
     const int64_t warps = (K + s.nch * kWarpVals - 1) / (s.nch * kWarpVals);
     s.threads = static_cast<int>(warps) * 32;
     return s;
+}
+
+// Blocks of the backward on an SM: 512 threads' worth, four at most.
+int blocks_per_sm(const Shape &sh)
+{
+    const int n = 512 / sh.threads;
+    return n < 1 ? 1 : n > 4 ? 4 : n;
 }
 
 template <int IN, int WT, int FMT>
@@ -209,26 +427,54 @@ cudaError_t launch_forward_fmt(const NormParams &p, cudaStream_t s)
                                 : launch_forward<IN, WT, kNoFmt>(p, s);
 }
 
+constexpr int kRingBytes = 220 * 1024;  // shared memory of an SM's rings
+
+template <int IN, int WT, int DEPTH>
+cudaError_t launch_ring(const NormBackParams &p, int threads, int64_t blocks, size_t smem, cudaStream_t s)
+{
+    static const cudaError_t opt_in = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, DEPTH>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (opt_in != cudaSuccess)
+        return opt_in;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), threads, smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_backward_ring_kernel<IN, WT, DEPTH>, p);
+}
+
 template <int IN, int WT>
 cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s)
 {
     const Shape sh = pick_shape(p.K);
-    int64_t blocks = 2 * num_sms;
-    blocks = blocks < kNormBackBlocks ? blocks : kNormBackBlocks;
-    blocks = blocks < p.rows ? blocks : p.rows;
+    int64_t blocks = norm_back_blocks(p.rows, p.K);
+    const int per_sm = blocks_per_sm(sh);
+    blocks = blocks < static_cast<int64_t>(num_sms) * per_sm ? blocks : static_cast<int64_t>(num_sms) * per_sm;
+    cudaError_t e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), sh.threads, 0, s, attr);
-    const cudaError_t e = sh.nch == 1   ? cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 1>, p)
-                          : sh.nch == 2 ? cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 2>, p)
-                                        : cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 4>, p);
+    if (sh.nch == 1) {
+        const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sh.threads * kLaneVals * ElemBytes<IN>::value;
+        const int64_t depth = kRingBytes / per_sm / row;
+        e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, blocks, 4 * row, s)
+            : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, blocks, 3 * row, s)
+                         : launch_ring<IN, WT, 2>(p, sh.threads, blocks, 2 * row, s);
+    } else {
+        const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), sh.threads, 0, s, attr);
+        e = sh.nch == 2 ? cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 2>, p)
+                        : cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 4>, p);
+    }
     if (e != cudaSuccess)
         return e;
-    const cudaLaunchConfig_t cfg2 = row_launch(static_cast<unsigned>(p.K / 32), 256, 0, s, attr);
-    return cudaLaunchKernelEx(&cfg2, rmsnorm_dweight_kernel, static_cast<const float *>(p.partial),
+    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.K / 32), 32 * kSlices, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel, static_cast<const float *>(p.partial),
                               static_cast<int>(blocks), p.K, p.dweight);
 }
 
 }  // namespace
+
+int64_t norm_back_blocks(int64_t rows, int64_t K)
+{
+    const int64_t most = static_cast<int64_t>(kNormBackSms) * blocks_per_sm(pick_shape(K));
+    return rows < most ? rows : most;
+}
 
 cudaError_t launch_rmsnorm(const NormParams &p, int in_dtype, int weight_dtype, int num_sms, cudaStream_t s)
 {

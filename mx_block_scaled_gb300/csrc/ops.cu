@@ -136,8 +136,7 @@ size_t mxgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t K)
 {
     if (rows < 1 || rows > kMaxRows || K < 32 || K % 32 != 0 || K > mxg::kNormMaxK)
         return 0;
-    const int64_t blocks = rows < mxg::kNormBackBlocks ? rows : mxg::kNormBackBlocks;
-    return static_cast<size_t>(blocks * K) * sizeof(float);
+    return static_cast<size_t>(mxg::norm_back_blocks(rows, K) * K) * sizeof(float);
 }
 
 int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *h, int64_t h_stride,
@@ -258,22 +257,34 @@ int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_t dy_stride
     return status_of(mxg::launch_glu_backward(p, act, in_dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
+size_t mxgemm_moe_sort_workspace_bytes(int64_t slots, int64_t groups)
+{
+    if (slots < 1 || slots > kMaxRows || groups < 1 || groups > mxg::kMaxSortGroups)
+        return 0;
+    const int64_t tiles = mxg::sort_tiles(slots, groups);
+    return tiles == 1 ? 0 : static_cast<size_t>(tiles * (groups + 1)) * sizeof(int);
+}
+
 int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t groups, int64_t *offsets,
-                    int32_t *row_of_slot, int32_t *slot_of_row, void *stream)
+                    int32_t *row_of_slot, int32_t *slot_of_row, void *workspace, size_t ws_bytes, void *stream)
 {
     if (!expert_ids || !offsets || !row_of_slot || (id_bytes != 4 && id_bytes != 8))
         return MXGEMM_ERR_ARG;
     if (slots < 1 || slots > kMaxRows || groups < 1 || groups > mxg::kMaxSortGroups)
         return MXGEMM_ERR_SHAPE;
     if (!aligned(expert_ids, static_cast<unsigned>(id_bytes)) || !aligned(offsets, 8) || !aligned(row_of_slot, 4) ||
-        !aligned(slot_of_row, 4))
+        !aligned(slot_of_row, 4) || !aligned(workspace, 16))
         return MXGEMM_ERR_ALIGN;
+    const size_t need = mxgemm_moe_sort_workspace_bytes(slots, groups);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return MXGEMM_ERR_WORKSPACE;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)
         return st;
     return status_of(mxg::launch_moe_sort(expert_ids, id_bytes == 8, slots, static_cast<int>(groups), offsets,
-                                          row_of_slot, slot_of_row, static_cast<cudaStream_t>(stream)));
+                                          row_of_slot, slot_of_row, static_cast<int *>(workspace),
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 // tokens x topk slots fit the sort's 32-bit rows
@@ -281,6 +292,9 @@ static bool slots_ok(int64_t tokens, int64_t topk)
 {
     return tokens >= 1 && topk >= 1 && tokens <= kMaxRows && topk <= kMaxRows / tokens;
 }
+
+// one warp for every 512 values of a token, numbered in 32 bits
+static bool warps_ok(int64_t tokens, int64_t cols) { return tokens * ((cols + 511) / 512) < (1ll << 32) - 64; }
 
 int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride, int64_t tokens, int64_t topk, int64_t K,
                         const int32_t *row_of_slot, int fmt, void *rows, uint8_t *scales, void *stream)
@@ -296,6 +310,8 @@ int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride, int64_t t
     if (!rows_align_ok(x, x_stride, tokens, e) || !aligned(row_of_slot, 4) || !aligned(rows, plain ? 32 : 16) ||
         !aligned(scales, 16))
         return MXGEMM_ERR_ALIGN;
+    if (!warps_ok(tokens, K))
+        return MXGEMM_ERR_UNSUPPORTED;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -327,6 +343,8 @@ int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride, int64_t to
     if (!rows_align_ok(y, y_stride, tokens * topk, e) || !rows_align_ok(add, add_stride, tokens, e) ||
         !aligned(row_of_slot, 4) || !aligned(weights, 4) || !aligned(out, 32))
         return MXGEMM_ERR_ALIGN;
+    if (!warps_ok(tokens, N))
+        return MXGEMM_ERR_UNSUPPORTED;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)

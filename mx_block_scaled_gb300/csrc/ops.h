@@ -59,8 +59,10 @@ struct NormBackParams {
     float *dweight;
     float *partial;                                // [blocks][K]
 };
-// Blocks of the first pass at most (each leaves one row of partial sums).
-constexpr int64_t kNormBackBlocks = 304;
+// Blocks of the first pass at most (each leaves one row of partial sums), on a part
+// of at most kNormBackSms multiprocessors.
+constexpr int kNormBackSms = 152;
+int64_t norm_back_blocks(int64_t rows, int64_t K);
 cudaError_t launch_rmsnorm_backward(const NormBackParams &p, int in_dtype, int weight_dtype, int num_sms,
                                     cudaStream_t s);
 
@@ -96,8 +98,11 @@ constexpr int kMaxSortGroups = 512;
 // Set the sort's shared-memory opt-in on the current device; once per device,
 // before its first launch.
 cudaError_t prepare_moe();
+// Blocks that share a sort; with more than one, `counts` holds one int for each
+// (block, expert or dropped).
+int64_t sort_tiles(int64_t slots, int64_t groups);
 cudaError_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int groups, int64_t *offsets,
-                            int32_t *row_of_slot, int32_t *slot_of_row, cudaStream_t s);
+                            int32_t *row_of_slot, int32_t *slot_of_row, int *counts, cudaStream_t s);
 
 struct DispatchParams {
     const char *x;

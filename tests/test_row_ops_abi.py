@@ -98,16 +98,24 @@ def test_glu_backward(lib, change, expect):
     assert _call(lib, "mxgemm_glu_backward", GLUB, change) == expect
 
 
-SORT = dict(expert_ids=64, id_bytes=8, slots=16, groups=4, offsets=64, row_of_slot=64, slot_of_row=64, stream=None)
+SORT = dict(expert_ids=64, id_bytes=8, slots=16, groups=4, offsets=64, row_of_slot=64, slot_of_row=64,
+            workspace=None, ws_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("change,expect", [
     (dict(expert_ids=None), ARG), (dict(offsets=None), ARG), (dict(row_of_slot=None), ARG), (dict(id_bytes=2), ARG),
     (dict(slots=0), SHAPE), (dict(slots=1 << 31), SHAPE), (dict(groups=0), SHAPE), (dict(groups=513), SHAPE),
     (dict(expert_ids=68), ALIGN), (dict(offsets=4), ALIGN), (dict(row_of_slot=66), ALIGN), (dict(slot_of_row=1), ALIGN),
+    (dict(workspace=8), ALIGN), (dict(slots=1 << 20), WORKSPACE), (dict(slots=1 << 20, workspace=64, ws_bytes=64), WORKSPACE),
 ])
 def test_moe_sort(lib, change, expect):
     assert _call(lib, "mxgemm_moe_sort", SORT, change) == expect
+
+
+def test_moe_sort_workspace(lib):
+    f = lib.mxgemm_moe_sort_workspace_bytes
+    assert f(16, 4) == 0 and f(0, 4) == 0 and f(1 << 20, 513) == 0
+    assert 0 < f(1 << 20, 64) <= 1 << 20 and 0 < f((1 << 31) - 1, 512) <= 1 << 20
 
 
 SEND = dict(in_dtype=2, x=64, x_stride=256, tokens=4, topk=2, K=256, row_of_slot=64, fmt=1, rows=64, scales=64,
@@ -121,6 +129,7 @@ SEND = dict(in_dtype=2, x=64, x_stride=256, tokens=4, topk=2, K=256, row_of_slot
     (dict(x_stride=128), SHAPE),
     (dict(x=16), ALIGN), (dict(x_stride=257), ALIGN), (dict(row_of_slot=2), ALIGN), (dict(rows=8), ALIGN),
     (dict(scales=8), ALIGN), (dict(fmt=3, scales=None, rows=16), ALIGN),
+    (dict(tokens=1 << 29, K=8192, x_stride=8192), UNSUPPORTED),
 ])
 def test_moe_dispatch(lib, change, expect):
     assert _call(lib, "mxgemm_moe_dispatch", SEND, change) == expect
@@ -135,7 +144,7 @@ COMB = dict(in_dtype=2, y=64, y_stride=256, tokens=4, topk=2, N=256, row_of_slot
     (dict(tokens=0), SHAPE), (dict(topk=-1), SHAPE), (dict(N=250), SHAPE), (dict(y_stride=0), SHAPE),
     (dict(add_stride=100), SHAPE),
     (dict(y=16), ALIGN), (dict(add=16), ALIGN), (dict(out=16), ALIGN), (dict(weights=2), ALIGN),
-    (dict(y_stride=260), ALIGN),
+    (dict(y_stride=260), ALIGN), (dict(tokens=1 << 29, N=8192, y_stride=8192, add_stride=8192), UNSUPPORTED),
 ])
 def test_moe_combine(lib, change, expect):
     assert _call(lib, "mxgemm_moe_combine", COMB, change) == expect
