@@ -409,23 +409,26 @@ class GluGrad(NamedTuple):
 _IN_DTYPE = {}  # torch dtype -> MXGEMM_IN_*, filled by the first call (torch is imported lazily)
 
 
-def _in_dtype(t, what: str) -> int:
+def _in_dtype(dtype, what: str) -> int:
     if not _IN_DTYPE:
         import torch
         _IN_DTYPE.update({torch.float32: MXGEMM_IN_F32, torch.bfloat16: MXGEMM_IN_BF16})
-    d = _IN_DTYPE.get(t.dtype)
+    d = _IN_DTYPE.get(dtype)
     if d is None:
-        raise ValueError(f"{what}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+        raise ValueError(f"{what}: unsupported dtype {dtype} (float32 or bfloat16)")
     return d
 
 
-def _in_rows(t, like, shape, what: str):
+def _in_rows(t, shape, dtype, device, what: str):
     """(pointer, row stride) of an input matrix whose rows are contiguous; None -> (0, 0)."""
     if t is None:
         return 0, 0
-    if t.shape != shape or t.dtype is not like.dtype or t.device != like.device or t.stride(1) != 1:
-        raise ValueError(f"{what} must be a {tuple(shape)} {like.dtype} tensor on {like.device} with contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{what} must be a {tuple(shape)} {dtype} tensor on {device}")
+    row, col = t.stride()
+    if col != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), row
 
 
 def _dense(t, shape, dtype, device, what: str) -> int:
@@ -458,10 +461,15 @@ def _workspace(t, need: int, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _cuda_matrix(t, what: str):
-    if t.dim() != 2 or not t.is_cuda or t.stride(1) != 1:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor with contiguous rows")
-    return t.shape
+def _matrix(t, what: str):
+    """(shape, dtype, device, row stride) of the CUDA matrix that sets a call's sizes."""
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    row, col = t.stride()
+    if col != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return shape, t.dtype, t.device, row
 
 
 def _mx_out(fmt: int, tiled: bool, rows: int, K: int, codes, scales, device, what: str):
@@ -513,20 +521,21 @@ def rmsnorm(x, weight, eps: float, residual=None, fmt: int = 0, tiled: bool = Fa
     [rows] float32.  Outputs that are passed in are written in place.
     """
     import torch
-    rows, K = shape = _cuda_matrix(x, "x")
-    dt, dev = _in_dtype(x, "x"), x.device
-    rp, rs = _in_rows(residual, x, shape, "residual")
+    shape, dtype, dev, stride = _matrix(x, "x")
+    rows, K = shape
+    dt = _in_dtype(dtype, "x")
+    rp, rs = _in_rows(residual, shape, dtype, dev, "residual")
     if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
     if h is None and residual is not None:
-        h = torch.empty(shape, dtype=x.dtype, device=dev)
+        h = torch.empty(shape, dtype=dtype, device=dev)
     if y is None and plain:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
+        y = torch.empty(shape, dtype=dtype, device=dev)
     if rstd is None:
         rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
     codes, scales, cp, sp = _mx_out(fmt, tiled, rows, K, codes, scales, dev, "rmsnorm")
-    _check(_lib.mxgemm_rmsnorm(dt, x.data_ptr(), x.stride(0), rp, rs, weight.data_ptr(), _in_dtype(weight, "weight"),
-                               eps, rows, K, _dense(h, shape, x.dtype, dev, "h"), _dense(y, shape, x.dtype, dev, "y"),
+    _check(_lib.mxgemm_rmsnorm(dt, x.data_ptr(), stride, rp, rs, weight.data_ptr(), _in_dtype(weight.dtype, "weight"),
+                               eps, rows, K, _dense(h, shape, dtype, dev, "h"), _dense(y, shape, dtype, dev, "y"),
                                fmt, cp, sp, _dense(rstd, (rows,), torch.float32, dev, "rstd"),
                                MXGEMM_QUANT_SF_TILED if tiled else 0, _raw_stream(dev)), "mxgemm_rmsnorm")
     return RmsNorm(h, y, codes, scales, rstd)
@@ -541,21 +550,22 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, worksp
     gradient of x and of the residual.
     """
     import torch
-    rows, K = shape = _cuda_matrix(dy, "dy")
-    dt, dev = _in_dtype(dy, "dy"), dy.device
-    hp, hs = _in_rows(h, dy, shape, "h")
-    gp, gs = _in_rows(dh, dy, shape, "dh")
+    shape, dtype, dev, stride = _matrix(dy, "dy")
+    rows, K = shape
+    dt = _in_dtype(dtype, "dy")
+    hp, hs = _in_rows(h, shape, dtype, dev, "h")
+    gp, gs = _in_rows(dh, shape, dtype, dev, "dh")
     if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
     if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+        dx = torch.empty(shape, dtype=dtype, device=dev)
     if dweight is None:
         dweight = torch.empty((K,), dtype=torch.float32, device=dev)
     wp, ws = _workspace(workspace, mxgemm_rmsnorm_backward_workspace_bytes(rows, K), dev)
-    _check(_lib.mxgemm_rmsnorm_backward(dt, dy.data_ptr(), dy.stride(0), hp, hs,
+    _check(_lib.mxgemm_rmsnorm_backward(dt, dy.data_ptr(), stride, hp, hs,
                                         _dense(rstd, (rows,), torch.float32, dev, "rstd"), weight.data_ptr(),
-                                        _in_dtype(weight, "weight"), gp, gs, rows, K,
-                                        _dense(dx, shape, dy.dtype, dev, "dx"),
+                                        _in_dtype(weight.dtype, "weight"), gp, gs, rows, K,
+                                        _dense(dx, shape, dtype, dev, "dx"),
                                         _dense(dweight, (K,), torch.float32, dev, "dweight"), wp, ws,
                                         _raw_stream(dev)), "mxgemm_rmsnorm_backward")
     return dx, dweight
@@ -572,21 +582,22 @@ def glu(gate, up, act: int, fmt: int = 0, tiled: bool = False, plain: bool = Fal
     checkpoint (codes [rows, 2F], scales [rows, 2F/32]) for :func:`glu_backward`.
     """
     import torch
-    rows, F = shape = _cuda_matrix(gate, "gate")
-    dt, dev = _in_dtype(gate, "gate"), gate.device
-    up_ptr, up_stride = _in_rows(up, gate, shape, "up")
-    if up_ptr == 0 or (rows > 1 and up_stride != gate.stride(0)):
+    shape, dtype, dev, stride = _matrix(gate, "gate")
+    rows, F = shape
+    dt = _in_dtype(dtype, "gate")
+    up_ptr, up_stride = _in_rows(up, shape, dtype, dev, "up")
+    if up_ptr == 0 or (rows > 1 and up_stride != stride):
         raise ValueError("gate and up must have the same row stride")
     if y is None and plain:
-        y = torch.empty(shape, dtype=gate.dtype, device=dev)
+        y = torch.empty(shape, dtype=dtype, device=dev)
     if keep or kept_codes is not None or kept_scales is not None:
         kept_codes, kept_scales, kc, ks = _mx_out(MXGEMM_FMT_MXFP8_E4M3, False, rows, 2 * F, kept_codes, kept_scales,
                                                   dev, "glu")
     else:
         kc = ks = 0
     codes, scales, cp, sp = _mx_out(fmt, tiled, rows, F, codes, scales, dev, "glu")
-    _check(_lib.mxgemm_glu(act, dt, gate.data_ptr(), up_ptr, gate.stride(0), rows, F,
-                           _dense(y, shape, gate.dtype, dev, "y"), fmt, cp, sp, MXGEMM_QUANT_SF_TILED if tiled else 0,
+    _check(_lib.mxgemm_glu(act, dt, gate.data_ptr(), up_ptr, stride, rows, F,
+                           _dense(y, shape, dtype, dev, "y"), fmt, cp, sp, MXGEMM_QUANT_SF_TILED if tiled else 0,
                            kc, ks, _raw_stream(dev)), "mxgemm_glu")
     return Glu(y, codes, scales, kept_codes, kept_scales)
 
@@ -602,22 +613,23 @@ def glu_backward(dy, act: int, gate=None, up=None, kept_codes=None, kept_scales=
     forward's output ``a`` [rows, F] again.
     """
     import torch
-    rows, F = shape = _cuda_matrix(dy, "dy")
-    dt, dev = _in_dtype(dy, "dy"), dy.device
-    gp, gs = _in_rows(gate, dy, shape, "gate")
-    up_ptr, up_stride = _in_rows(up, dy, shape, "up")
+    shape, dtype, dev, stride = _matrix(dy, "dy")
+    rows, F = shape
+    dt = _in_dtype(dtype, "dy")
+    gp, gs = _in_rows(gate, shape, dtype, dev, "gate")
+    up_ptr, up_stride = _in_rows(up, shape, dtype, dev, "up")
     if rows > 1 and up_stride != gs:
         raise ValueError("gate and up must have the same row stride")
     if dgu is None and plain:
-        dgu = torch.empty((rows, 2 * F), dtype=dy.dtype, device=dev)
+        dgu = torch.empty((rows, 2 * F), dtype=dtype, device=dev)
     if a is None and recompute:
-        a = torch.empty(shape, dtype=dy.dtype, device=dev)
+        a = torch.empty(shape, dtype=dtype, device=dev)
     codes, scales, cp, sp = _mx_out(fmt, tiled, rows, 2 * F, codes, scales, dev, "glu_backward")
-    _check(_lib.mxgemm_glu_backward(act, dt, dy.data_ptr(), dy.stride(0), gp, up_ptr, gs,
+    _check(_lib.mxgemm_glu_backward(act, dt, dy.data_ptr(), stride, gp, up_ptr, gs,
                                     _dense(kept_codes, (rows, 2 * F), torch.uint8, dev, "kept_codes"),
                                     _dense(kept_scales, (rows, F // 16), torch.uint8, dev, "kept_scales"), rows, F,
-                                    _dense(dgu, (rows, 2 * F), dy.dtype, dev, "dgu"), fmt, cp, sp,
-                                    MXGEMM_QUANT_SF_TILED if tiled else 0, _dense(a, shape, dy.dtype, dev, "a"),
+                                    _dense(dgu, (rows, 2 * F), dtype, dev, "dgu"), fmt, cp, sp,
+                                    MXGEMM_QUANT_SF_TILED if tiled else 0, _dense(a, shape, dtype, dev, "a"),
                                     _raw_stream(dev)), "mxgemm_glu_backward")
     return GluGrad(dgu, codes, scales, a)
 
@@ -666,8 +678,8 @@ def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None):
     MXGEMM_FMT_BF16: bfloat16 rows, scales None.  Rows of dropped slots are zero.
     """
     import torch
-    tokens, K = _cuda_matrix(x, "x")
-    dt, dev, n = _in_dtype(x, "x"), x.device, row_of_slot.numel()
+    (tokens, K), dtype, dev, stride = _matrix(x, "x")
+    dt, n = _in_dtype(dtype, "x"), row_of_slot.numel()
     topk = _slots(row_of_slot, tokens)
     index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
     if fmt == MXGEMM_FMT_BF16:
@@ -678,7 +690,7 @@ def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None):
             raise ValueError("BF16 rows have no scales")
     else:
         rows, scales, rp, sp = _mx_out(fmt, False, n, K, rows, scales, dev, "moe_dispatch")
-    _check(_lib.mxgemm_moe_dispatch(dt, x.data_ptr(), x.stride(0), tokens, topk, K, index, fmt, rp, sp,
+    _check(_lib.mxgemm_moe_dispatch(dt, x.data_ptr(), stride, tokens, topk, K, index, fmt, rp, sp,
                                     _raw_stream(dev)), "mxgemm_moe_dispatch")
     return rows, scales
 
@@ -691,18 +703,18 @@ def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None):
     Without ``weights`` (all 1) this is the gradient of :func:`moe_dispatch`.
     """
     import torch
-    n, N = _cuda_matrix(y, "y")
-    dt, dev = _in_dtype(y, "y"), y.device
+    (n, N), dtype, dev, stride = _matrix(y, "y")
+    dt = _in_dtype(dtype, "y")
     if topk < 1 or n % topk or row_of_slot.numel() != n:
         raise ValueError("y must have one row for each of the tokens * topk slots")
     tokens = n // topk
     index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
-    ap, as_ = _in_rows(add, y, (tokens, N), "add")
+    ap, as_ = _in_rows(add, (tokens, N), dtype, dev, "add")
     if out is None:
-        out = torch.empty((tokens, N), dtype=y.dtype, device=dev)
+        out = torch.empty((tokens, N), dtype=dtype, device=dev)
     wp = 0 if weights is None else _flat(weights, n, torch.float32, dev, "weights")
-    _check(_lib.mxgemm_moe_combine(dt, y.data_ptr(), y.stride(0), tokens, topk, N, index, wp, ap, as_,
-                                   _dense(out, (tokens, N), y.dtype, dev, "out"), _raw_stream(dev)),
+    _check(_lib.mxgemm_moe_combine(dt, y.data_ptr(), stride, tokens, topk, N, index, wp, ap, as_,
+                                   _dense(out, (tokens, N), dtype, dev, "out"), _raw_stream(dev)),
            "mxgemm_moe_combine")
     return out
 
@@ -714,20 +726,20 @@ def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None):
     A dropped slot's row of dy and its weight's gradient are zero.
     """
     import torch
-    tokens, N = _cuda_matrix(dout, "dout")
-    dt, dev, n = _in_dtype(dout, "dout"), dout.device, row_of_slot.numel()
+    (tokens, N), dtype, dev, stride = _matrix(dout, "dout")
+    dt, n = _in_dtype(dtype, "dout"), row_of_slot.numel()
     topk = _slots(row_of_slot, tokens)
-    yp, ys = _in_rows(y, dout, (n, N), "y")
+    yp, ys = _in_rows(y, (n, N), dtype, dev, "y")
     if yp == 0:
         raise ValueError("y is missing")
     if dy is None:
-        dy = torch.empty((n, N), dtype=y.dtype, device=dev)
+        dy = torch.empty((n, N), dtype=dtype, device=dev)
     if dweights is None:
         dweights = torch.empty(weights.shape, dtype=torch.float32, device=dev)
-    _check(_lib.mxgemm_moe_combine_backward(dt, dout.data_ptr(), dout.stride(0), yp, ys, tokens, topk, N,
+    _check(_lib.mxgemm_moe_combine_backward(dt, dout.data_ptr(), stride, yp, ys, tokens, topk, N,
                                             _flat(row_of_slot, n, torch.int32, dev, "row_of_slot"),
                                             _flat(weights, n, torch.float32, dev, "weights"),
-                                            _dense(dy, (n, N), y.dtype, dev, "dy"),
+                                            _dense(dy, (n, N), dtype, dev, "dy"),
                                             _flat(dweights, n, torch.float32, dev, "dweights"),
                                             _raw_stream(dev)), "mxgemm_moe_combine_backward")
     return dy, dweights
