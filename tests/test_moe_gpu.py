@@ -63,6 +63,43 @@ def test_sort_one_expert_or_none(value):
     assert (o.cpu().numpy() == wo).all() and (r.cpu().numpy() == wr).all() and (s.cpu().numpy() == ws).all()
 
 
+def test_sort_workspaces_of_streams_threads_and_graphs():
+    """Sorts that overlap on two streams, in two threads and in a replayed graph do not share a workspace."""
+    import threading
+    import torch
+    b = lib()
+    rng = np.random.default_rng(77)
+    T, k, G = 30000, 4, 64
+    sets = [_ids(rng, T, k, G) for _ in range(4)]
+    want = [ref.moe_sort(i, G) for i in sets]
+    dev = [_dev(i) for i in sets]
+    torch.cuda.synchronize()
+    g, gs = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=gs):
+        in_graph = b.moe_sort(dev[0], G)
+    got, streams = {}, [torch.cuda.Stream() for _ in range(2)]
+
+    def work(i):
+        with torch.cuda.stream(streams[0]):     # both threads on one stream
+            for _ in range(20):
+                got[i] = b.moe_sort(dev[i], G)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (1, 2)]
+    for t in threads:
+        t.start()
+    for _ in range(20):
+        got[3] = b.moe_sort(dev[3], G, stream=streams[1])
+        with torch.cuda.stream(gs):
+            g.replay()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    got[0] = in_graph
+    for i in range(4):
+        for x, w in zip(got[i], want[i]):
+            assert (x.cpu().numpy() == w).all(), i
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("fmt", [1, 2, 3])
 @pytest.mark.parametrize("T,k,G,K,drop", [
