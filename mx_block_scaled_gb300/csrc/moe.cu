@@ -412,20 +412,6 @@ cudaError_t launch_dispatch_fmt(const DispatchParams &p, int num_sms, cudaStream
                              : launch_dispatch<IN, kRowsBf16>(p, num_sms, s);
 }
 
-}  // namespace
-
-cudaError_t prepare_moe()
-{
-    const int most = kSortWarps * (kMaxSortGroups + 1) * static_cast<int>(sizeof(int));
-    const cudaError_t e =
-        cudaFuncSetAttribute(moe_sort_kernel<long long>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    return e != cudaSuccess
-               ? e
-               : cudaFuncSetAttribute(moe_sort_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-}
-
-namespace {
-
 template <typename ID>
 cudaError_t launch_sort(const ID *ids, int64_t slots, int groups, int64_t *offsets, int32_t *row_of_slot,
                         int32_t *slot_of_row, int *counts, cudaStream_t s)

@@ -98,67 +98,77 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p
 }
 
 // ----------------------------------------------------------------- backward --
-// Blocks stride over the rows; a thread keeps its columns' share of dw in
-// registers and leaves it in partial[block].
-template <int IN, int WT, int NCH>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_kernel(const NormBackParams p)
+// Blocks stride over the rows; a thread sums its columns' share of dw and leaves it
+// in partial[block].  Rows of more than 8192 values: two passes over the row, the
+// second from L2, with dw in shared memory ([run][pair][thread], so that a warp's
+// accesses are consecutive).
+constexpr int kWideThreads = 512;
+constexpr int kWideVals = kWideThreads * kLaneVals;
+
+template <int IN, int WT>
+__global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(const NormBackParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
+    extern __shared__ __align__(16) F2 wide_dw[];
     __shared__ float part[2][32];
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int64_t K = p.K;
-    float dw[NCH][kLaneVals];
+    const int64_t K = p.K, k0 = threadIdx.x * kLaneVals;
+    F2 *const dw = wide_dw + threadIdx.x;
+    int n = 0;
+    for (int64_t k = k0; k < K; k += kWideVals, n += kLaneVals / 2)
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            dw[c][i] = 0.0f;
+        for (int i = 0; i < kLaneVals / 2; ++i)
+            dw[(n + i) * kWideThreads] = f2(0.0f, 0.0f);
     int flip = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-        Raw16<IN> dy[NCH], h[NCH], dh[NCH];
-        Raw16<WT> w[NCH];
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-            dy[c].load(p.dy + row * p.dy_stride + k * E, k < K);
-            h[c].load(p.h + row * p.h_stride + k * E, k < K);
-            dh[c].load(p.dh + row * p.dh_stride + k * E, k < K && p.dh != nullptr);
-            w[c].load(p.weight + k * ElemBytes<WT>::value, k < K);
-        }
+        const char *dy_row = p.dy + row * p.dy_stride, *h_row = p.h + row * p.h_stride;
         const float rstd = p.rstd[row];
         float dot = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
+#pragma unroll 2
+        for (int64_t k = k0; k < K; k += kWideVals) {
+            Raw16<IN> dy, h;
+            Raw16<WT> w;
+            dy.load(dy_row + k * E, true);
+            h.load(h_row + k * E, true);
+            w.load(p.weight + k * ElemBytes<WT>::value, true);
 #pragma unroll
             for (int i = 0; i < kLaneVals; ++i)
-                dot = fmaf(dy[c].at(i) * w[c].at(i), h[c].at(i), dot);
+                dot = fmaf(dy.at(i) * w.at(i), h.at(i), dot);
+        }
         dot = block_sum(dot, part[flip]);
         const float coef = rstd * rstd * rstd * (dot / static_cast<float>(K));
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
+        n = 0;
+        for (int64_t k = k0; k < K; k += kWideVals, n += kLaneVals / 2) {
+            Raw16<IN> dy, h, dh;
+            Raw16<WT> w;
+            dy.load(dy_row + k * E, true);
+            h.load(h_row + k * E, true);
+            dh.load(p.dh + row * p.dh_stride + k * E, p.dh != nullptr);
+            w.load(p.weight + k * ElemBytes<WT>::value, true);
             float dx[kLaneVals];
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i) {
-                const float g = dy[c].at(i), v = h[c].at(i);
-                dx[i] = fmaf(-v, coef, rstd * (g * w[c].at(i))) + dh[c].at(i);
-                dw[c][i] = fmaf(g, v * rstd, dw[c][i]);
+            for (int i = 0; i < kLaneVals; i += 2) {
+                F2 &sum = dw[(n + i / 2) * kWideThreads];
+                sum = f2_fma(f2(dy.at(i), dy.at(i + 1)), f2_mul(f2(h.at(i), h.at(i + 1)), f2(rstd, rstd)), sum);
+#pragma unroll
+                for (int q = i; q < i + 2; ++q)
+                    dx[q] = fmaf(-h.at(q), coef, rstd * (dy.at(q) * w.at(q))) + dh.at(q);
             }
-            if (k < K)
-                store16<IN>(p.dx + (row * K + k) * E, dx);
+            store16<IN>(p.dx + (row * K + k) * E, dx);
         }
     }
+    n = 0;
+    for (int64_t k = k0; k < K; k += kWideVals, n += kLaneVals / 2) {
+        float v[kLaneVals];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-        if (k < K)
-            store16<kF32>(reinterpret_cast<char *>(p.partial + blockIdx.x * K + k), dw[c]);
+        for (int i = 0; i < kLaneVals; i += 2)
+            f2_split(dw[(n + i / 2) * kWideThreads], v[i], v[i + 1]);
+        store16<kF32>(reinterpret_cast<char *>(p.partial + blockIdx.x * K + k), v);
     }
 }
 
-// The same for rows of at most 8192 values (16 a thread), as a pipeline.  Each
+// Rows of at most 8192 values (16 a thread), as a pipeline.  Each
 // thread copies its own values of dy, h and dh of the coming rows to its own places
 // in a ring in shared memory (cp.async) and reads them back itself, so the ring needs
 // no barrier.  Between two barriers a block forms the dot product's partial sums of
@@ -388,6 +398,7 @@ __global__ void __launch_bounds__(32 * kSlices)
     }
 }
 
+// Forward: a row in one block, runs of 16 values a thread.
 struct Shape {
     int nch, threads;
 };
@@ -401,11 +412,16 @@ Shape pick_shape(int64_t K)
     return s;
 }
 
-// Blocks of the backward on an SM: 512 threads' worth, four at most.
-int blocks_per_sm(const Shape &sh)
+// Backward: rows of up to 8192 values take the ring, with 512 threads' worth of
+// blocks on an SM (four at most); wider ones as many blocks as their sums in shared
+// memory allow, two at most (each leaves a row of partial sums).
+constexpr int64_t kRingMaxK = 8192;
+int blocks_per_sm(int64_t K)
 {
-    const int n = 512 / sh.threads;
-    return n < 1 ? 1 : n > 4 ? 4 : n;
+    if (K > kRingMaxK)
+        return K <= 2 * kWideVals ? 2 : 1;
+    const int n = 512 / pick_shape(K).threads;
+    return n > 4 ? 4 : n;
 }
 
 template <int IN, int WT, int FMT>
@@ -432,10 +448,6 @@ constexpr int kRingBytes = 220 * 1024;  // shared memory of an SM's rings
 template <int IN, int WT, int DEPTH>
 cudaError_t launch_ring(const NormBackParams &p, int threads, int64_t blocks, size_t smem, cudaStream_t s)
 {
-    static const cudaError_t opt_in = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, DEPTH>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (opt_in != cudaSuccess)
-        return opt_in;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), threads, smem, s, attr);
     return cudaLaunchKernelEx(&cfg, rmsnorm_backward_ring_kernel<IN, WT, DEPTH>, p);
@@ -446,20 +458,20 @@ cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s
 {
     const Shape sh = pick_shape(p.K);
     int64_t blocks = norm_back_blocks(p.rows, p.K);
-    const int per_sm = blocks_per_sm(sh);
+    const int per_sm = blocks_per_sm(p.K);
     blocks = blocks < static_cast<int64_t>(num_sms) * per_sm ? blocks : static_cast<int64_t>(num_sms) * per_sm;
     cudaError_t e;
     cudaLaunchAttribute attr[1];
-    if (sh.nch == 1) {
+    if (p.K <= kRingMaxK) {
         const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sh.threads * kLaneVals * ElemBytes<IN>::value;
         const int64_t depth = kRingBytes / per_sm / row;
         e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, blocks, 4 * row, s)
             : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, blocks, 3 * row, s)
                          : launch_ring<IN, WT, 2>(p, sh.threads, blocks, 2 * row, s);
     } else {
-        const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), sh.threads, 0, s, attr);
-        e = sh.nch == 2 ? cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 2>, p)
-                        : cudaLaunchKernelEx(&cfg, rmsnorm_backward_kernel<IN, WT, 4>, p);
+        const size_t smem = (p.K + kWideVals - 1) / kWideVals * kWideVals * sizeof(float);
+        const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kWideThreads, smem, s, attr);
+        e = cudaLaunchKernelEx(&cfg, rmsnorm_backward_wide_kernel<IN, WT>, p);
     }
     if (e != cudaSuccess)
         return e;
@@ -468,11 +480,35 @@ cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s
                               static_cast<int>(blocks), p.K, p.dweight);
 }
 
+template <int IN, int WT>
+cudaError_t prepare_backward()
+{
+    constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 2>, kAttr, kRingBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 3>, kAttr, kRingBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 4>, kAttr, kRingBytes);
+    return e == cudaSuccess ? cudaFuncSetAttribute(rmsnorm_backward_wide_kernel<IN, WT>, kAttr,
+                                                   static_cast<int>(kNormMaxK * sizeof(float)))
+                            : e;
+}
+
 }  // namespace
+
+cudaError_t prepare_norm()
+{
+    cudaError_t e = prepare_backward<kBf16, kBf16>();
+    if (e == cudaSuccess)
+        e = prepare_backward<kBf16, kF32>();
+    if (e == cudaSuccess)
+        e = prepare_backward<kF32, kBf16>();
+    return e == cudaSuccess ? prepare_backward<kF32, kF32>() : e;
+}
 
 int64_t norm_back_blocks(int64_t rows, int64_t K)
 {
-    const int64_t most = static_cast<int64_t>(kNormBackSms) * blocks_per_sm(pick_shape(K));
+    const int64_t most = static_cast<int64_t>(kNormBackSms) * blocks_per_sm(K);
     return rows < most ? rows : most;
 }
 

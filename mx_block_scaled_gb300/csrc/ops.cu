@@ -34,7 +34,7 @@ int ops_device(int *num_sms)
             cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return MXGEMM_ERR_CUDA;
         d.is_sm103 = major == 10 && minor == 3;
-        if (d.is_sm103 && mxg::prepare_moe() != cudaSuccess)
+        if (d.is_sm103 && mxg::prepare_norm() != cudaSuccess)
             return MXGEMM_ERR_CUDA;
         d.ready = true;
     }

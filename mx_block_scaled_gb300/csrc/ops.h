@@ -63,6 +63,9 @@ struct NormBackParams {
 // of at most kNormBackSms multiprocessors.
 constexpr int kNormBackSms = 152;
 int64_t norm_back_blocks(int64_t rows, int64_t K);
+// Set the backward kernels' shared-memory opt-in on the current device; once per
+// device, before the first launch.
+cudaError_t prepare_norm();
 cudaError_t launch_rmsnorm_backward(const NormBackParams &p, int in_dtype, int weight_dtype, int num_sms,
                                     cudaStream_t s);
 
@@ -95,9 +98,6 @@ cudaError_t launch_glu_backward(const GluBackParams &p, int act, int in_dtype, i
 
 // Expert ids 0 .. groups - 1, as many as a grouped GEMM plan takes.
 constexpr int kMaxSortGroups = 512;
-// Set the sort's shared-memory opt-in on the current device; once per device,
-// before its first launch.
-cudaError_t prepare_moe();
 // Blocks that share a sort; with more than one, `counts` holds one int for each
 // (block, expert or dropped).
 int64_t sort_tiles(int64_t slots, int64_t groups);
