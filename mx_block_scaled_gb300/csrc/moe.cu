@@ -15,21 +15,43 @@ namespace {
 
 // --------------------------------------------------------------------- sort --
 // A stable counting sort.  Every block owns a contiguous tile of slots and every
-// warp of it a contiguous run.  (1) With more than one tile, a first kernel counts
-// each tile's slots by expert.  (2) Each warp of the second kernel counts its run by
-// expert in its own row of shared memory (lanes with the same expert find each other
-// with match.any) and the columns are scanned over the warps; this does not need the
-// first kernel's counts and runs beside it.  (3) Each block adds up the counts: over
-// all tiles, which after a scan over the experts gives an expert's first row, and
-// over the tiles before its own.  (4) Each warp walks its run again and hands out
-// rows in slot order.
+// warp of it a contiguous run.  (1) Each warp counts its run by expert in its own row
+// of shared memory (lanes with the same expert find each other with match.any) and
+// the columns are scanned over the warps.  (2) Each block learns the tiles' counts:
+// over all tiles, which after a scan over the experts gives an expert's first row, and
+// over the tiles before its own.  Up to eight tiles are one cluster and read each
+// other's counts in distributed shared memory; more get them from a first kernel,
+// beside which (1) runs.  (3) Each warp walks its run again and hands out rows in slot
+// order.
 //
 // Latency-bound: 131072 slots are 2 MB of traffic.  What counts is that no SM gets
 // many slots, since match.any and the scattered stores of the inverse map go
-// through one SM slowly: 131072 slots on 8 SMs (one cluster) took 28 us.
+// through one SM slowly: 131072 slots of 64 experts take 7.6 us on 128 tiles, and took
+// 28 us on one cluster.  A cluster saves a launch: 4000 slots 4.1 us against 4.6, 8198
+// slots 4.5 against 4.7; at four steps a warp the counts' own kernel is faster (16000
+// slots 6.2 us, 6.8 as a cluster), so clusters take up to three.
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 4;
+constexpr int kSortCluster = 8;
+constexpr int64_t kClusterSlots = kSortCluster * 3 * kSortThreads;
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// *p in block `rank` of the cluster.
+__device__ __forceinline__ int ld_cluster(const int *p, int rank)
+{
+    int v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.b32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(smem_addr(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
 
 template <typename ID>
 __device__ __forceinline__ int expert_key(ID id, int groups)
@@ -59,13 +81,14 @@ __global__ void __launch_bounds__(kSortThreads)
         counts[static_cast<int64_t>(blockIdx.x) * keys + e] = total[e];
 }
 
-template <typename ID>
+template <typename ID, bool CLUSTER>
 __global__ void __launch_bounds__(kSortThreads)
     moe_sort_kernel(const ID *ids, int64_t slots, int groups, int64_t run, const int *counts, int64_t *offsets,
                     int32_t *row_of_slot, int32_t *slot_of_row)
 {
     extern __shared__ int hist[];  // [kSortWarps][groups + 1]
     __shared__ int all[kMaxSortGroups + 1];    // slots of an expert (the last entry: dropped)
+    __shared__ int own[CLUSTER ? kMaxSortGroups + 1 : 1];  // this tile's
     __shared__ int first[kMaxSortGroups + 1];  // slots of it in earlier tiles; then this tile's first row
     __shared__ int warp_part[kSortWarps];
     if (!counts)
@@ -119,8 +142,25 @@ __global__ void __launch_bounds__(kSortThreads)
                 hist[w * keys + e] = sum;
                 sum += c;
             }
-        if (!counts)
+        if (CLUSTER)
+            own[e] = sum;
+        else if (!counts)
             all[e] = sum;
+    }
+    if (CLUSTER) {
+        cluster_barrier();
+        for (int e = tid; e < keys; e += kSortThreads) {
+            int sum = 0, before = 0;
+#pragma unroll
+            for (int r = 0; r < kSortCluster; ++r)
+                if (r < tiles) {
+                    const int n = ld_cluster(&own[e], r);
+                    sum += n;
+                    before += r < tile ? n : 0;
+                }
+            all[e] = sum;
+            first[e] = before;
+        }
     }
     if (counts) {
         griddep_wait();
@@ -188,6 +228,8 @@ __global__ void __launch_bounds__(kSortThreads)
             __syncwarp();
         }
     }
+    if (CLUSTER)
+        cluster_barrier();  // no block leaves while another may still read its counts
 }
 
 // ----------------------------------------------------------------- dispatch --
@@ -419,7 +461,7 @@ cudaError_t launch_sort(const ID *ids, int64_t slots, int groups, int64_t *offse
     const int64_t tiles = sort_tiles(slots, groups), warps = tiles * kSortWarps;
     const int64_t run = ((slots + warps - 1) / warps + 31) / 32 * 32;
     cudaLaunchAttribute attr[1];
-    if (tiles == 1) {
+    if (slots <= kClusterSlots) {
         counts = nullptr;
     } else {
         const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, 0, s, attr);
@@ -428,22 +470,39 @@ cudaError_t launch_sort(const ID *ids, int64_t slots, int groups, int64_t *offse
             return e;
     }
     const size_t smem = static_cast<size_t>(kSortWarps) * (groups + 1) * sizeof(int);
-    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<ID>, ids, slots, groups, run, static_cast<const int *>(counts),
-                              offsets, row_of_slot, slot_of_row);
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, smem, s, attr);
+    if (counts || tiles == 1)
+        return cudaLaunchKernelEx(&cfg, moe_sort_kernel<ID, false>, ids, slots, groups, run,
+                                  static_cast<const int *>(counts), offsets, row_of_slot, slot_of_row);
+    cudaLaunchAttribute both[2] = {attr[0]};
+    both[1].id = cudaLaunchAttributeClusterDimension;
+    both[1].val.clusterDim.x = static_cast<unsigned>(tiles);
+    both[1].val.clusterDim.y = 1;
+    both[1].val.clusterDim.z = 1;
+    cfg.attrs = both;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<ID, true>, ids, slots, groups, run,
+                              static_cast<const int *>(nullptr), offsets, row_of_slot, slot_of_row);
 }
 
 }  // namespace
 
-// Tiles of a sort.  One block (and one launch) while its warps have at most four
-// steps; from there 1024 slots a tile, up to 128 tiles, and fewer where many
-// experts make the tables of counts long (each tile reads them all).
+// Tiles of a sort.  One block while its warps have at most four steps, then a
+// cluster of up to eight with 1024 to 1536 slots each; past that 1024 slots a tile
+// again, up to 128 tiles, and fewer where many experts make the tables of counts long
+// (each tile reads them all).
 int64_t sort_tiles(int64_t slots, int64_t groups)
 {
     if (slots <= 4 * kSortThreads)
         return 1;
-    const int64_t most = groups > 128 ? 64 : 128, tiles = (slots + 1023) / 1024;
+    const int64_t most = slots <= kClusterSlots ? kSortCluster : groups > 128 ? 64 : 128;
+    const int64_t tiles = (slots + 1023) / 1024;
     return tiles < most ? tiles : most;
+}
+
+size_t sort_workspace(int64_t slots, int64_t groups)
+{
+    return slots <= kClusterSlots ? 0 : static_cast<size_t>(sort_tiles(slots, groups) * (groups + 1)) * sizeof(int);
 }
 
 cudaError_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int groups, int64_t *offsets,

@@ -261,8 +261,7 @@ size_t mxgemm_moe_sort_workspace_bytes(int64_t slots, int64_t groups)
 {
     if (slots < 1 || slots > kMaxRows || groups < 1 || groups > mxg::kMaxSortGroups)
         return 0;
-    const int64_t tiles = mxg::sort_tiles(slots, groups);
-    return tiles == 1 ? 0 : static_cast<size_t>(tiles * (groups + 1)) * sizeof(int);
+    return mxg::sort_workspace(slots, groups);
 }
 
 int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t groups, int64_t *offsets,

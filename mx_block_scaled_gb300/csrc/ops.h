@@ -98,9 +98,9 @@ cudaError_t launch_glu_backward(const GluBackParams &p, int act, int in_dtype, i
 
 // Expert ids 0 .. groups - 1, as many as a grouped GEMM plan takes.
 constexpr int kMaxSortGroups = 512;
-// Blocks that share a sort; with more than one, `counts` holds one int for each
-// (block, expert or dropped).
+// Blocks that share a sort, and the bytes of `counts` that it needs.
 int64_t sort_tiles(int64_t slots, int64_t groups);
+size_t sort_workspace(int64_t slots, int64_t groups);
 cudaError_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int groups, int64_t *offsets,
                             int32_t *row_of_slot, int32_t *slot_of_row, int *counts, cudaStream_t s);
 

@@ -37,6 +37,7 @@ def _ids(rng, T, k, G, load="zipf", drop=0.0):
 @pytest.mark.parametrize("T,k,G", [
     (1, 1, 1), (1, 8, 64), (3, 2, 512), (31, 1, 5), (32, 8, 64), (129, 7, 60), (512, 8, 8), (513, 8, 8),
     (1000, 6, 256), (4099, 2, 8), (20011, 3, 512), (70001, 8, 64),
+    (2048, 1, 4), (2049, 1, 512), (12288, 1, 300), (12289, 1, 300), (5461, 3, 64),
 ])
 @pytest.mark.parametrize("drop", [0.0, 0.1])
 def test_sort(dtype, T, k, G, drop):
