@@ -374,28 +374,25 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
 
 // dw[k] = sum of partial[b][k] over the blocks, in block order within each of 32
 // slices and then over the slices: the same sum every run.
-constexpr int kSlices = 32;
+constexpr int kSlices = 32;  // as many as columns of a block: warp s finishes column s
 
 __global__ void __launch_bounds__(32 * kSlices)
     rmsnorm_dweight_kernel(const float *partial, int blocks, int64_t K, float *dw)
 {
-    __shared__ float part[kSlices][32];
+    __shared__ float part[kSlices][33];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * 32, k = k0 + lane;
     float v = 0.0f;
 #pragma unroll 10
     for (int b = slice; b < blocks; b += kSlices)
         v += partial[b * K + k];
     part[slice][lane] = v;
     __syncthreads();
-    if (slice == 0) {
-#pragma unroll
-        for (int s = 1; s < kSlices; ++s)
-            v += part[s][lane];
-        dw[k] = v;
-    }
+    v = warp_sum(part[lane][slice]);  // warp `slice` adds column `slice` over the slices
+    if (lane == 0)
+        dw[k0 + slice] = v;
 }
 
 // Forward: a row in one block, runs of 16 values a thread.
