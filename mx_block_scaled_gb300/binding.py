@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmxgemm.so (include/mxgemm.h), same names as the C ABI.
+"""Thin binding of libmxgemm.so (include/mxgemm.h), same names as the C ABI: ctypes,
+and a native module that marshals the row operators' tensors.
 
 Argument marshalling only: every step of the GEMM (scale relayout, the tcgen05
 GEMM, the split-K reduce) and of the operators around it (RMS norm, gated
@@ -12,11 +13,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
-import threading
 from typing import NamedTuple
 
-from .build import DEBUG_LIB_PATH, LIB_PATH
+from .build import DEBUG_LIB_PATH, LIB_PATH, ROWOPS_PATH
 
 MXGEMM_FMT_MXFP8_E4M3 = 1
 MXGEMM_FMT_MXFP4_E2M1 = 2
@@ -215,6 +216,48 @@ def mxgemm_grouped_run(plan, offsets_ptr: int, A_ptr: int, SA_ptr: int, B_ptr: i
                                    run_flags, stream)
 
 
+# The row operators' entry points, arguments in the header's order.
+
+def mxgemm_rmsnorm(*args) -> int:
+    return _lib.mxgemm_rmsnorm(*args)
+
+
+def mxgemm_rmsnorm_backward_workspace_bytes(rows: int, K: int) -> int:
+    return _lib.mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
+
+
+def mxgemm_rmsnorm_backward(*args) -> int:
+    return _lib.mxgemm_rmsnorm_backward(*args)
+
+
+def mxgemm_glu(*args) -> int:
+    return _lib.mxgemm_glu(*args)
+
+
+def mxgemm_glu_backward(*args) -> int:
+    return _lib.mxgemm_glu_backward(*args)
+
+
+def mxgemm_moe_sort_workspace_bytes(slots: int, groups: int) -> int:
+    return _lib.mxgemm_moe_sort_workspace_bytes(slots, groups)
+
+
+def mxgemm_moe_sort(*args) -> int:
+    return _lib.mxgemm_moe_sort(*args)
+
+
+def mxgemm_moe_dispatch(*args) -> int:
+    return _lib.mxgemm_moe_dispatch(*args)
+
+
+def mxgemm_moe_combine(*args) -> int:
+    return _lib.mxgemm_moe_combine(*args)
+
+
+def mxgemm_moe_combine_backward(*args) -> int:
+    return _lib.mxgemm_moe_combine_backward(*args)
+
+
 def mxgemm_device_status(stream: int, reset: bool = True) -> int:
     return _lib.mxgemm_device_status(stream, 1 if reset else 0)
 
@@ -373,16 +416,9 @@ def quantize(x, fmt: int, tiled: bool = False, codes=None, scales=None, stream=N
 # ---- row operators around the GEMM ----------------------------------------------
 #
 # Outputs that are not passed in are made; everything runs on torch's current
-# stream, or on `stream=`.
-
-def mxgemm_rmsnorm_backward_workspace_bytes(rows: int, K: int) -> int:
-    return _lib.mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
-
-
-
-def mxgemm_moe_sort_workspace_bytes(slots: int, groups: int) -> int:
-    return _lib.mxgemm_moe_sort_workspace_bytes(slots, groups)
-
+# stream, or on `stream=`.  Tensors are checked and their addresses read in the
+# native module _rowops (csrc/rowops_py.cpp): ValueError for one that does not fit,
+# MxGemmError for a call that the library refuses.
 
 class RmsNorm(NamedTuple):
     h: object
@@ -407,111 +443,37 @@ class GluGrad(NamedTuple):
     a: object
 
 
-_IN_DTYPE = {}  # torch dtype -> MXGEMM_IN_*, filled by the first call (torch is imported lazily)
+# in the order of the native module's table
+_ROWOPS_ENTRIES = ("mxgemm_rmsnorm", "mxgemm_rmsnorm_backward_workspace_bytes", "mxgemm_rmsnorm_backward", "mxgemm_glu",
+                   "mxgemm_glu_backward", "mxgemm_moe_sort_workspace_bytes", "mxgemm_moe_sort", "mxgemm_moe_dispatch",
+                   "mxgemm_moe_combine", "mxgemm_moe_combine_backward", "mxgemm_sf_bytes")
 
 
-def _in_dtype(dtype, what: str) -> int:
-    if not _IN_DTYPE:
-        import torch
-        _IN_DTYPE.update({torch.float32: MXGEMM_IN_F32, torch.bfloat16: MXGEMM_IN_BF16})
-    d = _IN_DTYPE.get(dtype)
-    if d is None:
-        raise ValueError(f"{what}: unsupported dtype {dtype} (float32 or bfloat16)")
-    return d
+class _Unloaded:
+    """Loads _rowops, which needs torch, at the first call of a row operator."""
+
+    def __getattr__(self, name):
+        import torch  # noqa: F401  (its libraries first)
+        if not os.path.exists(ROWOPS_PATH):
+            raise RuntimeError(f"{ROWOPS_PATH} is missing: build it first (python -m mx_block_scaled_gb300.build, or "
+                               "__graft_entry__.build()); there is no fallback implementation")
+        spec = importlib.util.spec_from_file_location("mx_block_scaled_gb300._rowops", ROWOPS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in _ROWOPS_ENTRIES))
+        global _rowops
+        _rowops = module
+        return getattr(module, name)
 
 
-def _in_rows(t, shape, dtype, device, what: str):
-    """(pointer, row stride) of an input matrix whose rows are contiguous; None -> (0, 0)."""
-    if t is None:
-        return 0, 0
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{what} must be a {tuple(shape)} {dtype} tensor on {device}")
-    row, col = t.stride()
-    if col != 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    return t.data_ptr(), row
+_rowops = _Unloaded()
 
 
-def _dense(t, shape, dtype, device, what: str) -> int:
-    """Pointer of a dense tensor of this shape and type; None -> 0."""
-    if t is None:
-        return 0
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
-    return t.data_ptr()
-
-
-def _flat(t, n: int, dtype, device, what: str) -> int:
-    """Pointer of a dense tensor of n elements, whatever its shape."""
-    if t.numel() != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {device}")
-    return t.data_ptr()
-
-
-class _Kept(threading.local):
-    def __init__(self):
-        self.workspaces = {}  # stream handle -> uint8 tensor
-
-
-_kept = _Kept()
-
-
-def _workspace(t, need: int, device, stream: int):
-    """(pointer, bytes) of the caller's workspace, or of one that this module keeps.
-
-    One is kept for each thread and stream (a call costs 4 us less than with an
-    allocation of its own) and grows as needed: calls that a thread makes on one
-    stream run in order, so they may share it, and a smaller one that is let go was
-    allocated on that stream and is reused in its order.  While a graph is captured
-    the workspace is the graph's own, since a replay may run beside other calls.
-    """
-    if t is None:
-        if need == 0:
-            return 0, 0
-        import torch
-        t = _kept.workspaces.get(stream)
-        if t is None or t.numel() < need or t.device != device or torch._C._cuda_isCurrentStreamCapturing():
-            t = torch.empty((need,), dtype=torch.uint8, device=device)
-            if not torch._C._cuda_isCurrentStreamCapturing():
-                _kept.workspaces[stream] = t
-    elif t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _matrix(t, what: str):
-    """(shape, dtype, device, row stride) of the CUDA matrix that sets a call's sizes."""
-    shape = t.shape
-    if len(shape) != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    row, col = t.stride()
-    if col != 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    return shape, t.dtype, t.device, row
-
-
-def _mx_out(fmt: int, tiled: bool, rows: int, K: int, codes, scales, device, what: str):
-    """Codes and scales of an MX output, made where they are missing, and their pointers."""
-    import torch
-    if fmt == 0:
-        if codes is not None or scales is not None or tiled:
-            raise ValueError(f"{what}: an MX output needs a format")
-        return None, None, 0, 0
-    u8 = torch.uint8
-    shape = (rows, K if fmt == MXGEMM_FMT_MXFP8_E4M3 else K // 2)
-    sf_shape = (mxgemm_sf_bytes(rows, K),) if tiled else (rows, K // 32)
-    if codes is None:
-        codes = torch.empty(shape, dtype=u8, device=device)
-    if scales is None:
-        scales = torch.empty(sf_shape, dtype=u8, device=device)
-    return codes, scales, _dense(codes, shape, u8, device, "codes"), _dense(scales, sf_shape, u8, device, "scales")
-
-
-def _raw_stream(device) -> int:
-    """Handle of torch's current stream on `device` (read without making a Stream
-    object: 0.1 us instead of 2)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _done(out, what: str):
+    """The outputs of a native call, or the error that the library returned."""
+    if type(out) is int:
+        _check(out, what)
+    return out
 
 
 def _on_stream(f):
@@ -538,25 +500,8 @@ def rmsnorm(x, weight, eps: float, residual=None, fmt: int = 0, tiled: bool = Fa
     ``y`` with ``plain=True``, MX ``codes`` and ``scales`` with ``fmt``, and ``rstd``
     [rows] float32.  Outputs that are passed in are written in place.
     """
-    import torch
-    shape, dtype, dev, stride = _matrix(x, "x")
-    rows, K = shape
-    dt = _in_dtype(dtype, "x")
-    rp, rs = _in_rows(residual, shape, dtype, dev, "residual")
-    if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
-    if h is None and residual is not None:
-        h = torch.empty(shape, dtype=dtype, device=dev)
-    if y is None and plain:
-        y = torch.empty(shape, dtype=dtype, device=dev)
-    if rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, K, codes, scales, dev, "rmsnorm")
-    _check(_lib.mxgemm_rmsnorm(dt, x.data_ptr(), stride, rp, rs, weight.data_ptr(), _in_dtype(weight.dtype, "weight"),
-                               eps, rows, K, _dense(h, shape, dtype, dev, "h"), _dense(y, shape, dtype, dev, "y"),
-                               fmt, cp, sp, _dense(rstd, (rows,), torch.float32, dev, "rstd"),
-                               MXGEMM_QUANT_SF_TILED if tiled else 0, _raw_stream(dev)), "mxgemm_rmsnorm")
-    return RmsNorm(h, y, codes, scales, rstd)
+    return tuple.__new__(RmsNorm, _done(_rowops.rmsnorm(x, weight, eps, residual, fmt, tiled, plain, h, y, codes,
+                                                        scales, rstd), "mxgemm_rmsnorm"))
 
 
 @_on_stream
@@ -567,27 +512,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, worksp
     residual); ``dh`` is the gradient that reaches h past the norm.  dx is the
     gradient of x and of the residual.
     """
-    import torch
-    shape, dtype, dev, stride = _matrix(dy, "dy")
-    rows, K = shape
-    dt = _in_dtype(dtype, "dy")
-    hp, hs = _in_rows(h, shape, dtype, dev, "h")
-    gp, gs = _in_rows(dh, shape, dtype, dev, "dh")
-    if weight.shape != (K,) or weight.device != dev or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous ({K},) tensor on {dev}")
-    if dx is None:
-        dx = torch.empty(shape, dtype=dtype, device=dev)
-    if dweight is None:
-        dweight = torch.empty((K,), dtype=torch.float32, device=dev)
-    stream = _raw_stream(dev)
-    wp, ws = _workspace(workspace, mxgemm_rmsnorm_backward_workspace_bytes(rows, K), dev, stream)
-    _check(_lib.mxgemm_rmsnorm_backward(dt, dy.data_ptr(), stride, hp, hs,
-                                        _dense(rstd, (rows,), torch.float32, dev, "rstd"), weight.data_ptr(),
-                                        _in_dtype(weight.dtype, "weight"), gp, gs, rows, K,
-                                        _dense(dx, shape, dtype, dev, "dx"),
-                                        _dense(dweight, (K,), torch.float32, dev, "dweight"), wp, ws, stream),
-           "mxgemm_rmsnorm_backward")
-    return dx, dweight
+    return _done(_rowops.rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight, workspace), "mxgemm_rmsnorm_backward")
 
 
 @_on_stream
@@ -600,25 +525,8 @@ def glu(gate, up, act: int, fmt: int = 0, tiled: bool = False, plain: bool = Fal
     ``fmt`` as MX codes and scales; ``keep=True`` also returns the inputs' 8-bit
     checkpoint (codes [rows, 2F], scales [rows, 2F/32]) for :func:`glu_backward`.
     """
-    import torch
-    shape, dtype, dev, stride = _matrix(gate, "gate")
-    rows, F = shape
-    dt = _in_dtype(dtype, "gate")
-    up_ptr, up_stride = _in_rows(up, shape, dtype, dev, "up")
-    if up_ptr == 0 or (rows > 1 and up_stride != stride):
-        raise ValueError("gate and up must have the same row stride")
-    if y is None and plain:
-        y = torch.empty(shape, dtype=dtype, device=dev)
-    if keep or kept_codes is not None or kept_scales is not None:
-        kept_codes, kept_scales, kc, ks = _mx_out(MXGEMM_FMT_MXFP8_E4M3, False, rows, 2 * F, kept_codes, kept_scales,
-                                                  dev, "glu")
-    else:
-        kc = ks = 0
-    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, F, codes, scales, dev, "glu")
-    _check(_lib.mxgemm_glu(act, dt, gate.data_ptr(), up_ptr, stride, rows, F,
-                           _dense(y, shape, dtype, dev, "y"), fmt, cp, sp, MXGEMM_QUANT_SF_TILED if tiled else 0,
-                           kc, ks, _raw_stream(dev)), "mxgemm_glu")
-    return Glu(y, codes, scales, kept_codes, kept_scales)
+    return tuple.__new__(Glu, _done(_rowops.glu(gate, up, act, fmt, tiled, plain, keep, y, codes, scales, kept_codes,
+                                                kept_scales), "mxgemm_glu"))
 
 
 @_on_stream
@@ -631,26 +539,9 @@ def glu_backward(dy, act: int, gate=None, up=None, kept_codes=None, kept_scales=
     codes and scales with ``fmt`` (row length 2F), and with ``recompute=True`` the
     forward's output ``a`` [rows, F] again.
     """
-    import torch
-    shape, dtype, dev, stride = _matrix(dy, "dy")
-    rows, F = shape
-    dt = _in_dtype(dtype, "dy")
-    gp, gs = _in_rows(gate, shape, dtype, dev, "gate")
-    up_ptr, up_stride = _in_rows(up, shape, dtype, dev, "up")
-    if rows > 1 and up_stride != gs:
-        raise ValueError("gate and up must have the same row stride")
-    if dgu is None and plain:
-        dgu = torch.empty((rows, 2 * F), dtype=dtype, device=dev)
-    if a is None and recompute:
-        a = torch.empty(shape, dtype=dtype, device=dev)
-    codes, scales, cp, sp = _mx_out(fmt, tiled, rows, 2 * F, codes, scales, dev, "glu_backward")
-    _check(_lib.mxgemm_glu_backward(act, dt, dy.data_ptr(), stride, gp, up_ptr, gs,
-                                    _dense(kept_codes, (rows, 2 * F), torch.uint8, dev, "kept_codes"),
-                                    _dense(kept_scales, (rows, F // 16), torch.uint8, dev, "kept_scales"), rows, F,
-                                    _dense(dgu, (rows, 2 * F), dtype, dev, "dgu"), fmt, cp, sp,
-                                    MXGEMM_QUANT_SF_TILED if tiled else 0, _dense(a, shape, dtype, dev, "a"),
-                                    _raw_stream(dev)), "mxgemm_glu_backward")
-    return GluGrad(dgu, codes, scales, a)
+    return tuple.__new__(GluGrad, _done(_rowops.glu_backward(dy, act, gate, up, kept_codes, kept_scales, fmt, tiled,
+                                                             plain, recompute, dgu, codes, scales, a),
+                                        "mxgemm_glu_backward"))
 
 
 @_on_stream
@@ -661,32 +552,7 @@ def moe_sort(expert_ids, groups: int, offsets=None, row_of_slot=None, slot_of_ro
     router leaves them).  Ids outside 0..groups-1 drop their slot: its row lies past
     offsets[groups] and its row_of_slot entry is -1 - row.
     """
-    import torch
-    dev, n = expert_ids.device, expert_ids.numel()
-    if not expert_ids.is_cuda or not expert_ids.is_contiguous() or expert_ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError("expert_ids must be a contiguous CUDA int32 or int64 tensor")
-    if offsets is None:
-        offsets = torch.empty((groups + 1,), dtype=torch.int64, device=dev)
-    if row_of_slot is None:
-        row_of_slot = torch.empty((n,), dtype=torch.int32, device=dev)
-    if slot_of_row is None:
-        slot_of_row = torch.empty((n,), dtype=torch.int32, device=dev)
-    stream = _raw_stream(dev)
-    wp, ws = _workspace(workspace, mxgemm_moe_sort_workspace_bytes(n, groups), dev, stream)
-    _check(_lib.mxgemm_moe_sort(expert_ids.data_ptr(), expert_ids.element_size(), n, groups,
-                                _dense(offsets, (groups + 1,), torch.int64, dev, "offsets"),
-                                _flat(row_of_slot, n, torch.int32, dev, "row_of_slot"),
-                                _flat(slot_of_row, n, torch.int32, dev, "slot_of_row"), wp, ws, stream),
-           "mxgemm_moe_sort")
-    return offsets, row_of_slot, slot_of_row
-
-
-def _slots(row_of_slot, tokens: int) -> int:
-    """Slots per token of a row_of_slot table."""
-    n = row_of_slot.numel()
-    if tokens < 1 or n < tokens or n % tokens:
-        raise ValueError("row_of_slot must hold the same number of slots for every token")
-    return n // tokens
+    return _done(_rowops.moe_sort(expert_ids, groups, offsets, row_of_slot, slot_of_row, workspace), "mxgemm_moe_sort")
 
 
 @_on_stream
@@ -697,22 +563,7 @@ def moe_dispatch(x, row_of_slot, fmt: int, rows=None, scales=None):
     and row-major scales [slots, K/32], ready for :class:`GroupedPlan`;
     MXGEMM_FMT_BF16: bfloat16 rows, scales None.  Rows of dropped slots are zero.
     """
-    import torch
-    (tokens, K), dtype, dev, stride = _matrix(x, "x")
-    dt, n = _in_dtype(dtype, "x"), row_of_slot.numel()
-    topk = _slots(row_of_slot, tokens)
-    index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
-    if fmt == MXGEMM_FMT_BF16:
-        if rows is None:
-            rows = torch.empty((n, K), dtype=torch.bfloat16, device=dev)
-        rp, sp = _dense(rows, (n, K), torch.bfloat16, dev, "rows"), 0
-        if scales is not None:
-            raise ValueError("BF16 rows have no scales")
-    else:
-        rows, scales, rp, sp = _mx_out(fmt, False, n, K, rows, scales, dev, "moe_dispatch")
-    _check(_lib.mxgemm_moe_dispatch(dt, x.data_ptr(), stride, tokens, topk, K, index, fmt, rp, sp,
-                                    _raw_stream(dev)), "mxgemm_moe_dispatch")
-    return rows, scales
+    return _done(_rowops.moe_dispatch(x, row_of_slot, fmt, rows, scales), "mxgemm_moe_dispatch")
 
 
 @_on_stream
@@ -722,21 +573,7 @@ def moe_combine(y, row_of_slot, topk: int, weights=None, add=None, out=None):
     Dropped slots add nothing, whatever their rows of ``y`` and their weights hold.
     Without ``weights`` (all 1) this is the gradient of :func:`moe_dispatch`.
     """
-    import torch
-    (n, N), dtype, dev, stride = _matrix(y, "y")
-    dt = _in_dtype(dtype, "y")
-    if topk < 1 or n % topk or row_of_slot.numel() != n:
-        raise ValueError("y must have one row for each of the tokens * topk slots")
-    tokens = n // topk
-    index = _flat(row_of_slot, n, torch.int32, dev, "row_of_slot")
-    ap, as_ = _in_rows(add, (tokens, N), dtype, dev, "add")
-    if out is None:
-        out = torch.empty((tokens, N), dtype=dtype, device=dev)
-    wp = 0 if weights is None else _flat(weights, n, torch.float32, dev, "weights")
-    _check(_lib.mxgemm_moe_combine(dt, y.data_ptr(), stride, tokens, topk, N, index, wp, ap, as_,
-                                   _dense(out, (tokens, N), dtype, dev, "out"), _raw_stream(dev)),
-           "mxgemm_moe_combine")
-    return out
+    return _done(_rowops.moe_combine(y, row_of_slot, topk, weights, add, out), "mxgemm_moe_combine")[0]
 
 
 @_on_stream
@@ -745,24 +582,8 @@ def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None):
 
     A dropped slot's row of dy and its weight's gradient are zero.
     """
-    import torch
-    (tokens, N), dtype, dev, stride = _matrix(dout, "dout")
-    dt, n = _in_dtype(dtype, "dout"), row_of_slot.numel()
-    topk = _slots(row_of_slot, tokens)
-    yp, ys = _in_rows(y, (n, N), dtype, dev, "y")
-    if yp == 0:
-        raise ValueError("y is missing")
-    if dy is None:
-        dy = torch.empty((n, N), dtype=dtype, device=dev)
-    if dweights is None:
-        dweights = torch.empty(weights.shape, dtype=torch.float32, device=dev)
-    _check(_lib.mxgemm_moe_combine_backward(dt, dout.data_ptr(), stride, yp, ys, tokens, topk, N,
-                                            _flat(row_of_slot, n, torch.int32, dev, "row_of_slot"),
-                                            _flat(weights, n, torch.float32, dev, "weights"),
-                                            _dense(dy, (n, N), dtype, dev, "dy"),
-                                            _flat(dweights, n, torch.float32, dev, "dweights"),
-                                            _raw_stream(dev)), "mxgemm_moe_combine_backward")
-    return dy, dweights
+    return _done(_rowops.moe_combine_backward(dout, y, row_of_slot, weights, dy, dweights),
+                 "mxgemm_moe_combine_backward")
 
 
 def mxgemm_placement_scan(k: int, sa_ptr: int, sb_ptr: int, npairs: int, counts_ptr: int, first_ptr: int,

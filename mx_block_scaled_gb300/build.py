@@ -7,13 +7,17 @@ expert routing) are compiled in parallel and linked into
 ``mx_block_scaled_gb300/lib/libmxgemm.so``.  The four that hold the GEMM
 kernels and their host code are compiled a second time with MXGEMM_DEBUG
 (bounds-checked loads and stores, NaN-filled C, synchronous status) and linked
-with the others into ``lib/libmxgemm_debug.so``.
+with the others into ``lib/libmxgemm_debug.so``.  The Python module that
+marshals the row operators' tensors (rowops_py.cpp, host code against the
+installed PyTorch's headers) becomes ``lib/_rowops.so``.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +28,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmxgemm.so")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libmxgemm_debug.so")
+ROWOPS_PATH = os.path.join(LIB_DIR, "_rowops.so")
 
 SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu", "quantize.cu", "placement.cu", "probe.cu",
            "ops.cu", "norm.cu", "glu.cu", "moe.cu"]
@@ -48,9 +53,10 @@ def _deps():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(DEBUG_LIB_PATH):
+    made = (LIB_PATH, DEBUG_LIB_PATH, ROWOPS_PATH)
+    if not all(os.path.exists(p) for p in made):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(DEBUG_LIB_PATH))
+    t = min(os.path.getmtime(p) for p in made)
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -62,9 +68,29 @@ def _link(nvcc: str, objs, path: str) -> None:
     os.replace(tmp, path)
 
 
+def _build_rowops(nvcc: str) -> None:
+    """rowops_py.cpp -> _rowops.so, against the installed PyTorch (found, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: the row operators' Python module is built against its headers")
+    torch_dir = list(spec.submodule_search_locations)[0]
+    torch_lib = os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = ROWOPS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in include),
+           os.path.join(CSRC, "rowops_py.cpp"), "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for rowops_py.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ROWOPS_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libmxgemm.so and libmxgemm_debug.so if either is missing
-    or stale; return the release library's path."""
+    """Compile and link libmxgemm.so, libmxgemm_debug.so and _rowops.so if one of
+    them is missing or stale; return the release library's path."""
     if not force and not needs_build():
         return LIB_PATH
     nvcc = _nvcc()
@@ -84,8 +110,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     jobs = [(src, False) for src in SOURCES] + [(src, True) for src in DEBUG_SOURCES]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        rowops = ex.submit(_build_rowops, nvcc)
         objs = list(ex.map(compile_one, jobs))
+        rowops.result()
     release = objs[:len(SOURCES)]
     debug = objs[len(SOURCES):] + [o for (src, _), o in zip(jobs, release) if src not in DEBUG_SOURCES]
     _link(nvcc, release, LIB_PATH)
