@@ -490,8 +490,8 @@ MXGEMM_API int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, con
  *   dweight[k] = sum over rows of dy * h * rstd          (FP32, K values)
  * dx is the gradient of x and of the residual alike.  dx may be dh itself where
  * that is dense.  workspace: mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
- * bytes (0 for sizes the call refuses), 32-byte aligned, holding nothing between
- * calls.
+ * bytes (0 for few rows, NULL then, and for sizes the call refuses), 32-byte
+ * aligned, holding nothing between calls.
  */
 MXGEMM_API size_t mxgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t K);
 MXGEMM_API int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *h,

@@ -181,20 +181,107 @@ __device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 
 // A thread's values come in 16-byte pieces `threads` pieces apart, so that a warp's
 // copies are 512 consecutive bytes (two 16-byte halves of a 32-byte run per thread
-// would fetch every sector twice).
+// would fetch every sector twice).  The kernels for few and for many rows share this
+// layout and these sums, so a row's dx does not depend on how many rows there are.
+template <int IN>
+struct Pieces {
+    static constexpr int kPer = 16 / ElemBytes<IN>::value;  // values of a piece
+    static constexpr int kCount = kLaneVals / kPer;         // pieces of a thread
+    static constexpr int kPairs = kPer / 2;                 // FP32 pairs of a piece
+
+    static __device__ __forceinline__ F2 pair(const uint4 &v, int n)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (IN == kBf16)
+            return f2_bf16(w[n]);
+        else
+            return f2(__uint_as_float(w[2 * n]), __uint_as_float(w[2 * n + 1]));
+    }
+
+    // The weight at values k .. of this thread's piece.
+    template <int WT>
+    static __device__ __forceinline__ void load_weight(F2 (&w)[kPairs], const char *weight, uint32_t k, bool inside)
+    {
+#pragma unroll
+        for (int n = 0; n < kPairs; ++n) {
+            w[n] = f2(0.0f, 0.0f);
+            if (inside) {
+                if constexpr (WT == kBf16) {
+                    w[n] = f2_bf16(reinterpret_cast<const uint32_t *>(weight)[k / 2 + n]);
+                } else {
+                    const float2 v = reinterpret_cast<const float2 *>(weight)[k / 2 + n];
+                    w[n] = f2(v.x, v.y);
+                }
+            }
+        }
+    }
+
+    // dot += dy * w * h of one piece
+    static __device__ __forceinline__ F2 dot(F2 sum, const uint4 &dy, const uint4 &h, const F2 (&w)[kPairs])
+    {
+#pragma unroll
+        for (int n = 0; n < kPairs; ++n)
+            sum = f2_fma(f2_mul(pair(dy, n), w[n]), pair(h, n), sum);
+        return sum;
+    }
+
+    // dx of a pair of values; coef is -rstd^3 * mean(p * h)
+    static __device__ __forceinline__ F2 dx(F2 dy, F2 h, F2 dh, F2 w, F2 coef, F2 rstd)
+    {
+        return f2_fma(h, coef, f2_fma(f2_mul(dy, w), rstd, dh));
+    }
+
+    static __device__ __forceinline__ uint4 pack(const F2 (&v)[kPairs])
+    {
+        float d[kPer];
+#pragma unroll
+        for (int n = 0; n < kPairs; ++n)
+            f2_split(v[n], d[2 * n], d[2 * n + 1]);
+        if constexpr (IN == kBf16)
+            return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]),
+                              pack_bf16(d[6], d[7]));
+        else
+            return make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]),
+                              __float_as_uint(d[3]));
+    }
+};
+
+// A warp's share of a row's dot product into its entry; entries of warps that there
+// are not hold zero.
+__device__ __forceinline__ void leave_dot(F2 dot, float *part)
+{
+    float lo, hi;
+    f2_split(dot, lo, hi);
+    lo = warp_sum(lo + hi);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = lo;
+}
+
+__device__ __forceinline__ float row_coef(const float *part, float rstd, float inv_k)
+{
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kMaxThreads / 128; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(part)[i];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    return -(rstd * rstd * rstd * (((s.x + s.y) + (s.z + s.w)) * inv_k));
+}
+
 template <int IN, int WT, int DEPTH>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(const NormBackParams p)
 {
-    constexpr int E = ElemBytes<IN>::value;
-    constexpr int kPer = 16 / E;                 // values of a piece
-    constexpr int kPieces = kLaneVals / kPer;    // pieces of a thread
-    constexpr int kPairs = kPer / 2;             // FP32 pairs of a piece
+    using P = Pieces<IN>;
+    constexpr int E = ElemBytes<IN>::value, kPer = P::kPer, kPieces = P::kCount, kPairs = P::kPairs;
     extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][dy, h, dh][piece][thread]
     __shared__ __align__(16) float part[2][kMaxThreads / 32];
     __shared__ float row_rstd[2];  // by thread 0, a row ahead; each iteration's barrier shows it to the others
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t threads = blockDim.x, tid = threadIdx.x;
     const int64_t K = p.K, step = gridDim.x;
     const bool with_dh = p.dh != nullptr;
     const uint32_t plane = threads * 16;                                   // bytes of one piece of all threads
@@ -240,33 +327,17 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
                          : "memory");
         return v;
     };
-    auto pair = [](const uint4 &v, int n) -> F2 {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (IN == kBf16)
-            return f2_bf16(w[n]);
-        else
-            return f2(__uint_as_float(w[2 * n]), __uint_as_float(w[2 * n + 1]));
-    };
 #pragma unroll
     for (int d = 0; d < DEPTH - 1; ++d)
         fetch();
     F2 w[kPieces][kPairs], dw[kPieces][kPairs];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < kPieces; ++i) {
+        P::template load_weight<WT>(w[i], p.weight, (i * threads + tid) * kPer, inside[i]);
 #pragma unroll
-        for (int n = 0; n < kPairs; ++n) {
-            const uint32_t k = (i * threads + tid) * kPer + 2 * n;
-            w[i][n] = f2(0.0f, 0.0f);
-            if (inside[i]) {
-                if constexpr (WT == kBf16) {
-                    w[i][n] = f2_bf16(reinterpret_cast<const uint32_t *>(p.weight)[k / 2]);
-                } else {
-                    const float2 v = reinterpret_cast<const float2 *>(p.weight)[k / 2];
-                    w[i][n] = f2(v.x, v.y);
-                }
-            }
+        for (int n = 0; n < kPairs; ++n)
             dw[i][n] = f2(0.0f, 0.0f);
-        }
+    }
     uint4 next_dy[kPieces], next_h[kPieces];
     // partial sums of p * h of a row that has landed; its dy and h stay in registers for its turn
     auto dot_row = [&](uint32_t from, int buf) {
@@ -275,15 +346,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
         for (int i = 0; i < kPieces; ++i) {
             next_dy[i] = take(from + i * plane, i);
             next_h[i] = take(from + (kPieces + i) * plane, i);
-#pragma unroll
-            for (int n = 0; n < kPairs; ++n)
-                dot = f2_fma(f2_mul(pair(next_dy[i], n), w[i][n]), pair(next_h[i], n), dot);
+            dot = P::dot(dot, next_dy[i], next_h[i], w[i]);
         }
-        float lo, hi;
-        f2_split(dot, lo, hi);
-        lo = warp_sum(lo + hi);
-        if (lane == 0)
-            part[buf][warp] = lo;
+        leave_dot(dot, part[buf]);
     };
     int64_t row = blockIdx.x;
     char *dx = p.dx + row * K * E + tid * 16;
@@ -308,16 +373,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
             row_rstd[buf ^ 1] = next_rstd;
             next_rstd = row + 2 * step < p.rows ? p.rstd[row + 2 * step] : 0.0f;
         }
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < kMaxThreads / 128; ++i) {
-            const float4 v = reinterpret_cast<const float4 *>(part[buf])[i];
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
-        const float sum = (s.x + s.y) + (s.z + s.w);
+        const float coef = row_coef(part[buf], rstd, inv_k);
         uint4 dy[kPieces], h[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
@@ -327,31 +383,21 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
         if (row + step < p.rows)
             dot_row(following, buf ^ 1);
-        const float coef = -(rstd * rstd * rstd * (sum * inv_k));
         const F2 coef2 = f2(coef, coef), rstd2 = f2(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             uint4 dh = make_uint4(0, 0, 0, 0);
             if (with_dh)
                 dh = take(stage + (2 * kPieces + i) * plane, i);
-            float d[kPer];
+            F2 o[kPairs];
 #pragma unroll
             for (int n = 0; n < kPairs; ++n) {
-                const F2 g = pair(dy[i], n), v = pair(h[i], n);
-                const F2 o = f2_fma(v, coef2, f2_fma(f2_mul(g, w[i][n]), rstd2, pair(dh, n)));
-                f2_split(o, d[2 * n], d[2 * n + 1]);
+                const F2 g = P::pair(dy[i], n), v = P::pair(h[i], n);
+                o[n] = P::dx(g, v, P::pair(dh, n), w[i][n], coef2, rstd2);
                 dw[i][n] = f2_fma(g, f2_mul(v, rstd2), dw[i][n]);
             }
-            if (inside[i]) {
-                uint4 o;
-                if constexpr (IN == kBf16)
-                    o = make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]),
-                                   pack_bf16(d[6], d[7]));
-                else
-                    o = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]),
-                                   __float_as_uint(d[3]));
-                *reinterpret_cast<uint4 *>(dx + i * plane) = o;
-            }
+            if (inside[i])
+                *reinterpret_cast<uint4 *>(dx + i * plane) = P::pack(o);
         }
         dx += step * K * E;
         stage = following;
@@ -395,6 +441,110 @@ __global__ void __launch_bounds__(32 * kSlices)
         dw[k0 + slice] = v;
 }
 
+// Few rows: dw needs no dx, so one launch does both.  The first blocks sum the
+// columns' products over all rows (two neighbouring columns a lane in BF16, one in
+// FP32, the rows dealt to the warps), the others take a row each; dy and h are read
+// twice, the second time from L2, and there is neither a second launch nor partial
+// sums to wait for: 64 x 4096 BF16 2.6 us against 5.6 with the ring, 301 x 4096 FP32
+// 6.9 against 9.7, 1024 BF16 rows of 1024 to 8192 values 7.1-14.9 against 8.8-18.6;
+// from 2048 rows on the columns' blocks are too long (2048 x 1024: 15.3 against 11.5).
+// Two blocks an SM (64 registers): with one, 301 x 5120 FP32 takes 12.3 us instead of 7.8.
+constexpr int64_t kFewRows = 1024;
+
+template <int IN, int WT>
+__global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_backward_few_kernel(const NormBackParams p, int column_blocks)
+{
+    using P = Pieces<IN>;
+    constexpr int E = ElemBytes<IN>::value;
+    constexpr int kCols = IN == kBf16 ? 64 : 32;
+    __shared__ __align__(16) float part[kMaxThreads / 32];
+    __shared__ float2 sums[kMaxThreads / 32][32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int64_t K = p.K;
+    if (static_cast<int>(blockIdx.x) < column_blocks) {
+        const int64_t k = static_cast<int64_t>(blockIdx.x) * kCols + lane * (kCols / 32);
+        const char *dy = p.dy + k * E, *h = p.h + k * E;
+        float2 sum = make_float2(0.0f, 0.0f);
+        if (k < K)
+#pragma unroll 8
+            for (int64_t row = warp; row < p.rows; row += nwarps) {
+                const float rstd = p.rstd[row];
+                if constexpr (IN == kBf16) {
+                    const uint32_t g = *reinterpret_cast<const uint32_t *>(dy + row * p.dy_stride);
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(h + row * p.h_stride);
+                    sum.x = fmaf(__uint_as_float(g << 16), __uint_as_float(v << 16) * rstd, sum.x);
+                    sum.y = fmaf(__uint_as_float(g & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u) * rstd, sum.y);
+                } else {
+                    sum.x = fmaf(*reinterpret_cast<const float *>(dy + row * p.dy_stride),
+                                 *reinterpret_cast<const float *>(h + row * p.h_stride) * rstd, sum.x);
+                }
+            }
+        sums[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && k < K) {
+            for (int w = 1; w < nwarps; ++w) {
+                sum.x += sums[w][lane].x;
+                sum.y += sums[w][lane].y;
+            }
+            if constexpr (IN == kBf16)
+                *reinterpret_cast<float2 *>(p.dweight + k) = sum;
+            else
+                p.dweight[k] = sum.x;
+        }
+        return;
+    }
+    const int64_t row = blockIdx.x - column_blocks;
+    const uint32_t threads = (static_cast<uint32_t>(K) + kWarpVals - 1) / kWarpVals * 32, tid = threadIdx.x;
+    uint4 dy[P::kCount], h[P::kCount], dh[P::kCount];
+    F2 w[P::kCount][P::kPairs], dot = f2(0.0f, 0.0f);
+    bool inside[P::kCount];
+#pragma unroll
+    for (int i = 0; i < P::kCount; ++i) {
+        const uint32_t k = (i * threads + tid) * P::kPer;
+        inside[i] = tid < threads && k < K;
+        dy[i] = h[i] = dh[i] = make_uint4(0, 0, 0, 0);
+        if (inside[i]) {
+            dy[i] = *reinterpret_cast<const uint4 *>(p.dy + row * p.dy_stride + static_cast<int64_t>(k) * E);
+            h[i] = *reinterpret_cast<const uint4 *>(p.h + row * p.h_stride + static_cast<int64_t>(k) * E);
+        }
+        P::template load_weight<WT>(w[i], p.weight, k, inside[i]);
+    }
+    // dh is needed last: in FP32 its registers would be one block less on an SM, so it is loaded after the sum
+    auto load_dh = [&]() {
+        if (p.dh)
+#pragma unroll
+            for (int i = 0; i < P::kCount; ++i)
+                if (inside[i])
+                    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(dh[i].x), "=r"(dh[i].y), "=r"(dh[i].z), "=r"(dh[i].w)
+                                 : "l"(p.dh + row * p.dh_stride + static_cast<int64_t>((i * threads + tid) * P::kPer) * E)
+                                 : "memory");
+    };
+    if (IN == kBf16)
+        load_dh();
+    const float rstd = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < P::kCount; ++i)
+        dot = P::dot(dot, dy[i], h[i], w[i]);
+    leave_dot(dot, part);
+    if (IN != kBf16)
+        load_dh();
+    __syncthreads();
+    const float coef = row_coef(part, rstd, 1.0f / static_cast<float>(K));
+#pragma unroll
+    for (int i = 0; i < P::kCount; ++i) {
+        F2 o[P::kPairs];
+#pragma unroll
+        for (int n = 0; n < P::kPairs; ++n)
+            o[n] = P::dx(P::pair(dy[i], n), P::pair(h[i], n), P::pair(dh[i], n), w[i][n], f2(coef, coef),
+                         f2(rstd, rstd));
+        if (inside[i])
+            *reinterpret_cast<uint4 *>(p.dx + (row * K + (i * threads + tid) * P::kPer) * E) = P::pack(o);
+    }
+}
+
 // Forward: a row in one block, runs of 16 values a thread.
 struct Shape {
     int nch, threads;
@@ -412,7 +562,8 @@ Shape pick_shape(int64_t K)
 // Backward: rows of up to 8192 values take the ring, with 512 threads' worth of
 // blocks on an SM (four at most); wider ones as many blocks as their sums in shared
 // memory allow, two at most (each leaves a row of partial sums).
-constexpr int64_t kRingMaxK = 8192;
+constexpr int64_t kRingMaxK = 8192;  // kMaxThreads threads' values
+bool few_rows(int64_t rows, int64_t K) { return K <= kRingMaxK && rows <= kFewRows; }
 int blocks_per_sm(int64_t K)
 {
     if (K > kRingMaxK)
@@ -459,6 +610,11 @@ cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s
     blocks = blocks < static_cast<int64_t>(num_sms) * per_sm ? blocks : static_cast<int64_t>(num_sms) * per_sm;
     cudaError_t e;
     cudaLaunchAttribute attr[1];
+    if (few_rows(p.rows, p.K)) {
+        const int columns = static_cast<int>((p.K + (IN == kBf16 ? 63 : 31)) / (IN == kBf16 ? 64 : 32));
+        const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(columns + p.rows), kMaxThreads, 0, s, attr);
+        return cudaLaunchKernelEx(&cfg, rmsnorm_backward_few_kernel<IN, WT>, p, columns);
+    }
     if (p.K <= kRingMaxK) {
         const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sh.threads * kLaneVals * ElemBytes<IN>::value;
         const int64_t depth = kRingBytes / per_sm / row;
@@ -505,6 +661,8 @@ cudaError_t prepare_norm()
 
 int64_t norm_back_blocks(int64_t rows, int64_t K)
 {
+    if (few_rows(rows, K))
+        return 0;
     const int64_t most = static_cast<int64_t>(kNormBackSms) * blocks_per_sm(K);
     return rows < most ? rows : most;
 }

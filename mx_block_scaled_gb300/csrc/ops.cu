@@ -157,7 +157,8 @@ int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, con
         return MXGEMM_ERR_ALIGN;
     if (K > mxg::kNormMaxK)
         return MXGEMM_ERR_UNSUPPORTED;
-    if (!workspace || ws_bytes < mxgemm_rmsnorm_backward_workspace_bytes(rows, K))
+    const size_t need = mxgemm_rmsnorm_backward_workspace_bytes(rows, K);
+    if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
     int sms = 0;
     const int st = ops_device(&sms);

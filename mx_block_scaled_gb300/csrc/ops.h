@@ -59,8 +59,8 @@ struct NormBackParams {
     float *dweight;
     float *partial;                                // [blocks][K]
 };
-// Blocks of the first pass at most (each leaves one row of partial sums), on a part
-// of at most kNormBackSms multiprocessors.
+// Blocks of the first pass at most (each leaves one row of partial sums; none where
+// one launch does it all), on a part of at most kNormBackSms multiprocessors.
 constexpr int kNormBackSms = 152;
 int64_t norm_back_blocks(int64_t rows, int64_t K);
 // Set the backward kernels' shared-memory opt-in on the current device; once per

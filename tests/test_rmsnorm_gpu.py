@@ -137,6 +137,8 @@ def test_strided_inputs_in_place_h_and_guards(dtype):
 @pytest.mark.parametrize("rows,K,dh", [
     (1, 32, True), (2, 160, False), (33, 512, True), (400, 1056, True), (700, 128, False), (19, 4096, True),
     (40, 8192, False), (3, 8224, True), (5, 16384, True), (2, 16416, False), (3, 32768, True),
+    (1024, 96, True), (1025, 32, True), (1300, 160, False), (2000, 1056, True), (1100, 2080, True), (1030, 4096, False),
+    (1025, 8192, True),
 ])
 def test_backward(dtype, rows, K, dh):
     import torch
@@ -161,7 +163,7 @@ def test_backward_in_place_strided_and_mixed_weight():
     import torch
     b = lib()
     rng = np.random.default_rng(21)
-    rows, K = 50, 288
+    rows, K = 1200, 288
     hw, hw64 = _make(rng, (rows, 2 * K), _dtype("bf16"))
     dyw, dyw64 = _make(rng, (rows, K + 96), _dtype("bf16"))
     dh, dh64 = _make(rng, (rows, K), _dtype("bf16"))

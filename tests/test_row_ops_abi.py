@@ -39,7 +39,7 @@ def test_rmsnorm(lib, change, expect):
 
 
 BACK = dict(in_dtype=1, dy=64, dy_stride=256, h=64, h_stride=256, rstd=64, weight=64, weight_dtype=1, dh=64,
-            dh_stride=256, rows=4, K=256, dx=64, dweight=64, workspace=64, ws_bytes=4096, stream=None)
+            dh_stride=256, rows=1500, K=256, dx=64, dweight=64, workspace=64, ws_bytes=1 << 20, stream=None)
 
 
 @pytest.mark.parametrize("change,expect", [
@@ -48,7 +48,7 @@ BACK = dict(in_dtype=1, dy=64, dy_stride=256, h=64, h_stride=256, rstd=64, weigh
     (dict(rows=-1), SHAPE), (dict(K=33), SHAPE), (dict(dh_stride=8), SHAPE), (dict(h_stride=255), SHAPE),
     (dict(dy=48), ALIGN), (dict(dh_stride=260), ALIGN), (dict(dx=16), ALIGN), (dict(dweight=16), ALIGN),
     (dict(workspace=16), ALIGN),
-    (dict(workspace=None), WORKSPACE), (dict(ws_bytes=4095), WORKSPACE),
+    (dict(workspace=None), WORKSPACE), (dict(ws_bytes=608 * 256 * 4 - 1), WORKSPACE),
     (dict(K=65536, dy_stride=65536, h_stride=65536, dh_stride=65536, ws_bytes=1 << 30), UNSUPPORTED),
 ])
 def test_rmsnorm_backward(lib, change, expect):
@@ -57,7 +57,8 @@ def test_rmsnorm_backward(lib, change, expect):
 
 def test_rmsnorm_backward_workspace(lib):
     f = lib.mxgemm_rmsnorm_backward_workspace_bytes
-    assert f(4, 256) == 4 * 256 * 4
+    assert f(4, 256) == f(1024, 8192) == 0          # one launch, no partial sums
+    assert f(1500, 256) == 608 * 256 * 4 and f(4, 16384) == 4 * 16384 * 4
     assert f(0, 256) == f(4, 40) == f(4, 65536) == 0
     assert f(1 << 20, 8192) == f(1 << 21, 8192) <= 1 << 24
 
