@@ -553,7 +553,8 @@ MXGEMM_API int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slo
                                void *stream);
 
 /*
- * Write each token's row to the rows of its slots: rows[row_of_slot[s]] = x[s / topk].
+ * Write each token's row to the rows of its slots: rows[row_of_slot[s]] = x[s / topk]
+ * (here and below topk is 1 .. 2^20 and tokens * topk below 2^31).
  *   fmt MXGEMM_FMT_MXFP8_E4M3 / MXGEMM_FMT_MXFP4_E2M1: codes and row-major scales
  *   [tokens*topk, K/32], the A and SA of mxgemm_grouped_run (each token is encoded
  *   once); MXGEMM_FMT_BF16: BF16 rows, scales NULL.
@@ -570,8 +571,8 @@ MXGEMM_API int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride
  *   out[t] = add[t] + sum_j weights[t*topk + j] * y[row_of_slot[t*topk + j]]
  *   weights: FP32, or NULL for 1.   add: [tokens, N] (the residual stream), or
  *   NULL; out may be add itself where that is dense.
- * Dropped slots add nothing: neither their rows nor their weights are read (they
- * may hold NaN); a token without slots gets add[t] or zero.
+ * Dropped slots add nothing: their rows are not read and their weights not used
+ * (either may hold NaN); a token without slots gets add[t] or zero.
  */
 MXGEMM_API int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride, int64_t tokens, int64_t topk,
                                   int64_t N, const int32_t *row_of_slot, const float *weights, const void *add,

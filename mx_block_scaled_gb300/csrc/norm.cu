@@ -8,9 +8,9 @@
 // registers of one block between its reduction and its use and writes h, y, codes
 // and scales from them, in FP32 until the final rounding; blocks on the same SM
 // cover each other's reductions: 16384 x 8192 BF16 with residual and tiled MXFP8
-// (944 MB) 137 us, 6.9 TB/s.  The backward also sums over rows, so its blocks stay
-// and hide the reduction in a pipeline instead: 16384 x 8192 BF16 (1074 MB) 175 us,
-// 6.1 TB/s, 8192 x 4096 (268 MB) 51 us, of which 4 are the second launch.
+// (944 MB) 135 us, 7.0 TB/s.  The backward also sums over rows, so its blocks stay
+// and hide the reduction in a pipeline instead: 16384 x 8192 BF16 (1074 MB) 174 us,
+// 6.2 TB/s, 8192 x 4096 (268 MB) 50 us, of which 4 are the second launch.
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"

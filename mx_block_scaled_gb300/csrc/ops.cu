@@ -287,10 +287,10 @@ int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t
                                           static_cast<cudaStream_t>(stream)));
 }
 
-// tokens x topk slots fit the sort's 32-bit rows
+// tokens x topk slots fit the sort's 32-bit rows, and a token's slots a 32-bit count with room to step past it
 static bool slots_ok(int64_t tokens, int64_t topk)
 {
-    return tokens >= 1 && topk >= 1 && tokens <= kMaxRows && topk <= kMaxRows / tokens;
+    return tokens >= 1 && topk >= 1 && topk <= (1 << 20) && tokens <= kMaxRows / topk;
 }
 
 // one warp for every 512 values of a token, numbered in 32 bits

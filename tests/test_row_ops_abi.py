@@ -126,7 +126,8 @@ SEND = dict(in_dtype=2, x=64, x_stride=256, tokens=4, topk=2, K=256, row_of_slot
 @pytest.mark.parametrize("change,expect", [
     (dict(x=None), ARG), (dict(row_of_slot=None), ARG), (dict(rows=None), ARG), (dict(fmt=0), ARG), (dict(fmt=4), ARG),
     (dict(scales=None), ARG), (dict(fmt=3), ARG), (dict(in_dtype=3), ARG),
-    (dict(tokens=0), SHAPE), (dict(topk=0), SHAPE), (dict(tokens=1 << 20, topk=1 << 12), SHAPE), (dict(K=48), SHAPE),
+    (dict(tokens=0), SHAPE), (dict(topk=0), SHAPE), (dict(tokens=1 << 20, topk=1 << 12), SHAPE), (dict(tokens=1, topk=(1 << 20) + 1), SHAPE),
+    (dict(K=48), SHAPE),
     (dict(x_stride=128), SHAPE),
     (dict(x=16), ALIGN), (dict(x_stride=257), ALIGN), (dict(row_of_slot=2), ALIGN), (dict(rows=8), ALIGN),
     (dict(scales=8), ALIGN), (dict(fmt=3, scales=None, rows=16), ALIGN),
@@ -142,7 +143,7 @@ COMB = dict(in_dtype=2, y=64, y_stride=256, tokens=4, topk=2, N=256, row_of_slot
 
 @pytest.mark.parametrize("change,expect", [
     (dict(y=None), ARG), (dict(row_of_slot=None), ARG), (dict(out=None), ARG), (dict(in_dtype=0), ARG),
-    (dict(tokens=0), SHAPE), (dict(topk=-1), SHAPE), (dict(N=250), SHAPE), (dict(y_stride=0), SHAPE),
+    (dict(tokens=0), SHAPE), (dict(topk=-1), SHAPE), (dict(tokens=1, topk=1 << 30), SHAPE), (dict(N=250), SHAPE), (dict(y_stride=0), SHAPE),
     (dict(add_stride=100), SHAPE),
     (dict(y=16), ALIGN), (dict(add=16), ALIGN), (dict(out=16), ALIGN), (dict(weights=2), ALIGN),
     (dict(y_stride=260), ALIGN), (dict(tokens=1 << 29, N=8192, y_stride=8192, add_stride=8192), UNSUPPORTED),
