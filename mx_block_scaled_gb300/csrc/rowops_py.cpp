@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -242,9 +243,20 @@ int64_t integer(PyObject *o)
     return v;
 }
 
-template <typename... O>
-PyObject *result(int status, O &...out)
+// The outputs of call(), an entry point of the library: it runs without the
+// interpreter's lock, since a launch waits while the stream's queue is full.
+template <typename F, typename... O>
+PyObject *result(F call, O &...out)
 {
+    struct Unlocked {
+        PyThreadState *const state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    };
+    int status;
+    {
+        const Unlocked unlocked;
+        status = call();
+    }
     if (status != MXGEMM_OK)
         return PyLong_FromLong(status);
     PyObject *t = PyTuple_New(sizeof...(O));
@@ -273,10 +285,12 @@ PyObject *rmsnorm(Args a)
     output(y, a[8], plain, {s.rows, s.cols}, s.dtype, s, "y");
     mx_output(codes, scales, a[9], a[10], fmt, tiled, s.rows, s.cols, s, "rmsnorm");
     output(rstd, a[11], true, {s.rows}, at::kFloat, s, "rstd");
-    return result(g_entry.rmsnorm(s.in_dtype, s.ptr, s.stride, r.ptr, r.stride, w, wt, static_cast<float>(eps), s.rows,
-                                  s.cols, h.ptr, y.ptr, fmt, codes.ptr, static_cast<uint8_t *>(scales.ptr),
-                                  static_cast<float *>(rstd.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, current_stream(s)),
-                  h, y, codes, scales, rstd);
+    const auto call = [&] {
+        return g_entry.rmsnorm(s.in_dtype, s.ptr, s.stride, r.ptr, r.stride, w, wt, static_cast<float>(eps), s.rows,
+                               s.cols, h.ptr, y.ptr, fmt, codes.ptr, static_cast<uint8_t *>(scales.ptr),
+                               static_cast<float *>(rstd.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, current_stream(s));
+    };
+    return result(call, h, y, codes, scales, rstd);
 }
 
 // (dy, h, rstd, weight, dh, dx, dweight, workspace)
@@ -291,11 +305,13 @@ PyObject *rmsnorm_backward(Args a)
     output(dx, a[5], true, {s.rows, s.cols}, s.dtype, s, "dx");
     output(dw, a[6], true, {s.cols}, at::kFloat, s, "dweight");
     const Workspace ws(a[7], g_entry.rmsnorm_backward_workspace_bytes(s.rows, s.cols), s);
-    return result(g_entry.rmsnorm_backward(s.in_dtype, s.ptr, s.stride, h.ptr, h.stride,
-                                           static_cast<const float *>(rstd.ptr), w, wt, dh.ptr, dh.stride, s.rows,
-                                           s.cols, dx.ptr, static_cast<float *>(dw.ptr), ws.ptr, ws.bytes,
-                                           current_stream(s)),
-                  dx, dw);
+    const auto call = [&] {
+        return g_entry.rmsnorm_backward(s.in_dtype, s.ptr, s.stride, h.ptr, h.stride,
+                                        static_cast<const float *>(rstd.ptr), w, wt, dh.ptr, dh.stride, s.rows,
+                                        s.cols, dx.ptr, static_cast<float *>(dw.ptr), ws.ptr, ws.bytes,
+                                        current_stream(s));
+    };
+    return result(call, dx, dw);
 }
 
 // gate and up have one stride
@@ -320,10 +336,12 @@ PyObject *glu(Args a)
     output(y, a[7], plain, {s.rows, s.cols}, s.dtype, s, "y");
     mx_output(codes, scales, a[8], a[9], fmt, tiled, s.rows, s.cols, s, "glu");
     mx_output(kc, ks, a[10], a[11], keep ? MXGEMM_FMT_MXFP8_E4M3 : 0, false, s.rows, 2 * s.cols, s, "glu");
-    return result(g_entry.glu(act, s.in_dtype, s.ptr, up.ptr, s.stride, s.rows, s.cols, y.ptr, fmt, codes.ptr,
-                              static_cast<uint8_t *>(scales.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, kc.ptr,
-                              static_cast<uint8_t *>(ks.ptr), current_stream(s)),
-                  y, codes, scales, kc, ks);
+    const auto call = [&] {
+        return g_entry.glu(act, s.in_dtype, s.ptr, up.ptr, s.stride, s.rows, s.cols, y.ptr, fmt, codes.ptr,
+                           static_cast<uint8_t *>(scales.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, kc.ptr,
+                           static_cast<uint8_t *>(ks.ptr), current_stream(s));
+    };
+    return result(call, y, codes, scales, kc, ks);
 }
 
 // (dy, act, gate, up, kept_codes, kept_scales, fmt, tiled, plain, recompute, dgu, codes, scales, a)
@@ -341,11 +359,13 @@ PyObject *glu_backward(Args a)
     output(dgu, a[10], plain, {s.rows, 2 * s.cols}, s.dtype, s, "dgu");
     mx_output(codes, scales, a[11], a[12], fmt, tiled, s.rows, 2 * s.cols, s, "glu_backward");
     output(again, a[13], recompute, {s.rows, s.cols}, s.dtype, s, "a");
-    return result(g_entry.glu_backward(act, s.in_dtype, s.ptr, s.stride, gate.ptr, up.ptr, gate.stride, kc.ptr,
-                                       static_cast<const uint8_t *>(ks.ptr), s.rows, s.cols, dgu.ptr, fmt, codes.ptr,
-                                       static_cast<uint8_t *>(scales.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, again.ptr,
-                                       current_stream(s)),
-                  dgu, codes, scales, again);
+    const auto call = [&] {
+        return g_entry.glu_backward(act, s.in_dtype, s.ptr, s.stride, gate.ptr, up.ptr, gate.stride, kc.ptr,
+                                    static_cast<const uint8_t *>(ks.ptr), s.rows, s.cols, dgu.ptr, fmt, codes.ptr,
+                                    static_cast<uint8_t *>(scales.ptr), tiled ? MXGEMM_QUANT_SF_TILED : 0, again.ptr,
+                                    current_stream(s));
+    };
+    return result(call, dgu, codes, scales, again);
 }
 
 // (expert_ids, groups, offsets, row_of_slot, slot_of_row, workspace)
@@ -366,10 +386,12 @@ PyObject *moe_sort(Args a)
     output(row, a[3], true, {n}, at::kInt, s, "row_of_slot");
     output(slot, a[4], true, {n}, at::kInt, s, "slot_of_row");
     const Workspace ws(a[5], g_entry.moe_sort_workspace_bytes(n, groups), s);
-    return result(g_entry.moe_sort(ids->const_data_ptr(), static_cast<int>(ids->element_size()), n, groups,
-                                   static_cast<int64_t *>(offsets.ptr), static_cast<int32_t *>(row.ptr),
-                                   static_cast<int32_t *>(slot.ptr), ws.ptr, ws.bytes, current_stream(s)),
-                  offsets, row, slot);
+    const auto call = [&] {
+        return g_entry.moe_sort(ids->const_data_ptr(), static_cast<int>(ids->element_size()), n, groups,
+                                static_cast<int64_t *>(offsets.ptr), static_cast<int32_t *>(row.ptr),
+                                static_cast<int32_t *>(slot.ptr), ws.ptr, ws.bytes, current_stream(s));
+    };
+    return result(call, offsets, row, slot);
 }
 
 // Slots of a token of a row_of_slot table, and the table's address.
@@ -399,9 +421,11 @@ PyObject *moe_dispatch(Args a)
     } else {
         mx_output(rows, scales, a[3], a[4], fmt, false, n, s.cols, s, "moe_dispatch");
     }
-    return result(g_entry.moe_dispatch(s.in_dtype, s.ptr, s.stride, s.rows, topk, s.cols, table, fmt, rows.ptr,
-                                       static_cast<uint8_t *>(scales.ptr), current_stream(s)),
-                  rows, scales);
+    const auto call = [&] {
+        return g_entry.moe_dispatch(s.in_dtype, s.ptr, s.stride, s.rows, topk, s.cols, table, fmt, rows.ptr,
+                                    static_cast<uint8_t *>(scales.ptr), current_stream(s));
+    };
+    return result(call, rows, scales);
 }
 
 // (y, row_of_slot, topk, weights, add, out)
@@ -417,9 +441,11 @@ PyObject *moe_combine(Args a)
     const Rows add = in_rows(a[4], s, tokens, s.cols, "add");
     Out out;
     output(out, a[5], true, {tokens, s.cols}, s.dtype, s, "out");
-    return result(g_entry.moe_combine(s.in_dtype, s.ptr, s.stride, tokens, topk, s.cols, table, w, add.ptr, add.stride,
-                                      out.ptr, current_stream(s)),
-                  out);
+    const auto call = [&] {
+        return g_entry.moe_combine(s.in_dtype, s.ptr, s.stride, tokens, topk, s.cols, table, w, add.ptr, add.stride,
+                                   out.ptr, current_stream(s));
+    };
+    return result(call, out);
 }
 
 // (dout, y, row_of_slot, weights, dy, dweights)
@@ -443,9 +469,11 @@ PyObject *moe_combine_backward(Args a)
         if (!dw.object)
             throw python_error();
     }
-    return result(g_entry.moe_combine_backward(s.in_dtype, s.ptr, s.stride, y.ptr, y.stride, s.rows, topk, s.cols,
-                                               table, w, dy.ptr, static_cast<float *>(dw.ptr), current_stream(s)),
-                  dy, dw);
+    const auto call = [&] {
+        return g_entry.moe_combine_backward(s.in_dtype, s.ptr, s.stride, y.ptr, y.stride, s.rows, topk, s.cols, table,
+                                            w, dy.ptr, static_cast<float *>(dw.ptr), current_stream(s));
+    };
+    return result(call, dy, dw);
 }
 
 // One Python entry: argument count, C++ exceptions to Python ones.
@@ -488,7 +516,8 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t count)
     Py_RETURN_NONE;
 }
 
-#define ROWOP(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<name, n>)), METH_FASTCALL, nullptr}
+#define ROWOP(name, n) \
+    {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(bind)), METH_FASTCALL, nullptr},
     ROWOP(rmsnorm, 12),
