@@ -206,15 +206,16 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) glu_backward_kernel
                 store_codes(codes, k, qg);
                 store_codes(codes, F + k, qu);
             }
-            // rows of 2F values: the blocks of dup follow those of dgate.  A tile or a word of four scales may hold
-            // both where F is not a multiple of 128, so scales go out one byte at a time.
+            // Rows of 2F values: the blocks of dup follow those of dgate.  A tile or a word of four scales may hold
+            // both where F is not a multiple of 128, so scales go out one byte at a time (words, where they can be,
+            // take two shuffles more each: 132 us against 122 at 8192 x 14336 MXFP8).
             if (inside && (lane & 1) == 0) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int64_t kk = k + half * F;
                     const int64_t to = p.mx.mode == kScaleTiled
                                            ? tile_scale_offset(row, kk >> 7, F >> 6) + ((kk >> 5) & 3)
-                                           : (2 * row * F + half * F + k) >> 5;
+                                           : (2 * row * F + kk) >> 5;
                     p.mx.scales[to] = static_cast<uint8_t>(half ? qu.scode : qg.scode);
                 }
             }

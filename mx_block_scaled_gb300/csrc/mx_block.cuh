@@ -51,6 +51,43 @@ __device__ __forceinline__ void st_row32(void *p, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// Pairs of FP32 values in one 64-bit register: the packed product and
+// multiply-add round each half as the scalar ones do.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_split(F2 v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// A word of two BF16 values as an FP32 pair.
+__device__ __forceinline__ F2 f2_bf16(uint32_t w)
+{
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // Sixteen values as loaded: one 32-byte access in BF16, two in FP32.
 template <int DT>
 struct Raw16 {
@@ -78,6 +115,15 @@ struct Raw16 {
             return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
         }
         return __uint_as_float(r[(i >> 3) & (kParts - 1)][i & 7]);
+    }
+
+    // values 2i and 2i + 1
+    __device__ __forceinline__ F2 pair(int i) const
+    {
+        if constexpr (DT == kBf16)
+            return f2_bf16(r[0][i]);
+        else
+            return f2(at(2 * i), at(2 * i + 1));
     }
 };
 
@@ -116,34 +162,6 @@ __device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, f
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
-
-// Pairs of FP32 values in one 64-bit register: the packed product and
-// multiply-add round each half as the scalar ones do.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 f2(float lo, float hi)
-{
-    F2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void f2_split(F2 v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-// A word of two BF16 values as an FP32 pair.
-__device__ __forceinline__ F2 f2_bf16(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
 // max(|a|, |b|, |c|); a NaN among them gives NaN.
 __device__ __forceinline__ float max_abs3(float a, float b, float c)

@@ -34,66 +34,92 @@ __device__ __forceinline__ float block_sum(float v, float *part)
 }
 
 // ------------------------------------------------------------------ forward --
-// One block per row, a thread holds NCH runs of 16 values.
-template <int IN, int WT, int FMT, int NCH>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p)
+// A block takes ROWS neighbouring rows at once, a thread NCH runs of 16 values of
+// each.  Sums and products are packed pairs: at 3 bytes a value (BF16 to MXFP8 without
+// a residual) a value may cost 17 instructions before they bind instead of HBM.
+template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
+__global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 2 : 0) rmsnorm_kernel(const NormParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
-    __shared__ float part[32];
+    __shared__ float part[ROWS][32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int64_t row = blockIdx.x, K = p.K;
-    const char *xrow = p.x + row * p.x_stride;
-    const char *rrow = p.residual ? p.residual + row * p.residual_stride : nullptr;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS, K = p.K;
 
-    Raw16<IN> x[NCH], r[NCH];
+    Raw16<IN> x[ROWS][NCH], r[RES ? ROWS : 1][RES ? NCH : 1];
     Raw16<WT> w[NCH];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-        x[c].load(xrow + k * E, k < K);
-        r[c].load(rrow + k * E, k < K && rrow != nullptr);
-    }
+    for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
+            const bool inside = k < K && (ROWS == 1 || row0 + q < p.rows);
+            x[q][c].load(p.x + (row0 + q) * p.x_stride + k * E, inside);
+            if constexpr (RES)
+                r[q][c].load(p.residual + (row0 + q) * p.residual_stride + k * E, inside);
+        }
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
         w[c].load(p.weight + k * ElemBytes<WT>::value, k < K);
     }
-    float h[NCH][kLaneVals];
-    float ss = 0.0f;
+    F2 h[ROWS][NCH][kLaneVals / 2];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int q = 0; q < ROWS; ++q) {
+        F2 ss = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) {
-            h[c][i] = rrow ? x[c].at(i) + r[c].at(i) : x[c].at(i);
-            ss = fmaf(h[c][i], h[c][i], ss);
-        }
-    const float rstd = __frsqrt_rn(block_sum(ss, part) / static_cast<float>(K) + p.eps);
-    if (threadIdx.x == 0 && p.rstd)
-        p.rstd[row] = rstd;
+        for (int c = 0; c < NCH; ++c)
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        const int64_t k0 = (c * nwarps + warp) * kWarpVals;
-        const int64_t k = k0 + lane * kLaneVals;
-        const bool inside = k < K;
-        if (p.h && inside)
-            store16<IN>(p.h + (row * K + k) * E, h[c]);
-        float y[kLaneVals];
+            for (int i = 0; i < kLaneVals / 2; ++i) {
+                h[q][c][i] = x[q][c].pair(i);
+                if constexpr (RES)
+                    h[q][c][i] = f2_add(h[q][c][i], r[q][c].pair(i));
+                ss = f2_fma(h[q][c][i], h[q][c][i], ss);
+            }
+        float lo, hi;
+        f2_split(ss, lo, hi);
+        lo = warp_sum(lo + hi);
+        if (lane == 0)
+            part[q][warp] = lo;
+    }
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            y[i] = h[c][i] * rstd * w[c].at(i);
-        if (p.y && inside)
-            store16<IN>(p.y + (row * K + k) * E, y);
-        if (FMT != kNoFmt) {
-            const auto q = mx_encode<FMT == kNoFmt ? kMxfp8 : FMT>(y);
-            if (inside)
-                store_codes(p.mx.codes + row * (FMT == kMxfp8 ? K : K >> 1), k, q);
-            store_scales(p.mx.scales, p.mx.mode, row, k0, K, lane, q.scode);
+    for (int q = 0; q < ROWS; ++q) {
+        const int64_t row = row0 + q;
+        if (ROWS > 1 && row >= p.rows)
+            break;  // block-uniform
+        const float ss = warp_sum(lane < nwarps ? part[q][lane] : 0.0f);
+        const float rstd = __frsqrt_rn(ss / static_cast<float>(K) + p.eps);
+        if (threadIdx.x == 0 && p.rstd)
+            p.rstd[row] = rstd;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int64_t k0 = (c * nwarps + warp) * kWarpVals;
+            const int64_t k = k0 + lane * kLaneVals;
+            const bool inside = k < K;
+            float v[kLaneVals];
+            if (p.h && inside) {
+#pragma unroll
+                for (int i = 0; i < kLaneVals / 2; ++i)
+                    f2_split(h[q][c][i], v[2 * i], v[2 * i + 1]);
+                store16<IN>(p.h + (row * K + k) * E, v);
+            }
+#pragma unroll
+            for (int i = 0; i < kLaneVals / 2; ++i)
+                f2_split(f2_mul(f2_mul(h[q][c][i], f2(rstd, rstd)), w[c].pair(i)), v[2 * i], v[2 * i + 1]);
+            if (p.y && inside)
+                store16<IN>(p.y + (row * K + k) * E, v);
+            if (FMT != kNoFmt) {
+                const auto e = mx_encode<FMT == kNoFmt ? kMxfp8 : FMT>(v);
+                if (inside)
+                    store_codes(p.mx.codes + row * (FMT == kMxfp8 ? K : K >> 1), k, e);
+                store_scales(p.mx.scales, p.mx.mode, row, k0, K, lane, e.scode);
+            }
         }
     }
     if (FMT != kNoFmt && p.mx.mode == kScaleTiled)
-        pad_tiled_scales(p.mx.scales, p.rows, K, row * blockDim.x + threadIdx.x,
+        pad_tiled_scales(p.mx.scales, p.rows, K, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
                          static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
@@ -545,15 +571,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_backward_few_kernel(co
     }
 }
 
-// Forward: a row in one block, runs of 16 values a thread.
+// Runs of 16 values a thread takes of a row of K values, at least `least`, with at
+// most kMaxThreads threads.
 struct Shape {
     int nch, threads;
 };
 
-Shape pick_shape(int64_t K)
+Shape pick_shape(int64_t K, int least = 1)
 {
     Shape s;
-    s.nch = K <= 8192 ? 1 : K <= 16384 ? 2 : 4;
+    s.nch = K <= 8192 && least == 1 ? 1 : K <= 16384 ? 2 : 4;
     const int64_t warps = (K + s.nch * kWarpVals - 1) / (s.nch * kWarpVals);
     s.threads = static_cast<int>(warps) * 32;
     return s;
@@ -572,23 +599,44 @@ int blocks_per_sm(int64_t K)
     return n > 4 ? 4 : n;
 }
 
-template <int IN, int WT, int FMT>
+template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
+cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        row_launch(static_cast<unsigned>((p.rows + ROWS - 1) / ROWS), threads, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS>, p);
+}
+
+// Without a residual a row brings half the bytes to hide its reduction behind, so
+// more of it is in flight in FP32, two rows a block (8192 x 4096: 46 us, 51 with one),
+// and BF16, where instructions bind as well, gives a thread 32 values to spread the
+// fixed ones over (16384 x 8192 to MXFP8: 74 us, 84 with two rows of 16, 88 with one).
+// With a residual one row of 16 values is best (16384 x 8192: 135 us, 138 with 32).
+template <int IN, int WT, int FMT, bool RES>
 cudaError_t launch_forward(const NormParams &p, cudaStream_t s)
 {
-    const Shape sh = pick_shape(p.K);
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows), sh.threads, 0, s, attr);
-    return sh.nch == 1   ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, 1>, p)
-           : sh.nch == 2 ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, 2>, p)
-                         : cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, 4>, p);
+    constexpr int kLeast = IN == kBf16 && !RES ? 2 : 1;
+    const Shape sh = pick_shape(p.K, kLeast);
+    if constexpr (kLeast == 1)
+        if (sh.nch == 1)
+            return launch_rows<IN, WT, FMT, 1, RES, RES ? 1 : 2>(p, sh.threads, s);
+    return sh.nch == 2 ? launch_rows<IN, WT, FMT, 2, RES, 1>(p, sh.threads, s)
+                       : launch_rows<IN, WT, FMT, 4, RES, 1>(p, sh.threads, s);
+}
+
+template <int IN, int WT, int FMT>
+cudaError_t launch_forward_res(const NormParams &p, cudaStream_t s)
+{
+    return p.residual ? launch_forward<IN, WT, FMT, true>(p, s) : launch_forward<IN, WT, FMT, false>(p, s);
 }
 
 template <int IN, int WT>
 cudaError_t launch_forward_fmt(const NormParams &p, cudaStream_t s)
 {
-    return p.mx.fmt == kMxfp8   ? launch_forward<IN, WT, kMxfp8>(p, s)
-           : p.mx.fmt == kMxfp4 ? launch_forward<IN, WT, kMxfp4>(p, s)
-                                : launch_forward<IN, WT, kNoFmt>(p, s);
+    return p.mx.fmt == kMxfp8   ? launch_forward_res<IN, WT, kMxfp8>(p, s)
+           : p.mx.fmt == kMxfp4 ? launch_forward_res<IN, WT, kMxfp4>(p, s)
+                                : launch_forward_res<IN, WT, kNoFmt>(p, s);
 }
 
 constexpr int kRingBytes = 220 * 1024;  // shared memory of an SM's rings
