@@ -34,27 +34,31 @@ template <int IN, bool KEEP>
 constexpr int kForwardBlocks = IN == kBf16 && !KEEP ? 4 : 2;
 constexpr int kBackwardBlocks = 2;  // 8192 x 14336 from the checkpoint: 177 us; three 181, four 252 (spills)
 
-// q of the activation's gate: the hardware's 2^x and 1/x, each within two ulps,
-// on an argument that carries the conversion to base 2 in its last constant.
-// 2^x overflows to infinity for far negative gates, where q is then 0, and the
-// reciprocal flushes below 2^-126.  `inner` is the argument's slope by g.
+// q of the activation's gate for a pair of values: the hardware's 2^x and 1/x, each
+// within two ulps, on an argument that carries the conversion to base 2 in its last
+// constant.  2^x overflows to infinity for far negative gates, where q is then 0, and
+// the reciprocal flushes below 2^-126.  `inner` is the argument's slope by g (GELU).
 template <int ACT>
-__device__ __forceinline__ float act_gate(float g, float &inner)
+__device__ __forceinline__ F2 act_gate(F2 g, F2 &inner)
 {
     constexpr float kLog2e = 1.4426950408889634f;
-    float t;
-    inner = 1.0f;
+    F2 t;
     if (ACT == kActGeluTanh) {
         constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
-        t = -c * kLog2e * fmaf(0.044715f * g * g, g, g);
-        inner = c * fmaf(0.134145f * g, g, 1.0f);
+        const F2 gg = f2_mul(g, g), k = f2(-c * kLog2e, -c * kLog2e), one = f2(1.0f, 1.0f);
+        t = f2_mul(k, f2_mul(g, f2_fma(gg, f2(0.044715f, 0.044715f), one)));
+        inner = f2_mul(f2(c, c), f2_fma(gg, f2(0.134145f, 0.134145f), one));
     } else {
-        t = -kLog2e * g;
+        t = f2_mul(g, f2(-kLog2e, -kLog2e));
     }
-    float e, q;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
-    return q;
+    float t0, t1, e0, e1, q0, q1;
+    f2_split(t, t0, t1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+    f2_split(f2_add(f2(e0, e1), f2(1.0f, 1.0f)), e0, e1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(e0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(e1));
+    return f2(q0, q1);
 }
 
 template <int ACT, int IN, int FMT, bool KEEP>
@@ -84,11 +88,10 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks<IN, KEEP>) glu_kernel
         fetch();
         float a[kLaneVals];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; i += 2) {
-            float s0, s1;
-            const float q0 = act_gate<ACT>(rg.at(i), s0), q1 = act_gate<ACT>(rg.at(i + 1), s1);
-            mul2(a[i], a[i + 1], rg.at(i), rg.at(i + 1), q0, q1);
-            mul2(a[i], a[i + 1], a[i], a[i + 1], ru.at(i), ru.at(i + 1));
+        for (int i = 0; i < kLaneVals / 2; ++i) {
+            F2 inner;
+            const F2 g = rg.pair(i);
+            f2_split(f2_mul(f2_mul(g, act_gate<ACT>(g, inner)), ru.pair(i)), a[2 * i], a[2 * i + 1]);
         }
         if (p.y && inside)
             store16<IN>(p.y + (row * F + k) * E, a);
@@ -169,29 +172,42 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) glu_backward_kernel
         const bool inside = k < F;
         at.next();
         next.load(p, at.row, static_cast<int64_t>(at.chunk) * kWarpVals + lane * kLaneVals);
-        float g[kLaneVals], u[kLaneVals];
+        F2 g[kLaneVals / 2], u[kLaneVals / 2];
         if (KEPT) {
             decode_e4m3(in.qg, in.sg, g);
             decode_e4m3(in.qu, in.su, u);
         } else {
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i) {
-                g[i] = in.g.at(i);
-                u[i] = in.u.at(i);
+            for (int i = 0; i < kLaneVals / 2; ++i) {
+                g[i] = in.g.pair(i);
+                u[i] = in.u.pair(i);
             }
         }
-        float dg[kLaneVals], du[kLaneVals], a[kLaneVals];
+        F2 dg2[kLaneVals / 2], du2[kLaneVals / 2], a2[kLaneVals / 2];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) {
-            float inner;
-            const float q = act_gate<ACT>(g[i], inner), dy = in.dy.at(i), f = g[i] * q;
-            // where q has reached 0 or 1 the slope is q, also where `inner` has overflowed
-            const float m = f * (1.0f - q);
-            const float slope = ACT == kActSilu ? m + q : m == 0.0f ? q : fmaf(m, inner, q);
-            dg[i] = dy * u[i] * slope;
-            du[i] = dy * f;
-            a[i] = f * u[i];
+        for (int i = 0; i < kLaneVals / 2; ++i) {
+            F2 inner;
+            const F2 q = act_gate<ACT>(g[i], inner), dy = in.dy.pair(i), f = f2_mul(g[i], q);
+            const F2 m = f2_mul(f, f2_fma(q, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)));
+            F2 slope;
+            if (ACT == kActSilu) {
+                slope = f2_add(m, q);
+            } else {
+                // where q has reached 0 or 1 the slope is q, also where `inner` has overflowed
+                float m0, m1, s0, s1, q0, q1;
+                f2_split(m, m0, m1);
+                f2_split(f2_fma(m, inner, q), s0, s1);
+                f2_split(q, q0, q1);
+                slope = f2(m0 == 0.0f ? q0 : s0, m1 == 0.0f ? q1 : s1);
+            }
+            dg2[i] = f2_mul(f2_mul(dy, u[i]), slope);
+            du2[i] = f2_mul(dy, f);
+            a2[i] = f2_mul(f, u[i]);
         }
+        float dg[kLaneVals], du[kLaneVals], a[kLaneVals];
+        f2_unpack(dg2, dg);
+        f2_unpack(du2, du);
+        f2_unpack(a2, a);
         if (p.a && inside)
             store16<IN>(p.a + (row * F + k) * E, a);
         if (p.dgu && inside) {

@@ -329,14 +329,15 @@ __device__ __forceinline__ void pad_tiled_scales(uint8_t *scales, int64_t rows, 
         *reinterpret_cast<uint32_t *>(scales + tile_scale_offset(rows + i / num_kt, i % num_kt, num_kt)) = 0x7F7F7F7Fu;
 }
 
-// Sixteen MXFP8 codes (16 bytes at p) times their block's scale.  Code 0xFF of
-// the scale is NaN.  The product of an E4M3 value and a power of two is exact in
-// FP32 unless it underflows past the smallest subnormal.
-__device__ __forceinline__ void decode_e4m3(const uint4 q, uint32_t scode, float (&v)[kLaneVals])
+// Sixteen MXFP8 codes times their block's scale, as pairs.  Code 0xFF of the scale is
+// NaN.  The product of an E4M3 value and a power of two is exact in FP32 unless it
+// underflows past the smallest subnormal.
+__device__ __forceinline__ void decode_e4m3(const uint4 q, uint32_t scode, F2 (&v)[kLaneVals / 2])
 {
     // 2^(scode - 127): scode 0 is the subnormal 2^-127
     const float s = scode == 255u ? __uint_as_float(0x7FC00000u)
                                   : __uint_as_float(scode == 0 ? 0x00400000u : scode << 23);
+    const F2 s2 = f2(s, s);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -347,9 +348,16 @@ __device__ __forceinline__ void decode_e4m3(const uint4 q, uint32_t scode, float
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h2));
-        v[2 * i] = lo * s;
-        v[2 * i + 1] = hi * s;
+        v[i] = f2_mul(f2(lo, hi), s2);
     }
+}
+
+// The sixteen values of eight pairs.
+__device__ __forceinline__ void f2_unpack(const F2 (&p)[kLaneVals / 2], float (&v)[kLaneVals])
+{
+#pragma unroll
+    for (int i = 0; i < kLaneVals / 2; ++i)
+        f2_split(p[i], v[2 * i], v[2 * i + 1]);
 }
 
 // A warp's walk over chunks of a matrix's rows (512 values, or `len`), every
