@@ -247,12 +247,15 @@ __global__ void __launch_bounds__(THREADS)
 // ----------------------------------------------------------------- dispatch --
 // A warp reads 512 or 1024 values of a token once, encodes them once and writes
 // them to the rows of all the token's slots.  One unit of work per warp and a block
-// for every eight: with persistent warps on four blocks an SM the writes of 16384
+// for every four: with persistent warps, 32 an SM, the writes of 16384
 // tokens x 2048 to 8 of 64 experts (346 MB) took 71 us, so they take 52 us (6.6
 // TB/s).  Two chunks a warp keep more bytes in flight where there are warps enough
-// (4099 x 4096, top 2, MXFP4: 10.1 us against 11.9); with few, one chunk is faster
-// (32 x 2048, top 8: 2.0 us against 2.3).
-constexpr int kThreads = 256;
+// (4099 x 4096, top 2, MXFP4: 10.0 us against 11.9); with few, one chunk is faster
+// (32 x 2048, top 8: 1.8 us against 2.3).
+//
+// Blocks of dispatch and combine are four warps: a multiprocessor refills sooner than
+// with eight (combine 41.7 us and 1.9 us at the sizes below; with eight 42.6 and 2.2).
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 // Warps below which a call is latency-bound: sixteen a multiprocessor.
@@ -267,7 +270,7 @@ __device__ __forceinline__ int slot_row(int r, int64_t slots, bool &dropped)
 }
 
 template <int IN, int FMT, int CHUNKS>
-__global__ void __launch_bounds__(kThreads, 4) moe_dispatch_kernel(const DispatchParams p)
+__global__ void __launch_bounds__(kThreads, 8) moe_dispatch_kernel(const DispatchParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
@@ -345,13 +348,13 @@ __global__ void __launch_bounds__(kThreads, 4) moe_dispatch_kernel(const Dispatc
 // ------------------------------------------------------------------ combine --
 // A warp sums 512 values of a token over its slots, in slot order; the rows of
 // AHEAD slots are loaded before the first is added.  Neighbouring warps read
-// neighbouring parts of the same rows.  Two slots ahead fit 64 registers, and four
-// blocks an SM then keep HBM busy: 8192 x 4096, top 2, with residual (269 MB) 42.5
-// us (6.3 TB/s), 8192 x 2048, top 8 (336 MB) 51.5 us (6.5); four ahead on three
-// blocks 54.9.  With few warps the latency of a batch counts: 32 x 2048, top 8, takes
-// 2.2 us eight ahead, 2.9 two ahead.
+// neighbouring parts of the same rows.  Two slots ahead fit 64 registers, and 32 warps
+// an SM then keep HBM busy: 8192 x 4096, top 2, with residual (269 MB) 41.7 us (6.4
+// TB/s), 8192 x 2048, top 8 (336 MB) 50.7 us (6.6); four ahead on 24 warps 54.9.  With
+// few warps the latency of a batch counts: 32 x 2048, top 8, takes 1.9 us eight ahead,
+// 2.9 two ahead.
 template <int IN, int AHEAD>
-__global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 4 : 2) moe_combine_kernel(const CombineParams p)
+__global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 8 : 3) moe_combine_kernel(const CombineParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
@@ -485,7 +488,8 @@ cudaError_t launch_sort(const ID *ids, int64_t slots, int groups, int64_t *offse
         counts = nullptr;
     } else {
         const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, 0, s, attr);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_count_kernel<ID>, ids, slots, groups, run * kSortWarps, counts);
+        const cudaError_t e =
+            cudaLaunchKernelEx(&cfg, moe_count_kernel<ID>, ids, slots, groups, run * kSortWarps, counts);
         if (e != cudaSuccess)
             return e;
     }
@@ -561,7 +565,7 @@ cudaError_t launch_moe_combine(const CombineParams &p, int in_dtype, int num_sms
 cudaError_t launch_moe_combine_backward(const CombineBackParams &p, int in_dtype, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(strided_blocks(p.tokens * p.topk, num_sms, 8), kThreads, 0, s, attr);
+    const cudaLaunchConfig_t cfg = row_launch(strided_blocks(p.tokens * p.topk, num_sms, 16), kThreads, 0, s, attr);
     return in_dtype == kBf16 ? cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kBf16>, p)
                              : cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kF32>, p);
 }

@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_backward_few_kernel(co
                 if (inside[i])
                     asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(dh[i].x), "=r"(dh[i].y), "=r"(dh[i].z), "=r"(dh[i].w)
-                                 : "l"(p.dh + row * p.dh_stride + static_cast<int64_t>((i * threads + tid) * P::kPer) * E)
+                                 : "l"(p.dh + row * p.dh_stride + ((i * threads + tid) * P::kPer) * E)
                                  : "memory");
     };
     if (IN == kBf16)
