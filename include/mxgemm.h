@@ -455,6 +455,8 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  *    (`..._stride`, at least the row length; ignored for a single row).  Plain
  *    matrices start on 32-byte boundaries and so does each of their rows.
  *    Outputs are dense; codes and scales are 16-byte aligned.
+ *  - An output touches no input matrix (MXGEMM_ERR_ARG), but may be the input
+ *    itself where a call names that and the input is dense.
  *  - fmt 0 asks for no MX output (codes and scales NULL); MXGEMM_FMT_MXFP8_E4M3
  *    and MXGEMM_FMT_MXFP4_E2M1 write codes [rows, K] bytes or [rows, K/2] bytes
  *    and scales, row-major [rows, K/32] or, with MXGEMM_QUANT_SF_TILED (K a
@@ -472,9 +474,8 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  * RMS norm:  h = x + residual (or x);  rstd = 1/sqrt(mean(h^2) + eps);
  *            y = h * rstd * weight.
  *   residual: NULL for none.   weight: K values of type weight_dtype.
- *   h, y:     [rows, K] of type in_dtype, either may be NULL; h may be x or
- *             residual itself where that is dense.  y is computed from the
- *             unrounded h.
+ *   h, y:     [rows, K] of type in_dtype, either may be NULL and either may be x
+ *             or residual itself.  y is computed from the unrounded h.
  *   codes, scales: MX(y), see above.    rstd: [rows] FP32, or NULL.
  * K up to 32768 (MXGEMM_ERR_UNSUPPORTED beyond: a row is held on chip).
  */
@@ -488,10 +489,10 @@ MXGEMM_API int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, con
  * (or NULL) the gradient that reaches h past the norm:
  *   p = dy * weight;  dx = rstd * p - h * rstd^3 * mean(p * h) + dh
  *   dweight[k] = sum over rows of dy * h * rstd          (FP32, K values)
- * dx is the gradient of x and of the residual alike.  dx may be dh itself where
- * that is dense.  workspace: mxgemm_rmsnorm_backward_workspace_bytes(rows, K)
- * bytes (0 for few rows, NULL then, and for sizes the call refuses), 32-byte
- * aligned, holding nothing between calls.
+ * dx is the gradient of x and of the residual alike.  dx may be dh itself.
+ * workspace: mxgemm_rmsnorm_backward_workspace_bytes(rows, K) bytes (0 for few
+ * rows, NULL then, and for sizes the call refuses), 32-byte aligned, holding
+ * nothing between calls.
  */
 MXGEMM_API size_t mxgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t K);
 MXGEMM_API int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *h,
@@ -507,7 +508,8 @@ MXGEMM_API int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_
  * Gated activation  a = act(gate) * up.
  *   gate, up: [rows, F] with one stride; a product's [rows, 2F] output is passed
  *             as (p, p + F) with stride 2F.
- *   y:        [rows, F] of type in_dtype, or NULL.   codes, scales: MX(a).
+ *   y:        [rows, F] of type in_dtype, or NULL; may be gate or up itself.
+ *   codes, scales: MX(a).
  *   kept_codes, kept_scales: both or neither; an 8-bit checkpoint of the inputs
  *             for mxgemm_glu_backward in 1.03 bytes a value: MXFP8 codes [rows, 2F]
  *             (gate, then up) and row-major scales [rows, 2F/32].  The output is
@@ -521,10 +523,12 @@ MXGEMM_API int mxgemm_glu(int act, int in_dtype, const void *gate, const void *u
  * Its gradient, given dy = the gradient of a:
  *   dgate = dy * up * act'(gate),   dup = dy * act(gate)
  * from gate and up, or (with those NULL) from the forward's checkpoint.
- *   dgu:  [rows, 2F] of type in_dtype (dgate, then dup), or NULL.
+ *   dgu:  [rows, 2F] of type in_dtype (dgate, then dup), or NULL; may be the
+ *         matrix whose halves gate and up are.
  *   codes, scales: MX of that [rows, 2F] matrix (its row length is 2F).
  *   a:    [rows, F] of type in_dtype: the forward's output computed again, for
- *         the gradient of the weight that follows; or NULL.
+ *         the gradient of the weight that follows; or NULL.  May be dy, gate or
+ *         up itself.
  */
 MXGEMM_API int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_t dy_stride, const void *gate,
                                    const void *up, int64_t stride, const void *kept_codes,
@@ -570,7 +574,7 @@ MXGEMM_API int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride
  * Sum the experts' rows back to tokens:
  *   out[t] = add[t] + sum_j weights[t*topk + j] * y[row_of_slot[t*topk + j]]
  *   weights: FP32, or NULL for 1.   add: [tokens, N] (the residual stream), or
- *   NULL; out may be add itself where that is dense.
+ *   NULL; out may be add itself.
  * Dropped slots add nothing: their rows are not read and their weights not used
  * (either may hold NaN); a token without slots gets add[t] or zero.
  */
@@ -581,7 +585,7 @@ MXGEMM_API int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride,
 /*
  * Its gradient:  dy[row_of_slot[s]] = weights[s] * dout[s / topk] (a dropped
  * slot's row is zero) and dweights[s] = <dout[s / topk], y[row_of_slot[s]]> (FP32,
- * zero for a dropped slot).
+ * zero for a dropped slot).  dy may be y itself.
  */
 MXGEMM_API int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64_t dout_stride, const void *y,
                                            int64_t y_stride, int64_t tokens, int64_t topk, int64_t N,

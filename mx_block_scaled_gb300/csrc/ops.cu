@@ -64,6 +64,22 @@ bool rows_align_ok(const void *p, int64_t stride, int64_t rows, int64_t elem)
     return p == nullptr || (aligned(p, 32) && (rows == 1 || stride * elem % 32 == 0));
 }
 
+// A dense output of `orows` rows of `orow` bytes touches no byte of a strided input:
+// blocks read inputs while others write.  `in_place`: it may be the input itself where
+// that is dense, each value then being read by the thread that writes it, before it does.
+bool apart(const void *out, int64_t orows, int64_t orow, const void *in, int64_t rows, int64_t stride, int64_t row,
+           bool in_place)
+{
+    if (!out || !in || (in_place && out == in && (rows == 1 || stride == row)))
+        return true;
+    using Wide = unsigned __int128;  // no size that the other checks pass overflows it
+    const Wide o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    return o + static_cast<Wide>(orows) * orow <= i || i + static_cast<Wide>(rows - 1) * stride + row <= o;
+}
+
+// Bytes of a row of n MX codes.
+int64_t code_bytes(int fmt, int64_t n) { return fmt == MXGEMM_FMT_MXFP4_E2M1 ? n / 2 : n; }
+
 // The MX output of a call: fmt 0 has neither codes nor scales.
 int check_mx(int fmt, const void *codes, const uint8_t *scales, uint32_t flags, int64_t K)
 {
@@ -112,6 +128,14 @@ int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, const void *re
         return MXGEMM_ERR_ALIGN;
     if (K > mxg::kNormMaxK)
         return MXGEMM_ERR_UNSUPPORTED;
+    const int64_t row = K * e;
+    for (const void *const out : {h, y})
+        if (!apart(out, rows, row, x, rows, x_stride * e, row, true) ||
+            !apart(out, rows, row, residual, rows, residual_stride * e, row, true))
+            return MXGEMM_ERR_ARG;
+    if (!apart(codes, rows, code_bytes(fmt, K), x, rows, x_stride * e, row, false) ||
+        !apart(codes, rows, code_bytes(fmt, K), residual, rows, residual_stride * e, row, false))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -160,6 +184,11 @@ int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, con
     const size_t need = mxgemm_rmsnorm_backward_workspace_bytes(rows, K);
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
+    const int64_t row = K * e;
+    if (!apart(dx, rows, row, dy, rows, dy_stride * e, row, false) ||
+        !apart(dx, rows, row, h, rows, h_stride * e, row, false) ||
+        !apart(dx, rows, row, dh, rows, dh_stride * e, row, true))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -199,6 +228,12 @@ int mxgemm_glu(int act, int in_dtype, const void *gate, const void *up, int64_t 
     if (!rows_align_ok(gate, stride, rows, e) || !aligned(up, 32) || !aligned(y, 32) || !aligned(kept_codes, 16) ||
         !aligned(kept_scales, 16))
         return MXGEMM_ERR_ALIGN;
+    const int64_t row = F * e;
+    for (const void *const in : {gate, up})
+        if (!apart(y, rows, row, in, rows, stride * e, row, true) ||
+            !apart(codes, rows, code_bytes(fmt, F), in, rows, stride * e, row, false) ||
+            !apart(kept_codes, rows, 2 * F, in, rows, stride * e, row, false))
+            return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -238,6 +273,18 @@ int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_t dy_stride
     if (!rows_align_ok(dy, dy_stride, rows, e) || !rows_align_ok(gate, stride, rows, e) || !aligned(up, 32) ||
         !aligned(kept_codes, 16) || !aligned(kept_scales, 16) || !aligned(dgu, 32) || !aligned(a, 32))
         return MXGEMM_ERR_ALIGN;
+    const int64_t row = F * e;
+    // dgu may be the [rows, 2F] matrix that gate and up are the halves of
+    const bool halves = dgu && dgu == gate && up == bytes(gate) + row && (rows == 1 || stride == 2 * F);
+    if (!apart(dgu, rows, 2 * row, dy, rows, dy_stride * e, row, false) ||
+        !apart(codes, rows, code_bytes(fmt, 2 * F), dy, rows, dy_stride * e, row, false) ||
+        !apart(a, rows, row, dy, rows, dy_stride * e, row, true))
+        return MXGEMM_ERR_ARG;
+    for (const void *const in : {gate, up})
+        if ((!halves && !apart(dgu, rows, 2 * row, in, rows, stride * e, row, false)) ||
+            !apart(codes, rows, code_bytes(fmt, 2 * F), in, rows, stride * e, row, false) ||
+            !apart(a, rows, row, in, rows, stride * e, row, true))
+            return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -312,6 +359,8 @@ int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride, int64_t t
         return MXGEMM_ERR_ALIGN;
     if (!warps_ok(tokens, K))
         return MXGEMM_ERR_UNSUPPORTED;
+    if (!apart(rows, tokens * topk, plain ? 2 * K : code_bytes(fmt, K), x, tokens, x_stride * e, K * e, false))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -345,6 +394,10 @@ int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride, int64_t to
         return MXGEMM_ERR_ALIGN;
     if (!warps_ok(tokens, N))
         return MXGEMM_ERR_UNSUPPORTED;
+    const int64_t row = N * e;
+    if (!apart(out, tokens, row, y, tokens * topk, y_stride * e, row, false) ||
+        !apart(out, tokens, row, add, tokens, add_stride * e, row, true))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -376,6 +429,10 @@ int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64_t dout_str
     if (!rows_align_ok(y, y_stride, tokens * topk, e) || !rows_align_ok(dout, dout_stride, tokens, e) ||
         !aligned(row_of_slot, 4) || !aligned(weights, 4) || !aligned(dy, 32) || !aligned(dweights, 4))
         return MXGEMM_ERR_ALIGN;
+    const int64_t row = N * e;
+    if (!apart(dy, tokens * topk, row, dout, tokens, dout_stride * e, row, false) ||
+        !apart(dy, tokens * topk, row, y, tokens * topk, y_stride * e, row, true))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)

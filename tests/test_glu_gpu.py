@@ -180,3 +180,25 @@ def test_offsets_past_32_bits():
     full = b.glu_backward(dy, ref.ACT_SILU, kept_codes=out.kept_codes, kept_scales=out.kept_scales)
     part = b.glu_backward(dy[-8:], ref.ACT_SILU, kept_codes=tail.kept_codes, kept_scales=tail.kept_scales)
     assert torch.equal(full.dgu[-8:], part.dgu)
+
+
+@pytest.mark.parametrize("rows,F", [(3, 96), (700, 4096)])
+def test_outputs_over_inputs(rows, F):
+    """y over a dense gate, dgu over the halves, a over dy; overlaps of other kinds are refused."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng(rows)
+    gu = _make(rng, (rows, 2 * F), _dtype("bf16"))[0]
+    dy = _make(rng, (rows, F), _dtype("bf16"))[0]
+    want = b.glu(gu[:, :F], gu[:, F:], ref.ACT_SILU, plain=True, keep=True)
+    grad = b.glu_backward(dy, ref.ACT_SILU, gate=gu[:, :F], up=gu[:, F:], recompute=True, fmt=1)
+    for kw in (dict(dgu=gu, gate=gu[:, F:], up=gu[:, :F]), dict(a=gu.view(2 * rows, F)[:rows], gate=gu[:, :F], up=gu[:, F:])):
+        with pytest.raises(b.MxGemmError) as e:
+            b.glu_backward(dy, ref.ACT_SILU, **kw)
+        assert e.value.status == b.MXGEMM_ERR_ARG
+    g, u = gu[:, :F].contiguous(), gu[:, F:].contiguous()
+    got = b.glu(g, u, ref.ACT_SILU, plain=True, keep=True, y=g)
+    assert got.y is g and torch.equal(g, want.y) and torch.equal(got.kept_codes, want.kept_codes)
+    got = b.glu_backward(dy, ref.ACT_SILU, gate=gu[:, :F], up=gu[:, F:], recompute=True, fmt=1, dgu=gu, a=dy)
+    assert got.dgu is gu and got.a is dy
+    assert all(torch.equal(p, q) for p, q in zip(got, grad))

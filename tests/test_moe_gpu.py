@@ -282,3 +282,25 @@ def test_offsets_past_32_bits():
     dy, dw = b.moe_combine_backward(x, rows, table, w)
     pdy, pdw = b.moe_combine_backward(x[-3:], part, small, w[-3:].contiguous())
     assert torch.equal(dy[-3 * k:], pdy) and torch.equal(dw[-3:], pdw)
+
+
+@pytest.mark.parametrize("T", [6, 900])
+def test_outputs_over_inputs(T):
+    """dy over y gives what an apart output gives; outputs over other inputs are refused."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng(T)
+    k, N = 2, 1056
+    _, slot, _ = ref.moe_sort(_ids(rng, T, k, 4, drop=0.2), 4)
+    slot = _dev(slot.astype(np.int32))
+    y, dout = (_make(rng, (n, N), _dtype("bf16"))[0] for n in (T * k, T))
+    w = _dev(rng.random((T, k)).astype(np.float32))
+    want = b.moe_combine_backward(dout, y, slot, w)
+    for call in (lambda: b.moe_combine(y, slot, k, out=y[:T]),
+                 lambda: b.moe_dispatch(y[:T], slot, b.MXGEMM_FMT_BF16, rows=y),
+                 lambda: b.moe_combine_backward(y[:T], y.clone(), slot, w, dy=y)):
+        with pytest.raises(b.MxGemmError) as e:
+            call()
+        assert e.value.status == b.MXGEMM_ERR_ARG
+    got = b.moe_combine_backward(dout, y, slot, w, dy=y)
+    assert got[0] is y and torch.equal(y, want[0]) and torch.equal(got[1], want[1])

@@ -241,3 +241,25 @@ def test_offsets_past_32_bits():
     dx, _ = b.rmsnorm_backward(out.y, x, out.rstd, w)
     dt, _ = b.rmsnorm_backward(tail.y, x[-64:], tail.rstd, w)
     assert torch.equal(dx[-64:], dt)
+
+
+@pytest.mark.parametrize("rows", [5, 1100])
+def test_outputs_over_inputs(rows):
+    """y over x and h over the residual give what apart outputs give; dx over dy is refused."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng(rows)
+    x, r, dy = (_make(rng, (rows, 512), _dtype("bf16"))[0] for _ in range(3))
+    w = _make(rng, (512,), _dtype("bf16"))[0]
+    want = b.rmsnorm(x, w, EPS, residual=r, plain=True, fmt=1)
+    grads = b.rmsnorm_backward(dy, want.h, want.rstd, w, dh=x.clone())
+    for kw in (dict(dx=dy), dict(dx=want.h)):
+        with pytest.raises(b.MxGemmError) as e:
+            b.rmsnorm_backward(dy, want.h, want.rstd, w, dh=x.clone(), **kw)
+        assert e.value.status == b.MXGEMM_ERR_ARG
+    xc = x.clone()
+    over = b.rmsnorm_backward(dy, want.h, want.rstd, w, dh=xc, dx=xc)
+    assert torch.equal(over[0], grads[0]) and torch.equal(over[1], grads[1])
+    got = b.rmsnorm(x, w, EPS, residual=r, plain=True, fmt=1, h=r, y=x)
+    assert got.y is x and got.h is r
+    assert all(torch.equal(p, q) for p, q in zip(got, want))

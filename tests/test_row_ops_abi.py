@@ -186,3 +186,48 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
         lib.moe_combine(x, ids.int(), 2)
     with pytest.raises(ValueError):
         lib.moe_combine_backward(x, x, ids.int(), w)
+
+
+# outputs that touch an input: at 1 << 20 .. of a matrix that the good call has elsewhere
+APART = dict(
+    mxgemm_rmsnorm=dict(in_dtype=2, x=1 << 20, x_stride=256, residual=2 << 20, residual_stride=512, weight=64,
+                        weight_dtype=2, eps=1e-5, rows=4, K=256, h=3 << 20, y=4 << 20, fmt=1, codes=5 << 20, scales=64,
+                        rstd=64, flags=0, stream=None),
+    mxgemm_rmsnorm_backward=dict(in_dtype=1, dy=1 << 20, dy_stride=256, h=2 << 20, h_stride=256, rstd=64, weight=64,
+                                 weight_dtype=1, dh=3 << 20, dh_stride=512, rows=4, K=256, dx=4 << 20, dweight=64,
+                                 workspace=None, ws_bytes=0, stream=None),
+    mxgemm_glu=dict(act=1, in_dtype=2, gate=1 << 20, up=(1 << 20) + 512, stride=512, rows=4, F=256, y=2 << 20, fmt=2,
+                    codes=3 << 20, scales=64, flags=1, kept_codes=4 << 20, kept_scales=64, stream=None),
+    mxgemm_glu_backward=dict(act=2, in_dtype=2, dy=1 << 20, dy_stride=256, gate=2 << 20, up=(2 << 20) + 512,
+                             stride=512, kept_codes=None, kept_scales=None, rows=4, F=256, dgu=3 << 20, fmt=1,
+                             codes=4 << 20, scales=64, flags=1, a=5 << 20, stream=None),
+    mxgemm_moe_dispatch=dict(in_dtype=2, x=1 << 20, x_stride=512, tokens=4, topk=2, K=256, row_of_slot=64, fmt=1,
+                             rows=2 << 20, scales=64, stream=None),
+    mxgemm_moe_combine=dict(in_dtype=2, y=1 << 20, y_stride=256, tokens=4, topk=2, N=256, row_of_slot=64, weights=64,
+                            add=2 << 20, add_stride=512, out=3 << 20, stream=None),
+    mxgemm_moe_combine_backward=dict(in_dtype=2, dout=1 << 20, dout_stride=256, y=2 << 20, y_stride=512, tokens=4,
+                                     topk=2, N=256, row_of_slot=64, weights=64, dy=3 << 20, dweights=64, stream=None),
+)
+
+
+@pytest.mark.parametrize("name,change", [
+    ("mxgemm_rmsnorm", dict(h=2 << 20)),                       # the residual itself, but with a stride
+    ("mxgemm_rmsnorm", dict(y=(1 << 20) + 512)),               # x, a row on
+    ("mxgemm_rmsnorm", dict(y=(1 << 20) - 4 * 512 + 32)),      # its end in x
+    ("mxgemm_rmsnorm", dict(codes=(2 << 20) + 3 * 1024)),      # the residual's last row
+    ("mxgemm_rmsnorm_backward", dict(dx=1 << 20)), ("mxgemm_rmsnorm_backward", dict(dx=2 << 20)),
+    ("mxgemm_rmsnorm_backward", dict(dx=3 << 20)),
+    ("mxgemm_rmsnorm_backward", dict(dh_stride=256, dx=(3 << 20) + 32)),
+    ("mxgemm_glu", dict(y=1 << 20)), ("mxgemm_glu", dict(codes=1 << 20)), ("mxgemm_glu", dict(kept_codes=(1 << 20) + 64)),
+    ("mxgemm_glu_backward", dict(dgu=1 << 20)), ("mxgemm_glu_backward", dict(dgu=(2 << 20) + 32)),
+    ("mxgemm_glu_backward", dict(dgu=2 << 20, stride=1024)),
+    ("mxgemm_glu_backward", dict(dgu=2 << 20, gate=(2 << 20) + 512, up=2 << 20)),  # the halves the other way round
+    ("mxgemm_glu_backward", dict(a=2 << 20)), ("mxgemm_glu_backward", dict(a=(1 << 20) + 32)),
+    ("mxgemm_glu_backward", dict(codes=1 << 20)),
+    ("mxgemm_moe_dispatch", dict(rows=(1 << 20) + 3 * 1024)), ("mxgemm_moe_dispatch", dict(rows=(1 << 20) - 8 * 256 + 16)),
+    ("mxgemm_moe_combine", dict(out=1 << 20)), ("mxgemm_moe_combine", dict(out=2 << 20)),
+    ("mxgemm_moe_combine", dict(out=(1 << 20) + 7 * 512)),
+    ("mxgemm_moe_combine_backward", dict(dy=1 << 20)), ("mxgemm_moe_combine_backward", dict(dy=2 << 20)),
+])
+def test_outputs_apart_from_inputs(lib, name, change):
+    assert _call(lib, name, APART[name], change) == ARG
