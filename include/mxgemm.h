@@ -455,8 +455,8 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  *    (`..._stride`, at least the row length; ignored for a single row).  Plain
  *    matrices start on 32-byte boundaries and so does each of their rows.
  *    Outputs are dense; codes and scales are 16-byte aligned.
- *  - An output touches no input matrix (MXGEMM_ERR_ARG), but may be the input
- *    itself where a call names that and the input is dense.
+ *  - An output touches no input matrix and no expert id (MXGEMM_ERR_ARG), but may
+ *    be an input itself where a call names that and the input is dense.
  *  - fmt 0 asks for no MX output (codes and scales NULL); MXGEMM_FMT_MXFP8_E4M3
  *    and MXGEMM_FMT_MXFP4_E2M1 write codes [rows, K] bytes or [rows, K/2] bytes
  *    and scales, row-major [rows, K/32] or, with MXGEMM_QUANT_SF_TILED (K a

@@ -325,6 +325,10 @@ int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t
     const size_t need = mxgemm_moe_sort_workspace_bytes(slots, groups);
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
+    if (!apart(offsets, groups + 1, 8, expert_ids, slots, id_bytes, id_bytes, false) ||
+        !apart(row_of_slot, slots, 4, expert_ids, slots, id_bytes, id_bytes, false) ||
+        !apart(slot_of_row, slots, 4, expert_ids, slots, id_bytes, id_bytes, false))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
     if (st != MXGEMM_OK)

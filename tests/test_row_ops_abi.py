@@ -201,6 +201,8 @@ APART = dict(
     mxgemm_glu_backward=dict(act=2, in_dtype=2, dy=1 << 20, dy_stride=256, gate=2 << 20, up=(2 << 20) + 512,
                              stride=512, kept_codes=None, kept_scales=None, rows=4, F=256, dgu=3 << 20, fmt=1,
                              codes=4 << 20, scales=64, flags=1, a=5 << 20, stream=None),
+    mxgemm_moe_sort=dict(expert_ids=1 << 20, id_bytes=4, slots=600, groups=8, offsets=2 << 20, row_of_slot=3 << 20,
+                         slot_of_row=4 << 20, workspace=None, ws_bytes=0, stream=None),
     mxgemm_moe_dispatch=dict(in_dtype=2, x=1 << 20, x_stride=512, tokens=4, topk=2, K=256, row_of_slot=64, fmt=1,
                              rows=2 << 20, scales=64, stream=None),
     mxgemm_moe_combine=dict(in_dtype=2, y=1 << 20, y_stride=256, tokens=4, topk=2, N=256, row_of_slot=64, weights=64,
@@ -224,6 +226,8 @@ APART = dict(
     ("mxgemm_glu_backward", dict(dgu=2 << 20, gate=(2 << 20) + 512, up=2 << 20)),  # the halves the other way round
     ("mxgemm_glu_backward", dict(a=2 << 20)), ("mxgemm_glu_backward", dict(a=(1 << 20) + 32)),
     ("mxgemm_glu_backward", dict(codes=1 << 20)),
+    ("mxgemm_moe_sort", dict(row_of_slot=1 << 20)), ("mxgemm_moe_sort", dict(slot_of_row=(1 << 20) + 599 * 4)),
+    ("mxgemm_moe_sort", dict(offsets=(1 << 20) - 64)), ("mxgemm_moe_sort", dict(id_bytes=8, row_of_slot=(1 << 20) + 4796)),
     ("mxgemm_moe_dispatch", dict(rows=(1 << 20) + 3 * 1024)), ("mxgemm_moe_dispatch", dict(rows=(1 << 20) - 8 * 256 + 16)),
     ("mxgemm_moe_combine", dict(out=1 << 20)), ("mxgemm_moe_combine", dict(out=2 << 20)),
     ("mxgemm_moe_combine", dict(out=(1 << 20) + 7 * 512)),
