@@ -44,6 +44,15 @@ __device__ __forceinline__ void ld_row32(const void *p, uint32_t (&r)[8])
                  : "memory");
 }
 
+// 32 bytes that other warps of the SM read as well.
+__device__ __forceinline__ void ld_kept32(const void *p, uint32_t (&r)[8])
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 __device__ __forceinline__ void st_row32(void *p, const uint32_t (&r)[8])
 {
     asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
@@ -94,12 +103,16 @@ struct Raw16 {
     static constexpr int kParts = DT == kBf16 ? 1 : 2;
     uint32_t r[kParts][8];
 
+    template <bool KEPT = false>
     __device__ __forceinline__ void load(const char *p, bool inside)
     {
 #pragma unroll
         for (int l = 0; l < kParts; ++l) {
             if (inside) {
-                ld_row32(p + 32 * l, r[l]);
+                if (KEPT)
+                    ld_kept32(p + 32 * l, r[l]);
+                else
+                    ld_row32(p + 32 * l, r[l]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

@@ -36,16 +36,22 @@ __device__ __forceinline__ float block_sum(float v, float *part)
 // ------------------------------------------------------------------ forward --
 // A block takes ROWS neighbouring rows at once, a thread NCH runs of 16 values of
 // each.  Sums and products are packed pairs: at 3 bytes a value (BF16 to MXFP8 without
-// a residual) a value may cost 17 instructions before they bind instead of HBM.
-template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
-__global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 2 : 0) rmsnorm_kernel(const NormParams p)
+// a residual) a value may cost 17 instructions before they bind instead of HBM.  The
+// weight is kept in L1 for the SM's next rows: fetched from L2 for every row, its few
+// lines hold up all SMs (8192 x 2016 FP32: 32 us, 46 without; 1504: 24 and 38).
+// SIDE: blockDim.y such groups of rows beside each other.
+template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS, bool SIDE>
+__global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 2 : 0)
+    rmsnorm_kernel(const NormParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
     __shared__ float part[ROWS][32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS, K = p.K;
+    const int64_t unit = SIDE ? static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
+    const int64_t row0 = unit * ROWS, K = p.K;
+    const int part0 = SIDE ? threadIdx.y * nwarps : 0;
 
     Raw16<IN> x[ROWS][NCH], r[RES ? ROWS : 1][RES ? NCH : 1];
     Raw16<WT> w[NCH];
@@ -54,7 +60,7 @@ __global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-            const bool inside = k < K && (ROWS == 1 || row0 + q < p.rows);
+            const bool inside = k < K && ((ROWS == 1 && !SIDE) || row0 + q < p.rows);
             x[q][c].load(p.x + (row0 + q) * p.x_stride + k * E, inside);
             if constexpr (RES)
                 r[q][c].load(p.residual + (row0 + q) * p.residual_stride + k * E, inside);
@@ -62,7 +68,7 @@ __global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-        w[c].load(p.weight + k * ElemBytes<WT>::value, k < K);
+        w[c].template load<true>(p.weight + k * ElemBytes<WT>::value, k < K);
     }
     F2 h[ROWS][NCH][kLaneVals / 2];
 #pragma unroll
@@ -81,15 +87,15 @@ __global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 
         f2_split(ss, lo, hi);
         lo = warp_sum(lo + hi);
         if (lane == 0)
-            part[q][warp] = lo;
+            part[q][part0 + warp] = lo;
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < ROWS; ++q) {
         const int64_t row = row0 + q;
-        if (ROWS > 1 && row >= p.rows)
-            break;  // block-uniform
-        const float ss = warp_sum(lane < nwarps ? part[q][lane] : 0.0f);
+        if ((ROWS > 1 || SIDE) && row >= p.rows)
+            break;  // warp-uniform, and no barrier follows
+        const float ss = warp_sum(lane < nwarps ? part[q][part0 + lane] : 0.0f);
         const float rstd = __frsqrt_rn(ss / static_cast<float>(K) + p.eps);
         if (threadIdx.x == 0 && p.rstd)
             p.rstd[row] = rstd;
@@ -119,8 +125,8 @@ __global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 
         }
     }
     if (FMT != kNoFmt && p.mx.mode == kScaleTiled)
-        pad_tiled_scales(p.mx.scales, p.rows, K, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-                         static_cast<int64_t>(gridDim.x) * blockDim.x);
+        pad_tiled_scales(p.mx.scales, p.rows, K, unit * blockDim.x + threadIdx.x,
+                         static_cast<int64_t>(gridDim.x) * (SIDE ? blockDim.y : 1) * blockDim.x);
 }
 
 // ----------------------------------------------------------------- backward --
@@ -599,13 +605,28 @@ int blocks_per_sm(int64_t K)
     return n > 4 ? 4 : n;
 }
 
+// Many narrow rows (up to 1024 values): rows side by side in blocks of four warps, since
+// a multiprocessor takes up small blocks too slowly (16384 x 384: 10.2 us, 17.0 with a
+// block a row; 16384 x 608 without a residual 11.6 and 17.1).  Wider rows gain nothing
+// (16384 x 2016 without a residual 21.7 us against 19.8), nor do fewer (2048 x 512: 3.2
+// against 3.0).
+constexpr int64_t kSideK = 1024, kSideRows = 4096;
+constexpr int kSideThreads = 128;
+
 template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
 cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        row_launch(static_cast<unsigned>((p.rows + ROWS - 1) / ROWS), threads, 0, s, attr);
-    return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS>, p);
+    const int side = p.K <= kSideK && p.rows >= kSideRows ? kSideThreads / threads : 1;
+    const int64_t of_block = static_cast<int64_t>(ROWS) * side;
+    cudaLaunchConfig_t cfg =
+        row_launch(static_cast<unsigned>((p.rows + of_block - 1) / of_block), threads, 0, s, attr);
+    if constexpr (NCH <= 2)
+        if (side > 1) {
+            cfg.blockDim.y = side;
+            return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, true>, p);
+        }
+    return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, false>, p);
 }
 
 // Without a residual a row brings half the bytes to hide its reduction behind, so

@@ -263,3 +263,32 @@ def test_outputs_over_inputs(rows):
     got = b.rmsnorm(x, w, EPS, residual=r, plain=True, fmt=1, h=r, y=x)
     assert got.y is x and got.h is r
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,K", [(4096, 96), (4099, 512), (4098, 544), (4097, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_narrow_rows(rows, K, dtype, residual):
+    """Rows that share a block: the same results as in calls of few rows, nothing past the last one."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng([rows, K])
+    x, r = (_make(rng, (rows, K), _dtype(dtype))[0] for _ in range(2))
+    w = _make(rng, (K,), _dtype(dtype))[0]
+    tiled, pad = K % 128 == 0, 64
+    buf = torch.full((rows * K + 2 * pad,), 3.0, dtype=x.dtype, device="cuda")
+    y = buf[pad:-pad].view(rows, K)
+    got = b.rmsnorm(x, w, EPS, residual=r if residual else None, plain=True, fmt=1, tiled=tiled, y=y)
+    for at in range(0, rows, 2048):
+        few = slice(at, min(at + 2048, rows))
+        want = b.rmsnorm(x[few], w, EPS, residual=r[few] if residual else None, plain=True, fmt=1)
+        for name in ("h", "y", "codes", "rstd"):
+            if getattr(got, name) is not None:
+                assert torch.equal(getattr(got, name)[few], getattr(want, name)), name
+        scales = got.scales.cpu().numpy()
+        scales = ref.untile(scales, rows, K) if tiled else scales
+        assert np.array_equal(scales[few], want.scales.cpu().numpy())
+    assert (buf[:pad] == 3.0).all() and (buf[-pad:] == 3.0).all()
+    if tiled:  # rows up to the tile's end hold 1.0
+        padded = (rows + 127) // 128 * 128
+        assert (ref.untile(got.scales.cpu().numpy(), padded, K)[rows:] == 127).all()
