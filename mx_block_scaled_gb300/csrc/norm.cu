@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(con
             Raw16<WT> w;
             dy.load(dy_row + k * E, true);
             h.load(h_row + k * E, true);
-            w.load(p.weight + k * ElemBytes<WT>::value, true);
+            w.template load<true>(p.weight + k * ElemBytes<WT>::value, true);
 #pragma unroll
             for (int i = 0; i < kLaneVals; ++i)
                 dot = fmaf(dy.at(i) * w.at(i), h.at(i), dot);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(con
             dy.load(dy_row + k * E, true);
             h.load(h_row + k * E, true);
             dh.load(p.dh + row * p.dh_stride + k * E, p.dh != nullptr);
-            w.load(p.weight + k * ElemBytes<WT>::value, true);
+            w.template load<true>(p.weight + k * ElemBytes<WT>::value, true);
             float dx[kLaneVals];
 #pragma unroll
             for (int i = 0; i < kLaneVals; i += 2) {
@@ -605,6 +605,17 @@ int blocks_per_sm(int64_t K)
     return n > 4 ? 4 : n;
 }
 
+// Without a residual a row brings half the bytes to hide its reduction behind, so
+// more of it is in flight in FP32, two rows a block (8192 x 4096: 46 us, 51 with one),
+// and BF16, where instructions bind as well, gives a thread 32 values to spread the
+// fixed ones over (16384 x 8192 to MXFP8: 74 us, 84 with two rows of 16, 88 with one).
+// With a residual one row of 16 values is best (16384 x 8192: 135 us, 138 with 32).
+template <int IN, bool RES>
+constexpr int fewest_runs()
+{
+    return IN == kBf16 && !RES ? 2 : 1;
+}
+
 // Many narrow rows (up to 1024 values): rows side by side in blocks of four warps, since
 // a multiprocessor takes up small blocks too slowly (16384 x 384: 10.2 us, 17.0 with a
 // block a row; 16384 x 608 without a residual 11.6 and 17.1).  Wider rows gain nothing
@@ -617,11 +628,12 @@ template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
 cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const int side = p.K <= kSideK && p.rows >= kSideRows ? kSideThreads / threads : 1;
+    constexpr bool kNarrow = NCH == fewest_runs<IN, RES>();
+    const int side = kNarrow && p.K <= kSideK && p.rows >= kSideRows ? kSideThreads / threads : 1;
     const int64_t of_block = static_cast<int64_t>(ROWS) * side;
     cudaLaunchConfig_t cfg =
         row_launch(static_cast<unsigned>((p.rows + of_block - 1) / of_block), threads, 0, s, attr);
-    if constexpr (NCH <= 2)
+    if constexpr (kNarrow)
         if (side > 1) {
             cfg.blockDim.y = side;
             return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, true>, p);
@@ -629,15 +641,10 @@ cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, false>, p);
 }
 
-// Without a residual a row brings half the bytes to hide its reduction behind, so
-// more of it is in flight in FP32, two rows a block (8192 x 4096: 46 us, 51 with one),
-// and BF16, where instructions bind as well, gives a thread 32 values to spread the
-// fixed ones over (16384 x 8192 to MXFP8: 74 us, 84 with two rows of 16, 88 with one).
-// With a residual one row of 16 values is best (16384 x 8192: 135 us, 138 with 32).
 template <int IN, int WT, int FMT, bool RES>
 cudaError_t launch_forward(const NormParams &p, cudaStream_t s)
 {
-    constexpr int kLeast = IN == kBf16 && !RES ? 2 : 1;
+    constexpr int kLeast = fewest_runs<IN, RES>();
     const Shape sh = pick_shape(p.K, kLeast);
     if constexpr (kLeast == 1)
         if (sh.nch == 1)
