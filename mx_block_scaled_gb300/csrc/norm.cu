@@ -20,6 +20,14 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 
+// Many narrow rows (up to 1024 values): rows side by side in blocks of four warps, since
+// a multiprocessor takes up small blocks too slowly (16384 x 384: 10.2 us, 17.0 with a
+// block a row; 16384 x 608 without a residual 11.6 and 17.1).  Wider rows gain nothing
+// (16384 x 2016 without a residual 21.7 us against 19.8), nor do fewer (2048 x 512: 3.2
+// against 3.0).
+constexpr int64_t kSideK = 1024, kSideRows = 4096;
+constexpr int kSideThreads = 128;
+
 // Sum of v over the block; `part` holds one float per warp.  One barrier: a
 // caller that sums again passes the other of two buffers.
 __device__ __forceinline__ float block_sum(float v, float *part)
@@ -206,6 +214,7 @@ __global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(con
 // no barrier.  Between two barriers a block forms the dot product's partial sums of
 // one row and finishes the row before it, whose sums the last barrier made visible:
 // the reduction's latency is covered by work instead of being waited out.
+// SIDE: blockDim.y rows beside each other, whose weight sums are joined at the end.
 __device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -303,29 +312,36 @@ __device__ __forceinline__ float row_coef(const float *part, float rstd, float i
     return -(rstd * rstd * rstd * (((s.x + s.y) + (s.z + s.w)) * inv_k));
 }
 
-template <int IN, int WT, int DEPTH>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(const NormBackParams p)
+template <int IN, int WT, int DEPTH, bool SIDE>
+__global__ void __launch_bounds__(SIDE ? kSideThreads : kMaxThreads, SIDE ? 4 : 0)
+    rmsnorm_backward_ring_kernel(const NormBackParams p)
 {
     using P = Pieces<IN>;
     constexpr int E = ElemBytes<IN>::value, kPer = P::kPer, kPieces = P::kCount, kPairs = P::kPairs;
-    extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][dy, h, dh][piece][thread]
-    __shared__ __align__(16) float part[2][kMaxThreads / 32];
-    __shared__ float row_rstd[2];  // by thread 0, a row ahead; each iteration's barrier shows it to the others
+    constexpr int kSides = SIDE ? kSideThreads / 32 : 1;
+    extern __shared__ __align__(16) uint4 ring[];  // [side][DEPTH][dy, h, dh][piece][thread]
+    __shared__ __align__(16) float parts[kSides][2][kMaxThreads / 32];
+    __shared__ float rstds[kSides][2];  // by thread 0, a row ahead; each iteration's barrier shows it to the others
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t threads = blockDim.x, tid = threadIdx.x;
-    const int64_t K = p.K, step = gridDim.x;
+    const uint32_t threads = blockDim.x, tid = threadIdx.x, side = SIDE ? threadIdx.y : 0;
+    const uint32_t sides = SIDE ? blockDim.y : 1;
+    float(&part)[2][kMaxThreads / 32] = parts[side];
+    float(&row_rstd)[2] = rstds[side];
+    const int64_t K = p.K, step = static_cast<int64_t>(gridDim.x) * sides;
+    const int64_t block_row = static_cast<int64_t>(blockIdx.x) * sides;
     const bool with_dh = p.dh != nullptr;
     const uint32_t plane = threads * 16;                                   // bytes of one piece of all threads
     const uint32_t stage_bytes = (with_dh ? 3 : 2) * kPieces * plane;
-    const uint32_t ring0 = smem_addr(ring) + tid * 16, ring_end = ring0 + DEPTH * stage_bytes;
+    const uint32_t ring0 = smem_addr(ring) + side * DEPTH * stage_bytes + tid * 16;
+    const uint32_t ring_end = ring0 + DEPTH * stage_bytes;
     bool inside[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
         inside[i] = (i * threads + tid) * kPer < K;
 
     // the row that is fetched next, and where to
-    int64_t ahead_row = blockIdx.x;
+    int64_t ahead_row = block_row + side;
     const char *src_dy = p.dy + ahead_row * p.dy_stride + tid * 16, *src_h = p.h + ahead_row * p.h_stride + tid * 16,
                *src_dh = p.dh + ahead_row * p.dh_stride + tid * 16;
     uint32_t to = ring0;
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
         }
         leave_dot(dot, part[buf]);
     };
-    int64_t row = blockIdx.x;
+    int64_t row = block_row + side;
     char *dx = p.dx + row * K * E + tid * 16;
     float next_rstd = 0.0f;
     if (tid == 0 && row < p.rows) {
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
     const float inv_k = 1.0f / static_cast<float>(K);
     uint32_t stage = ring0;
     int buf = 0;
-    for (; row < p.rows; row += step, buf ^= 1) {
+    for (; row - side < p.rows; row += step, buf ^= 1) {  // all sides of a block take part in its barriers
         uint32_t following = stage + stage_bytes;
         following = following == ring_end ? ring0 : following;
         fetch();  // into the stage that the last row left
@@ -416,8 +432,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
         if (row + step < p.rows)
             dot_row(following, buf ^ 1);
         const F2 coef2 = f2(coef, coef), rstd2 = f2(rstd, rstd);
+        const bool live = !SIDE || row < p.rows;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < kPieces && live; ++i) {
             uint4 dh = make_uint4(0, 0, 0, 0);
             if (with_dh)
                 dh = take(stage + (2 * kPieces + i) * plane, i);
@@ -436,6 +453,22 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_ring_kernel(cons
         __syncthreads();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (SIDE) {  // the sides' sums in order, through the ring that nothing uses any more
+        __syncthreads();
+        F2 *const sums = reinterpret_cast<F2 *>(ring) + tid;
+        if (side > 0)
+#pragma unroll
+            for (int i = 0; i < kPieces * kPairs; ++i)
+                sums[((side - 1) * kPieces * kPairs + i) * threads] = dw[i / kPairs][i % kPairs];
+        __syncthreads();
+        if (side > 0)
+            return;
+        for (uint32_t other = 0; other + 1 < sides; ++other)
+#pragma unroll
+            for (int i = 0; i < kPieces * kPairs; ++i)
+                dw[i / kPairs][i % kPairs] =
+                    f2_add(dw[i / kPairs][i % kPairs], sums[(other * kPieces * kPairs + i) * threads]);
+    }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
         if (inside[i]) {
@@ -616,14 +649,6 @@ constexpr int fewest_runs()
     return IN == kBf16 && !RES ? 2 : 1;
 }
 
-// Many narrow rows (up to 1024 values): rows side by side in blocks of four warps, since
-// a multiprocessor takes up small blocks too slowly (16384 x 384: 10.2 us, 17.0 with a
-// block a row; 16384 x 608 without a residual 11.6 and 17.1).  Wider rows gain nothing
-// (16384 x 2016 without a residual 21.7 us against 19.8), nor do fewer (2048 x 512: 3.2
-// against 3.0).
-constexpr int64_t kSideK = 1024, kSideRows = 4096;
-constexpr int kSideThreads = 128;
-
 template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
 cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
 {
@@ -670,19 +695,30 @@ cudaError_t launch_forward_fmt(const NormParams &p, cudaStream_t s)
 constexpr int kRingBytes = 220 * 1024;  // shared memory of an SM's rings
 
 template <int IN, int WT, int DEPTH>
-cudaError_t launch_ring(const NormBackParams &p, int threads, int64_t blocks, size_t smem, cudaStream_t s)
+cudaError_t launch_ring(const NormBackParams &p, int threads, int sides, int64_t blocks, size_t smem, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), threads, smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, rmsnorm_backward_ring_kernel<IN, WT, DEPTH>, p);
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), threads, smem, s, attr);
+    cfg.blockDim.y = sides;
+    if constexpr (IN == kBf16 && DEPTH == 4)
+        if (sides > 1)
+            return cudaLaunchKernelEx(&cfg, rmsnorm_backward_ring_kernel<IN, WT, DEPTH, true>, p);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_backward_ring_kernel<IN, WT, DEPTH, false>, p);
 }
 
+// Narrow rows (up to 1024 values) in BF16 share a block, two or four at a time: 16384 x
+// 992 29 us with dh, 40 with a row a block, 25 and 36 without.  In FP32 the registers for
+// that spill (8192 x 992: 36 us against 29).  Blocks of 128 threads that read dh run best
+// three to an SM (16384 x 2048: 52 us, 59 with four), those that do not with four (41 us, 45).
 template <int IN, int WT>
 cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s)
 {
     const Shape sh = pick_shape(p.K);
+    const int sides = IN == kBf16 && p.K <= kSideK ? kSideThreads / sh.threads : 1;
     int64_t blocks = norm_back_blocks(p.rows, p.K);
-    const int per_sm = blocks_per_sm(p.K);
+    int per_sm = blocks_per_sm(p.K);
+    if (p.dh && per_sm == 4 && sh.threads * sides == 128)
+        per_sm = 3;
     blocks = blocks < static_cast<int64_t>(num_sms) * per_sm ? blocks : static_cast<int64_t>(num_sms) * per_sm;
     cudaError_t e;
     cudaLaunchAttribute attr[1];
@@ -692,11 +728,11 @@ cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s
         return cudaLaunchKernelEx(&cfg, rmsnorm_backward_few_kernel<IN, WT>, p, columns);
     }
     if (p.K <= kRingMaxK) {
-        const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sh.threads * kLaneVals * ElemBytes<IN>::value;
+        const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sides * sh.threads * kLaneVals * ElemBytes<IN>::value;
         const int64_t depth = kRingBytes / per_sm / row;
-        e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, blocks, 4 * row, s)
-            : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, blocks, 3 * row, s)
-                         : launch_ring<IN, WT, 2>(p, sh.threads, blocks, 2 * row, s);
+        e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, sides, blocks, 4 * row, s)
+            : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, sides, blocks, 3 * row, s)
+                         : launch_ring<IN, WT, 2>(p, sh.threads, sides, blocks, 2 * row, s);
     } else {
         const size_t smem = (p.K + kWideVals - 1) / kWideVals * kWideVals * sizeof(float);
         const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kWideThreads, smem, s, attr);
@@ -713,11 +749,15 @@ template <int IN, int WT>
 cudaError_t prepare_backward()
 {
     constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 2>, kAttr, kRingBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 3>, kAttr, kRingBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 4>, kAttr, kRingBytes);
+    cudaError_t e = cudaSuccess;
+    for (const auto ring :
+         {rmsnorm_backward_ring_kernel<IN, WT, 2, false>, rmsnorm_backward_ring_kernel<IN, WT, 3, false>,
+          rmsnorm_backward_ring_kernel<IN, WT, 4, false>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(ring, kAttr, kRingBytes);
+    if constexpr (IN == kBf16)  // a block's share of the ring always holds four rows of at most 1024 values
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 4, true>, kAttr, kRingBytes);
     return e == cudaSuccess ? cudaFuncSetAttribute(rmsnorm_backward_wide_kernel<IN, WT>, kAttr,
                                                    static_cast<int>(kNormMaxK * sizeof(float)))
                             : e;

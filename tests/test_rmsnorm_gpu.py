@@ -292,3 +292,29 @@ def test_many_narrow_rows(rows, K, dtype, residual):
     if tiled:  # rows up to the tile's end hold 1.0
         padded = (rows + 127) // 128 * 128
         assert (ref.untile(got.scales.cpu().numpy(), padded, K)[rows:] == 127).all()
+
+
+@pytest.mark.parametrize("rows,K", [(1025, 96), (1301, 512), (2437, 544), (3000, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [False, True])
+def test_backward_many_narrow_rows(rows, K, dtype, dh):
+    """Rows that share a block: dx as in calls of few rows, dw within the sum's bound, the same from run to run."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng([rows, K])
+    dt, bf16 = _dtype(dtype), dtype == "bf16"
+    h, h64 = _make(rng, (rows, K), dt)
+    dy, dy64 = _make(rng, (rows, K), dt)
+    g, g64 = _make(rng, (rows, K), dt) if dh else (None, None)
+    w, w64 = _make(rng, (K,), dt)
+    rstd = torch.from_numpy((1 / np.sqrt((h64 * h64).mean(1) + EPS)).astype(np.float32)).cuda()
+    dx, dw = b.rmsnorm_backward(dy, h, rstd, w, dh=g)
+    want, err, wdw, size = ref.rmsnorm_backward(dy64, h64, _np(rstd), w64, g64)
+    ref.assert_near(_np(dx), want, err, bf16, "dx")
+    ref.assert_near(_np(dw), wdw, (rows + 64) * ref.U * size, False, "dw")
+    for at in range(0, rows, 1000):
+        few = slice(at, min(at + 1000, rows))
+        part = b.rmsnorm_backward(dy[few], h[few], rstd[few], w, dh=g[few] if dh else None)
+        assert torch.equal(part[0], dx[few])
+    again = b.rmsnorm_backward(dy, h, rstd, w, dh=g)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw), "two runs differ"
