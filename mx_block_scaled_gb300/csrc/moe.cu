@@ -402,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 8 : 3) moe_combine_kern
         store16<IN>(p.out + (t * p.N + k) * E, acc);
 }
 
-// A warp per slot: dy[row] = w * dout[t] and dw = <dout[t], y[row]>.
+// A warp per slot: dy[row] = w * dout[t] and dw = <dout[t], y[row]>.  The next slot's
+// entry is loaded ahead of its row.  More blocks than are resident even out the end: 32
+// an SM 16384 x 512, top 8, 48 us, 3814 x 2048 FP32, top 8, 79 us; 16 an SM 48 and 86;
+// without the entry ahead 52 and 85.
 template <int IN>
 __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(const CombineBackParams p)
 {
@@ -411,12 +414,19 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(const Co
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t N = p.N, slots = p.tokens * p.topk;
-    for (int64_t s = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); s < slots;
-         s += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t s = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    int next_entry = s < slots ? p.row_of_slot[s] : 0;
+    float next_w = s < slots ? p.weights[s] : 0.0f;
+    for (; s < slots; s += step) {
         const int64_t t = s / p.topk;
         bool dropped;
-        const int64_t row = slot_row(p.row_of_slot[s], slots, dropped);
-        const float w = dropped ? 0.0f : p.weights[s];
+        const int64_t row = slot_row(next_entry, slots, dropped);
+        const float w = dropped ? 0.0f : next_w;
+        if (s + step < slots) {
+            next_entry = p.row_of_slot[s + step];
+            next_w = p.weights[s + step];
+        }
         float dot = 0.0f;
         if (row >= 0) {
 #pragma unroll 2
@@ -565,7 +575,7 @@ cudaError_t launch_moe_combine(const CombineParams &p, int in_dtype, int num_sms
 cudaError_t launch_moe_combine_backward(const CombineBackParams &p, int in_dtype, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(strided_blocks(p.tokens * p.topk, num_sms, 16), kThreads, 0, s, attr);
+    const cudaLaunchConfig_t cfg = row_launch(strided_blocks(p.tokens * p.topk, num_sms, 32), kThreads, 0, s, attr);
     return in_dtype == kBf16 ? cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kBf16>, p)
                              : cudaLaunchKernelEx(&cfg, moe_combine_backward_kernel<kF32>, p);
 }
