@@ -42,98 +42,84 @@ __device__ __forceinline__ float block_sum(float v, float *part)
 }
 
 // ------------------------------------------------------------------ forward --
-// A block takes ROWS neighbouring rows at once, a thread NCH runs of 16 values of
-// each.  Sums and products are packed pairs: at 3 bytes a value (BF16 to MXFP8 without
-// a residual) a value may cost 17 instructions before they bind instead of HBM.  The
-// weight is kept in L1 for the SM's next rows: fetched from L2 for every row, its few
-// lines hold up all SMs (8192 x 2016 FP32: 32 us, 46 without; 1504: 24 and 38).
-// SIDE: blockDim.y such groups of rows beside each other.
-template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS, bool SIDE>
-__global__ void __launch_bounds__(kMaxThreads, NCH == 1 && !RES && IN == kF32 ? 2 : 0)
-    rmsnorm_kernel(const NormParams p)
+// A block takes a row, a thread NCH runs of 16 values of it.  Sums and products are
+// packed pairs: at 3 bytes a value (BF16 to MXFP8 without a residual) a value may cost
+// 17 instructions before they bind instead of HBM.  The weight is kept in L1 for the
+// SM's next rows: fetched from L2 for every row, its few lines hold up all SMs (8192 x
+// 2016 FP32: 32 us, 46 without; 1504: 24 and 38).  SIDE: blockDim.y rows beside each
+// other.
+template <int IN, int WT, int FMT, int NCH, bool RES, bool SIDE>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p)
 {
     constexpr int E = ElemBytes<IN>::value;
-    __shared__ float part[ROWS][32];
+    __shared__ float part[32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int64_t unit = SIDE ? static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
-    const int64_t row0 = unit * ROWS, K = p.K;
+    const int64_t row = SIDE ? static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x, K = p.K;
     const int part0 = SIDE ? threadIdx.y * nwarps : 0;
+    const bool live = !SIDE || row < p.rows;
 
-    Raw16<IN> x[ROWS][NCH], r[RES ? ROWS : 1][RES ? NCH : 1];
+    Raw16<IN> x[NCH], r[RES ? NCH : 1];
     Raw16<WT> w[NCH];
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
-            const bool inside = k < K && ((ROWS == 1 && !SIDE) || row0 + q < p.rows);
-            x[q][c].load(p.x + (row0 + q) * p.x_stride + k * E, inside);
-            if constexpr (RES)
-                r[q][c].load(p.residual + (row0 + q) * p.residual_stride + k * E, inside);
-        }
+    for (int c = 0; c < NCH; ++c) {
+        const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
+        x[c].load(p.x + row * p.x_stride + k * E, live && k < K);
+        if constexpr (RES)
+            r[c].load(p.residual + row * p.residual_stride + k * E, live && k < K);
+    }
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         const int64_t k = (c * nwarps + warp) * kWarpVals + lane * kLaneVals;
         w[c].template load<true>(p.weight + k * ElemBytes<WT>::value, k < K);
     }
-    F2 h[ROWS][NCH][kLaneVals / 2];
+    F2 h[NCH][kLaneVals / 2], ss2 = f2(0.0f, 0.0f);
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        F2 ss = f2(0.0f, 0.0f);
+    for (int c = 0; c < NCH; ++c)
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
-#pragma unroll
-            for (int i = 0; i < kLaneVals / 2; ++i) {
-                h[q][c][i] = x[q][c].pair(i);
-                if constexpr (RES)
-                    h[q][c][i] = f2_add(h[q][c][i], r[q][c].pair(i));
-                ss = f2_fma(h[q][c][i], h[q][c][i], ss);
-            }
-        float lo, hi;
-        f2_split(ss, lo, hi);
-        lo = warp_sum(lo + hi);
-        if (lane == 0)
-            part[q][part0 + warp] = lo;
-    }
+        for (int i = 0; i < kLaneVals / 2; ++i) {
+            h[c][i] = x[c].pair(i);
+            if constexpr (RES)
+                h[c][i] = f2_add(h[c][i], r[c].pair(i));
+            ss2 = f2_fma(h[c][i], h[c][i], ss2);
+        }
+    float ss, odd;
+    f2_split(ss2, ss, odd);
+    ss = warp_sum(ss + odd);
+    if (lane == 0)
+        part[part0 + warp] = ss;
     __syncthreads();
+    ss = warp_sum(lane < nwarps ? part[part0 + lane] : 0.0f);
+    const float rstd = __frsqrt_rn(ss / static_cast<float>(K) + p.eps);
+    if (threadIdx.x == 0 && p.rstd && live)
+        p.rstd[row] = rstd;
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        const int64_t row = row0 + q;
-        if ((ROWS > 1 || SIDE) && row >= p.rows)
-            break;  // warp-uniform, and no barrier follows
-        const float ss = warp_sum(lane < nwarps ? part[q][part0 + lane] : 0.0f);
-        const float rstd = __frsqrt_rn(ss / static_cast<float>(K) + p.eps);
-        if (threadIdx.x == 0 && p.rstd)
-            p.rstd[row] = rstd;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int64_t k0 = (c * nwarps + warp) * kWarpVals;
-            const int64_t k = k0 + lane * kLaneVals;
-            const bool inside = k < K;
-            float v[kLaneVals];
-            if (p.h && inside) {
-#pragma unroll
-                for (int i = 0; i < kLaneVals / 2; ++i)
-                    f2_split(h[q][c][i], v[2 * i], v[2 * i + 1]);
-                store16<IN>(p.h + (row * K + k) * E, v);
-            }
+    for (int c = 0; c < NCH && live; ++c) {
+        const int64_t k0 = (c * nwarps + warp) * kWarpVals;
+        const int64_t k = k0 + lane * kLaneVals;
+        const bool inside = k < K;
+        float v[kLaneVals];
+        if (p.h && inside) {
 #pragma unroll
             for (int i = 0; i < kLaneVals / 2; ++i)
-                f2_split(f2_mul(f2_mul(h[q][c][i], f2(rstd, rstd)), w[c].pair(i)), v[2 * i], v[2 * i + 1]);
-            if (p.y && inside)
-                store16<IN>(p.y + (row * K + k) * E, v);
-            if (FMT != kNoFmt) {
-                const auto e = mx_encode<FMT == kNoFmt ? kMxfp8 : FMT>(v);
-                if (inside)
-                    store_codes(p.mx.codes + row * (FMT == kMxfp8 ? K : K >> 1), k, e);
-                store_scales(p.mx.scales, p.mx.mode, row, k0, K, lane, e.scode);
-            }
+                f2_split(h[c][i], v[2 * i], v[2 * i + 1]);
+            store16<IN>(p.h + (row * K + k) * E, v);
+        }
+#pragma unroll
+        for (int i = 0; i < kLaneVals / 2; ++i)
+            f2_split(f2_mul(f2_mul(h[c][i], f2(rstd, rstd)), w[c].pair(i)), v[2 * i], v[2 * i + 1]);
+        if (p.y && inside)
+            store16<IN>(p.y + (row * K + k) * E, v);
+        if (FMT != kNoFmt) {
+            const auto e = mx_encode<FMT == kNoFmt ? kMxfp8 : FMT>(v);
+            if (inside)
+                store_codes(p.mx.codes + row * (FMT == kMxfp8 ? K : K >> 1), k, e);
+            store_scales(p.mx.scales, p.mx.mode, row, k0, K, lane, e.scode);
         }
     }
     if (FMT != kNoFmt && p.mx.mode == kScaleTiled)
-        pad_tiled_scales(p.mx.scales, p.rows, K, unit * blockDim.x + threadIdx.x,
+        pad_tiled_scales(p.mx.scales, p.rows, K, row * blockDim.x + threadIdx.x,
                          static_cast<int64_t>(gridDim.x) * (SIDE ? blockDim.y : 1) * blockDim.x);
 }
 
@@ -638,32 +624,29 @@ int blocks_per_sm(int64_t K)
     return n > 4 ? 4 : n;
 }
 
-// Without a residual a row brings half the bytes to hide its reduction behind, so
-// more of it is in flight in FP32, two rows a block (8192 x 4096: 46 us, 51 with one),
-// and BF16, where instructions bind as well, gives a thread 32 values to spread the
-// fixed ones over (16384 x 8192 to MXFP8: 74 us, 84 with two rows of 16, 88 with one).
-// With a residual one row of 16 values is best (16384 x 8192: 135 us, 138 with 32).
+// BF16 without a residual brings half the bytes to hide a row's reduction behind, and
+// instructions bind as well: a thread takes 32 values to spread the fixed ones over
+// (16384 x 8192 to MXFP8: 73 us, 87 with 16).  Elsewhere 16 are as good or better (with
+// a residual 135 us either way).
 template <int IN, bool RES>
 constexpr int fewest_runs()
 {
     return IN == kBf16 && !RES ? 2 : 1;
 }
 
-template <int IN, int WT, int FMT, int NCH, bool RES, int ROWS>
+template <int IN, int WT, int FMT, int NCH, bool RES>
 cudaError_t launch_rows(const NormParams &p, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
     constexpr bool kNarrow = NCH == fewest_runs<IN, RES>();
     const int side = kNarrow && p.K <= kSideK && p.rows >= kSideRows ? kSideThreads / threads : 1;
-    const int64_t of_block = static_cast<int64_t>(ROWS) * side;
-    cudaLaunchConfig_t cfg =
-        row_launch(static_cast<unsigned>((p.rows + of_block - 1) / of_block), threads, 0, s, attr);
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>((p.rows + side - 1) / side), threads, 0, s, attr);
     if constexpr (kNarrow)
         if (side > 1) {
             cfg.blockDim.y = side;
-            return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, true>, p);
+            return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, true>, p);
         }
-    return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, ROWS, false>, p);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<IN, WT, FMT, NCH, RES, false>, p);
 }
 
 template <int IN, int WT, int FMT, bool RES>
@@ -673,9 +656,9 @@ cudaError_t launch_forward(const NormParams &p, cudaStream_t s)
     const Shape sh = pick_shape(p.K, kLeast);
     if constexpr (kLeast == 1)
         if (sh.nch == 1)
-            return launch_rows<IN, WT, FMT, 1, RES, RES ? 1 : 2>(p, sh.threads, s);
-    return sh.nch == 2 ? launch_rows<IN, WT, FMT, 2, RES, 1>(p, sh.threads, s)
-                       : launch_rows<IN, WT, FMT, 4, RES, 1>(p, sh.threads, s);
+            return launch_rows<IN, WT, FMT, 1, RES>(p, sh.threads, s);
+    return sh.nch == 2 ? launch_rows<IN, WT, FMT, 2, RES>(p, sh.threads, s)
+                       : launch_rows<IN, WT, FMT, 4, RES>(p, sh.threads, s);
 }
 
 template <int IN, int WT, int FMT>
