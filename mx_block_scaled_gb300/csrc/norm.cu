@@ -2,7 +2,10 @@
 // gradient.
 //
 //   h = x + r;  rstd = 1/sqrt(mean(h^2) + eps);  y = h * rstd * w
-//   p = dy * w;  dx = rstd * p - h * rstd^3 * mean(p * h) + dh;  dw = sum_rows dy * h * rstd
+//   p = dy * w;  n = h * rstd;  dx = rstd * (p - n * mean(p * n)) + dh;  dw = sum_rows dy * n
+//
+// (mean(p * n) is taken as rstd * mean(p * h), one factor a row.  No power of rstd is
+// formed: rstd^3 leaves FP32 for rows of 1e13 or 1e-13, which n and the factor do not.)
 //
 // Both are one pass over the rows, bound by HBM.  The forward keeps a row in the
 // registers of one block between its reduction and its use and writes h, y, codes
@@ -128,6 +131,12 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p
 // in partial[block].  Rows of more than 8192 values: two passes over the row, the
 // second from L2, with dw in shared memory ([run][pair][thread], so that a warp's
 // accesses are consecutive).
+// dx of a pair of values; unit is h * rstd, coef -mean(p * unit) of the row
+__device__ __forceinline__ F2 norm_dx(F2 dy, F2 unit, F2 dh, F2 w, F2 coef, F2 rstd)
+{
+    return f2_fma(f2_fma(unit, coef, f2_mul(dy, w)), rstd, dh);
+}
+
 constexpr int kWideThreads = 512;
 constexpr int kWideVals = kWideThreads * kLaneVals;
 
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(con
                 dot = fmaf(dy.at(i) * w.at(i), h.at(i), dot);
         }
         dot = block_sum(dot, part[flip]);
-        const float coef = rstd * rstd * rstd * (dot / static_cast<float>(K));
+        const float coef = rstd * (dot / static_cast<float>(K));
         n = 0;
         for (int64_t k = k0; k < K; k += kWideVals, n += kLaneVals / 2) {
             Raw16<IN> dy, h, dh;
@@ -176,10 +185,10 @@ __global__ void __launch_bounds__(kWideThreads) rmsnorm_backward_wide_kernel(con
 #pragma unroll
             for (int i = 0; i < kLaneVals; i += 2) {
                 F2 &sum = dw[(n + i / 2) * kWideThreads];
-                sum = f2_fma(f2(dy.at(i), dy.at(i + 1)), f2_mul(f2(h.at(i), h.at(i + 1)), f2(rstd, rstd)), sum);
-#pragma unroll
-                for (int q = i; q < i + 2; ++q)
-                    dx[q] = fmaf(-h.at(q), coef, rstd * (dy.at(q) * w.at(q))) + dh.at(q);
+                const F2 g = dy.pair(i / 2), unit = f2_mul(h.pair(i / 2), f2(rstd, rstd));
+                sum = f2_fma(g, unit, sum);
+                f2_split(norm_dx(g, unit, dh.pair(i / 2), w.pair(i / 2), f2(-coef, -coef), f2(rstd, rstd)), dx[i],
+                         dx[i + 1]);
             }
             store16<IN>(p.dx + (row * K + k) * E, dx);
         }
@@ -252,12 +261,6 @@ struct Pieces {
         return sum;
     }
 
-    // dx of a pair of values; coef is -rstd^3 * mean(p * h)
-    static __device__ __forceinline__ F2 dx(F2 dy, F2 h, F2 dh, F2 w, F2 coef, F2 rstd)
-    {
-        return f2_fma(h, coef, f2_fma(f2_mul(dy, w), rstd, dh));
-    }
-
     static __device__ __forceinline__ uint4 pack(const F2 (&v)[kPairs])
     {
         float d[kPer];
@@ -284,6 +287,7 @@ __device__ __forceinline__ void leave_dot(F2 dot, float *part)
         part[threadIdx.x >> 5] = lo;
 }
 
+// -mean(p * h * rstd) of a row
 __device__ __forceinline__ float row_coef(const float *part, float rstd, float inv_k)
 {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -295,7 +299,7 @@ __device__ __forceinline__ float row_coef(const float *part, float rstd, float i
         s.z += v.z;
         s.w += v.w;
     }
-    return -(rstd * rstd * rstd * (((s.x + s.y) + (s.z + s.w)) * inv_k));
+    return -(rstd * (((s.x + s.y) + (s.z + s.w)) * inv_k));
 }
 
 template <int IN, int WT, int DEPTH, bool SIDE>
@@ -427,9 +431,9 @@ __global__ void __launch_bounds__(SIDE ? kSideThreads : kMaxThreads, SIDE ? 4 : 
             F2 o[kPairs];
 #pragma unroll
             for (int n = 0; n < kPairs; ++n) {
-                const F2 g = P::pair(dy[i], n), v = P::pair(h[i], n);
-                o[n] = P::dx(g, v, P::pair(dh, n), w[i][n], coef2, rstd2);
-                dw[i][n] = f2_fma(g, f2_mul(v, rstd2), dw[i][n]);
+                const F2 g = P::pair(dy[i], n), unit = f2_mul(P::pair(h[i], n), rstd2);
+                o[n] = norm_dx(g, unit, P::pair(dh, n), w[i][n], coef2, rstd2);
+                dw[i][n] = f2_fma(g, unit, dw[i][n]);
             }
             if (inside[i])
                 *reinterpret_cast<uint4 *>(dx + i * plane) = P::pack(o);
@@ -589,8 +593,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_backward_few_kernel(co
         F2 o[P::kPairs];
 #pragma unroll
         for (int n = 0; n < P::kPairs; ++n)
-            o[n] = P::dx(P::pair(dy[i], n), P::pair(h[i], n), P::pair(dh[i], n), w[i][n], f2(coef, coef),
-                         f2(rstd, rstd));
+            o[n] = norm_dx(P::pair(dy[i], n), f2_mul(P::pair(h[i], n), f2(rstd, rstd)), P::pair(dh[i], n), w[i][n],
+                           f2(coef, coef), f2(rstd, rstd));
         if (inside[i])
             *reinterpret_cast<uint4 *>(p.dx + (row * K + (i * threads + tid) * P::kPer) * E) = P::pack(o);
     }

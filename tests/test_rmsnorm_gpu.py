@@ -318,3 +318,29 @@ def test_backward_many_narrow_rows(rows, K, dtype, dh):
         assert torch.equal(part[0], dx[few])
     again = b.rmsnorm_backward(dy, h, rstd, w, dh=g)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw), "two runs differ"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,dh", [(12, 512, False), (12, 96, True), (1100, 512, True), (1100, 2080, False),
+                                       (12, 8224, True), (12, 16384, False)])
+def test_backward_of_extreme_rows(dtype, rows, K, dh):
+    """Rows whose rstd is far from 1, where its powers leave FP32 and dx does not; a row of zeros with a tiny eps."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng([rows, K, 7])
+    dt = _dtype(dtype)
+    scale = np.ones((rows, 1), np.float32)
+    scale[:12, 0] = [1, 1e4, 1e12, 1e13, 1e15, 1e17, 1e-4, 1e-10, 1e-13, 1e-15, 1e-17, 0]
+    h = torch.from_numpy((rng.standard_normal((rows, K)) * scale).astype(np.float32)).cuda().to(dt)
+    h64 = _np(h)
+    dy, dy64 = _make(rng, (rows, K), dt)
+    w, w64 = _make(rng, (K,), dt)
+    g = g64 = None
+    rstd = torch.from_numpy((1 / np.sqrt((h64 * h64).mean(1) + (scale[:, 0] == 0) * 1e-30)).astype(np.float32)).cuda()
+    if dh:  # of dx's own size, so that it hides nothing
+        g = (torch.from_numpy(rng.standard_normal((rows, K)).astype(np.float32)).cuda() * rstd[:, None]).to(dt)
+        g64 = _np(g)
+    dx, dw = b.rmsnorm_backward(dy, h, rstd, w, dh=g)
+    want, err, wdw, size = ref.rmsnorm_backward(dy64, h64, _np(rstd), w64, g64)
+    ref.assert_near(_np(dx), want, err, dtype == "bf16", "dx")
+    ref.assert_near(_np(dw), wdw, (rows + 64) * ref.U * size, False, "dw")
