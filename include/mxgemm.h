@@ -455,8 +455,9 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  *    (`..._stride`, at least the row length; ignored for a single row).  Plain
  *    matrices start on 32-byte boundaries and so does each of their rows.
  *    Outputs are dense; codes and scales are 16-byte aligned.
- *  - An output touches no input matrix and no expert id (MXGEMM_ERR_ARG), but may
- *    be an input itself where a call names that and the input is dense.
+ *  - An output (scales, statistics and the workspace among them) touches no byte
+ *    from an input's first to its last, nor another output's (MXGEMM_ERR_ARG), but
+ *    may be an input itself where a call names that and the input is dense.
  *  - fmt 0 asks for no MX output (codes and scales NULL); MXGEMM_FMT_MXFP8_E4M3
  *    and MXGEMM_FMT_MXFP4_E2M1 write codes [rows, K] bytes or [rows, K/2] bytes
  *    and scales, row-major [rows, K/32] or, with MXGEMM_QUANT_SF_TILED (K a
@@ -585,7 +586,7 @@ MXGEMM_API int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride,
 /*
  * Its gradient:  dy[row_of_slot[s]] = weights[s] * dout[s / topk] (a dropped
  * slot's row is zero) and dweights[s] = <dout[s / topk], y[row_of_slot[s]]> (FP32,
- * zero for a dropped slot).  dy may be y itself.
+ * zero for a dropped slot).  dy may be y itself, dweights may be weights itself.
  */
 MXGEMM_API int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64_t dout_stride, const void *y,
                                            int64_t y_stride, int64_t tokens, int64_t topk, int64_t N,

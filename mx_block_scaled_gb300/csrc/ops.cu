@@ -2,6 +2,7 @@
 // activation, expert sort / dispatch / combine): argument checks and launches.
 #include "ops.h"
 
+#include <initializer_list>
 #include <mutex>
 
 #include "mx_block.cuh"
@@ -64,21 +65,62 @@ bool rows_align_ok(const void *p, int64_t stride, int64_t rows, int64_t elem)
     return p == nullptr || (aligned(p, 32) && (rows == 1 || stride * elem % 32 == 0));
 }
 
-// A dense output of `orows` rows of `orow` bytes touches no byte of a strided input:
-// blocks read inputs while others write.  `in_place`: it may be the input itself where
-// that is dense, each value then being read by the thread that writes it, before it does.
-bool apart(const void *out, int64_t orows, int64_t orow, const void *in, int64_t rows, int64_t stride, int64_t row,
-           bool in_place)
+// Bytes of a matrix, from its first to its last; p NULL for one that there is not.
+struct Span {
+    const void *p;
+    int64_t rows, stride, row;
+};
+Span dense(const void *p, int64_t rows, int64_t row) { return {p, rows, row, row}; }
+Span flat(const void *p, int64_t n) { return {p, 1, n, n}; }
+
+bool apart(const Span &a, const Span &b)
 {
-    if (!out || !in || (in_place && out == in && (rows == 1 || stride == row)))
+    if (!a.p || !b.p)
         return true;
     using Wide = unsigned __int128;  // no size that the other checks pass overflows it
-    const Wide o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
-    return o + static_cast<Wide>(orows) * orow <= i || i + static_cast<Wide>(rows - 1) * stride + row <= o;
+    const Wide a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a0 + static_cast<Wide>(a.rows - 1) * a.stride + a.row <= b0 ||
+           b0 + static_cast<Wide>(b.rows - 1) * b.stride + b.row <= a0;
+}
+
+// An output, and the inputs (bit i: input i) that it may be itself: whole and dense,
+// where the thread that writes a value is the one that read it, and had read it before.
+struct Output {
+    Span at;
+    unsigned over = 0;
+
+    bool is(const Span &in) const
+    {
+        return at.p == in.p && at.rows == in.rows && at.row == in.row && (in.rows == 1 || in.stride == in.row);
+    }
+};
+
+// No output touches a byte of an input, apart from those that it may be, nor of another
+// output: blocks read inputs while others write.
+bool outputs_apart(std::initializer_list<Output> outs, std::initializer_list<Span> ins)
+{
+    for (const Output *o = outs.begin(); o != outs.end(); ++o) {
+        unsigned bit = 1;
+        for (const Span &in : ins) {
+            if (!apart(o->at, in) && !((o->over & bit) && o->is(in)))
+                return false;
+            bit <<= 1;
+        }
+        for (const Output *other = outs.begin(); other != o; ++other)
+            if (!apart(o->at, other->at))
+                return false;
+    }
+    return true;
 }
 
 // Bytes of a row of n MX codes.
 int64_t code_bytes(int fmt, int64_t n) { return fmt == MXGEMM_FMT_MXFP4_E2M1 ? n / 2 : n; }
+
+// Bytes of the scales of [rows, K].
+int64_t scale_bytes(uint32_t flags, int64_t rows, int64_t K)
+{
+    return ((flags & MXGEMM_QUANT_SF_TILED) ? (rows + 127) / 128 * 128 : rows) * (K / 32);
+}
 
 // The MX output of a call: fmt 0 has neither codes nor scales.
 int check_mx(int fmt, const void *codes, const uint8_t *scales, uint32_t flags, int64_t K)
@@ -129,12 +171,14 @@ int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, const void *re
     if (K > mxg::kNormMaxK)
         return MXGEMM_ERR_UNSUPPORTED;
     const int64_t row = K * e;
-    for (const void *const out : {h, y})
-        if (!apart(out, rows, row, x, rows, x_stride * e, row, true) ||
-            !apart(out, rows, row, residual, rows, residual_stride * e, row, true))
-            return MXGEMM_ERR_ARG;
-    if (!apart(codes, rows, code_bytes(fmt, K), x, rows, x_stride * e, row, false) ||
-        !apart(codes, rows, code_bytes(fmt, K), residual, rows, residual_stride * e, row, false))
+    if (!outputs_apart({{dense(h, rows, row), 0b11},
+                        {dense(y, rows, row), 0b11},
+                        {dense(codes, rows, code_bytes(fmt, K))},
+                        {flat(scales, scale_bytes(flags, rows, K))},
+                        {flat(rstd, 4 * rows)}},
+                       {{x, rows, x_stride * e, row},
+                        {residual, rows, residual_stride * e, row},
+                        flat(weight, K * elem_bytes(weight_dtype))}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
@@ -185,9 +229,14 @@ int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, con
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
     const int64_t row = K * e;
-    if (!apart(dx, rows, row, dy, rows, dy_stride * e, row, false) ||
-        !apart(dx, rows, row, h, rows, h_stride * e, row, false) ||
-        !apart(dx, rows, row, dh, rows, dh_stride * e, row, true))
+    if (!outputs_apart({{dense(dx, rows, row), 0b100},
+                        {flat(dweight, 4 * K)},
+                        {flat(need > 0 ? workspace : nullptr, static_cast<int64_t>(need))}},
+                       {{dy, rows, dy_stride * e, row},
+                        {h, rows, h_stride * e, row},
+                        {dh, rows, dh_stride * e, row},
+                        flat(rstd, 4 * rows),
+                        flat(weight, K * elem_bytes(weight_dtype))}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
@@ -229,11 +278,13 @@ int mxgemm_glu(int act, int in_dtype, const void *gate, const void *up, int64_t 
         !aligned(kept_scales, 16))
         return MXGEMM_ERR_ALIGN;
     const int64_t row = F * e;
-    for (const void *const in : {gate, up})
-        if (!apart(y, rows, row, in, rows, stride * e, row, true) ||
-            !apart(codes, rows, code_bytes(fmt, F), in, rows, stride * e, row, false) ||
-            !apart(kept_codes, rows, 2 * F, in, rows, stride * e, row, false))
-            return MXGEMM_ERR_ARG;
+    if (!outputs_apart({{dense(y, rows, row), 0b11},
+                        {dense(codes, rows, code_bytes(fmt, F))},
+                        {flat(scales, scale_bytes(flags, rows, F))},
+                        {dense(kept_codes, rows, 2 * F)},
+                        {flat(kept_scales, scale_bytes(0, rows, 2 * F))}},
+                       {{gate, rows, stride * e, row}, {up, rows, stride * e, row}}))
+        return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -274,17 +325,18 @@ int mxgemm_glu_backward(int act, int in_dtype, const void *dy, int64_t dy_stride
         !aligned(kept_codes, 16) || !aligned(kept_scales, 16) || !aligned(dgu, 32) || !aligned(a, 32))
         return MXGEMM_ERR_ALIGN;
     const int64_t row = F * e;
-    // dgu may be the [rows, 2F] matrix that gate and up are the halves of
+    // dgu may be the [rows, 2F] matrix that gate and up are the halves of: one input then
     const bool halves = dgu && dgu == gate && up == bytes(gate) + row && (rows == 1 || stride == 2 * F);
-    if (!apart(dgu, rows, 2 * row, dy, rows, dy_stride * e, row, false) ||
-        !apart(codes, rows, code_bytes(fmt, 2 * F), dy, rows, dy_stride * e, row, false) ||
-        !apart(a, rows, row, dy, rows, dy_stride * e, row, true))
+    if (!outputs_apart({{dense(dgu, rows, 2 * row), 0b10},
+                        {dense(codes, rows, code_bytes(fmt, 2 * F))},
+                        {flat(scales, scale_bytes(flags, rows, 2 * F))},
+                        {dense(a, rows, row), 0b111}},
+                       {{dy, rows, dy_stride * e, row},
+                        halves ? dense(gate, rows, 2 * row) : Span{gate, rows, stride * e, row},
+                        {halves ? nullptr : up, rows, stride * e, row},
+                        dense(kept_codes, rows, 2 * F),
+                        flat(kept_scales, scale_bytes(0, rows, 2 * F))}))
         return MXGEMM_ERR_ARG;
-    for (const void *const in : {gate, up})
-        if ((!halves && !apart(dgu, rows, 2 * row, in, rows, stride * e, row, false)) ||
-            !apart(codes, rows, code_bytes(fmt, 2 * F), in, rows, stride * e, row, false) ||
-            !apart(a, rows, row, in, rows, stride * e, row, true))
-            return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms);
     if (st != MXGEMM_OK)
@@ -325,9 +377,11 @@ int mxgemm_moe_sort(const void *expert_ids, int id_bytes, int64_t slots, int64_t
     const size_t need = mxgemm_moe_sort_workspace_bytes(slots, groups);
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
-    if (!apart(offsets, groups + 1, 8, expert_ids, slots, id_bytes, id_bytes, false) ||
-        !apart(row_of_slot, slots, 4, expert_ids, slots, id_bytes, id_bytes, false) ||
-        !apart(slot_of_row, slots, 4, expert_ids, slots, id_bytes, id_bytes, false))
+    if (!outputs_apart({{flat(offsets, 8 * (groups + 1))},
+                        {flat(row_of_slot, 4 * slots)},
+                        {flat(slot_of_row, 4 * slots)},
+                        {flat(need > 0 ? workspace : nullptr, static_cast<int64_t>(need))}},
+                       {flat(expert_ids, id_bytes * slots)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
@@ -363,7 +417,9 @@ int mxgemm_moe_dispatch(int in_dtype, const void *x, int64_t x_stride, int64_t t
         return MXGEMM_ERR_ALIGN;
     if (!warps_ok(tokens, K))
         return MXGEMM_ERR_UNSUPPORTED;
-    if (!apart(rows, tokens * topk, plain ? 2 * K : code_bytes(fmt, K), x, tokens, x_stride * e, K * e, false))
+    const int64_t slots = tokens * topk;
+    if (!outputs_apart({{dense(rows, slots, plain ? 2 * K : code_bytes(fmt, K))}, {flat(scales, scale_bytes(0, slots, K))}},
+                       {{x, tokens, x_stride * e, K * e}, flat(row_of_slot, 4 * slots)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
@@ -398,9 +454,12 @@ int mxgemm_moe_combine(int in_dtype, const void *y, int64_t y_stride, int64_t to
         return MXGEMM_ERR_ALIGN;
     if (!warps_ok(tokens, N))
         return MXGEMM_ERR_UNSUPPORTED;
-    const int64_t row = N * e;
-    if (!apart(out, tokens, row, y, tokens * topk, y_stride * e, row, false) ||
-        !apart(out, tokens, row, add, tokens, add_stride * e, row, true))
+    const int64_t row = N * e, slots = tokens * topk;
+    if (!outputs_apart({{dense(out, tokens, row), 0b10}},
+                       {{y, slots, y_stride * e, row},
+                        {add, tokens, add_stride * e, row},
+                        flat(row_of_slot, 4 * slots),
+                        flat(weights, 4 * slots)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);
@@ -433,9 +492,12 @@ int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64_t dout_str
     if (!rows_align_ok(y, y_stride, tokens * topk, e) || !rows_align_ok(dout, dout_stride, tokens, e) ||
         !aligned(row_of_slot, 4) || !aligned(weights, 4) || !aligned(dy, 32) || !aligned(dweights, 4))
         return MXGEMM_ERR_ALIGN;
-    const int64_t row = N * e;
-    if (!apart(dy, tokens * topk, row, dout, tokens, dout_stride * e, row, false) ||
-        !apart(dy, tokens * topk, row, y, tokens * topk, y_stride * e, row, true))
+    const int64_t row = N * e, slots = tokens * topk;
+    if (!outputs_apart({{dense(dy, slots, row), 0b10}, {flat(dweights, 4 * slots), 0b1000}},
+                       {{dout, tokens, dout_stride * e, row},
+                        {y, slots, y_stride * e, row},
+                        flat(row_of_slot, 4 * slots),
+                        flat(weights, 4 * slots)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     const int st = ops_device(&sms);

@@ -304,3 +304,18 @@ def test_outputs_over_inputs(T):
         assert e.value.status == b.MXGEMM_ERR_ARG
     got = b.moe_combine_backward(dout, y, slot, w, dy=y)
     assert got[0] is y and torch.equal(y, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_weight_gradient_over_the_weights():
+    """dweights over weights gives what an apart output gives, also where a warp takes several slots."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng(31)
+    for T, k in ((5, 3), (9000, 4)):
+        _, slot, _ = ref.moe_sort(_ids(rng, T, k, 8, drop=0.1), 8)
+        slot = _dev(slot.astype(np.int32))
+        y, dout = (_make(rng, (n, 96), _dtype("bf16"))[0] for n in (T * k, T))
+        w = _dev(rng.random((T, k)).astype(np.float32))
+        want = b.moe_combine_backward(dout, y, slot, w)
+        got = b.moe_combine_backward(dout, y, slot, w, dweights=w)
+        assert got[1] is w and torch.equal(w, want[1]) and torch.equal(got[0], want[0])
