@@ -515,6 +515,9 @@ MXGEMM_API int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_
  *             for mxgemm_glu_backward in 1.03 bytes a value: MXFP8 codes [rows, 2F]
  *             (gate, then up) and row-major scales [rows, 2F/32].  The output is
  *             computed from the inputs themselves.
+ * FP32 operands keep FP32's precision (GELU: that of its FP32 argument).  With BF16
+ * operands the activation is exact to 2^-14 of its value before it is rounded, and
+ * 0 where act(gate) / gate is below 2^-126.
  */
 MXGEMM_API int mxgemm_glu(int act, int in_dtype, const void *gate, const void *up, int64_t stride, int64_t rows,
                           int64_t F, void *y, int fmt, void *codes, uint8_t *scales, uint32_t flags,

@@ -12,8 +12,8 @@
 // with the checkpoint 833 MB in 130 us (6.4 TB/s), without it 591 MB in 87 us (6.8),
 // backward from the checkpoint 1182 MB in 177 us (6.7).  To get there each value
 // must cost fewer than 38 instructions: packed FP32 products, three-input
-// magnitude maxima and the hardware's 2^x and 1/x (with expf and an IEEE division
-// the forward took 257 us).
+// magnitude maxima and, where operands are BF16, the hardware's 2^x and 1/x (with expf and
+// an IEEE division the forward took 257 us).
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -34,31 +34,62 @@ template <int IN, bool KEEP>
 constexpr int kForwardBlocks = IN == kBf16 && !KEEP ? 4 : 2;
 constexpr int kBackwardBlocks = 2;  // 8192 x 14336 from the checkpoint: 177 us; three 181, four 252 (spills)
 
-// q of the activation's gate for a pair of values: the hardware's 2^x and 1/x, each
-// within two ulps, on an argument that carries the conversion to base 2 in its last
-// constant.  2^x overflows to infinity for far negative gates, where q is then 0, and
-// the reciprocal flushes below 2^-126.  `inner` is the argument's slope by g (GELU).
-template <int ACT>
-__device__ __forceinline__ F2 act_gate(F2 g, F2 &inner)
+// The activation's gate for a pair of values: q, 1 - q, and (GELU) the slope of q's
+// argument t = 2z by g.
+struct Gate {
+    F2 q, rest, inner;
+};
+
+// BF16 operands: the hardware's 2^x and 1/x, each within two ulps, on an argument that
+// carries the conversion to base 2 in its last constant.  Its rounding moves q by up to
+// |t| 2^-24 of its value (4e-6 at -85), far below the 2^-9 of a BF16 result, and 2^x
+// overflows to infinity for far negative gates, where q is then 0, as it is below
+// 2^-126 (off by less than |g u| 2^-126).
+//
+// FP32 operands: results keep FP32's precision.  e = exp(-|t|) does not overflow and
+// keeps the argument's last bits, 1 / (1 + e) lies in [1/2, 1], and of q and 1 - q the
+// smaller is e / (1 + e), without a difference.  It is
+// hidden behind HBM but in small calls: SiLU to MXFP8 with checkpoint, 4096 x 14336 FP32
+// 96.2 us (95.0 with the other form), 301 x 5120 5.6 (5.1).
+template <int ACT, int IN>
+__device__ __forceinline__ Gate act_gate(F2 g)
 {
-    constexpr float kLog2e = 1.4426950408889634f;
-    F2 t;
+    Gate o;
+    constexpr bool kFull = IN == kF32;
+    constexpr float kTo = kFull ? 1.0f : -1.4426950408889634f;
+    F2 t;  // FP32: t; BF16: -t log2(e)
     if (ACT == kActGeluTanh) {
         constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
-        const F2 gg = f2_mul(g, g), k = f2(-c * kLog2e, -c * kLog2e), one = f2(1.0f, 1.0f);
+        const F2 gg = f2_mul(g, g), k = f2(c * kTo, c * kTo), one = f2(1.0f, 1.0f);
         t = f2_mul(k, f2_mul(g, f2_fma(gg, f2(0.044715f, 0.044715f), one)));
-        inner = f2_mul(f2(c, c), f2_fma(gg, f2(0.134145f, 0.134145f), one));
+        o.inner = f2_mul(f2(c, c), f2_fma(gg, f2(0.134145f, 0.134145f), one));
     } else {
-        t = f2_mul(g, f2(-kLog2e, -kLog2e));
+        t = kFull ? g : f2_mul(g, f2(kTo, kTo));
     }
     float t0, t1, e0, e1, q0, q1;
     f2_split(t, t0, t1);
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
-    f2_split(f2_add(f2(e0, e1), f2(1.0f, 1.0f)), e0, e1);
+    if (kFull) {
+        e0 = expf(-fabsf(t0));
+        e1 = expf(-fabsf(t1));
+    } else {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+    }
+    const F2 e = f2(e0, e1);
+    f2_split(f2_add(e, f2(1.0f, 1.0f)), e0, e1);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(e0));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(e1));
-    return f2(q0, q1);
+    const F2 r = f2(q0, q1);
+    if (kFull) {
+        float s0, s1;
+        f2_split(f2_mul(e, r), s0, s1);
+        o.q = f2(t0 < 0.0f ? s0 : q0, t1 < 0.0f ? s1 : q1);
+        o.rest = f2(t0 < 0.0f ? q0 : s0, t1 < 0.0f ? q1 : s1);
+    } else {
+        o.q = r;
+        o.rest = f2_fma(r, f2(-1.0f, -1.0f), f2(1.0f, 1.0f));
+    }
+    return o;
 }
 
 template <int ACT, int IN, int FMT, bool KEEP>
@@ -89,9 +120,8 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks<IN, KEEP>) glu_kernel
         float a[kLaneVals];
 #pragma unroll
         for (int i = 0; i < kLaneVals / 2; ++i) {
-            F2 inner;
             const F2 g = rg.pair(i);
-            f2_split(f2_mul(f2_mul(g, act_gate<ACT>(g, inner)), ru.pair(i)), a[2 * i], a[2 * i + 1]);
+            f2_split(f2_mul(f2_mul(g, act_gate<ACT, IN>(g).q), ru.pair(i)), a[2 * i], a[2 * i + 1]);
         }
         if (p.y && inside)
             store16<IN>(p.y + (row * F + k) * E, a);
@@ -186,17 +216,16 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) glu_backward_kernel
         F2 dg2[kLaneVals / 2], du2[kLaneVals / 2], a2[kLaneVals / 2];
 #pragma unroll
         for (int i = 0; i < kLaneVals / 2; ++i) {
-            F2 inner;
-            const F2 q = act_gate<ACT>(g[i], inner), dy = in.dy.pair(i), f = f2_mul(g[i], q);
-            const F2 m = f2_mul(f, f2_fma(q, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)));
+            const Gate gate = act_gate<ACT, IN>(g[i]);
+            const F2 q = gate.q, dy = in.dy.pair(i), f = f2_mul(g[i], q), m = f2_mul(f, gate.rest);
             F2 slope;
             if (ACT == kActSilu) {
                 slope = f2_add(m, q);
             } else {
-                // where q has reached 0 or 1 the slope is q, also where `inner` has overflowed
+                // where q has reached 0 or 1 the slope is q, also where the inner slope has overflowed
                 float m0, m1, s0, s1, q0, q1;
                 f2_split(m, m0, m1);
-                f2_split(f2_fma(m, inner, q), s0, s1);
+                f2_split(f2_fma(m, gate.inner, q), s0, s1);
                 f2_split(q, q0, q1);
                 slope = f2(m0 == 0.0f ? q0 : s0, m1 == 0.0f ? q1 : s1);
             }

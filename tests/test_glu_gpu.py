@@ -202,3 +202,35 @@ def test_outputs_over_inputs(rows, F):
     got = b.glu_backward(dy, ref.ACT_SILU, gate=gu[:, :F], up=gu[:, F:], recompute=True, fmt=1, dgu=gu, a=dy)
     assert got.dgu is gu and got.a is dy
     assert all(torch.equal(p, q) for p, q in zip(got, grad))
+
+
+@pytest.mark.parametrize("act", [ref.ACT_SILU, ref.ACT_GELU])
+def test_float32_keeps_its_precision(act):
+    """FP32 operands: the exponential's argument is not rounded on the way (SiLU) and nothing is flushed.  exp is
+    within two ulps, then an addition, a reciprocal within an ulp and a product: 8 roundings of q and of 1 - q.  GELU's
+    argument has seven, which move q by |t| (1 - q) and 1 - q by |t| q as much.  Below 2^-126 q is off by a few 2^-149."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng(40 + act)
+    F, floor = 2080, 2.0 ** -147
+    g = rng.standard_normal((4, F)) * np.array([[1], [3], [30], [1]])
+    g[0] = np.linspace(-104, 104, F)
+    gu = np.concatenate([g, rng.standard_normal((4, F)) * 1e3], 1).astype(np.float32)
+    dy = rng.standard_normal((4, F)).astype(np.float32)
+    gd, dyd = torch.from_numpy(gu).cuda(), torch.from_numpy(dy).cuda()
+    y = _np(b.glu(gd[:, :F], gd[:, F:], act, plain=True).y)
+    back = b.glu_backward(dyd, act, gate=gd[:, :F], up=gd[:, F:], recompute=True)
+    g, u, dy = gu[:, :F].astype(np.float64), gu[:, F:].astype(np.float64), dy.astype(np.float64)
+    with np.errstate(over="ignore"):
+        q, t, slope = ref._gate(g, act)
+        rest = 1 / (1 + np.exp(t))
+    arg = 0 if act == ref.ACT_SILU else 7 * np.abs(t)
+    f, eq, er = g * q, (8 + arg * rest) * ref.U, (8 + arg * q) * ref.U
+    err = (eq + 3 * ref.U) * np.abs(f * u) + floor * np.abs(g * u)
+    ref.assert_near(y, f * u, err, False, "a")
+    ref.assert_near(_np(back.a), f * u, err, False, "a again")
+    part = np.abs(f) * rest * slope
+    dg = dy * u * (q + f * rest * slope)
+    edg = np.abs(dy * u) * (q * eq + part * (eq + er + 8 * ref.U) + floor * (1 + np.abs(g) * slope)) + 4 * ref.U * np.abs(dg)
+    ref.assert_near(_np(back.dgu)[:, :F], dg, edg, False, "dgate")
+    ref.assert_near(_np(back.dgu)[:, F:], dy * f, (eq + 3 * ref.U) * np.abs(dy * f) + floor * np.abs(dy * g), False, "dup")
