@@ -455,8 +455,9 @@ class _Unloaded:
     def __getattr__(self, name):
         import torch  # noqa: F401  (its libraries first)
         if not os.path.exists(ROWOPS_PATH):
-            raise RuntimeError(f"{ROWOPS_PATH} is missing: build it first (python -m mx_block_scaled_gb300.build, or "
-                               "__graft_entry__.build()); there is no fallback implementation")
+            raise RuntimeError(f"{ROWOPS_PATH} is missing: build it first where PyTorch is installed (python -m "
+                               "mx_block_scaled_gb300.build, or __graft_entry__.build()); there is no fallback "
+                               "implementation")
         spec = importlib.util.spec_from_file_location("mx_block_scaled_gb300._rowops", ROWOPS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
