@@ -234,3 +234,34 @@ def test_float32_keeps_its_precision(act):
     edg = np.abs(dy * u) * (q * eq + part * (eq + er + 8 * ref.U) + floor * (1 + np.abs(g) * slope)) + 4 * ref.U * np.abs(dg)
     ref.assert_near(_np(back.dgu)[:, :F], dg, edg, False, "dgate")
     ref.assert_near(_np(back.dgu)[:, F:], dy * f, (eq + 3 * ref.U) * np.abs(dy * f) + floor * np.abs(dy * g), False, "dup")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,tiled", [(1, True), (2, True), (1, False), (2, False)])
+@pytest.mark.parametrize("rows,F", [(1501, 1664), (2501, 1088), (900, 4096)])
+def test_many_rows(oracle_mod, dtype, fmt, tiled, rows, F):
+    """Several chunks to every warp, both directions, the gradient from the checkpoint."""
+    b = lib()
+    rng = np.random.default_rng([rows, F])
+    bf16 = dtype == "bf16"
+    tiled = tiled and F % 128 == 0
+    gu, gu64 = _make(rng, (rows, 2 * F), _dtype(dtype), 2.0)
+    dy, dy64 = _make(rng, (rows, F), _dtype(dtype))
+    out = b.glu(gu[:, :F], gu[:, F:], ref.ACT_SILU, fmt=fmt, tiled=tiled, plain=True, keep=True)
+    a, err = ref.glu(gu64[:, :F], gu64[:, F:], ref.ACT_SILU)
+    ref.assert_near(_np(out.y), a, err, bf16, "a")
+    ref.assert_mx(out.codes.cpu().numpy(), _scales(out.scales, tiled, rows, F), a, err + ref.TINY_F32, fmt, "MX(a)")
+    codes, scales = oracle_mod.quantize(1, gu.float().cpu().numpy(), oracle_mod.IN_F32)
+    assert (out.kept_codes.cpu().numpy() == codes).all() and (out.kept_scales.cpu().numpy() == scales).all()
+    sc = np.exp2(scales.astype(np.float64) - 127)
+    kept64 = ref.decode_codes(codes, 1) * np.repeat(sc, 32, axis=1)
+    for src, v64 in ((dict(kept_codes=out.kept_codes, kept_scales=out.kept_scales), kept64),
+                     (dict(gate=gu[:, :F], up=gu[:, F:]), gu64)):
+        back = b.glu_backward(dy, ref.ACT_SILU, fmt=fmt, tiled=tiled, recompute=True, **src)
+        dg, edg, du, edu = ref.glu_backward(dy64, v64[:, :F], v64[:, F:], ref.ACT_SILU)
+        ref.assert_near(_np(back.dgu)[:, :F], dg, edg, bf16, "dgate")
+        ref.assert_near(_np(back.dgu)[:, F:], du, edu, bf16, "dup")
+        a, ea = ref.glu(v64[:, :F], v64[:, F:], ref.ACT_SILU)
+        ref.assert_near(_np(back.a), a, ea, bf16, "a again")
+        both, e = np.concatenate([dg, du], 1), np.concatenate([edg, edu], 1) + ref.TINY_F32
+        ref.assert_mx(back.codes.cpu().numpy(), _scales(back.scales, tiled, rows, 2 * F), both, e, fmt, "MX(dgu)")

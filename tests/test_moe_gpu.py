@@ -319,3 +319,69 @@ def test_weight_gradient_over_the_weights():
         want = b.moe_combine_backward(dout, y, slot, w)
         got = b.moe_combine_backward(dout, y, slot, w, dweights=w)
         assert got[1] is w and torch.equal(w, want[1]) and torch.equal(got[0], want[0])
+
+
+# Calls with more units than sixteen warps a multiprocessor take other kernels, or several slots a warp.
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [1, 2, 3])
+@pytest.mark.parametrize("T,k,K", [(5000, 2, 672), (3001, 3, 1056), (2500, 1, 1536), (2600, 5, 96)])
+def test_dispatch_of_many_tokens(oracle_mod, dtype, fmt, T, k, K):
+    import torch
+    b = lib()
+    rng = np.random.default_rng([T, k, K, fmt])
+    ids = _ids(rng, T, k, 16, drop=0.1)
+    x, _ = _make(rng, (T, K), _dtype(dtype))
+    x[3, 40] = float("nan")
+    x[T - 1, K - 1] = float("inf")
+    offsets, slot, src = ref.moe_sort(ids, 16)
+    pad = 64
+    width = K if fmt == 1 else K // 2 if fmt == 2 else K
+    buf = torch.full((T * k * width + 2 * pad,), 0x25, dtype=torch.bfloat16 if fmt == 3 else torch.uint8, device="cuda")
+    rows, scales = b.moe_dispatch(x, _dev(slot.astype(np.int32)), fmt, rows=buf[pad:-pad].view(T * k, width))
+    live = (np.arange(T * k) < offsets[-1])[:, None]
+    assert (buf[:pad] == 0x25).all() and (buf[-pad:] == 0x25).all()
+    if fmt == 3:
+        want = torch.where(_dev(live), x.to(torch.bfloat16)[_dev(src // k)],
+                           torch.zeros((), dtype=torch.bfloat16, device="cuda"))
+        assert torch.equal(rows.view(torch.int16), want.view(torch.int16))
+        return
+    codes, sc = oracle_mod.quantize(fmt, x.float().cpu().numpy(), oracle_mod.IN_F32)
+    assert (rows.cpu().numpy() == np.where(live, codes[src // k], 0)).all()
+    assert (scales.cpu().numpy() == np.where(live, sc[src // k], 127)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weighted,add", [(True, True), (False, False), (True, False)])
+@pytest.mark.parametrize("T,k,N", [(1301, 3, 1056), (2600, 1, 96), (2433, 2, 512), (1500, 5, 672), (1220, 8, 640)])
+def test_combine_of_many_tokens(dtype, weighted, add, T, k, N):
+    b = lib()
+    rng = np.random.default_rng([T, k, N])
+    dt = _dtype(dtype)
+    offsets, slot, _ = ref.moe_sort(_ids(rng, T, k, 16, drop=0.15), 16)
+    y, y64 = _make(rng, (T * k, N), dt)
+    y[offsets[-1]:] = float("nan")
+    w = rng.random((T, k)).astype(np.float32)
+    w[(slot < 0).reshape(T, k)] = np.nan
+    r, r64 = _make(rng, (T, N), dt) if add else (None, None)
+    out = b.moe_combine(y, _dev(slot.astype(np.int32)), k, weights=_dev(w) if weighted else None, add=r)
+    want, err = ref.moe_combine(y64, slot, k, w.astype(np.float64) if weighted else None, r64)
+    ref.assert_near(_np(out), want, err, dtype == "bf16", "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,k,N", [(7001, 3, 96), (5000, 8, 544), (20001, 1, 512), (10000, 2, 640)])
+def test_combine_backward_of_many_slots(dtype, T, k, N):
+    b = lib()
+    rng = np.random.default_rng([T, k, N, 1])
+    dt = _dtype(dtype)
+    offsets, slot, _ = ref.moe_sort(_ids(rng, T, k, 16, drop=0.1), 16)
+    y, y64 = _make(rng, (T * k, N), dt)
+    y[offsets[-1]:] = float("nan")
+    dout, dout64 = _make(rng, (T, N), dt)
+    w = rng.random((T, k)).astype(np.float32)
+    w[(slot < 0).reshape(T, k)] = np.nan
+    dy, dw = b.moe_combine_backward(dout, y, _dev(slot.astype(np.int32)), _dev(w))
+    wdy, wdw, err = ref.moe_combine_backward(dout64, y64, slot, w.astype(np.float64))
+    ref.assert_near(_np(dy), wdy, ref.U * np.abs(wdy), dtype == "bf16", "dy")
+    ref.assert_near(_np(dw).reshape(-1), wdw, err, False, "dweights")

@@ -344,3 +344,40 @@ def test_backward_of_extreme_rows(dtype, rows, K, dh):
     want, err, wdw, size = ref.rmsnorm_backward(dy64, h64, _np(rstd), w64, g64)
     ref.assert_near(_np(dx), want, err, dtype == "bf16", "dx")
     ref.assert_near(_np(dw), wdw, (rows + 64) * ref.U * size, False, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,dh", [
+    (8001, 96, True), (8001, 96, False), (7999, 512, True), (7999, 512, False), (9001, 544, True), (4000, 992, False),
+    (5000, 2080, True), (3001, 4096, True), (1500, 8192, False), (700, 8224, True), (311, 16384, False), (320, 32768, True),
+])
+def test_backward_of_many_rows(dtype, rows, K, dh):
+    """Several rows to every block: the ring past its depth, rows side by side, the last rows of some blocks missing."""
+    import torch
+    b = lib()
+    rng = np.random.default_rng([rows, K, 11])
+    dt = _dtype(dtype)
+    h, h64 = _make(rng, (rows, K), dt, 2.0)
+    dy, dy64 = _make(rng, (rows, K), dt)
+    g, g64 = _make(rng, (rows, K), dt) if dh else (None, None)
+    w, w64 = _make(rng, (K,), dt)
+    rstd = torch.from_numpy((1 / np.sqrt((h64 * h64).mean(1) + EPS)).astype(np.float32)).cuda()
+    dx, dw = b.rmsnorm_backward(dy, h, rstd, w, dh=g)
+    want, err, wdw, size = ref.rmsnorm_backward(dy64, h64, _np(rstd), w64, g64)
+    ref.assert_near(_np(dx), want, err, dtype == "bf16", "dx")
+    ref.assert_near(_np(dw), wdw, (rows + 64) * ref.U * size, False, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,residual", [(5001, 96, True), (4500, 544, False), (4100, 1024, True), (3000, 2016, False)])
+def test_forward_of_many_rows(dtype, rows, K, residual):
+    b = lib()
+    rng = np.random.default_rng([rows, K])
+    dt = _dtype(dtype)
+    x, x64 = _make(rng, (rows, K), dt, 3.0)
+    r, r64 = _make(rng, (rows, K), dt) if residual else (None, None)
+    w, w64 = _make(rng, (K,), dt)
+    want = ref.rmsnorm(x64, w64, EPS, r64)
+    for fmt in (1, 2):
+        out = b.rmsnorm(x, w, EPS, residual=r, fmt=fmt, tiled=K % 128 == 0, plain=True)
+        _check_forward(b, out, want, fmt, K % 128 == 0, dtype == "bf16", residual, True)
