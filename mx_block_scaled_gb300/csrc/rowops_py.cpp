@@ -243,6 +243,21 @@ int64_t integer(PyObject *o)
     return v;
 }
 
+// A format or an activation; numbers past an int are as unknown to the library as -1.
+int code(PyObject *o)
+{
+    const int64_t v = integer(o);
+    return v == static_cast<int>(v) ? static_cast<int>(v) : -1;
+}
+
+bool truth(PyObject *o)
+{
+    const int t = PyObject_IsTrue(o);
+    if (t < 0)
+        throw python_error();
+    return t != 0;
+}
+
 // The outputs of call(), an entry point of the library: it runs without the
 // interpreter's lock, since a launch waits while the stream's queue is full.
 template <typename F, typename... O>
@@ -278,8 +293,8 @@ PyObject *rmsnorm(Args a)
     if (eps == -1.0 && PyErr_Occurred())
         throw python_error();
     const Rows r = in_rows(a[3], s, s.rows, s.cols, "residual");
-    const int fmt = static_cast<int>(integer(a[4]));
-    const bool tiled = PyObject_IsTrue(a[5]) == 1, plain = PyObject_IsTrue(a[6]) == 1;
+    const int fmt = code(a[4]);
+    const bool tiled = truth(a[5]), plain = truth(a[6]);
     Out h, y, codes, scales, rstd;
     output(h, a[7], r.ptr != nullptr, {s.rows, s.cols}, s.dtype, s, "h");
     output(y, a[8], plain, {s.rows, s.cols}, s.dtype, s, "y");
@@ -329,9 +344,9 @@ PyObject *glu(Args a)
     if (!up.ptr)
         throw BadTensor("up is missing");
     check_strides(s, s.stride, up.stride);
-    const int act = static_cast<int>(integer(a[2])), fmt = static_cast<int>(integer(a[3]));
-    const bool tiled = PyObject_IsTrue(a[4]) == 1, plain = PyObject_IsTrue(a[5]) == 1;
-    const bool keep = PyObject_IsTrue(a[6]) == 1 || a[10] != Py_None || a[11] != Py_None;
+    const int act = code(a[2]), fmt = code(a[3]);
+    const bool tiled = truth(a[4]), plain = truth(a[5]);
+    const bool keep = truth(a[6]) || a[10] != Py_None || a[11] != Py_None;
     Out y, codes, scales, kc, ks;
     output(y, a[7], plain, {s.rows, s.cols}, s.dtype, s, "y");
     mx_output(codes, scales, a[8], a[9], fmt, tiled, s.rows, s.cols, s, "glu");
@@ -348,11 +363,10 @@ PyObject *glu(Args a)
 PyObject *glu_backward(Args a)
 {
     const Sizes s = matrix(a[0], "dy");
-    const int act = static_cast<int>(integer(a[1])), fmt = static_cast<int>(integer(a[6]));
+    const int act = code(a[1]), fmt = code(a[6]);
     const Rows gate = in_rows(a[2], s, s.rows, s.cols, "gate"), up = in_rows(a[3], s, s.rows, s.cols, "up");
     check_strides(s, gate.stride, up.stride);
-    const bool tiled = PyObject_IsTrue(a[7]) == 1, plain = PyObject_IsTrue(a[8]) == 1,
-               recompute = PyObject_IsTrue(a[9]) == 1;
+    const bool tiled = truth(a[7]), plain = truth(a[8]), recompute = truth(a[9]);
     Out kc, ks, dgu, codes, scales, again;
     output(kc, a[4], false, {s.rows, 2 * s.cols}, at::kByte, s, "kept_codes");
     output(ks, a[5], false, {s.rows, s.cols / 16}, at::kByte, s, "kept_scales");
@@ -411,7 +425,7 @@ PyObject *moe_dispatch(Args a)
     const Sizes s = matrix(a[0], "x");
     const int32_t *table = nullptr;
     const int64_t topk = slots_of(a[1], s.rows, s, &table), n = topk * s.rows;
-    const int fmt = static_cast<int>(integer(a[2]));
+    const int fmt = code(a[2]);
     Out rows, scales;
     if (fmt == MXGEMM_FMT_BF16) {
         output(rows, a[3], true, {n, s.cols}, at::kBFloat16, s, "rows");

@@ -265,3 +265,22 @@ def test_many_rows(oracle_mod, dtype, fmt, tiled, rows, F):
         ref.assert_near(_np(back.a), a, ea, bf16, "a again")
         both, e = np.concatenate([dg, du], 1), np.concatenate([edg, edu], 1) + ref.TINY_F32
         ref.assert_mx(back.codes.cpu().numpy(), _scales(back.scales, tiled, rows, 2 * F), both, e, fmt, "MX(dgu)")
+
+
+def test_flags_and_numbers_that_are_none():
+    """A flag without a truth value raises its own error; a format past 32 bits is no format."""
+    import torch
+    b = lib()
+    x, w = torch.ones((4, 64), device="cuda"), torch.ones(64, device="cuda")
+    both = torch.tensor([True, False])
+    for call in (lambda: b.glu(x, x, ref.ACT_SILU, plain=both), lambda: b.glu(x, x, ref.ACT_SILU, fmt=1, tiled=both),
+                 lambda: b.glu(x, x, ref.ACT_SILU, keep=both), lambda: b.rmsnorm(x, w, 1e-5, plain=both),
+                 lambda: b.glu_backward(x, ref.ACT_SILU, gate=x, up=x, recompute=both)):
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            call()
+    for call in (lambda: b.glu(x, x, ref.ACT_SILU, fmt=(1 << 32) + 1), lambda: b.glu(x, x, (1 << 32) + 1, plain=True),
+                 lambda: b.rmsnorm(x, w, 1e-5, fmt=(1 << 32) + 1),
+                 lambda: b.moe_dispatch(x, torch.arange(4, dtype=torch.int32, device="cuda"), (1 << 32) + 3)):
+        with pytest.raises(b.MxGemmError) as e:
+            call()
+        assert e.value.status == b.MXGEMM_ERR_ARG
