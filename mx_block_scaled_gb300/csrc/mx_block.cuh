@@ -373,17 +373,17 @@ __device__ __forceinline__ void f2_unpack(const F2 (&p)[kLaneVals / 2], float (&
         f2_split(p[i], v[2 * i], v[2 * i + 1]);
 }
 
-// A warp's walk over chunks of a matrix's rows (512 values, or `len`), every
-// `step`-th chunk from `first` on: one division at the start, additions from then on.
+// A warp's walk over the 512-value chunks of a matrix's rows, every `step`-th chunk
+// from `first` on: one division at the start, additions from then on.
 struct ChunkWalk {
     int64_t row;
     int chunk, per_row;
     int64_t row_step;
     int chunk_step;
 
-    __device__ __forceinline__ ChunkWalk(int64_t row_len, int64_t first, int64_t step, int64_t len = kWarpVals)
+    __device__ __forceinline__ ChunkWalk(int64_t row_len, int64_t first, int64_t step)
     {
-        per_row = static_cast<int>((row_len + len - 1) / len);
+        per_row = static_cast<int>((row_len + kWarpVals - 1) / kWarpVals);
         row = first / per_row;
         chunk = static_cast<int>(first - row * per_row);
         row_step = step / per_row;

@@ -716,10 +716,15 @@ cudaError_t launch_backward(const NormBackParams &p, int num_sms, cudaStream_t s
     }
     if (p.K <= kRingMaxK) {
         const int64_t row = static_cast<int64_t>(p.dh ? 3 : 2) * sides * sh.threads * kLaneVals * ElemBytes<IN>::value;
-        const int64_t depth = kRingBytes / per_sm / row;
-        e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, sides, blocks, 4 * row, s)
-            : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, sides, blocks, 3 * row, s)
-                         : launch_ring<IN, WT, 2>(p, sh.threads, sides, blocks, 2 * row, s);
+        // an SM's blocks have at most 512 threads: their stages take at most 48 KB in BF16, 96 in FP32
+        if constexpr (IN == kBf16) {
+            e = launch_ring<IN, WT, 4>(p, sh.threads, sides, blocks, 4 * row, s);
+        } else {
+            const int64_t depth = kRingBytes / per_sm / row;
+            e = depth >= 4   ? launch_ring<IN, WT, 4>(p, sh.threads, sides, blocks, 4 * row, s)
+                : depth == 3 ? launch_ring<IN, WT, 3>(p, sh.threads, sides, blocks, 3 * row, s)
+                             : launch_ring<IN, WT, 2>(p, sh.threads, sides, blocks, 2 * row, s);
+        }
     } else {
         const size_t smem = (p.K + kWideVals - 1) / kWideVals * kWideVals * sizeof(float);
         const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kWideThreads, smem, s, attr);
@@ -736,15 +741,16 @@ template <int IN, int WT>
 cudaError_t prepare_backward()
 {
     constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaSuccess;
-    for (const auto ring :
-         {rmsnorm_backward_ring_kernel<IN, WT, 2, false>, rmsnorm_backward_ring_kernel<IN, WT, 3, false>,
-          rmsnorm_backward_ring_kernel<IN, WT, 4, false>})
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(ring, kAttr, kRingBytes);
-    if constexpr (IN == kBf16)  // a block's share of the ring always holds four rows of at most 1024 values
+    cudaError_t e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 4, false>, kAttr, kRingBytes);
+    if constexpr (IN == kBf16) {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 4, true>, kAttr, kRingBytes);
+    } else {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 3, false>, kAttr, kRingBytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<IN, WT, 2, false>, kAttr, kRingBytes);
+    }
     return e == cudaSuccess ? cudaFuncSetAttribute(rmsnorm_backward_wide_kernel<IN, WT>, kAttr,
                                                    static_cast<int>(kNormMaxK * sizeof(float)))
                             : e;
@@ -770,9 +776,8 @@ int64_t norm_back_blocks(int64_t rows, int64_t K)
     return rows < most ? rows : most;
 }
 
-cudaError_t launch_rmsnorm(const NormParams &p, int in_dtype, int weight_dtype, int num_sms, cudaStream_t s)
+cudaError_t launch_rmsnorm(const NormParams &p, int in_dtype, int weight_dtype, cudaStream_t s)
 {
-    (void)num_sms;
     if (in_dtype == kBf16)
         return weight_dtype == kBf16 ? launch_forward_fmt<kBf16, kBf16>(p, s) : launch_forward_fmt<kBf16, kF32>(p, s);
     return weight_dtype == kBf16 ? launch_forward_fmt<kF32, kBf16>(p, s) : launch_forward_fmt<kF32, kF32>(p, s);

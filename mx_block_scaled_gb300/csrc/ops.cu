@@ -197,7 +197,7 @@ int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, const void *re
     p.y = static_cast<char *>(y);
     p.rstd = rstd;
     p.mx = make_mx(fmt, codes, scales, flags, K);
-    return status_of(mxg::launch_rmsnorm(p, in_dtype, weight_dtype, sms, static_cast<cudaStream_t>(stream)));
+    return status_of(mxg::launch_rmsnorm(p, in_dtype, weight_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mxgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t K)

@@ -47,7 +47,7 @@ struct NormParams {
     MxOut mx;
 };
 constexpr int64_t kNormMaxK = 32768;
-cudaError_t launch_rmsnorm(const NormParams &p, int in_dtype, int weight_dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_rmsnorm(const NormParams &p, int in_dtype, int weight_dtype, cudaStream_t s);
 
 struct NormBackParams {
     const char *dy, *h, *dh;                       // dh may be NULL
