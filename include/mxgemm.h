@@ -464,7 +464,7 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  *    multiple of 128), in the tile layout of mxgemm_relayout_scales with
  *    mxgemm_sf_bytes(rows, K) bytes.
  *  - Stream-ordered, no allocation, no host synchronisation; every result is the
- *    same from run to run (no atomics).
+ *    same from run to run (no floating-point atomics).
  *  - Errors: MXGEMM_ERR_ARG (a missing pointer, an unknown type, format, flag or
  *    activation, nothing to write), MXGEMM_ERR_SHAPE, MXGEMM_ERR_ALIGN,
  *    MXGEMM_ERR_UNSUPPORTED, MXGEMM_ERR_WORKSPACE, MXGEMM_ERR_ARCH,

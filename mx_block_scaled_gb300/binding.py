@@ -419,6 +419,13 @@ def quantize(x, fmt: int, tiled: bool = False, codes=None, scales=None, stream=N
 # stream, or on `stream=`.  Tensors are checked and their addresses read in the
 # native module _rowops (csrc/rowops_py.cpp): ValueError for one that does not fit,
 # MxGemmError for a call that the library refuses.
+#
+# None of these is part of autograd, like the rest of this module: a tensor that
+# requires a gradient is read as it is, the result has no graph, and an output that is
+# written in place does not count as a change to a saved tensor.  A program calls the
+# `_backward` functions itself (in a torch.autograd.Function, or as examples/moe_block.py
+# does).  With `stream=` the tensors' order and life on that stream are the caller's, as
+# under torch.cuda.stream.
 
 class RmsNorm(NamedTuple):
     h: object

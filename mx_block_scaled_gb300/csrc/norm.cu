@@ -12,8 +12,8 @@
 // and scales from them, in FP32 until the final rounding; blocks on the same SM
 // cover each other's reductions: 16384 x 8192 BF16 with residual and tiled MXFP8
 // (944 MB) 135 us, 7.0 TB/s.  The backward also sums over rows, so its blocks stay
-// and hide the reduction in a pipeline instead: 16384 x 8192 BF16 (1074 MB) 174 us,
-// 6.2 TB/s, 8192 x 4096 (268 MB) 50 us, of which 4 are the second launch.
+// and hide the reduction in a pipeline instead: 16384 x 8192 BF16 (1074 MB) 175 us,
+// 6.1 TB/s, 8192 x 4096 (268 MB) 51 us, of which 4 are the second launch.
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -500,10 +500,12 @@ __global__ void __launch_bounds__(32 * kSlices)
 // columns' products over all rows (two neighbouring columns a lane in BF16, one in
 // FP32, the rows dealt to the warps), the others take a row each; dy and h are read
 // twice, the second time from L2, and there is neither a second launch nor partial
-// sums to wait for: 64 x 4096 BF16 2.6 us against 5.6 with the ring, 301 x 4096 FP32
-// 6.9 against 9.7, 1024 BF16 rows of 1024 to 8192 values 7.1-14.9 against 8.8-18.6;
-// from 2048 rows on the columns' blocks are too long (2048 x 1024: 15.3 against 11.5).
-// Two blocks an SM (64 registers): with one, 301 x 5120 FP32 takes 12.3 us instead of 7.8.
+// sums to wait for (all with dh): 64 x 4096 BF16 2.6 us against 5.6 with the ring, 301 x
+// 4096 FP32 6.5 against 9.7, 1024 BF16 rows of 1024 to 8192 values 6.9-15.0 against
+// 7.4-18.4; from 2048 rows on the columns' blocks are too long (2048 x 1024: 15.2 against
+// 10.1).  Two blocks an SM (64 registers): with one, 301 x 5120 FP32 takes 11.8 us instead
+// of 7.6.  What binds it is the number of blocks that fit at once, 304 of those 461: all
+// have 512 threads, of which a row of 5120 values uses 320.
 constexpr int64_t kFewRows = 1024;
 
 template <int IN, int WT>

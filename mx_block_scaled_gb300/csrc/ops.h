@@ -12,7 +12,9 @@ namespace mxg {
 
 // Launch configuration of the row operators: programmatic stream serialization,
 // so a kernel's CTAs may become resident while the preceding kernel drains; each
-// kernel waits for it (griddepcontrol.wait) before its first access to memory.
+// kernel waits for it (griddepcontrol.wait) before its first access to memory.  One
+// exception: the expert sort reads its ids before it waits for its own counting kernel,
+// which lets it start only after a wait of its own.
 inline cudaLaunchConfig_t row_launch(unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
                                      cudaLaunchAttribute (&attr)[1])
 {
