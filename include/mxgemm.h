@@ -479,6 +479,8 @@ MXGEMM_API int mxgemm_grouped_run(mxgemm_grouped_plan_t plan, const int64_t *gro
  *             or residual itself.  y is computed from the unrounded h.
  *   codes, scales: MX(y), see above.    rstd: [rows] FP32, or NULL.
  * K up to 32768 (MXGEMM_ERR_UNSUPPORTED beyond: a row is held on chip).
+ * The sum of squares is FP32 and unscaled: where it passes FP32's range (a root mean
+ * square above 1.8e19 / sqrt(K)) rstd is 0, and with eps 0 it is infinite below 1e-23.
  */
 MXGEMM_API int mxgemm_rmsnorm(int in_dtype, const void *x, int64_t x_stride, const void *residual,
                               int64_t residual_stride, const void *weight, int weight_dtype, float eps, int64_t rows,
