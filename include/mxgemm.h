@@ -599,6 +599,149 @@ MXGEMM_API int mxgemm_moe_combine_backward(int in_dtype, const void *dout, int64
                                            float *dweights, void *stream);
 
 /*
+ * Row operators at a model's ends and between its products: rows of the embedding
+ * table and their gradient, the norm and rotation of query and key heads, log
+ * probabilities from logits, and the norm and clipping of all gradients.  What is
+ * said above of the row operators (types, strides, alignment, overlap, errors, no
+ * allocation, the same result in every run) holds for them too, unless a call says
+ * otherwise.  Ids, positions and targets are int32 or int64 (id_bytes 4 or 8).
+ */
+
+/*
+ * Embedding:  out[t] = scale * table[ids[t]]
+ *   table: [vocab, K] of type in_dtype.   ids: [tokens].
+ *   out:   [tokens, K] of type out_dtype.
+ * An id outside 0..vocab-1 (padding) gives a row of zeros.
+ */
+MXGEMM_API int mxgemm_embed(int in_dtype, const void *table, int64_t table_stride, int64_t vocab, int64_t K,
+                            const void *ids, int id_bytes, int64_t tokens, float scale, int out_dtype, void *out,
+                            void *stream);
+
+/*
+ * Its gradient:  dtable[v] = add[v] + scale * (sum over t with ids[t] = v of dy[t])
+ *   dy:     [tokens, K] of type in_dtype.   dtable: [vocab, K] of type out_dtype.
+ *   add:    [vocab, K] of type out_dtype (the gradient so far), or NULL for zeros.
+ *           dtable may be add itself: rows whose id does not occur are then neither
+ *           read nor written.
+ * Sums are FP32, of an id's rows in the order of its tokens (in parts of 32 sorted
+ * rows), rounded once.  Ids outside the table add nothing, whatever their rows of dy
+ * hold.  workspace: mxgemm_embed_backward_workspace_bytes(tokens, vocab, K) bytes (0
+ * for sizes that the call refuses), 32-byte aligned, holding nothing between calls:
+ * 16 bytes a token, a bit an id, and for more than 32 tokens 8 K bytes for every 32.
+ * vocab below 2^30.
+ */
+MXGEMM_API size_t mxgemm_embed_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t K);
+MXGEMM_API int mxgemm_embed_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *ids, int id_bytes,
+                                     int64_t tokens, int64_t vocab, int64_t K, float scale, const void *add,
+                                     int out_dtype, void *dtable, void *workspace, size_t ws_bytes, void *stream);
+
+#define MXGEMM_ROPE_INTERLEAVED (1u << 0) /* pairs are values 2i, 2i+1; else i, i + rotary/2 */
+
+/*
+ * RMS norm of every query and key head, and the rotation of its position:
+ *   n = x * rstd * weight, rstd = 1/sqrt(mean(x^2) + eps) over a head's D values;
+ *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin) for the pairs (a, b) of the
+ *   first `rotary` values, pair i by angle i of the token's position; the rest as it is.
+ *   x, y:   [tokens, q_heads + k_heads, D], queries first, D values contiguous, with
+ *           the elements from token to token and from head to head (the heads inside a
+ *           q|k|v product's rows, or [heads, tokens, D]).  y may be x itself, with
+ *           x's strides.
+ *   q_weight, k_weight: [D] of type weight_dtype; both NULL for no norm (rotation
+ *           alone); one may be missing where there are no such heads.
+ *   rope:   [rope_rows, rotary] FP32, row p the cosines and then the sines of position
+ *           p's rotary/2 angles; NULL, with positions NULL, for no rotation.
+ *   positions: [tokens].  A token whose position is outside the table (padding) gets
+ *           heads of zeros and rstd 0, whatever x holds.
+ *   rstd:   [tokens, heads] FP32 for the gradient, or NULL.
+ * D and rotary are multiples of 16, D up to 512 (MXGEMM_ERR_UNSUPPORTED beyond).  The
+ * sum of squares is FP32, as in mxgemm_rmsnorm.
+ */
+MXGEMM_API int mxgemm_qk_norm_rope(int in_dtype, const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                                   int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t D, const void *q_weight,
+                                   const void *k_weight, int weight_dtype, float eps, const float *rope,
+                                   int64_t rope_rows, int64_t rotary, const void *positions, int position_bytes,
+                                   uint32_t flags, void *y, int64_t y_token_stride, int64_t y_head_stride, float *rstd,
+                                   void *stream);
+
+/*
+ * Its gradient, with x and rstd as the forward had and left them:
+ *   g = dy rotated back;  dx = rstd * (g * weight - n * mean(g * weight * n)), n = x * rstd
+ *   dq_weight, dk_weight: sums of g * n over all query and all key heads (FP32, [D]),
+ *   either may be NULL.
+ * dx may be dy or x itself, with its strides.  Without weights x is not read (NULL, as
+ * rstd and the weights' gradients) and dx is dy rotated back.  Tokens whose position is
+ * outside the table have a gradient of zero and add nothing to the weights'.
+ * workspace: mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, D) bytes (none
+ * without weights), 32-byte aligned, holding nothing between calls.
+ */
+MXGEMM_API size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t D);
+MXGEMM_API int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_stride,
+                                            int64_t dy_head_stride, const void *x, int64_t x_token_stride,
+                                            int64_t x_head_stride, const float *rstd, int64_t tokens, int64_t q_heads,
+                                            int64_t k_heads, int64_t D, const void *q_weight, const void *k_weight,
+                                            int weight_dtype, const float *rope, int64_t rope_rows, int64_t rotary,
+                                            const void *positions, int position_bytes, uint32_t flags, void *dx,
+                                            int64_t dx_token_stride, int64_t dx_head_stride, float *dq_weight,
+                                            float *dk_weight, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Log probabilities of the tokens of softmax(scale * logits), row by row:
+ *   logprob[r]  = that of targets[r] (0 for a target outside 0..V-1); targets and
+ *                 logprob are both given or both NULL
+ *   entropy[r]  = -sum p ln p, or NULL
+ *   stats[r]    = (m, l), m the largest logit and l = ln sum exp(scale (x - m)), so that
+ *                 ln p_v = scale (x_v - m) - l; for the gradient, or NULL
+ *   top_ids, top_logprobs: [rows, top], the `top` (0..32) largest logits' ids (int64) and
+ *                 log probabilities, largest first, equal ones by id.
+ *   logits: [rows, V], any V and any stride of at least V elements, rows aligned to
+ *           their type only.   scale: above 0 (1 / temperature).
+ * A logit of -infinity has probability 0: its log probability is -infinity, it adds
+ * nothing to the entropy, and it is not among the top ones; where fewer than `top` are
+ * left, the others are id -1 and -infinity.  A row without another value has log
+ * probability -infinity for every target, entropy 0 and stats (-infinity, 0).  A NaN or
+ * +infinity in a row makes its sums NaN.
+ */
+MXGEMM_API int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride, int64_t rows, int64_t V, float scale,
+                               const void *targets, int id_bytes, float *logprob, float *entropy, float *stats,
+                               int64_t top, int64_t *top_ids, float *top_logprobs, void *stream);
+
+/*
+ * The logits' gradient from those of logprob and of entropy:
+ *   dlogits_v = scale * (dlogprob * ([v = target] - p_v) - dentropy * p_v * (ln p_v + entropy))
+ *   stats and entropy as the forward left them; targets and dlogprob are both given or
+ *   both NULL, and so is entropy where dentropy is (NULL: 0).
+ *   dlogits: [rows, V] dense, of type in_dtype; may be logits itself.
+ * A target outside 0..V-1 leaves only the entropy's part; a row without a value above
+ * -infinity has a gradient of zero.
+ */
+MXGEMM_API int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, int64_t rows, int64_t V,
+                                        float scale, const void *targets, int id_bytes, const float *stats,
+                                        const float *dlogprob, const float *entropy, const float *dentropy,
+                                        void *dlogits, void *stream);
+
+/*
+ * The norm of n gradients together, and the gradients clipped to it:
+ *   norm = sqrt(sum of g^2 over all of them);  out = g * min(1, max_norm / (norm + 1e-6))
+ *   grads, sizes, dtypes: host arrays of n device pointers, numbers of elements (0 and
+ *       a NULL pointer are allowed) and types; tensors are dense, aligned to their type.
+ *   out, out_dtypes: host arrays of where to, which may be the gradient itself, and of
+ *       which type; both NULL: all in place (written only where the factor is not 1).
+ *   norm: device, one FP32 value.
+ * The sum is kept in FP64 and takes squares outside FP32's range; a norm of NaN makes
+ * every output NaN, one of infinity zeros (NaN where the gradient is not finite).
+ * An output touches no other output and no other tensor's input: a tensor that is given
+ * twice can be summed, but not clipped in place.
+ * workspace: mxgemm_grad_workspace_bytes(n) bytes, 16-byte aligned, holding nothing
+ * between calls.  n 0 .. 2^20: the host arrays are read before the call returns.
+ */
+MXGEMM_API size_t mxgemm_grad_workspace_bytes(int64_t n);
+MXGEMM_API int mxgemm_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int *dtypes,
+                                float *norm, void *workspace, size_t ws_bytes, void *stream);
+MXGEMM_API int mxgemm_clip_grads(int64_t n, const void *const *grads, const int64_t *sizes, const int *dtypes,
+                                 void *const *out, const int *out_dtypes, float max_norm, float *norm,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Scale-placement checker for MXFP4 dot products ("Deciding Scale Placement in
  * MXFP4 Dot Products with Integer Arithmetic", AI-compiler daily digest of
  * 2026-10-22, item 2): for each scale pair (sa[p], sb[p]) (E8M0 codes 0..254)

@@ -57,6 +57,7 @@ MXGEMM_IN_BF16 = 2
 MXGEMM_QUANT_SF_TILED = 1 << 0
 MXGEMM_ACT_SILU = 1
 MXGEMM_ACT_GELU_TANH = 2
+MXGEMM_ROPE_INTERLEAVED = 1 << 0
 
 # (name, restype, argtypes) for every entry point declared in include/mxgemm.h
 _P = ctypes.c_void_p
@@ -100,6 +101,25 @@ SIGNATURES = [
     ("mxgemm_moe_combine", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
     ("mxgemm_moe_combine_backward", ctypes.c_int,
      [_I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    ("mxgemm_embed", ctypes.c_int, [_I, _P, _I64, _I64, _I64, _P, _I, _I64, ctypes.c_float, _I, _P, _P]),
+    ("mxgemm_embed_backward_workspace_bytes", ctypes.c_size_t, [_I64, _I64, _I64]),
+    ("mxgemm_embed_backward", ctypes.c_int,
+     [_I, _P, _I64, _P, _I, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, ctypes.c_size_t, _P]),
+    ("mxgemm_qk_norm_rope", ctypes.c_int,
+     [_I, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, ctypes.c_float, _P, _I64, _I64, _P, _I, ctypes.c_uint32,
+      _P, _I64, _I64, _P, _P]),
+    ("mxgemm_qk_norm_rope_backward_workspace_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("mxgemm_qk_norm_rope_backward", ctypes.c_int,
+     [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _I64, _I64, _P, _I,
+      ctypes.c_uint32, _P, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("mxgemm_logprobs", ctypes.c_int,
+     [_I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, _P, _I64, _P, _P, _P]),
+    ("mxgemm_logprobs_backward", ctypes.c_int,
+     [_I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P]),
+    ("mxgemm_grad_workspace_bytes", ctypes.c_size_t, [_I64]),
+    ("mxgemm_grad_norm", ctypes.c_int, [_I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("mxgemm_clip_grads", ctypes.c_int,
+     [_I64, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
     ("mxgemm_placement_scan", ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P]),
     ("mxgemm_probe_tensor_rate", ctypes.c_int,
      [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_double), _P]),
@@ -256,6 +276,50 @@ def mxgemm_moe_combine(*args) -> int:
 
 def mxgemm_moe_combine_backward(*args) -> int:
     return _lib.mxgemm_moe_combine_backward(*args)
+
+
+def mxgemm_embed(*args) -> int:
+    return _lib.mxgemm_embed(*args)
+
+
+def mxgemm_embed_backward_workspace_bytes(*args) -> int:
+    return _lib.mxgemm_embed_backward_workspace_bytes(*args)
+
+
+def mxgemm_embed_backward(*args) -> int:
+    return _lib.mxgemm_embed_backward(*args)
+
+
+def mxgemm_qk_norm_rope(*args) -> int:
+    return _lib.mxgemm_qk_norm_rope(*args)
+
+
+def mxgemm_qk_norm_rope_backward_workspace_bytes(*args) -> int:
+    return _lib.mxgemm_qk_norm_rope_backward_workspace_bytes(*args)
+
+
+def mxgemm_qk_norm_rope_backward(*args) -> int:
+    return _lib.mxgemm_qk_norm_rope_backward(*args)
+
+
+def mxgemm_logprobs(*args) -> int:
+    return _lib.mxgemm_logprobs(*args)
+
+
+def mxgemm_logprobs_backward(*args) -> int:
+    return _lib.mxgemm_logprobs_backward(*args)
+
+
+def mxgemm_grad_workspace_bytes(*args) -> int:
+    return _lib.mxgemm_grad_workspace_bytes(*args)
+
+
+def mxgemm_grad_norm(*args) -> int:
+    return _lib.mxgemm_grad_norm(*args)
+
+
+def mxgemm_clip_grads(*args) -> int:
+    return _lib.mxgemm_clip_grads(*args)
 
 
 def mxgemm_device_status(stream: int, reset: bool = True) -> int:
@@ -450,10 +514,26 @@ class GluGrad(NamedTuple):
     a: object
 
 
+class QkNormRope(NamedTuple):
+    y: object
+    rstd: object
+
+
+class LogProbs(NamedTuple):
+    logprob: object
+    entropy: object
+    stats: object
+    top_ids: object
+    top_logprobs: object
+
+
 # in the order of the native module's table
 _ROWOPS_ENTRIES = ("mxgemm_rmsnorm", "mxgemm_rmsnorm_backward_workspace_bytes", "mxgemm_rmsnorm_backward", "mxgemm_glu",
                    "mxgemm_glu_backward", "mxgemm_moe_sort_workspace_bytes", "mxgemm_moe_sort", "mxgemm_moe_dispatch",
-                   "mxgemm_moe_combine", "mxgemm_moe_combine_backward", "mxgemm_sf_bytes")
+                   "mxgemm_moe_combine", "mxgemm_moe_combine_backward", "mxgemm_sf_bytes", "mxgemm_embed",
+                   "mxgemm_embed_backward_workspace_bytes", "mxgemm_embed_backward", "mxgemm_qk_norm_rope",
+                   "mxgemm_qk_norm_rope_backward_workspace_bytes", "mxgemm_qk_norm_rope_backward", "mxgemm_logprobs",
+                   "mxgemm_logprobs_backward", "mxgemm_grad_workspace_bytes", "mxgemm_grad_norm", "mxgemm_clip_grads")
 
 
 class _Unloaded:
@@ -592,6 +672,105 @@ def moe_combine_backward(dout, y, row_of_slot, weights, dy=None, dweights=None):
     """
     return _done(_rowops.moe_combine_backward(dout, y, row_of_slot, weights, dy, dweights),
                  "mxgemm_moe_combine_backward")
+
+
+# ---- row operators at a model's ends and between its products --------------------
+
+@_on_stream
+def embed(ids, table, scale: float = 1.0, dtype=None, out=None):
+    """out[t] = scale * table[ids[t]]  ([ids.numel(), K]).
+
+    ``ids``: contiguous CUDA int32 or int64, any shape; ``table`` [vocab, K] float32
+    or bfloat16 (any row stride whose rows stay 32-byte aligned); ``dtype`` the output's (the
+    table's).  An id outside the table (padding) gives a row of zeros.
+    """
+    return _done(_rowops.embed(ids, table, scale, dtype, out), "mxgemm_embed")[0]
+
+
+@_on_stream
+def embed_backward(dy, ids, vocab: int, scale: float = 1.0, dtype=None, add=None, dtable=None, workspace=None):
+    """Gradient of :func:`embed`: dtable[v] = add[v] + scale * sum of dy[t] over ids[t] = v.
+
+    ``dtype`` (float32) is dtable's [vocab, K] and ``add``'s, the gradient so far.  With
+    ``dtable`` the same tensor as ``add`` only the rows whose id occurs are touched.
+    """
+    return _done(_rowops.embed_backward(dy, ids, vocab, scale, dtype, add, dtable, workspace),
+                 "mxgemm_embed_backward")[0]
+
+
+@_on_stream
+def qk_norm_rope(x, q_heads: int, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None, positions=None,
+                 interleaved: bool = False, y=None, rstd=None) -> QkNormRope:
+    """RMS norm of every head of ``x`` [tokens, heads, D], then the rotation of its position.
+
+    The first ``q_heads`` heads are queries (``q_weight`` [D]), the others keys
+    (``k_weight``); without weights heads are only rotated.  ``rope`` [positions, rotary]
+    float32: the cosines, then the sines, of every position's rotary/2 angles; ``positions``
+    [tokens] int32 or int64, or neither for no rotation.  Pairs are values i and
+    i + rotary/2, or 2i and 2i + 1 with ``interleaved``.  ``x`` may be a view into a
+    product's q|k|v rows or of [heads, tokens, D]; ``y`` may be any such tensor, x itself too.
+    ``rstd`` [tokens, heads] is made where there are weights.
+    """
+    return tuple.__new__(QkNormRope, _done(_rowops.qk_norm_rope(x, q_heads, q_weight, k_weight, eps, rope, positions,
+                                                                interleaved, y, rstd), "mxgemm_qk_norm_rope"))
+
+
+@_on_stream
+def qk_norm_rope_backward(dy, x, rstd, q_heads: int, q_weight=None, k_weight=None, rope=None, positions=None,
+                          interleaved: bool = False, dx=None, dq_weight=None, dk_weight=None, workspace=None):
+    """Gradients of :func:`qk_norm_rope`: (dx, dq_weight, dk_weight), the weights' [D] float32.
+
+    ``x`` and ``rstd`` as the forward had and left them; without weights both are None, and
+    so are the weights' gradients.  ``dx`` may be ``dy`` or ``x`` itself.
+    """
+    return _done(_rowops.qk_norm_rope_backward(dy, x, rstd, q_heads, q_weight, k_weight, rope, positions, interleaved,
+                                               dx, dq_weight, dk_weight, workspace), "mxgemm_qk_norm_rope_backward")
+
+
+@_on_stream
+def logprobs(logits, targets=None, scale: float = 1.0, top: int = 0, logprob=None, entropy=False, stats=None,
+             top_ids=None, top_logprobs=None) -> LogProbs:
+    """Log probabilities under softmax(scale * logits), for ``logits`` [rows, V] float32 or bfloat16 (any row stride).
+
+    ``logprob`` [rows] of ``targets`` [rows] (0 for a target outside the vocabulary),
+    ``entropy`` [rows] (True, or a tensor to write), ``stats`` [rows, 2] for
+    :func:`logprobs_backward`, and the ``top`` (up to 32) most probable tokens' ids (int64)
+    and log probabilities, equal ones by id; -1 and -inf where fewer have a probability.
+    """
+    return tuple.__new__(LogProbs, _done(_rowops.logprobs(logits, targets, scale, top, logprob, entropy, stats,
+                                                          top_ids, top_logprobs), "mxgemm_logprobs"))
+
+
+@_on_stream
+def logprobs_backward(logits, targets, stats, dlogprob=None, entropy=None, dentropy=None, scale: float = 1.0,
+                      dlogits=None):
+    """Gradient of :func:`logprobs`: dlogits [rows, V], which may be ``logits`` itself.
+
+    From ``dlogprob`` [rows] with ``targets``, from ``dentropy`` [rows] with the forward's
+    ``entropy``, or from both.
+    """
+    return _done(_rowops.logprobs_backward(logits, targets, stats, dlogprob, entropy, dentropy, scale, dlogits),
+                 "mxgemm_logprobs_backward")[0]
+
+
+@_on_stream
+def grad_norm(grads, norm=None, workspace=None):
+    """sqrt of the sum of all squares of the tensors of a list: a [1] float32 tensor.
+
+    ``grads``: dense CUDA float32 or bfloat16 tensors of any shapes, mixed as they come.
+    """
+    return _done(_rowops.grad_norm(grads, norm, workspace), "mxgemm_grad_norm")[0]
+
+
+@_on_stream
+def clip_grads(grads, max_norm: float, out=None, norm=None, workspace=None):
+    """Gradients times min(1, max_norm / (norm + 1e-6)): (norm [1], out).
+
+    ``out``: a tensor of float32 or bfloat16 for every gradient, of its shape; without it the
+    gradients are clipped in place.
+    """
+    return (_done(_rowops.clip_grads(grads, max_norm, out, norm, workspace), "mxgemm_clip_grads")[0],
+            grads if out is None else out)
 
 
 def mxgemm_placement_scan(k: int, sa_ptr: int, sb_ptr: int, npairs: int, counts_ptr: int, first_ptr: int,

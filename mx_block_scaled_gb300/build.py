@@ -1,10 +1,11 @@
 """Build libmxgemm.so and libmxgemm_debug.so in-tree with nvcc for sm_103a.
 
-Eleven translation units (host API + relayout/reduce kernels, MXFP8 GEMM,
+Sixteen translation units (host API + relayout/reduce kernels, MXFP8 GEMM,
 MXFP4 GEMM, BF16 GEMM, MX quantiser, scale-placement checker, tensor-pipe
 probe, and the row operators: their host API, RMS norm, gated activation,
-expert routing) are compiled in parallel and linked into
-``mx_block_scaled_gb300/lib/libmxgemm.so``.  The four that hold the GEMM
+expert routing; the host API of those of a whole model, embedding, norm and
+rotation of heads, log probabilities, gradient clipping) are compiled in
+parallel and linked into ``mx_block_scaled_gb300/lib/libmxgemm.so``.  The four that hold the GEMM
 kernels and their host code are compiled a second time with MXGEMM_DEBUG
 (bounds-checked loads and stores, NaN-filled C, synchronous status) and linked
 with the others into ``lib/libmxgemm_debug.so``.  The Python module that
@@ -32,7 +33,7 @@ DEBUG_LIB_PATH = os.path.join(LIB_DIR, "libmxgemm_debug.so")
 ROWOPS_PATH = os.path.join(LIB_DIR, "_rowops.so")
 
 SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu", "quantize.cu", "placement.cu", "probe.cu",
-           "ops.cu", "norm.cu", "glu.cu", "moe.cu"]
+           "ops.cu", "norm.cu", "glu.cu", "moe.cu", "ops_model.cu", "embed.cu", "heads.cu", "logprobs.cu", "clip.cu"]
 MODULE_SOURCE = "rowops_py.cpp"
 DEBUG_SOURCES = ["mxgemm.cu", "gemm_fp8.cu", "gemm_fp4.cu", "gemm_bf16.cu"]  # the rest is shared
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

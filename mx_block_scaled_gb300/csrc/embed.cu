@@ -1,0 +1,510 @@
+// embed.cu -- embedding rows of token ids, and the table's gradient.
+//
+//   out[t] = scale * table[ids[t]]                            (zeros for an id outside the table)
+//   dtable[v] = add[v] + scale * sum over t with ids[t] = v of dy[t]
+//
+// The gradient is a sum of rows by key.  The ids are sorted (stable), so that the
+// rows of an id are neighbours in token order; a warp sums 512 columns of 32 sorted
+// rows in FP32 registers and writes every run that lies inside its 32 rows at once.
+// Runs that cross into the next 32 leave partial sums, which a last kernel adds in
+// order.  No atomics on values: the same sums in every run.
+#include "mx_block.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace mxg {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t t)
+{
+    return wide ? static_cast<const int64_t *>(ids)[t] : static_cast<const int32_t *>(ids)[t];
+}
+
+// ------------------------------------------------------------------- lookup --
+// A warp copies 512 values of a row, CHUNKS times.
+template <int IN, int OUT, int CHUNKS>
+__global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p)
+{
+    constexpr int E = ElemBytes<IN>::value;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const uint32_t per_row = static_cast<uint32_t>((p.K + CHUNKS * kWarpVals - 1) / (CHUNKS * kWarpVals));
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = unit / per_row;
+    if (token >= p.tokens)
+        return;
+    const int64_t id = load_id(p.ids, p.ids64, token);
+    const bool real = id >= 0 && id < p.vocab;
+    const int64_t k0 = static_cast<int64_t>(unit - token * per_row) * (CHUNKS * kWarpVals) + lane * kLaneVals;
+    Raw16<IN> x[CHUNKS];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+        x[c].load(p.table + id * p.table_stride + (k0 + c * kWarpVals) * E, real && k0 + c * kWarpVals < p.K);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        float v[kLaneVals];
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            v[i] = x[c].at(i) * p.scale;
+        if (!real)  // zeros, whatever the sign of the scale
+#pragma unroll
+            for (int i = 0; i < kLaneVals; ++i)
+                v[i] = 0.0f;
+        const int64_t k = k0 + c * kWarpVals;
+        if (k < p.K)
+            store16<OUT>(p.out + (token * p.K + k) * ElemBytes<OUT>::value, v);
+    }
+}
+
+// --------------------------------------------------------------------- sort --
+// Stable radix sort of (id, token) by id in one cluster: every block owns a
+// contiguous part of the entries and every warp of it a contiguous run.  A pass
+// counts its run's digits by warp (lanes with the same digit find each other with
+// match.any), scans the counts over the warps, adds the other blocks' counts from
+// their shared memory, and walks the run again to write the entries in order.  Ids
+// outside the table get the key `vocab`, the last one.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortAhead = 4;
+constexpr int kMaxDigits = 1 << kEmbedDigitBits;
+
+__device__ __forceinline__ int ld_cluster(const int *p, int rank)
+{
+    int v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.b32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(smem_addr(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const EmbedSortParams p)
+{
+    extern __shared__ int hist[];  // [kSortWarps][digits]
+    __shared__ int own[kMaxDigits], first[kMaxDigits], warp_part[kSortWarps];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tile = static_cast<int>(blockIdx.x), tiles = static_cast<int>(gridDim.x);
+    const int digits = 1 << p.bits;
+    int *const mine = hist + warp * digits;
+    const int64_t s0 = (static_cast<int64_t>(tile) * kSortWarps + warp) * p.run;
+    const int64_t s1 = s0 + p.run < p.tokens ? s0 + p.run : p.tokens;
+    for (int64_t i = static_cast<int64_t>(tile) * kSortThreads + tid; i < p.mark_words; i += tiles * kSortThreads)
+        p.marks[i] = 0;
+
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const uint2 *from = pass & 1 ? p.entries0 : p.entries1;
+        uint2 *to = pass & 1 ? p.entries1 : p.entries0;
+        const int shift = pass * p.bits;
+        uint2 e[kSortAhead];
+        auto load = [&](int64_t b) {
+#pragma unroll
+            for (int i = 0; i < kSortAhead; ++i) {
+                const int64_t s = b + 32 * i + lane;
+                if (s >= s1) {
+                    e[i] = make_uint2(0xFFFFFFFFu, 0);
+                } else if (pass == 0) {
+                    const int64_t id = load_id(p.ids, p.ids64, s);
+                    e[i] = make_uint2(id >= 0 && id < p.vocab ? static_cast<uint32_t>(id) : p.vocab,
+                                      static_cast<uint32_t>(s));
+                } else {
+                    e[i] = __ldcg(from + s);  // other blocks of the cluster wrote it
+                }
+            }
+        };
+        auto digit = [&](const uint2 &v) { return static_cast<int>((v.x >> shift) & (digits - 1)); };
+        load(s0);
+        for (int i = lane; i < digits; i += 32)
+            mine[i] = 0;
+        __syncwarp();
+        for (int64_t b = s0; b < s1; b += 32 * kSortAhead) {
+            if (b > s0)
+                load(b);
+#pragma unroll
+            for (int i = 0; i < kSortAhead; ++i) {
+                if (b + 32 * i >= s1)
+                    break;  // warp-uniform
+                const bool live = b + 32 * i + lane < s1;
+                const int d = live ? digit(e[i]) : -1;
+                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+                if (live && lane == __ffs(peers) - 1)
+                    mine[d] += __popc(peers);
+                __syncwarp();
+            }
+        }
+        __syncthreads();
+        for (int d = tid; d < digits; d += kSortThreads) {
+            int sum = 0;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int n = hist[w * digits + d];
+                hist[w * digits + d] = sum;
+                sum += n;
+            }
+            own[d] = sum;
+        }
+        cluster_sync();
+        // one digit a thread: the digits' counts over all blocks, scanned, and those of the blocks before
+        int total = 0, before = 0;
+        if (tid < digits)
+#pragma unroll 4
+            for (int r = 0; r < tiles; ++r) {
+                const int n = ld_cluster(&own[tid], r);
+                total += n;
+                before += r < tile ? n : 0;
+            }
+        int incl = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            incl += lane >= o ? v : 0;
+        }
+        if (lane == 31)
+            warp_part[warp] = incl;
+        __syncthreads();
+        int start = lane < warp ? warp_part[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            start += __shfl_xor_sync(0xFFFFFFFFu, start, o);
+        if (tid < digits)
+            first[tid] = start + incl - total + before;
+        __syncthreads();
+        for (int64_t b = s0; b < s1; b += 32 * kSortAhead) {
+            if (p.run > 32 * kSortAhead)
+                load(b);
+#pragma unroll
+            for (int i = 0; i < kSortAhead; ++i) {
+                if (b + 32 * i >= s1)
+                    break;  // warp-uniform
+                const bool live = b + 32 * i + lane < s1;
+                const int d = live ? digit(e[i]) : -1;
+                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+                const int at = live ? mine[d] : 0;
+                __syncwarp();
+                if (live) {
+                    if (lane == __ffs(peers) - 1)
+                        mine[d] = at + __popc(peers);
+                    __stcg(to + first[d] + at + __popc(peers & ((1u << lane) - 1u)), e[i]);
+                    if (pass == p.passes - 1 && p.mark_words > 0 && e[i].x < p.vocab)
+                        atomicOr(p.marks + (e[i].x >> 5), 1u << (e[i].x & 31));
+                }
+                __syncwarp();
+            }
+        }
+        cluster_sync();  // entries are written, and no block reads own[] any more
+    }
+}
+
+// --------------------------------------------------------------------- sums --
+constexpr int kRun = 32;  // sorted rows of a warp
+
+// Sixteen sums of a lane as the gradient's values at k of row `id`.
+template <int OUT>
+__device__ __forceinline__ void finish_row(const EmbedBackParams &p, uint32_t id, int64_t k, const float (&sum)[kLaneVals])
+{
+    constexpr int E = ElemBytes<OUT>::value;
+    Raw16<OUT> add;
+    add.load(p.add + (static_cast<int64_t>(id) * p.K + k) * E, p.add != nullptr);
+    float v[kLaneVals];
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i)
+        v[i] = fmaf(sum[i], p.scale, add.at(i));
+    store16<OUT>(p.dtable + (static_cast<int64_t>(id) * p.K + k) * E, v);
+}
+
+// The first `sum_blocks` blocks sum, the others write the rows whose id does not occur.
+template <int IN, int OUT>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBackParams p, uint32_t sum_blocks, int fill_rows)
+{
+    constexpr int E = ElemBytes<IN>::value;
+    constexpr int kAhead = IN == kBf16 ? 4 : 2;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t K = p.K;
+    if (blockIdx.x >= sum_blocks) {
+        const int64_t v0 = (static_cast<int64_t>(blockIdx.x - sum_blocks) * kWarps + (threadIdx.x >> 5)) * fill_rows;
+        const int64_t v1 = v0 + fill_rows < p.vocab ? v0 + fill_rows : p.vocab;
+        for (int64_t v = v0; v < v1; ++v) {
+            if ((p.marks[v >> 5] >> (v & 31)) & 1)
+                continue;
+            const int64_t row = v * K;
+            for (int64_t k = lane * kLaneVals; k < K; k += kWarpVals) {
+                Raw16<OUT> a;
+                a.load(p.add + (row + k) * ElemBytes<OUT>::value, p.add != nullptr);
+#pragma unroll
+                for (int l = 0; l < Raw16<OUT>::kParts; ++l)
+                    st_row32(p.dtable + (row + k) * ElemBytes<OUT>::value + 32 * l, a.r[l]);
+            }
+        }
+        return;
+    }
+    const uint32_t slices = static_cast<uint32_t>((K + kWarpVals - 1) / kWarpVals);
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), run = unit / slices;
+    const int64_t c0 = static_cast<int64_t>(run) * kRun, k = (unit - run * slices) * kWarpVals + lane * kLaneVals;
+    if (c0 >= p.tokens)
+        return;
+    const bool inside = k < K;
+    const uint2 none = make_uint2(p.vocab, 0);
+    const uint2 e = c0 + lane < p.tokens ? p.entries[c0 + lane] : none;
+    const uint32_t before = c0 > 0 ? p.entries[c0 - 1].x : 0xFFFFFFFFu;
+    const uint32_t after = c0 + kRun < p.tokens ? p.entries[c0 + kRun].x : 0xFFFFFFFFu;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, e.x < p.vocab));  // ids outside the table come last
+    bool open = __shfl_sync(0xFFFFFFFFu, e.x, 0) == before;           // the current run began before these rows
+    float sum[kLaneVals];
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i)
+        sum[i] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        Raw16<IN> x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t t = __shfl_sync(0xFFFFFFFFu, e.y, (i0 + j) & 31);
+            x[j].load(p.dy + t * p.dy_stride + k * E, inside && i0 + j < n);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i >= n)
+                break;  // warp-uniform
+#pragma unroll
+            for (int l = 0; l < kLaneVals; ++l)
+                sum[l] += x[j].at(l);
+            const uint32_t id = __shfl_sync(0xFFFFFFFFu, e.x, i);
+            const uint32_t next = i == kRun - 1 ? after : __shfl_sync(0xFFFFFFFFu, e.x, (i + 1) & 31);
+            if (i < kRun - 1 && next == id)
+                continue;
+            const bool goes_on = next == id;
+            if (inside) {
+                if (open || goes_on) {
+                    char *part = reinterpret_cast<char *>(p.partial + (static_cast<int64_t>(run) * 2 + (open ? 0 : 1)) * K + k);
+                    store16<kF32>(part, sum);
+                } else {
+                    finish_row<OUT>(p, id, k, sum);
+                }
+            }
+            open = false;
+#pragma unroll
+            for (int l = 0; l < kLaneVals; ++l)
+                sum[l] = 0.0f;
+        }
+    }
+}
+
+// Runs over more than one warp's rows: a warp looks at the run that leaves its 32 rows
+// and began in them, and adds its partial sums in order.  Long ones (more than kLong
+// parts) are added by all warps of the block, each every kJoinWarps-th part.
+constexpr int kJoinWarps = 8;
+constexpr int kLong = 32;
+
+template <int OUT>
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const EmbedBackParams p)
+{
+    __shared__ float sums[kJoinWarps][kWarpVals];
+    __shared__ int parts_of[kJoinWarps];
+    __shared__ uint32_t id_of[kJoinWarps];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t K = p.K, k = static_cast<int64_t>(blockIdx.y) * kWarpVals + lane * kLaneVals;
+    const bool inside = k < K;
+    const int64_t run0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps;
+    auto add_part = [&](float (&sum)[kLaneVals], int64_t run, int j) {  // the j-th part of a run that began in `run`
+        const char *part = reinterpret_cast<const char *>(p.partial + ((run + j) * 2 + (j == 0 ? 1 : 0)) * K + k);
+        Raw16<kF32> x;
+        x.load(part, inside);
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            sum[i] += x.at(i);
+    };
+    float sum[kLaneVals];
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i)
+        sum[i] = 0.0f;
+    {
+        const int64_t run = run0 + warp, c0 = run * kRun, end = c0 + kRun;
+        int parts = 0;
+        uint32_t id = p.vocab;
+        if (end < p.tokens) {
+            id = p.entries[end - 1].x;
+            const bool here = c0 == 0 || p.entries[c0 - 1].x != id;  // where the last id began
+            if (id < p.vocab && here && p.entries[end].x == id) {
+                parts = 1;
+                for (int64_t c = end + static_cast<int64_t>(lane) * kRun;; c += 32 * kRun) {
+                    const uint32_t same = __ballot_sync(0xFFFFFFFFu, c < p.tokens && p.entries[c].x == id);
+                    parts += __popc(same);  // ids are sorted: a prefix of the lanes
+                    if (same != 0xFFFFFFFFu)
+                        break;
+                }
+            }
+        }
+        if (lane == 0) {
+            parts_of[warp] = parts;
+            id_of[warp] = id;
+        }
+        if (parts > 0 && parts <= kLong) {
+#pragma unroll 4
+            for (int j = 0; j < parts; ++j)
+                add_part(sum, run, j);
+            if (inside)
+                finish_row<OUT>(p, id, k, sum);
+        }
+    }
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const int parts = parts_of[w];
+        if (parts <= kLong)
+            continue;  // block-uniform
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            sum[i] = 0.0f;
+#pragma unroll 4
+        for (int j = warp; j < parts; j += kJoinWarps)
+            add_part(sum, run0 + w, j);
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            sums[warp][i * 32 + lane] = sum[i];
+        __syncthreads();
+        if (warp == 0) {
+            for (int o = 1; o < kJoinWarps; ++o)
+#pragma unroll
+                for (int i = 0; i < kLaneVals; ++i)
+                    sum[i] += sums[o][i * 32 + lane];
+            if (inside)
+                finish_row<OUT>(p, id_of[w], k, sum);
+        }
+        __syncthreads();
+    }
+}
+
+unsigned warp_blocks(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
+
+template <int IN, int OUT>
+cudaError_t launch_lookup(const EmbedParams &p, int num_sms, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const int64_t units = p.tokens * ((p.K + kWarpVals - 1) / kWarpVals);
+    if (units <= 16ll * num_sms) {
+        const cudaLaunchConfig_t cfg = row_launch(warp_blocks(units), kThreads, 0, s, attr);
+        return cudaLaunchKernelEx(&cfg, embed_kernel<IN, OUT, 1>, p);
+    }
+    const int64_t pairs = p.tokens * ((p.K + 2 * kWarpVals - 1) / (2 * kWarpVals));
+    const cudaLaunchConfig_t cfg = row_launch(warp_blocks(pairs), kThreads, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, embed_kernel<IN, OUT, 2>, p);
+}
+
+int key_bits(int64_t vocab)
+{
+    int bits = 1;
+    while ((vocab >> bits) != 0)  // the keys are 0 .. vocab
+        ++bits;
+    return bits;
+}
+
+cudaError_t launch_sort(const EmbedSortParams &p, int tiles, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1], both[2];
+    const size_t smem = static_cast<size_t>(kSortWarps) * sizeof(int) << p.bits;
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, smem, s, attr);
+    both[0] = attr[0];
+    both[1].id = cudaLaunchAttributeClusterDimension;
+    both[1].val.clusterDim.x = static_cast<unsigned>(tiles);
+    both[1].val.clusterDim.y = 1;
+    both[1].val.clusterDim.z = 1;
+    cfg.attrs = both;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, p);
+}
+
+template <int IN, int OUT>
+cudaError_t launch_sums(const EmbedBackParams &p, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const int64_t slices = (p.K + kWarpVals - 1) / kWarpVals, runs = (p.tokens + kRun - 1) / kRun;
+    const unsigned sum_blocks = warp_blocks(runs * slices);
+    unsigned blocks = sum_blocks;
+    const int64_t row = p.K * ElemBytes<OUT>::value;
+    const int fill_rows = row >= 16384 ? 1 : static_cast<int>(16384 / row);
+    if (p.marks)
+        blocks += warp_blocks((p.vocab + fill_rows - 1) / fill_rows);
+    cudaLaunchConfig_t cfg = row_launch(blocks, kThreads, 0, s, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sum_kernel<IN, OUT>, p, sum_blocks, fill_rows);
+    if (e != cudaSuccess || runs == 1)
+        return e;
+    cfg = row_launch(static_cast<unsigned>((runs + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, s, attr);
+    cfg.gridDim.y = static_cast<unsigned>(slices);
+    return cudaLaunchKernelEx(&cfg, embed_join_kernel<OUT>, p);
+}
+
+int64_t round_up(int64_t n) { return (n + 31) / 32 * 32; }
+
+}  // namespace
+
+cudaError_t prepare_embed()
+{
+    const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSortWarps * kMaxDigits * static_cast<int>(sizeof(int)));
+    return e == cudaSuccess ? cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
+                            : e;
+}
+
+cudaError_t launch_embed(const EmbedParams &p, int in_dtype, int out_dtype, int num_sms, cudaStream_t s)
+{
+    if (in_dtype == kBf16)
+        return out_dtype == kBf16 ? launch_lookup<kBf16, kBf16>(p, num_sms, s) : launch_lookup<kBf16, kF32>(p, num_sms, s);
+    return out_dtype == kBf16 ? launch_lookup<kF32, kBf16>(p, num_sms, s) : launch_lookup<kF32, kF32>(p, num_sms, s);
+}
+
+// Two buffers of entries, the marks of the ids that occur, two rows of partial sums for every 32 tokens.
+EmbedWorkspace embed_workspace(int64_t tokens, int64_t vocab, int64_t K)
+{
+    EmbedWorkspace w;
+    w.entries[0] = 0;
+    w.entries[1] = round_up(tokens * static_cast<int64_t>(sizeof(uint2)));
+    w.marks = 2 * w.entries[1];
+    w.partial = w.marks + round_up((vocab + 31) / 32 * 4);
+    const int64_t runs = (tokens + kRun - 1) / kRun;
+    w.bytes = static_cast<size_t>(w.partial + (runs > 1 ? runs * 2 * K * 4 : 0));
+    return w;
+}
+
+cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64, char *workspace, int in_dtype,
+                                  int out_dtype, cudaStream_t s)
+{
+    const EmbedWorkspace w = embed_workspace(p.tokens, p.vocab, p.K);
+    EmbedSortParams o;
+    o.ids = ids;
+    o.ids64 = ids64;
+    o.tokens = p.tokens;
+    o.vocab = p.vocab;
+    const int bits = key_bits(p.vocab);
+    o.passes = (bits + kEmbedDigitBits - 1) / kEmbedDigitBits;
+    o.bits = (bits + o.passes - 1) / o.passes;
+    int tiles = 1;
+    while (tiles < kEmbedSortTiles && static_cast<int64_t>(tiles) * kSortThreads < p.tokens)
+        tiles *= 2;
+    const int64_t warps = static_cast<int64_t>(tiles) * kSortWarps;
+    o.run = ((p.tokens + warps - 1) / warps + 31) / 32 * 32;
+    o.entries0 = reinterpret_cast<uint2 *>(workspace + w.entries[0]);
+    o.entries1 = reinterpret_cast<uint2 *>(workspace + w.entries[1]);
+    // where the gradient is added to the table's own rows, no other row is touched
+    const bool fill = p.add != p.dtable;
+    o.marks = fill ? reinterpret_cast<uint32_t *>(workspace + w.marks) : nullptr;
+    o.mark_words = fill ? (static_cast<int64_t>(p.vocab) + 31) / 32 : 0;
+    const cudaError_t e = launch_sort(o, tiles, s);
+    if (e != cudaSuccess)
+        return e;
+    p.entries = o.passes & 1 ? o.entries0 : o.entries1;
+    p.marks = o.marks;
+    p.partial = reinterpret_cast<float *>(workspace + w.partial);
+    if (in_dtype == kBf16)
+        return out_dtype == kBf16 ? launch_sums<kBf16, kBf16>(p, s) : launch_sums<kBf16, kF32>(p, s);
+    return out_dtype == kBf16 ? launch_sums<kF32, kBf16>(p, s) : launch_sums<kF32, kF32>(p, s);
+}
+
+}  // namespace mxg

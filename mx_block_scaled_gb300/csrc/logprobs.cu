@@ -1,0 +1,713 @@
+// logprobs.cu -- log probabilities of given tokens with the distribution's entropy
+// and its most probable tokens, and the logits' gradient.
+//
+//   z_v = scale * (x_v - max x);  S = sum exp(z_v)
+//   logprob = z_target - ln S;  entropy = ln S - sum exp(z_v) z_v / S
+//   dx_v = scale * (dlogprob * ([v = target] - p_v) - dentropy * p_v * (ln p_v + entropy))
+//
+// One pass over a row: every thread sums 2^(c (x - r)), c = scale * log2(e), and its
+// product with the exponent relative to a reference r of its own, which it moves only
+// where a value is more than 2^kMargin above it; the sums are rebased to the row's
+// maximum at the end.  The most probable tokens: the threads' own maxima give a value
+// that at least `top` logits reach; the few logits that reach it are collected from
+// the chunks whose maximum does, and ranked against each other.
+#include "mx_block.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace mxg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMargin = 3.0f;
+constexpr int kCandidates = 1024;
+constexpr int kKeptMaxima = 32;  // maxima that a thread keeps, of one or more chunks each
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Below this a logit's share of the sums is zero, relative to the reference r: its
+// exponent is -1000 or less.  Values are raised to it so that an infinite one gives 0
+// times a finite number.  At least a BF16 step below r; -inf where there is no such
+// number (the sums then guard every product).
+__device__ __forceinline__ float floor_of(float r, float c)
+{
+    const float f = fminf(r - 1000.0f / c, r - fabsf(r) * 0.0078125f);
+    return __bfloat162float(__float2bfloat16_rd(f));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Largest of a chunk's sixteen values; NaN if one is.
+template <int IN>
+__device__ __forceinline__ float chunk_max(const Raw16<IN> &x)
+{
+    if constexpr (IN == kBf16) {
+        uint32_t m = x.r[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.r[0][i]));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    } else {
+        float m = x.at(0);
+#pragma unroll
+        for (int i = 1; i + 1 < kLaneVals; i += 2)
+            asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x.at(i)), "f"(x.at(i + 1)));
+        return max_nan(m, x.at(kLaneVals - 1));
+    }
+}
+
+// A chunk with its values raised to `low`.
+template <int IN>
+__device__ __forceinline__ Raw16<IN> raised(const Raw16<IN> &x, float low)
+{
+    Raw16<IN> y;
+    if constexpr (IN == kBf16) {
+        const uint32_t l = pack_bf16(low, low);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y.r[0][i]) : "r"(x.r[0][i]), "r"(l));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+            y.r[i >> 3][i & 7] = __float_as_uint(max_nan(x.at(i), low));
+    }
+    return y;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const char *p)
+{
+    if constexpr (DT == kBf16)
+        return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p)) << 16);
+    else
+        return *reinterpret_cast<const float *>(p);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_one(char *p, float v)
+{
+    if constexpr (DT == kBf16)
+        *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
+    else
+        *reinterpret_cast<float *>(p) = v;
+}
+
+// Sums of 2^z and of 2^z z, z = c (x - ref).
+struct Sums {
+    float ref, s, w;
+
+    __device__ __forceinline__ void rebase(float to, float c)
+    {
+        if (ref == neg_inf()) {  // nothing summed yet
+            ref = to;
+            return;
+        }
+        const float d = (ref - to) * c, f = exp2_fast(d);
+        w = f > 0.0f ? (w + d * s) * f : w * f;  // (a NaN stays one)
+        s *= f;
+        ref = to;
+    }
+};
+
+// The chunk's part of the sums; `low` = floor_of(ref).
+template <int IN, bool ENT>
+__device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Raw16<IN> &x, float ref, float low, float c)
+{
+    const F2 minus = f2(-ref, -ref), cc = f2(c, c);
+    if (ENT && low == neg_inf()) {
+#pragma unroll
+        for (int i = 0; i < kLaneVals / 2; ++i) {
+            float a, b;
+            f2_split(f2_mul(f2_add(x.pair(i), minus), cc), a, b);
+            const float ea = exp2_fast(a), eb = exp2_fast(b);
+            s2 = f2_add(s2, f2(ea, eb));
+            w2 = f2_add(w2, f2(ea > 0.0f ? ea * a : 0.0f, eb > 0.0f ? eb * b : 0.0f));
+        }
+        return;
+    }
+    Raw16<IN> y = x;
+    if constexpr (ENT)
+        y = raised(x, low);
+#pragma unroll
+    for (int i = 0; i < kLaneVals / 2; ++i) {
+        const F2 z = f2_mul(f2_add(y.pair(i), minus), cc);
+        float a, b;
+        f2_split(z, a, b);
+        const F2 e = f2(exp2_fast(a), exp2_fast(b));
+        s2 = f2_add(s2, e);
+        if constexpr (ENT)
+            w2 = f2_fma(e, z, w2);
+    }
+}
+
+// Order of logits: by value, equal ones by index; a larger key comes first.
+__device__ __forceinline__ unsigned long long key_of(float v, int64_t index)
+{
+    uint32_t u = __float_as_uint(v + 0.0f);  // -0 equals 0
+    u ^= (u >> 31) ? 0xFFFFFFFFu : 0x80000000u;
+    return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(index));
+}
+__device__ __forceinline__ float key_value(unsigned long long key)
+{
+    uint32_t u = static_cast<uint32_t>(key >> 32);
+    u ^= (u >> 31) ? 0x80000000u : 0xFFFFFFFFu;
+    return __uint_as_float(u);
+}
+
+__device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) { return map_to_cta(smem_addr(p), rank); }
+__device__ __forceinline__ float ld_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_u32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_u64(uint32_t a)
+{
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// A row as a block sees it: whole chunks of sixteen values from a 32-byte boundary on,
+// which the blocks of the cluster share, and up to 15 values before and after, one to a
+// thread of the first block.
+template <int IN>
+struct Row {
+    static constexpr int E = ElemBytes<IN>::value;
+    const char *x;
+    int64_t head, chunks, V;
+    int64_t from, to;  // this block's chunks
+    int extras;
+
+    __device__ __forceinline__ Row(const char *row, int64_t vocab, uint32_t rank, uint32_t blocks)
+        : x(row), V(vocab)
+    {
+        head = ((32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31) / E;
+        head = head < V ? head : V;
+        chunks = (V - head) / kLaneVals;
+        const int64_t per = (chunks + blocks - 1) / blocks;
+        from = rank * per < chunks ? rank * per : chunks;
+        to = from + per < chunks ? from + per : chunks;
+        extras = rank == 0 ? static_cast<int>(V - chunks * kLaneVals) : 0;
+    }
+    __device__ __forceinline__ int64_t first_of(int64_t chunk) const { return head + chunk * kLaneVals; }
+    __device__ __forceinline__ int64_t extra(int i) const { return i < head ? i : i + chunks * kLaneVals; }
+    __device__ __forceinline__ void load(Raw16<IN> &r, int64_t chunk) const { r.load(x + first_of(chunk) * E, true); }
+    __device__ __forceinline__ float one(int64_t v) const { return load_one<IN>(x + v * E); }
+};
+
+// TOP: every thread keeps the maxima of its chunks, `group` of them in one.
+template <int IN, bool ENT, bool TOP>
+__global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel(const LogprobsParams p, uint32_t blocks, int64_t group)
+{
+    extern __shared__ float maxima[];  // [kept][kThreads], TOP only
+    __shared__ float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps], warp_bound[kWarps];
+    __shared__ float block_m, block_s, block_w, block_bound;
+    __shared__ unsigned long long candidates[TOP ? kCandidates : 1];
+    __shared__ unsigned long long warp_best[kWarps], list[32];
+    __shared__ uint32_t count;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = blockIdx.x % blocks;
+    const int64_t row = blockIdx.x / blocks;
+    const Row<IN> r(p.x + row * p.stride, p.V, rank, blocks);
+    const float c = p.scale * kLog2E, step_up = kMargin / c;
+    float target_x = 0.0f;
+    bool real = false;
+    if (rank == 0 && tid == 0) {
+        count = 0;
+        if (p.targets) {
+            const int64_t t = p.targets64 ? static_cast<const int64_t *>(p.targets)[row]
+                                          : static_cast<const int32_t *>(p.targets)[row];
+            real = t >= 0 && t < p.V;
+            if (real)
+                target_x = r.one(t);
+        }
+    }
+
+    // ---- the pass over the row
+    Sums a = {neg_inf(), 0.0f, 0.0f};
+    float low = neg_inf(), own_max = neg_inf();
+    F2 s2 = f2(0.0f, 0.0f), w2 = f2(0.0f, 0.0f);
+    bool nan = false;
+    const int64_t mine = (r.to - r.from - tid + kThreads - 1) / kThreads;  // this thread's chunks (0 or less: none)
+    float kept = neg_inf();
+    int64_t in_group = 0;
+    float *keep = maxima + tid;
+    auto take = [&](const Raw16<IN> &x) {
+        float m = chunk_max<IN>(x);
+        if (!(m <= a.ref + step_up)) {  // (also where the reference is still missing, and for a NaN)
+            if (m != m) {
+                nan = true;
+                m = neg_inf();
+#pragma unroll
+                for (int i = 0; i < kLaneVals; ++i)
+                    m = fmaxf(m, x.at(i));
+            }
+            if (m > a.ref) {
+                float lo, hi;
+                f2_split(s2, lo, hi);
+                a.s = lo + hi;
+                f2_split(w2, lo, hi);
+                a.w = lo + hi;
+                a.rebase(m, c);
+                s2 = f2(a.s, 0.0f);
+                w2 = f2(a.w, 0.0f);
+                low = floor_of(m, c);
+            }
+        }
+        own_max = fmaxf(own_max, m);
+        if constexpr (TOP) {
+            kept = fmaxf(kept, m);
+            if (++in_group == group) {
+                *keep = kept;
+                keep += kThreads;
+                kept = neg_inf();
+                in_group = 0;
+            }
+        }
+        if (a.ref != neg_inf())  // else every value is -inf and adds nothing
+            add_chunk<IN, ENT>(s2, w2, x, a.ref, low, c);
+    };
+    {
+        Raw16<IN> x[2];
+        int64_t at = r.from + tid;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (j < mine)
+                r.load(x[j], at + j * kThreads);
+        // the first reference: the largest value of the warp's first chunks
+        float m = mine > 0 ? chunk_max<IN>(x[0]) : neg_inf();
+        a.ref = warp_max(m == m ? m : neg_inf());
+        low = floor_of(a.ref, c);
+        for (int64_t i = 0; i < mine; i += 2, at += 2 * kThreads) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (i + j >= mine)
+                    break;
+                const Raw16<IN> now = x[j];
+                if (i + j + 2 < mine)
+                    r.load(x[j], at + (j + 2) * kThreads);
+                take(now);
+            }
+        }
+        if (TOP && in_group > 0)
+            *keep = kept;
+        float lo, hi;
+        f2_split(s2, lo, hi);
+        a.s = lo + hi;
+        f2_split(w2, lo, hi);
+        a.w = lo + hi;
+    }
+    if (tid < r.extras) {
+        const float x = r.one(r.extra(tid));
+        nan |= x != x;
+        if (x > neg_inf()) {
+            if (x > a.ref)
+                a.rebase(x, c);
+            const float z = (x - a.ref) * c, e = exp2_fast(z);
+            a.s += e;
+            a.w += e > 0.0f ? e * z : 0.0f;
+            own_max = fmaxf(own_max, x);
+        }
+    }
+    if (nan)
+        a.s = a.w = __uint_as_float(0x7FC00000u);
+
+    // ---- sums and bounds of the block
+    const float m_warp = warp_max(own_max);
+    if (m_warp != neg_inf())
+        a.rebase(m_warp, c);
+    a.s = warp_sum(a.s);
+    a.w = warp_sum(a.w);
+    // at least `each` threads of every warp reach the warp's bound, and `of` warps the block's
+    const int need = TOP ? (p.top + static_cast<int>(blocks) - 1) / static_cast<int>(blocks) : 1;
+    const int each = (need + kWarps - 1) / kWarps, of = (need + each - 1) / each;
+    float bound = neg_inf();
+    if constexpr (TOP) {
+        float left = own_max;
+        for (int i = 0; i < each; ++i) {
+            bound = warp_max(left);
+            const uint32_t has = __ballot_sync(0xFFFFFFFFu, left == bound);
+            if (lane == __ffs(has) - 1)
+                left = neg_inf();
+        }
+    }
+    if (lane == 0) {
+        warp_m[warp] = m_warp;
+        warp_s[warp] = a.s;
+        warp_w[warp] = a.w;
+        warp_bound[warp] = bound;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        Sums b = {neg_inf(), 0.0f, 0.0f};
+        if (lane < kWarps)
+            b = {warp_m[lane], warp_s[lane], warp_w[lane]};
+        const float m = warp_max(b.ref);
+        if (m != neg_inf())
+            b.rebase(m, c);
+        b.s = warp_sum(b.s);
+        b.w = warp_sum(b.w);
+        if (lane == 0) {
+            block_m = m;
+            block_s = b.s;
+            block_w = b.w;
+        }
+        if constexpr (TOP) {
+            const float v = lane < kWarps ? warp_bound[lane] : neg_inf();
+            int larger = 0;
+            for (int i = 0; i < kWarps; ++i) {
+                const float o = __shfl_sync(0xFFFFFFFFu, v, i);
+                larger += o > v || (o == v && i < lane);
+            }
+            if (lane < kWarps && larger == of - 1)
+                block_bound = v;
+        }
+    }
+    if (blocks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // ---- the row's sums
+    float log_s = 0.0f, row_m = neg_inf();
+    if (rank == 0 && warp == 0) {
+        Sums b = {neg_inf(), 0.0f, 0.0f};
+        if (static_cast<uint32_t>(lane) < blocks) {
+            b.ref = ld_f32(in_block(&block_m, lane));
+            b.s = ld_f32(in_block(&block_s, lane));
+            b.w = ld_f32(in_block(&block_w, lane));
+        }
+        row_m = warp_max(b.ref);
+        if (row_m != neg_inf())
+            b.rebase(row_m, c);
+        b.s = warp_sum(b.s);
+        b.w = warp_sum(b.w);
+        log_s = logf(b.s);
+        if (lane == 0) {
+            // a row without a finite value: no token has a probability, and nothing is uncertain
+            const bool none = row_m == neg_inf() && b.s == 0.0f;
+            if (none)
+                log_s = 0.0f;
+            if (p.logprob)
+                p.logprob[row] = !real ? 0.0f : none ? neg_inf() : (target_x - row_m) * p.scale - log_s;
+            if (p.entropy)
+                p.entropy[row] = none ? 0.0f : log_s - kLn2 * (b.w / b.s);
+            if (p.stats)
+                reinterpret_cast<float2 *>(p.stats)[row] = make_float2(row_m, log_s);
+        }
+        if constexpr (TOP) {
+            if (lane == 0) {  // for the ranks below
+                warp_m[0] = row_m;
+                warp_s[0] = log_s;
+            }
+        }
+    }
+    if constexpr (!TOP) {
+        if (blocks > 1)
+            cluster_sync();  // no block leaves while the first may still read its sums
+        return;
+    }
+
+    // ---- the most probable tokens
+    float least = block_bound;
+    for (uint32_t b = 0; b < blocks && blocks > 1; ++b)
+        least = fminf(least, ld_f32(in_block(&block_bound, b)));
+    const uint32_t to_count = in_block(&count, 0), to_list = in_block(candidates, 0);
+    auto offer = [&](float v, int64_t index) {
+        if (!(v >= least) || v == neg_inf())
+            return;
+        uint32_t at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(to_count) : "memory");
+        if (at < kCandidates)
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
+    };
+    if (own_max >= least && own_max != neg_inf()) {
+        for (int64_t i = 0; i < mine; i += group) {
+            if (!(maxima[i / group * kThreads + tid] >= least))
+                continue;
+            for (int64_t j = i; j < i + group && j < mine; ++j) {
+                const int64_t chunk = r.from + tid + j * kThreads;
+                Raw16<IN> x;
+                r.load(x, chunk);
+#pragma unroll
+                for (int n = 0; n < kLaneVals; ++n)
+                    offer(x.at(n), r.first_of(chunk) + n);
+            }
+        }
+        if (tid < r.extras)
+            offer(r.one(r.extra(tid)), r.extra(tid));
+    }
+    if (blocks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    uint32_t n = blocks > 1 ? ld_u32(to_count) : count;
+    if (n > kCandidates) {
+        // More logits reach the bound than fit (long runs of equal ones, or the largest in few threads' chunks): every
+        // block finds its own best ones, one at a time, and the first block ranks those.
+        unsigned long long last = ~0ull;
+        for (int k = 0; k < p.top; ++k) {
+            unsigned long long best = 0;
+            auto look = [&](float v, int64_t index) {
+                const unsigned long long key = key_of(v, index);
+                if (v > neg_inf() && key < last && key > best)
+                    best = key;
+            };
+            for (int64_t chunk = r.from + tid; chunk < r.to; chunk += kThreads) {
+                Raw16<IN> x;
+                r.load(x, chunk);
+#pragma unroll
+                for (int i = 0; i < kLaneVals; ++i)
+                    look(x.at(i), r.first_of(chunk) + i);
+            }
+            if (tid < r.extras)
+                look(r.one(r.extra(tid)), r.extra(tid));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const unsigned long long v = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+                best = v > best ? v : best;
+            }
+            if (lane == 0)
+                warp_best[warp] = best;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w)
+                best = warp_best[w] > best ? warp_best[w] : best;
+            if (tid == 0)
+                list[k] = best;  // 0: there are no more
+            last = best;
+            __syncthreads();
+        }
+        if (blocks > 1)
+            cluster_sync();
+        n = static_cast<uint32_t>(p.top) * blocks;
+        if (rank == 0)
+            for (uint32_t i = tid; i < n; i += kThreads)
+                candidates[i] = ld_u64(in_block(list, i / p.top) + i % p.top * 8);
+        __syncthreads();
+    }
+    if (rank == 0) {
+        const float m = warp_m[0], ls = warp_s[0];
+        int64_t *ids = p.top_ids + row * p.top;
+        float *values = p.top_logprobs + row * p.top;
+        for (uint32_t i = tid; i < n; i += kThreads) {
+            const unsigned long long key = candidates[i];
+            if (key == 0)
+                continue;
+            uint32_t larger = 0;
+            for (uint32_t j = 0; j < n; ++j)
+                larger += candidates[j] > key;
+            if (larger < static_cast<uint32_t>(p.top)) {
+                ids[larger] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+                values[larger] = (key_value(key) - m) * p.scale - ls;
+            }
+        }
+        // fewer than `top` tokens with a probability: the rest is -1
+        uint32_t found = 0;
+        for (uint32_t j = lane; j < n; j += 32)
+            found += candidates[j] != 0;
+        found = __reduce_add_sync(0xFFFFFFFFu, found);
+        for (uint32_t i = found + tid; i < static_cast<uint32_t>(p.top); i += kThreads) {
+            ids[i] = -1;
+            values[i] = neg_inf();
+        }
+    }
+    if (blocks > 1)
+        cluster_sync();  // no block leaves while another may still read its memory
+}
+
+// ----------------------------------------------------------------- backward --
+// A block takes kBackChunks chunks a thread of a row.  VECTOR: the row and its gradient
+// start alike against 32-byte boundaries; else one value a thread at a time.
+constexpr int kBackChunks = 2;
+constexpr int64_t kBackVals = static_cast<int64_t>(kThreads) * kBackChunks * kLaneVals;
+
+struct RowGrad {
+    float m, c, shift;   // ln p = ln2 * t, t = (x - m) * c - shift
+    float a, b;          // p * (a + b * t) is the gradient, apart from the target's own term
+    float low;           // values are raised to it
+    bool none;           // a row without a finite value
+
+    __device__ __forceinline__ float at(float x) const
+    {
+        const float t = fmaf(x - m, c, -shift), p = exp2_fast(t);
+        return none || p == 0.0f ? 0.0f : p * fmaf(b, t, a);
+    }
+};
+
+template <int IN, bool ENT, bool VECTOR>
+__global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const LogprobsBackParams p, uint32_t per_row)
+{
+    constexpr int E = ElemBytes<IN>::value;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x;
+    const uint32_t part = blockIdx.x % per_row;
+    const int64_t row = blockIdx.x / per_row, V = p.V;
+    const char *x = p.x + row * p.stride;
+    char *d = p.dlogits + row * V * E;
+    const int64_t head = VECTOR ? min(static_cast<int64_t>(((32 - (reinterpret_cast<uintptr_t>(x) & 31)) & 31) / E), V) : 0;
+    const int64_t chunks = VECTOR ? (V - head) / kLaneVals : 0;
+    const int64_t c0 = static_cast<int64_t>(part) * kThreads * kBackChunks + tid;
+    Raw16<IN> v[kBackChunks];
+    if constexpr (VECTOR)
+#pragma unroll
+        for (int j = 0; j < kBackChunks; ++j)
+            v[j].load(x + (head + (c0 + j * kThreads) * kLaneVals) * E, c0 + j * kThreads < chunks);
+    const int64_t target = p.targets == nullptr ? -1
+                           : p.targets64        ? static_cast<const int64_t *>(p.targets)[row]
+                                                : static_cast<const int32_t *>(p.targets)[row];
+    const bool real = target >= 0 && target < V;
+    const float2 stats = reinterpret_cast<const float2 *>(p.stats)[row];
+    const float g = real && p.dlogprob ? p.dlogprob[row] : 0.0f;
+    const float h = ENT ? p.dentropy[row] : 0.0f;
+    RowGrad r;
+    r.m = stats.x;
+    r.c = p.scale * kLog2E;
+    r.shift = stats.y * kLog2E;
+    r.a = ENT ? -(g + h * p.entropy[row]) * p.scale : -g * p.scale;
+    r.b = -h * kLn2 * p.scale;
+    r.low = floor_of(stats.x, r.c);
+    r.none = stats.x == neg_inf();
+    const float peak = r.none ? 0.0f : g * p.scale;
+    auto single = [&](int64_t i) {
+        store_one<IN>(d + i * E, r.at(load_one<IN>(x + i * E)) + (i == target ? peak : 0.0f));
+    };
+    if constexpr (!VECTOR) {
+        for (int64_t i = part * kBackVals + tid; i < V && i < (part + 1) * kBackVals; i += kThreads)
+            single(i);
+        return;
+    }
+    const F2 minus = f2(-r.m, -r.m), cc = f2(r.c, r.c), shift = f2(-r.shift, -r.shift), a2 = f2(r.a, r.a),
+             b2 = f2(r.b, r.b);
+#pragma unroll
+    for (int j = 0; j < kBackChunks; ++j) {
+        if (c0 + j * kThreads >= chunks)
+            break;
+        const int64_t k = head + (c0 + j * kThreads) * kLaneVals;
+        float o[kLaneVals];
+        if (r.none || r.low == neg_inf()) {
+#pragma unroll
+            for (int i = 0; i < kLaneVals; ++i)
+                o[i] = r.at(v[j].at(i));
+        } else {
+            const Raw16<IN> y = ENT ? raised(v[j], r.low) : v[j];
+#pragma unroll
+            for (int i = 0; i < kLaneVals / 2; ++i) {
+                const F2 t = f2_fma(f2_add(y.pair(i), minus), cc, shift);
+                float lo, hi;
+                f2_split(t, lo, hi);
+                const F2 e = f2(exp2_fast(lo), exp2_fast(hi));
+                f2_split(f2_mul(e, ENT ? f2_fma(b2, t, a2) : a2), o[2 * i], o[2 * i + 1]);
+            }
+        }
+        if (target >= k && target < k + kLaneVals)
+#pragma unroll
+            for (int i = 0; i < kLaneVals; ++i)
+                if (target == k + i)
+                    o[i] += peak;
+        store16<IN>(d + k * E, o);
+    }
+    const int64_t extras = V - chunks * kLaneVals;
+    if (part == 0 && tid < extras)
+        single(tid < head ? tid : tid + chunks * kLaneVals);
+}
+
+template <int IN, bool ENT, bool TOP>
+cudaError_t launch_rows(const LogprobsParams &p, unsigned blocks, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1], both[2];
+    // chunks of a thread at most (a row that starts off a 32-byte boundary may have one less)
+    const int64_t chunks = (p.V / kLaneVals + blocks - 1) / blocks, mine = (chunks + kThreads - 1) / kThreads;
+    const int64_t group = mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1;
+    const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * kThreads * sizeof(float) : 0;
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), kThreads, smem, s, attr);
+    if (blocks > 1) {
+        both[0] = attr[0];
+        both[1].id = cudaLaunchAttributeClusterDimension;
+        both[1].val.clusterDim.x = blocks;
+        both[1].val.clusterDim.y = 1;
+        both[1].val.clusterDim.z = 1;
+        cfg.attrs = both;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP>, p, blocks, group);
+}
+
+template <int IN>
+cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
+{
+    // few rows: blocks of a cluster share one, while each has at least two chunks a thread
+    unsigned blocks = 1;
+    while (blocks < kLogprobsCluster && p.rows * blocks < 2ll * num_sms &&
+           p.V >= static_cast<int64_t>(blocks) * 4 * kThreads * kLaneVals)
+        blocks *= 2;
+    if (p.top > 0)
+        return p.entropy ? launch_rows<IN, true, true>(p, blocks, s) : launch_rows<IN, false, true>(p, blocks, s);
+    return p.entropy ? launch_rows<IN, true, false>(p, blocks, s) : launch_rows<IN, false, false>(p, blocks, s);
+}
+
+template <int IN, bool ENT>
+cudaError_t launch_backward(const LogprobsBackParams &p, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    constexpr int E = ElemBytes<IN>::value;
+    // every row and its gradient start alike where the first do and the rows' steps are alike
+    const uintptr_t off = reinterpret_cast<uintptr_t>(p.x) - reinterpret_cast<uintptr_t>(p.dlogits);
+    const bool vector = (off & 31) == 0 && (p.rows == 1 || ((p.stride - p.V * E) & 31) == 0);
+    const uint32_t per_row = static_cast<uint32_t>((p.V + kBackVals - 1) / kBackVals);
+    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * per_row), kThreads, 0, s, attr);
+    return vector ? cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, true>, p, per_row)
+                  : cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, false>, p, per_row);
+}
+
+}  // namespace
+
+bool logprobs_fits(int64_t rows, int64_t V)
+{
+    return rows * ((V + kBackVals - 1) / kBackVals) < (1ll << 31) && rows * kLogprobsCluster < (1ll << 31);
+}
+
+cudaError_t launch_logprobs(const LogprobsParams &p, int in_dtype, int num_sms, cudaStream_t s)
+{
+    return in_dtype == kBf16 ? launch_forward<kBf16>(p, num_sms, s) : launch_forward<kF32>(p, num_sms, s);
+}
+
+cudaError_t launch_logprobs_backward(const LogprobsBackParams &p, int in_dtype, cudaStream_t s)
+{
+    if (in_dtype == kBf16)
+        return p.dentropy ? launch_backward<kBf16, true>(p, s) : launch_backward<kBf16, false>(p, s);
+    return p.dentropy ? launch_backward<kF32, true>(p, s) : launch_backward<kF32, false>(p, s);
+}
+
+}  // namespace mxg

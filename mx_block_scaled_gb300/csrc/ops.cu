@@ -2,11 +2,11 @@
 // activation, expert sort / dispatch / combine): argument checks and launches.
 #include "ops.h"
 
-#include <initializer_list>
 #include <mutex>
 
 #include "mx_block.cuh"
 #include "mxgemm.h"
+#include "ops_check.h"
 
 namespace {
 
@@ -20,8 +20,9 @@ struct OpsDevice {
 OpsDevice g_ops_dev[kMaxDevices];
 std::mutex g_ops_mutex;
 
-// The current device's SM count; prepares it on first use.
-int ops_device(int *num_sms)
+}  // namespace
+
+int mxg::ops_device(int *num_sms)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -35,7 +36,7 @@ int ops_device(int *num_sms)
             cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return MXGEMM_ERR_CUDA;
         d.is_sm103 = major == 10 && minor == 3;
-        if (d.is_sm103 && mxg::prepare_norm() != cudaSuccess)
+        if (d.is_sm103 && (mxg::prepare_norm() != cudaSuccess || mxg::prepare_embed() != cudaSuccess))
             return MXGEMM_ERR_CUDA;
         d.ready = true;
     }
@@ -43,75 +44,9 @@ int ops_device(int *num_sms)
     return d.is_sm103 ? MXGEMM_OK : MXGEMM_ERR_ARCH;
 }
 
-int status_of(cudaError_t e) { return e == cudaSuccess ? MXGEMM_OK : MXGEMM_ERR_CUDA; }
+namespace {
 
-bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-constexpr int64_t kMaxRows = (1ll << 31) - 1;
-constexpr int64_t kMaxCols = 1ll << 30;
-
-bool known_dtype(int d) { return d == MXGEMM_IN_F32 || d == MXGEMM_IN_BF16; }
-int64_t elem_bytes(int d) { return d == MXGEMM_IN_BF16 ? 2 : 4; }
-const char *bytes(const void *p) { return static_cast<const char *>(p); }
-
-// A strided input matrix: NULL passes; rows start on 32-byte boundaries and do
-// not overlap (a stride of at least the row, or a single row).
-bool rows_shape_ok(const void *p, int64_t stride, int64_t rows, int64_t cols)
-{
-    return p == nullptr || rows == 1 || (stride >= cols && stride <= (1ll << 40));
-}
-bool rows_align_ok(const void *p, int64_t stride, int64_t rows, int64_t elem)
-{
-    return p == nullptr || (aligned(p, 32) && (rows == 1 || stride * elem % 32 == 0));
-}
-
-// Bytes of a matrix, from its first to its last; p NULL for one that there is not.
-struct Span {
-    const void *p;
-    int64_t rows, stride, row;
-};
-Span dense(const void *p, int64_t rows, int64_t row) { return {p, rows, row, row}; }
-Span flat(const void *p, int64_t n) { return {p, 1, n, n}; }
-
-bool apart(const Span &a, const Span &b)
-{
-    if (!a.p || !b.p)
-        return true;
-    using Wide = unsigned __int128;  // no size that the other checks pass overflows it
-    const Wide a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 + static_cast<Wide>(a.rows - 1) * a.stride + a.row <= b0 ||
-           b0 + static_cast<Wide>(b.rows - 1) * b.stride + b.row <= a0;
-}
-
-// An output, and the inputs (bit i: input i) that it may be itself: whole and dense,
-// where the thread that writes a value is the one that read it, and had read it before.
-struct Output {
-    Span at;
-    unsigned over = 0;
-
-    bool is(const Span &in) const
-    {
-        return at.p == in.p && at.rows == in.rows && at.row == in.row && (in.rows == 1 || in.stride == in.row);
-    }
-};
-
-// No output touches a byte of an input, apart from those that it may be, nor of another
-// output: blocks read inputs while others write.
-bool outputs_apart(std::initializer_list<Output> outs, std::initializer_list<Span> ins)
-{
-    for (const Output *o = outs.begin(); o != outs.end(); ++o) {
-        unsigned bit = 1;
-        for (const Span &in : ins) {
-            if (!apart(o->at, in) && !((o->over & bit) && o->is(in)))
-                return false;
-            bit <<= 1;
-        }
-        for (const Output *other = outs.begin(); other != o; ++other)
-            if (!apart(o->at, other->at))
-                return false;
-    }
-    return true;
-}
+using namespace mxg;
 
 // Bytes of a row of n MX codes.
 int64_t code_bytes(int fmt, int64_t n) { return fmt == MXGEMM_FMT_MXFP4_E2M1 ? n / 2 : n; }

@@ -1,6 +1,9 @@
 // ops.h -- internal interface of the row operators around the GEMM: RMS norm
-// (norm.cu), gated activation (glu.cu), expert dispatch and combine (moe.cu).
-// The launchers take arguments that the C ABI (ops.cu) has checked.
+// (norm.cu), gated activation (glu.cu), expert dispatch and combine (moe.cu); and
+// of those at a model's ends and between its products: embedding (embed.cu), norm
+// and rotation of heads (heads.cu), log probabilities (logprobs.cu), gradient norm
+// and clipping (clip.cu).
+// The launchers take arguments that the C ABI (ops.cu, ops_model.cu) has checked.
 #pragma once
 
 #include <cstddef>
@@ -140,5 +143,142 @@ struct CombineBackParams {
     float *dweights;
 };
 cudaError_t launch_moe_combine_backward(const CombineBackParams &p, int in_dtype, int num_sms, cudaStream_t s);
+
+struct EmbedParams {
+    const char *table;
+    int64_t table_stride;          // bytes
+    int64_t vocab, K;
+    const void *ids;
+    bool ids64;
+    int64_t tokens;
+    float scale;
+    char *out;                     // dense rows
+};
+cudaError_t launch_embed(const EmbedParams &p, int in_dtype, int out_dtype, int num_sms, cudaStream_t s);
+
+// The sort of a gradient's ids: passes of at most kEmbedDigitBits bits, a cluster of
+// at most kEmbedSortTiles blocks.
+constexpr int kEmbedDigitBits = 10;
+constexpr int kEmbedSortTiles = 16;
+constexpr int64_t kEmbedMaxVocab = 1ll << 30;
+struct EmbedSortParams {
+    const void *ids;
+    bool ids64;
+    int64_t tokens;
+    uint32_t vocab;
+    int bits, passes;
+    int64_t run;                   // entries of a warp, a multiple of 32
+    uint2 *entries0, *entries1;    // (id, token): the first pass writes entries0, the second entries1, and so on
+    uint32_t *marks;               // a bit for every id that occurs, or NULL
+    int64_t mark_words;
+};
+
+struct EmbedBackParams {
+    const char *dy;
+    int64_t dy_stride;             // bytes
+    int64_t tokens, K;
+    uint32_t vocab;
+    float scale;
+    const char *add;               // dense rows of the gradient's type, or NULL; dtable itself: only rows that occur
+    char *dtable;                  // dense rows
+    const uint2 *entries;          // (id, token) sorted; these three are the launcher's
+    const uint32_t *marks;
+    float *partial;
+};
+struct EmbedWorkspace {
+    int64_t entries[2], marks, partial;  // bytes from the workspace's start
+    size_t bytes;
+};
+EmbedWorkspace embed_workspace(int64_t tokens, int64_t vocab, int64_t K);
+// Set the sort's shared-memory and cluster opt-in on the current device.
+cudaError_t prepare_embed();
+cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64, char *workspace, int in_dtype,
+                                  int out_dtype, cudaStream_t s);
+
+// What the passes over heads have in common; strides in bytes.
+struct HeadsCommon {
+    int64_t tokens;
+    int heads, q_heads, D, rotary;
+    const char *q_weight, *k_weight;
+    const float *rope;             // rope_rows x rotary (cos | sin), or NULL
+    int64_t rope_rows;
+    const void *positions;
+    bool positions64;
+    const char *x;
+    int64_t x_token, x_head;
+};
+struct HeadsParams : HeadsCommon {
+    float eps;
+    bool inverse;                  // rotate by minus the angles
+    char *y;
+    int64_t y_token, y_head;
+    float *rstd;                   // tokens x heads, or NULL
+};
+constexpr int kHeadsMaxDim = 512;
+// weight_dtype 0: no norm
+cudaError_t launch_heads(const HeadsParams &p, int in_dtype, int weight_dtype, bool interleaved, int num_sms,
+                         cudaStream_t s);
+
+struct HeadsBackParams : HeadsCommon {
+    const char *dy;
+    int64_t dy_token, dy_head;
+    const float *rstd;
+    char *dx;
+    int64_t dx_token, dx_head;
+    float *dq_weight, *dk_weight;  // either may be NULL
+    float *partial;                // [blocks][2][D]
+};
+// Blocks that leave partial sums, at most, on a part of at most kHeadsBackSms multiprocessors.
+constexpr int kHeadsBackSms = 152;
+constexpr int kHeadsBackPerSm = 4;
+int64_t heads_back_blocks(int64_t tokens);
+cudaError_t launch_heads_backward(const HeadsBackParams &p, int in_dtype, int weight_dtype, bool interleaved,
+                                  int num_sms, cudaStream_t s);
+
+struct LogprobsParams {
+    const char *x;
+    int64_t stride;                // bytes
+    int64_t rows, V;
+    float scale;
+    const void *targets;           // or NULL
+    bool targets64;
+    float *logprob, *entropy, *stats;  // each or NULL; stats is rows x 2
+    int top;
+    int64_t *top_ids;
+    float *top_logprobs;
+};
+constexpr int kLogprobsMaxTop = 32;
+constexpr int kLogprobsCluster = 8;
+bool logprobs_fits(int64_t rows, int64_t V);
+cudaError_t launch_logprobs(const LogprobsParams &p, int in_dtype, int num_sms, cudaStream_t s);
+
+struct LogprobsBackParams {
+    const char *x;
+    int64_t stride;                // bytes
+    int64_t rows, V;
+    float scale;
+    const void *targets;
+    bool targets64;
+    const float *stats, *dlogprob, *entropy, *dentropy;  // dlogprob, or entropy and dentropy, may be NULL
+    char *dlogits;                 // dense rows
+};
+cudaError_t launch_logprobs_backward(const LogprobsBackParams &p, int in_dtype, cudaStream_t s);
+
+constexpr uint32_t kGradSrcBf16 = 1, kGradDstBf16 = 2, kGradSrcVector = 4, kGradDstVector = 8;
+struct GradTensor {
+    const void *src;
+    void *dst;
+    int64_t n;
+    uint32_t flags;                // kGrad*; Vector: starts on a 32-byte boundary
+};
+// Blocks of a launch (each leaves one partial sum), on at most kGradSms multiprocessors.
+constexpr int kGradSms = 152;
+unsigned grad_blocks(int num_sms);
+size_t grad_workspace(int64_t n);
+bool grads_fit(const GradTensor *tensors, int64_t n);
+cudaError_t launch_grad_norm(const GradTensor *tensors, int64_t n, double *partial, float *norm, int num_sms,
+                             cudaStream_t s);
+cudaError_t launch_clip_grads(const GradTensor *tensors, int64_t n, double *partial, float max_norm, float *norm,
+                              int num_sms, cudaStream_t s);
 
 }  // namespace mxg

@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -21,6 +22,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "mxgemm.h"
 
@@ -38,6 +40,17 @@ struct Entries {
     decltype(&mxgemm_moe_combine) moe_combine;
     decltype(&mxgemm_moe_combine_backward) moe_combine_backward;
     decltype(&mxgemm_sf_bytes) sf_bytes;
+    decltype(&mxgemm_embed) embed;
+    decltype(&mxgemm_embed_backward_workspace_bytes) embed_backward_workspace_bytes;
+    decltype(&mxgemm_embed_backward) embed_backward;
+    decltype(&mxgemm_qk_norm_rope) qk_norm_rope;
+    decltype(&mxgemm_qk_norm_rope_backward_workspace_bytes) qk_norm_rope_backward_workspace_bytes;
+    decltype(&mxgemm_qk_norm_rope_backward) qk_norm_rope_backward;
+    decltype(&mxgemm_logprobs) logprobs;
+    decltype(&mxgemm_logprobs_backward) logprobs_backward;
+    decltype(&mxgemm_grad_workspace_bytes) grad_workspace_bytes;
+    decltype(&mxgemm_grad_norm) grad_norm;
+    decltype(&mxgemm_clip_grads) clip_grads;
 };
 Entries g_entry;
 
@@ -490,6 +503,363 @@ PyObject *moe_combine_backward(Args a)
     return result(call, dy, dw);
 }
 
+// ---- the operators of a whole model
+
+float number(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred())
+        throw python_error();
+    return static_cast<float>(v);
+}
+
+// A torch dtype, or `otherwise` for None.
+at::ScalarType dtype_of(PyObject *o, at::ScalarType otherwise, const char *what)
+{
+    if (o == Py_None)
+        return otherwise;
+    if (!THPDtype_Check(o))
+        throw BadTensor(std::string(what) + " must be a torch dtype");
+    const at::ScalarType t = reinterpret_cast<THPDtype *>(o)->scalar_type;
+    in_dtype(t, what);
+    return t;
+}
+
+// Whole numbers of 32 or 64 bits, `n` of them (n < 0: any number).
+struct Ids {
+    const void *ptr = nullptr;
+    int64_t count = 0;
+    int bytes = 0;
+    c10::Device device = c10::Device(c10::kCPU);
+};
+
+Ids ids_of(PyObject *o, int64_t n, const Sizes *s, const char *what)
+{
+    Ids r;
+    const at::Tensor *t = tensor(o, what);
+    if (!t)
+        return r;
+    if (!t->is_contiguous() || (t->scalar_type() != at::kInt && t->scalar_type() != at::kLong) ||
+        (n >= 0 && t->numel() != n) || (s && t->device() != s->device))
+        throw BadTensor(std::string(what) + " must be a contiguous int32 or int64 tensor" +
+                        (n >= 0 ? " of " + std::to_string(n) + " elements" : "") + " on the inputs' device");
+    check_device(*t, what);
+    r.ptr = t->const_data_ptr();
+    r.count = t->numel();
+    r.bytes = static_cast<int>(t->element_size());
+    r.device = t->device();
+    return r;
+}
+
+// (ids, table, scale, dtype, out)
+PyObject *embed(Args a)
+{
+    const Sizes s = matrix(a[1], "table");
+    const Ids ids = ids_of(a[0], -1, &s, "ids");
+    if (!ids.ptr && ids.count == 0)
+        throw BadTensor("ids must hold at least one id");
+    const float scale = number(a[2]);
+    const at::Tensor *to = tensor(a[4], "out");
+    const at::ScalarType dt = to && a[3] == Py_None ? to->scalar_type() : dtype_of(a[3], s.dtype, "dtype");
+    const int out_dtype = in_dtype(dt, "out");
+    Out out;
+    output(out, a[4], true, {ids.count, s.cols}, dt, s, "out");
+    const auto call = [&] {
+        return g_entry.embed(s.in_dtype, s.ptr, s.stride, s.rows, s.cols, ids.ptr, ids.bytes, ids.count, scale,
+                             out_dtype, out.ptr, current_stream(s));
+    };
+    return result(call, out);
+}
+
+// (dy, ids, vocab, scale, dtype, add, dtable, workspace)
+PyObject *embed_backward(Args a)
+{
+    const Sizes s = matrix(a[0], "dy");
+    const Ids ids = ids_of(a[1], s.rows, &s, "ids");
+    const int64_t vocab = integer(a[2]);
+    const float scale = number(a[3]);
+    const at::Tensor *given = tensor(a[6], "dtable");
+    given = given ? given : tensor(a[5], "add");
+    const at::ScalarType dt = given && a[4] == Py_None ? given->scalar_type() : dtype_of(a[4], at::kFloat, "dtype");
+    const int out_dtype = in_dtype(dt, "dtable");
+    Out add, dtable;
+    output(add, a[5], false, {vocab, s.cols}, dt, s, "add");
+    // sizes that the library refuses make no tensor
+    output(dtable, a[6], vocab >= 1 && vocab < (1ll << 30), {vocab, s.cols}, dt, s, "dtable");
+    const Workspace ws(a[7], g_entry.embed_backward_workspace_bytes(s.rows, vocab, s.cols), s);
+    const auto call = [&] {
+        return g_entry.embed_backward(s.in_dtype, s.ptr, s.stride, ids.ptr, ids.bytes, s.rows, vocab, s.cols, scale,
+                                      add.ptr, out_dtype, dtable.ptr, ws.ptr, ws.bytes, current_stream(s));
+    };
+    return result(call, dtable);
+}
+
+// [tokens, heads, D] with contiguous values.
+struct HeadsTensor {
+    const void *ptr = nullptr;
+    int64_t token = 0, head = 0;
+};
+
+HeadsTensor heads_of(const at::Tensor &t, const char *what)
+{
+    if (t.dim() != 3 || t.stride(2) != 1)
+        throw BadTensor(std::string(what) + " must be a 3-D CUDA tensor [tokens, heads, D] with contiguous heads");
+    check_device(t, what);
+    HeadsTensor h;
+    h.ptr = t.const_data_ptr();
+    h.token = t.stride(0);
+    h.head = t.stride(1);
+    return h;
+}
+
+Sizes heads_sizes(PyObject *o, const char *what)
+{
+    const at::Tensor *t = tensor(o, what);
+    if (!t)
+        throw BadTensor(std::string(what) + " is missing");
+    heads_of(*t, what);
+    Sizes s{};
+    s.rows = t->size(0);
+    s.stride = t->size(1);  // heads
+    s.cols = t->size(2);
+    s.dtype = t->scalar_type();
+    s.device = t->device();
+    s.in_dtype = in_dtype(s.dtype, what);
+    return s;
+}
+
+HeadsTensor heads_like(PyObject *o, const Sizes &s, const char *what)
+{
+    const at::Tensor *t = tensor(o, what);
+    if (!t)
+        return HeadsTensor();
+    if (t->dim() != 3 || t->size(0) != s.rows || t->size(1) != s.stride || t->size(2) != s.cols ||
+        t->scalar_type() != s.dtype || t->device() != s.device)
+        throw BadTensor(std::string(what) + " must be a " + shape_text({s.rows, s.stride, s.cols}) +
+                        " tensor of the same dtype and device");
+    return heads_of(*t, what);
+}
+
+// The caller's strided heads, or new dense ones.
+HeadsTensor heads_output(Out &out, PyObject *o, const Sizes &s, const char *what)
+{
+    if (o != Py_None) {
+        const HeadsTensor h = heads_like(o, s, what);
+        Py_INCREF(o);
+        out.object = o;
+        return h;
+    }
+    output(out, o, true, {s.rows, s.stride, s.cols}, s.dtype, s, what);
+    HeadsTensor h;
+    h.ptr = out.ptr;
+    h.token = s.stride * s.cols;
+    h.head = s.cols;
+    return h;
+}
+
+// What both directions take besides the heads: weights, angles, positions.
+struct Turn {
+    const void *q = nullptr, *k = nullptr;
+    int weight_dtype = 0;
+    const float *rope = nullptr;
+    int64_t rope_rows = 0, rotary = 0;
+    Ids positions;
+    int64_t q_heads, k_heads;
+    uint32_t flags;
+
+    bool norm() const { return q || k; }
+    Turn(const Sizes &s, PyObject *count, PyObject *q_weight, PyObject *k_weight, PyObject *table, PyObject *at,
+         PyObject *interleaved)
+    {
+        q_heads = integer(count);
+        k_heads = s.stride - q_heads;
+        int other = 0;
+        if (q_weight != Py_None)
+            q = weight_of(q_weight, s, &weight_dtype);
+        if (k_weight != Py_None)
+            k = weight_of(k_weight, s, &other);
+        if (q && k && weight_dtype != other)
+            throw BadTensor("q_weight and k_weight must have the same dtype");
+        weight_dtype = q ? weight_dtype : other;
+        if (const at::Tensor *t = tensor(table, "rope")) {
+            if (t->dim() != 2 || t->scalar_type() != at::kFloat || t->device() != s.device || !t->is_contiguous())
+                throw BadTensor("rope must be a contiguous 2-D float32 tensor on the inputs' device");
+            rope = static_cast<const float *>(t->const_data_ptr());
+            rope_rows = t->size(0);
+            rotary = t->size(1);
+        }
+        positions = ids_of(at, s.rows, &s, "positions");
+        flags = truth(interleaved) ? MXGEMM_ROPE_INTERLEAVED : 0;
+    }
+};
+
+// (x, q_heads, q_weight, k_weight, eps, rope, positions, interleaved, y, rstd)
+PyObject *qk_norm_rope(Args a)
+{
+    const Sizes s = heads_sizes(a[0], "x");
+    const HeadsTensor x = heads_like(a[0], s, "x");
+    const Turn t(s, a[1], a[2], a[3], a[5], a[6], a[7]);
+    const float eps = number(a[4]);
+    Out y, rstd;
+    const HeadsTensor to = heads_output(y, a[8], s, "y");
+    output(rstd, a[9], t.norm(), {s.rows, s.stride}, at::kFloat, s, "rstd");
+    const auto call = [&] {
+        return g_entry.qk_norm_rope(s.in_dtype, x.ptr, x.token, x.head, s.rows, t.q_heads, t.k_heads, s.cols, t.q, t.k,
+                                    t.weight_dtype, eps, t.rope, t.rope_rows, t.rotary, t.positions.ptr,
+                                    t.positions.bytes, t.flags, const_cast<void *>(to.ptr), to.token, to.head,
+                                    static_cast<float *>(rstd.ptr), current_stream(s));
+    };
+    return result(call, y, rstd);
+}
+
+// (dy, x, rstd, q_heads, q_weight, k_weight, rope, positions, interleaved, dx, dq_weight, dk_weight, workspace)
+PyObject *qk_norm_rope_backward(Args a)
+{
+    const Sizes s = heads_sizes(a[0], "dy");
+    const HeadsTensor dy = heads_like(a[0], s, "dy"), x = heads_like(a[1], s, "x");
+    const Turn t(s, a[3], a[4], a[5], a[6], a[7], a[8]);
+    Out rstd, dx, dq, dk;
+    output(rstd, a[2], false, {s.rows, s.stride}, at::kFloat, s, "rstd");
+    const HeadsTensor to = heads_output(dx, a[9], s, "dx");
+    output(dq, a[10], t.q != nullptr, {s.cols}, at::kFloat, s, "dq_weight");
+    output(dk, a[11], t.k != nullptr, {s.cols}, at::kFloat, s, "dk_weight");
+    const Workspace ws(a[12], t.norm() ? g_entry.qk_norm_rope_backward_workspace_bytes(s.rows, s.cols) : 0, s);
+    const auto call = [&] {
+        return g_entry.qk_norm_rope_backward(
+            s.in_dtype, dy.ptr, dy.token, dy.head, x.ptr, x.token, x.head, static_cast<const float *>(rstd.ptr), s.rows,
+            t.q_heads, t.k_heads, s.cols, t.q, t.k, t.weight_dtype, t.rope, t.rope_rows, t.rotary, t.positions.ptr,
+            t.positions.bytes, t.flags, const_cast<void *>(to.ptr), to.token, to.head, static_cast<float *>(dq.ptr),
+            static_cast<float *>(dk.ptr), ws.ptr, ws.bytes, current_stream(s));
+    };
+    return result(call, dx, dq, dk);
+}
+
+// (logits, targets, scale, top, logprob, entropy, stats, top_ids, top_logprobs)
+PyObject *logprobs(Args a)
+{
+    const Sizes s = matrix(a[0], "logits");
+    const Ids targets = ids_of(a[1], s.rows, &s, "targets");
+    const float scale = number(a[2]);
+    const int64_t top = integer(a[3]);
+    const bool make = top >= 1 && top <= 1024;  // numbers that the library refuses make no tensors
+    Out logprob, entropy, stats, ids, values;
+    output(logprob, a[4], targets.ptr != nullptr, {s.rows}, at::kFloat, s, "logprob");
+    const bool asked = a[5] == Py_True, none = a[5] == Py_False;
+    output(entropy, asked || none ? Py_None : a[5], asked, {s.rows}, at::kFloat, s, "entropy");
+    output(stats, a[6], true, {s.rows, 2}, at::kFloat, s, "stats");
+    output(ids, a[7], make, {s.rows, top}, at::kLong, s, "top_ids");
+    output(values, a[8], make, {s.rows, top}, at::kFloat, s, "top_logprobs");
+    const auto call = [&] {
+        return g_entry.logprobs(s.in_dtype, s.ptr, s.stride, s.rows, s.cols, scale, targets.ptr, targets.bytes,
+                                static_cast<float *>(logprob.ptr), static_cast<float *>(entropy.ptr),
+                                static_cast<float *>(stats.ptr), top, static_cast<int64_t *>(ids.ptr),
+                                static_cast<float *>(values.ptr), current_stream(s));
+    };
+    return result(call, logprob, entropy, stats, ids, values);
+}
+
+// (logits, targets, stats, dlogprob, entropy, dentropy, scale, dlogits)
+PyObject *logprobs_backward(Args a)
+{
+    const Sizes s = matrix(a[0], "logits");
+    const Ids targets = ids_of(a[1], s.rows, &s, "targets");
+    const float *g = static_cast<const float *>(flat(a[3], s.rows, at::kFloat, s, "dlogprob"));
+    const float *entropy = static_cast<const float *>(flat(a[4], s.rows, at::kFloat, s, "entropy"));
+    const float *h = static_cast<const float *>(flat(a[5], s.rows, at::kFloat, s, "dentropy"));
+    const float scale = number(a[6]);
+    Out stats, dlogits;
+    output(stats, a[2], false, {s.rows, 2}, at::kFloat, s, "stats");
+    output(dlogits, a[7], true, {s.rows, s.cols}, s.dtype, s, "dlogits");
+    const auto call = [&] {
+        return g_entry.logprobs_backward(s.in_dtype, s.ptr, s.stride, s.rows, s.cols, scale, targets.ptr,
+                                         targets.bytes, static_cast<const float *>(stats.ptr), g, entropy, h,
+                                         dlogits.ptr, current_stream(s));
+    };
+    return result(call, dlogits);
+}
+
+// A list or tuple of gradients as host arrays.
+struct Grads {
+    std::vector<const void *> ptr;
+    std::vector<int64_t> n;
+    std::vector<int> dtype;
+
+    Grads() = default;
+    // `like`: another list, of the same shapes and strides.
+    Grads(PyObject *list, const char *what, PyObject *like)
+    {
+        if (!PyList_Check(list) && !PyTuple_Check(list))
+            throw BadTensor(std::string(what) + " must be a list or tuple of tensors");
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(list);
+        if (like && PySequence_Fast_GET_SIZE(like) != count)
+            throw BadTensor(std::string(what) + " must hold a tensor for every gradient");
+        ptr.reserve(count);
+        n.reserve(count);
+        dtype.reserve(count);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const at::Tensor *t = tensor(PySequence_Fast_GET_ITEM(list, i), what);
+            if (!t)
+                throw BadTensor(std::string(what) + ": an entry is None");
+            check_device(*t, what);
+            if (!t->is_non_overlapping_and_dense())
+                throw BadTensor(std::string(what) + " must be dense tensors");
+            if (like) {
+                const at::Tensor &g = THPVariable_Unpack(PySequence_Fast_GET_ITEM(like, i));
+                if (t->sizes() != g.sizes() || (t->strides() != g.strides() && !(t->is_contiguous() && g.is_contiguous())))
+                    throw BadTensor(std::string(what) + " must have the gradients' shapes and strides");
+            }
+            ptr.push_back(t->const_data_ptr());
+            n.push_back(t->numel());
+            dtype.push_back(in_dtype(t->scalar_type(), what));
+        }
+    }
+};
+
+// Sizes of a call on a list: nothing but the device.
+Sizes current_sizes()
+{
+    Sizes s{};
+    s.device = c10::Device(c10::kCUDA, c10::cuda::current_device());
+    return s;
+}
+
+// (grads, norm, workspace)
+PyObject *grad_norm(Args a)
+{
+    const Grads g(a[0], "grads", nullptr);
+    const Sizes s = current_sizes();
+    const int64_t n = static_cast<int64_t>(g.n.size());
+    Out norm;
+    output(norm, a[1], true, {1}, at::kFloat, s, "norm");
+    const Workspace ws(a[2], g_entry.grad_workspace_bytes(n), s);
+    const auto call = [&] {
+        return g_entry.grad_norm(n, g.ptr.data(), g.n.data(), g.dtype.data(), static_cast<float *>(norm.ptr), ws.ptr,
+                                 ws.bytes, current_stream(s));
+    };
+    return result(call, norm);
+}
+
+// (grads, max_norm, out, norm, workspace)
+PyObject *clip_grads(Args a)
+{
+    const Grads g(a[0], "grads", nullptr);
+    const float max_norm = number(a[1]);
+    const bool apart = a[2] != Py_None;
+    const Grads to = apart ? Grads(a[2], "out", a[0]) : Grads();
+    const Sizes s = current_sizes();
+    const int64_t n = static_cast<int64_t>(g.n.size());
+    Out norm;
+    output(norm, a[3], true, {1}, at::kFloat, s, "norm");
+    const Workspace ws(a[4], g_entry.grad_workspace_bytes(n), s);
+    const auto call = [&] {
+        return g_entry.clip_grads(n, g.ptr.data(), g.n.data(), g.dtype.data(),
+                                  apart ? const_cast<void *const *>(to.ptr.data()) : nullptr,
+                                  apart ? to.dtype.data() : nullptr, max_norm, static_cast<float *>(norm.ptr), ws.ptr,
+                                  ws.bytes, current_stream(s));
+    };
+    return result(call, norm);
+}
+
 // One Python entry: argument count, C++ exceptions to Python ones.
 template <PyObject *(*F)(Args), Py_ssize_t N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t count)
@@ -542,6 +912,14 @@ PyMethodDef g_methods[] = {
     ROWOP(moe_dispatch, 5),
     ROWOP(moe_combine, 6),
     ROWOP(moe_combine_backward, 6),
+    ROWOP(embed, 5),
+    ROWOP(embed_backward, 8),
+    ROWOP(qk_norm_rope, 10),
+    ROWOP(qk_norm_rope_backward, 13),
+    ROWOP(logprobs, 9),
+    ROWOP(logprobs_backward, 8),
+    ROWOP(grad_norm, 3),
+    ROWOP(clip_grads, 5),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_rowops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
