@@ -623,11 +623,11 @@ MXGEMM_API int mxgemm_embed(int in_dtype, const void *table, int64_t table_strid
  *   add:    [vocab, K] of type out_dtype (the gradient so far), or NULL for zeros.
  *           dtable may be add itself: rows whose id does not occur are then neither
  *           read nor written.
- * Sums are FP32, of an id's rows in the order of its tokens (in parts of 32 sorted
- * rows), rounded once.  Ids outside the table add nothing, whatever their rows of dy
+ * Sums are FP32, of an id's rows in the order of its tokens (in parts of 8 or 32
+ * sorted rows), rounded once.  Ids outside the table add nothing, whatever their rows of dy
  * hold.  workspace: mxgemm_embed_backward_workspace_bytes(tokens, vocab, K) bytes (0
  * for sizes that the call refuses), 32-byte aligned, holding nothing between calls:
- * 16 bytes a token, a bit an id, and for more than 32 tokens 8 K bytes for every 32.
+ * 16 bytes a token and 8 K bytes for every 32 tokens, or every 8 of a small batch.
  * vocab below 2^30.
  */
 MXGEMM_API size_t mxgemm_embed_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t K);
@@ -671,10 +671,10 @@ MXGEMM_API int mxgemm_qk_norm_rope(int in_dtype, const void *x, int64_t x_token_
  * dx may be dy or x itself, with its strides.  Without weights x is not read (NULL, as
  * rstd and the weights' gradients) and dx is dy rotated back.  Tokens whose position is
  * outside the table have a gradient of zero and add nothing to the weights'.
- * workspace: mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, D) bytes (none
- * without weights), 32-byte aligned, holding nothing between calls.
+ * workspace: mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, q_heads + k_heads,
+ * D) bytes (none without weights), 32-byte aligned, holding nothing between calls.
  */
-MXGEMM_API size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t D);
+MXGEMM_API size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t heads, int64_t D);
 MXGEMM_API int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_stride,
                                             int64_t dy_head_stride, const void *x, int64_t x_token_stride,
                                             int64_t x_head_stride, const float *rstd, int64_t tokens, int64_t q_heads,

@@ -108,7 +108,7 @@ SIGNATURES = [
     ("mxgemm_qk_norm_rope", ctypes.c_int,
      [_I, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, ctypes.c_float, _P, _I64, _I64, _P, _I, ctypes.c_uint32,
       _P, _I64, _I64, _P, _P]),
-    ("mxgemm_qk_norm_rope_backward_workspace_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("mxgemm_qk_norm_rope_backward_workspace_bytes", ctypes.c_size_t, [_I64, _I64, _I64]),
     ("mxgemm_qk_norm_rope_backward", ctypes.c_int,
      [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _I64, _I64, _P, _I,
       ctypes.c_uint32, _P, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),

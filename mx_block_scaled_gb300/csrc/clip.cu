@@ -5,8 +5,8 @@
 // All tensors of a call (a thousand a launch) are one list of chunks of 4096 values;
 // a block takes a contiguous part of it, so that the tensors' number and sizes do not
 // matter.  The table of tensors is a kernel parameter: no copy to the device, and a
-// captured call keeps its own.  Squares are summed in FP32 sixteen at a time where
-// that sum keeps its precision, else from FP64 squares, and on in FP64; a block leaves
+// captured call keeps its own.  Squares are summed in FP32 16 or 32 at a time where
+// that sum keeps its precision, else in FP64, and on in FP64; a block leaves
 // one partial sum, and every block of the second kernel adds those in the same order.
 // That kernel walks its part backwards: what the first read last is still in L2.
 #include "mx_block.cuh"
@@ -29,15 +29,29 @@ struct Table {
     uint32_t chunks;
 };
 
-// A block's walk over its part of the chunks.
-template <int N>
+// A thread's values of a tensor come eight at a time, a block's next to each other: a
+// BF16 load is 16 bytes, an FP32 one 32, and a warp's accesses are consecutive whatever
+// the two types.
+constexpr int kVals = 8;
+constexpr int kSteps = static_cast<int>(kChunk / (kThreads * kVals));  // of a chunk
+static_assert(kSteps == 2, "a thread takes two runs of eight values of a chunk");
+
+// Part of a tensor that is a block's: chunks [from, to) counted in the tensor.
+struct Part {
+    int i;
+    int64_t from, to;
+};
+
+// A block's walk over the tensors of its chunks [c0, c1), forwards or backwards.
+template <int N, bool BACKWARDS>
 struct Walk {
     const Table<N> &table;
-    int i;             // tensor
-    uint32_t first;    // its first chunk
+    uint32_t c0, c1;
+    int i;
 
-    __device__ __forceinline__ Walk(const Table<N> &t, uint32_t chunk) : table(t)
+    __device__ __forceinline__ Walk(const Table<N> &t, uint32_t from, uint32_t to) : table(t), c0(from), c1(to)
     {
+        const uint32_t chunk = BACKWARDS ? to - 1 : from;
         int lo = 0, hi = t.n - 1;  // the first tensor that ends past the chunk
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -47,72 +61,93 @@ struct Walk {
                 lo = mid + 1;
         }
         i = lo;
-        first = i > 0 ? t.end[i - 1] : 0;
     }
-    __device__ __forceinline__ void to(uint32_t chunk)  // a neighbour of the last one
+    __device__ __forceinline__ bool next(Part &p)
     {
-        while (chunk >= table.end[i])
-            first = table.end[i++];
-        while (chunk < first) {
-            --i;
-            first = i > 0 ? table.end[i - 1] : 0;
+        if (c0 >= c1)
+            return false;
+        uint32_t begin = i > 0 ? table.end[i - 1] : 0;
+        if (BACKWARDS) {
+            while (begin >= c1)  // (tensors without values)
+                begin = --i > 0 ? table.end[i - 1] : 0;
+            const uint32_t first = begin > c0 ? begin : c0;
+            p = {i, first - begin, c1 - begin};
+            c1 = first;
+        } else {
+            while (table.end[i] <= c0)
+                begin = table.end[i++];
+            const uint32_t last = table.end[i] < c1 ? table.end[i] : c1;
+            p = {i, c0 - begin, last - begin};
+            c0 = last;
         }
-    }
-    // Values of this thread in the chunk: from, and how many (at most sixteen).
-    __device__ __forceinline__ int64_t at(uint32_t chunk, int &count) const
-    {
-        const int64_t from = static_cast<int64_t>(chunk - first) * kChunk + threadIdx.x * kLaneVals;
-        const int64_t left = table.t[i].n - from;
-        count = left >= kLaneVals ? kLaneVals : left > 0 ? static_cast<int>(left) : 0;
-        return from;
+        return true;
     }
 };
 
-// Sixteen values of a tensor as FP32 (zeros past `count`).
-__device__ __forceinline__ void load_values(const GradTensor &t, int64_t from, int count, float (&v)[kLaneVals])
+// Eight values as they are in memory; zeros past the tensor's end.
+struct Values {
+    uint32_t r[8];
+
+    template <bool BF16>
+    __device__ __forceinline__ void load(const GradTensor &t, int64_t at)
+    {
+        const int64_t left = t.n - at;
+        if (left >= kVals && (t.flags & kGradSrcVector)) {
+            if constexpr (BF16)
+                asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                             : "l"(static_cast<const char *>(t.src) + at * 2)
+                             : "memory");
+            else
+                ld_row32(static_cast<const char *>(t.src) + at * 4, r);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i)
+            r[i] = 0;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i)
+            if (i < left) {
+                if constexpr (BF16)
+                    r[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(t.src)[at + i]) << (16 * (i & 1));
+                else
+                    r[i] = static_cast<const uint32_t *>(t.src)[at + i];
+            }
+    }
+    template <bool BF16>
+    __device__ __forceinline__ F2 pair(int i) const
+    {
+        if constexpr (BF16)
+            return f2_bf16(r[i]);
+        else
+            return f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store_values(const GradTensor &t, int64_t at, const float (&v)[kVals])
 {
-    if (count == kLaneVals && (t.flags & kGradSrcVector)) {
-        if (t.flags & kGradSrcBf16) {
-            Raw16<kBf16> x;
-            x.load(static_cast<const char *>(t.src) + from * 2, true);
-#pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
-                v[i] = x.at(i);
+    const int64_t left = t.n - at;
+    if (left >= kVals && (t.flags & kGradDstVector)) {
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4 *>(static_cast<char *>(t.dst) + at * 2) = make_uint4(
+                pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         } else {
-            Raw16<kF32> x;
-            x.load(static_cast<const char *>(t.src) + from * 4, true);
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
-                v[i] = x.at(i);
+            for (int i = 0; i < kVals; ++i)
+                w[i] = __float_as_uint(v[i]);
+            st_row32(static_cast<char *>(t.dst) + at * 4, w);
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) {
-        v[i] = 0.0f;
-        if (i < count)
-            v[i] = (t.flags & kGradSrcBf16)
-                       ? __bfloat162float(static_cast<const __nv_bfloat16 *>(t.src)[from + i])
-                       : static_cast<const float *>(t.src)[from + i];
-    }
-}
-
-__device__ __forceinline__ void store_values(const GradTensor &t, int64_t from, int count, const float (&v)[kLaneVals])
-{
-    if (count == kLaneVals && (t.flags & kGradDstVector)) {
-        if (t.flags & kGradDstBf16)
-            store16<kBf16>(static_cast<char *>(t.dst) + from * 2, v);
-        else
-            store16<kF32>(static_cast<char *>(t.dst) + from * 4, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kLaneVals; ++i)
-        if (i < count) {
-            if (t.flags & kGradDstBf16)
-                static_cast<__nv_bfloat16 *>(t.dst)[from + i] = __float2bfloat16_rn(v[i]);
+    for (int i = 0; i < kVals; ++i)
+        if (i < left) {
+            if constexpr (BF16)
+                static_cast<__nv_bfloat16 *>(t.dst)[at + i] = __float2bfloat16_rn(v[i]);
             else
-                static_cast<float *>(t.dst)[from + i] = v[i];
+                static_cast<float *>(t.dst)[at + i] = v[i];
         }
 }
 
@@ -137,10 +172,64 @@ __device__ __forceinline__ double block_sum64(double v, double *part)
     return s;
 }
 
-// Sums of sixteen squares between these keep FP32's precision: none overflowed, and
-// what underflowed is below 2^-35 of the sum.
+// Sums of squares between these keep FP32's precision: none overflowed, and what
+// underflowed is below 2^-33 of the sum.
 constexpr float kSumLeast = 7.7e-34f, kSumMost = 1.2e30f;  // about 2^-110 and 2^100
-constexpr int kWindow = 4;                                 // FP32 sums that are added up before they go to FP64
+
+// Runs of eight values that a thread has in flight: 64 bytes.
+template <bool BF16>
+constexpr int kAhead = BF16 ? 4 : 2;
+
+// The sum of the squares of a block's part of a tensor, added to this thread's.
+template <bool BF16>
+__device__ __forceinline__ void sum_part(const GradTensor &t, const Part &p, double &sum)
+{
+    constexpr int U = kAhead<BF16>;
+    const int64_t last = p.to * kSteps;
+    int64_t step = p.from * kSteps;  // runs of a thread, counted in the tensor
+    Values next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        next[u].template load<BF16>(t, step + u < last ? ((step + u) * kThreads + threadIdx.x) * kVals : t.n);
+    for (; step < last; step += U) {
+        Values v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = next[u];
+        if (step + U < last)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                next[u].template load<BF16>(t, step + U + u < last ? ((step + U + u) * kThreads + threadIdx.x) * kVals
+                                                                   : t.n);
+        F2 s2 = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < kVals / 2; ++i)
+                s2 = f2_fma(v[u].template pair<BF16>(i), v[u].template pair<BF16>(i), s2);
+        float a, b;
+        f2_split(s2, a, b);
+        const float s = a + b;
+        if (s > kSumLeast && s < kSumMost) {
+            sum += s;
+        } else {
+            uint32_t any = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < (BF16 ? 4 : 8); ++i)
+                    any |= v[u].r[i] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+            if (any != 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < kVals / 2; ++i) {
+                        f2_split(v[u].template pair<BF16>(i), a, b);
+                        sum += static_cast<double>(a) * a + static_cast<double>(b) * b;
+                    }
+        }
+    }
+}
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
@@ -152,53 +241,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * blockIdx.x / gridDim.x);
     const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * (blockIdx.x + 1) / gridDim.x);
     double sum = 0.0;
-    float window = 0.0f;
-    int in_window = 0;
     if (c0 < c1) {
-        Walk<N> walk(table, c0);
-        float next[kLaneVals];
-        int count;
-        int64_t from = walk.at(c0, count);
-        load_values(table.t[walk.i], from, count, next);
-        for (uint32_t c = c0; c < c1; ++c) {
-            float v[kLaneVals];
-#pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
-                v[i] = next[i];
-            if (c + 1 < c1) {
-                walk.to(c + 1);
-                from = walk.at(c + 1, count);
-                load_values(table.t[walk.i], from, count, next);
-            }
-            F2 s2 = f2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kLaneVals; i += 2)
-                s2 = f2_fma(f2(v[i], v[i + 1]), f2(v[i], v[i + 1]), s2);
-            float a, b;
-            f2_split(s2, a, b);
-            const float s = a + b;
-            if (s > kSumLeast && s < kSumMost) {
-                window += s;
-                if (++in_window == kWindow) {
-                    sum += window;
-                    window = 0.0f;
-                    in_window = 0;
-                }
-            } else {
-                uint32_t any = 0;
-#pragma unroll
-                for (int i = 0; i < kLaneVals; ++i)
-                    any |= __float_as_uint(v[i]) & 0x7FFFFFFFu;
-                if (any != 0)
-#pragma unroll 1
-                    for (int i = 0; i < kLaneVals; ++i) {
-                        const double d = v[i];
-                        sum += d * d;
-                    }
-            }
+        Walk<N, false> walk(table, c0, c1);
+        for (Part p; walk.next(p);) {
+            if (table.t[p.i].flags & kGradSrcBf16)
+                sum_part<true>(table.t[p.i], p, sum);
+            else
+                sum_part<false>(table.t[p.i], p, sum);
         }
     }
-    sum = block_sum64(sum + window, part);
+    sum = block_sum64(sum, part);
     if (threadIdx.x == 0)
         partial[blockIdx.x] = sum;
 }
@@ -240,6 +292,41 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
         *norm = norm_of(total);
 }
 
+// A block's part of a tensor times the factor, from its end to its start.
+template <bool SRC, bool DST>
+__device__ __forceinline__ void clip_part(const GradTensor &t, const Part &p, float factor)
+{
+    constexpr int U = kAhead<SRC>;
+    const int64_t first = p.from * kSteps;
+    int64_t step = p.to * kSteps;  // one past the run that is next
+    auto at = [&](int64_t run) { return (run * kThreads + threadIdx.x) * kVals; };
+    Values next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        next[u].template load<SRC>(t, step - 1 - u >= first ? at(step - 1 - u) : t.n);
+    const F2 f = f2(factor, factor);
+    for (; step > first; step -= U) {
+        Values v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = next[u];
+        if (step - U > first)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                next[u].template load<SRC>(t, step - U - 1 - u >= first ? at(step - U - 1 - u) : t.n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (step - 1 - u < first)
+                break;
+            float o[kVals];
+#pragma unroll
+            for (int i = 0; i < kVals / 2; ++i)
+                f2_split(f2_mul(v[u].template pair<SRC>(i), f), o[2 * i], o[2 * i + 1]);
+            store_values<DST>(t, at(step - 1 - u), o);
+        }
+    }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_clip_kernel(const __grid_constant__ Table<N> table, const double *partial, int n, float max_norm, float *norm)
@@ -260,26 +347,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const float factor = block_factor;
     if (c0 >= c1)
         return;
-    Walk<N> walk(table, c1 - 1);
-    float next[kLaneVals];
-    int count;
-    int64_t from = walk.at(c1 - 1, count);
-    load_values(table.t[walk.i], from, count, next);
-    for (uint32_t c = c1; c-- > c0;) {
-        const int64_t at = from;
-        const int had = count;
-        const GradTensor &t = table.t[walk.i];
-        float v[kLaneVals];
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            v[i] = next[i] * factor;
-        if (c > c0) {
-            walk.to(c - 1);
-            from = walk.at(c - 1, count);
-            load_values(table.t[walk.i], from, count, next);
+    Walk<N, true> walk(table, c0, c1);
+    for (Part p; walk.next(p);) {
+        const GradTensor &t = table.t[p.i];
+        if (factor == 1.0f && t.src == t.dst)
+            continue;  // what stays as it is need not be written
+        if (t.flags & kGradSrcBf16) {
+            if (t.flags & kGradDstBf16)
+                clip_part<true, true>(t, p, factor);
+            else
+                clip_part<true, false>(t, p, factor);
+        } else {
+            if (t.flags & kGradDstBf16)
+                clip_part<false, true>(t, p, factor);
+            else
+                clip_part<false, false>(t, p, factor);
         }
-        if (factor != 1.0f || t.src != t.dst)  // what stays as it is need not be written
-            store_values(t, at, had, v);
     }
 }
 

@@ -5,8 +5,8 @@
 //
 // The gradient is a sum of rows by key.  The ids are sorted (stable), so that the
 // rows of an id are neighbours in token order; a warp sums 512 columns of 32 sorted
-// rows in FP32 registers and writes every run that lies inside its 32 rows at once.
-// Runs that cross into the next 32 leave partial sums, which a last kernel adds in
+// (or 8) rows in FP32 registers and writes every run of an id that lies inside them at
+// once.  Runs that cross into the next rows leave partial sums, which a last kernel adds in
 // order.  No atomics on values: the same sums in every run.
 #include "mx_block.cuh"
 #include "ops.h"
@@ -60,42 +60,99 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const EmbedParams p)
 }
 
 // --------------------------------------------------------------------- sort --
-// Stable radix sort of (id, token) by id in one cluster: every block owns a
-// contiguous part of the entries and every warp of it a contiguous run.  A pass
-// counts its run's digits by warp (lanes with the same digit find each other with
-// match.any), scans the counts over the warps, adds the other blocks' counts from
-// their shared memory, and walks the run again to write the entries in order.  Ids
-// outside the table get the key `vocab`, the last one.
+// (id, token) in the order of the ids, tokens of one id in theirs.  Ids outside the
+// table get the key `vocab`, the last one.
+__device__ __forceinline__ uint32_t key_of(const void *ids, bool wide, int64_t t, uint32_t vocab)
+{
+    const int64_t id = load_id(ids, wide, t);
+    return id >= 0 && id < vocab ? static_cast<uint32_t>(id) : vocab;
+}
+
+// Few tokens: every entry's place is the number of entries before it, counted by
+// comparing it with all of them.  Id and token make one 32-bit number (the sizes below
+// see to that), so a comparison is two instructions, and the blocks, of 64 entries each,
+// have nothing to tell each other: 8192 tokens are 67 million comparisons, half a
+// million a multiprocessor, and no barrier between blocks.
+constexpr int kRankThreads = 256;
+constexpr int kRankEntries = 64;  // of a block: 16 lanes with four each
+constexpr int kRankParts = kRankThreads / (kRankEntries / 4);
+constexpr int kRankTokenBits = 13;
+constexpr int64_t kRankTokens = 1 << kRankTokenBits;
+constexpr int64_t kRankVocab = (1ll << (32 - kRankTokenBits)) - 1;
+
+__global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const EmbedSortParams p)
+{
+    __shared__ __align__(16) uint32_t keys[kRankTokens];
+    __shared__ int rank[kRankEntries];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, n = static_cast<int>(p.tokens), first = static_cast<int>(blockIdx.x) * kRankEntries;
+    const int padded = (n + 4 * kRankParts - 1) / (4 * kRankParts) * (4 * kRankParts);
+    if (tid < kRankEntries)
+        rank[tid] = 0;
+#pragma unroll 4
+    for (int t = tid; t < padded; t += kRankThreads)  // what is past the end comes after everything
+        keys[t] = t < n ? key_of(p.ids, p.ids64, t, p.vocab) << kRankTokenBits | static_cast<uint32_t>(t) : 0xFFFFFFFFu;
+    __syncthreads();
+    const int part = tid / (kRankEntries / 4), entry = tid % (kRankEntries / 4) * 4;
+    uint32_t own[4];
+    int before[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        own[i] = first + entry + i < n ? keys[first + entry + i] : 0u;
+    const int steps = padded / (4 * kRankParts);
+    const uint4 *from = reinterpret_cast<const uint4 *>(keys) + part * steps;
+#pragma unroll 4
+    for (int j = 0; j < steps; ++j) {
+        const uint4 k = from[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            before[i] += (k.x < own[i]) + (k.y < own[i]) + (k.z < own[i]) + (k.w < own[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        before[i] += __shfl_xor_sync(0xFFFFFFFFu, before[i], 16);  // the warp's other part
+        if ((tid & 16) == 0)
+            atomicAdd(&rank[entry + i], before[i]);  // whole numbers: the order does not matter
+    }
+    __syncthreads();
+    if (tid < kRankEntries && first + tid < n) {
+        const uint32_t k = keys[first + tid];
+        p.entries0[rank[tid]] = make_uint2(k >> kRankTokenBits, k & (kRankTokens - 1));
+    }
+}
+
+// More tokens: a stable radix sort in one cluster.  Every block owns a contiguous part
+// of the entries and every warp of it a contiguous run.  A pass counts its run's digits
+// by warp (lanes with the same digit find each other with match.any), scans the counts
+// over the warps, adds the other blocks' counts from their shared memory, and walks the
+// run again to write the entries in order.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 4;
 constexpr int kMaxDigits = 1 << kEmbedDigitBits;
+constexpr int kHistStep = kSortWarps + 1;  // counts of a digit by warp, and a word between for the banks
+static_assert(kSortWarps == 32 && kMaxDigits <= kSortThreads, "a lane for every warp, a thread for every digit");
 
 __device__ __forceinline__ int ld_cluster(const int *p, int rank)
 {
     int v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-                 "ld.shared::cluster.b32 %0, [a];\n\t}"
-                 : "=r"(v)
-                 : "r"(smem_addr(p)), "r"(rank)
-                 : "memory");
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_addr(p), rank)) : "memory");
     return v;
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const EmbedSortParams p)
 {
-    extern __shared__ int hist[];  // [kSortWarps][digits]
+    extern __shared__ int hist[];  // [digits][kHistStep]
     __shared__ int own[kMaxDigits], first[kMaxDigits], warp_part[kSortWarps];
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tile = static_cast<int>(blockIdx.x), tiles = static_cast<int>(gridDim.x);
     const int digits = 1 << p.bits;
-    int *const mine = hist + warp * digits;
+    int *const mine = hist + warp;
     const int64_t s0 = (static_cast<int64_t>(tile) * kSortWarps + warp) * p.run;
     const int64_t s1 = s0 + p.run < p.tokens ? s0 + p.run : p.tokens;
-    for (int64_t i = static_cast<int64_t>(tile) * kSortThreads + tid; i < p.mark_words; i += tiles * kSortThreads)
-        p.marks[i] = 0;
 
     for (int pass = 0; pass < p.passes; ++pass) {
         const uint2 *from = pass & 1 ? p.entries0 : p.entries1;
@@ -106,22 +163,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
 #pragma unroll
             for (int i = 0; i < kSortAhead; ++i) {
                 const int64_t s = b + 32 * i + lane;
-                if (s >= s1) {
+                if (s >= s1)
                     e[i] = make_uint2(0xFFFFFFFFu, 0);
-                } else if (pass == 0) {
-                    const int64_t id = load_id(p.ids, p.ids64, s);
-                    e[i] = make_uint2(id >= 0 && id < p.vocab ? static_cast<uint32_t>(id) : p.vocab,
-                                      static_cast<uint32_t>(s));
-                } else {
+                else if (pass == 0)
+                    e[i] = make_uint2(key_of(p.ids, p.ids64, s, p.vocab), static_cast<uint32_t>(s));
+                else
                     e[i] = __ldcg(from + s);  // other blocks of the cluster wrote it
-                }
             }
         };
         auto digit = [&](const uint2 &v) { return static_cast<int>((v.x >> shift) & (digits - 1)); };
         load(s0);
-        for (int i = lane; i < digits; i += 32)
-            mine[i] = 0;
-        __syncwarp();
+        for (int i = tid; i < digits * kHistStep; i += kSortThreads)
+            hist[i] = 0;
+        __syncthreads();
         for (int64_t b = s0; b < s1; b += 32 * kSortAhead) {
             if (b > s0)
                 load(b);
@@ -133,31 +187,36 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
                 const int d = live ? digit(e[i]) : -1;
                 const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
                 if (live && lane == __ffs(peers) - 1)
-                    mine[d] += __popc(peers);
+                    mine[d * kHistStep] += __popc(peers);
                 __syncwarp();
             }
         }
         __syncthreads();
-        for (int d = tid; d < digits; d += kSortThreads) {
-            int sum = 0;
+        // the counts of a digit scanned over the warps, one warp a lane
 #pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int n = hist[w * digits + d];
-                hist[w * digits + d] = sum;
-                sum += n;
+        for (int d = warp; d < digits; d += kSortWarps) {
+            const int n = hist[d * kHistStep + lane];
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                incl += lane >= o ? v : 0;
             }
-            own[d] = sum;
+            hist[d * kHistStep + lane] = incl - n;
+            if (lane == 31)
+                own[d] = incl;
         }
         cluster_sync();
         // one digit a thread: the digits' counts over all blocks, scanned, and those of the blocks before
         int total = 0, before = 0;
         if (tid < digits)
-#pragma unroll 4
-            for (int r = 0; r < tiles; ++r) {
-                const int n = ld_cluster(&own[tid], r);
-                total += n;
-                before += r < tile ? n : 0;
-            }
+#pragma unroll
+            for (int r = 0; r < kEmbedSortTiles; ++r)
+                if (r < tiles) {
+                    const int n = ld_cluster(&own[tid], r);
+                    total += n;
+                    before += r < tile ? n : 0;
+                }
         int incl = total;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -184,14 +243,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
                 const bool live = b + 32 * i + lane < s1;
                 const int d = live ? digit(e[i]) : -1;
                 const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
-                const int at = live ? mine[d] : 0;
+                const int at = live ? mine[d * kHistStep] : 0;
                 __syncwarp();
                 if (live) {
                     if (lane == __ffs(peers) - 1)
-                        mine[d] = at + __popc(peers);
+                        mine[d * kHistStep] = at + __popc(peers);
                     __stcg(to + first[d] + at + __popc(peers & ((1u << lane) - 1u)), e[i]);
-                    if (pass == p.passes - 1 && p.mark_words > 0 && e[i].x < p.vocab)
-                        atomicOr(p.marks + (e[i].x >> 5), 1u << (e[i].x & 31));
                 }
                 __syncwarp();
             }
@@ -201,7 +258,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
 }
 
 // --------------------------------------------------------------------- sums --
-constexpr int kRun = 32;  // sorted rows of a warp
+// Sorted rows of a warp; fewer where few warps would each wait for 32 rows one after the other.
+constexpr int kRun = 32, kShortRun = 8;
+constexpr int64_t kShortRunWarps = 2048;
 
 // Sixteen sums of a lane as the gradient's values at k of row `id`.
 template <int OUT>
@@ -217,43 +276,77 @@ __device__ __forceinline__ void finish_row(const EmbedBackParams &p, uint32_t id
     store16<OUT>(p.dtable + (static_cast<int64_t>(id) * p.K + k) * E, v);
 }
 
-// The first `sum_blocks` blocks sum, the others write the rows whose id does not occur.
-template <int IN, int OUT>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBackParams p, uint32_t sum_blocks, int fill_rows)
+// First entry whose id is not below `id`, found by the warp's 32 probes at a time.
+__device__ __forceinline__ int64_t lower_bound(const EmbedBackParams &p, uint32_t id, int64_t from)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t n = p.tokens - from;
+    while (n > 0) {
+        const int64_t step = (n + 31) / 32, at = lane * step;
+        const uint32_t below = __popc(__ballot_sync(0xFFFFFFFFu, at < n && p.entries[from + at].x < id));
+        if (below == 0)
+            break;
+        // the last probe below `id` and what follows it up to the next probe
+        const int64_t skip = (below - 1) * step + 1, end = below * step < n ? below * step : n;
+        from += skip;
+        n = end - skip;
+    }
+    return from;
+}
+
+// The warp writes those of the rows v0 .. v0 + rows - 1 whose id does not occur.
+template <int OUT>
+__device__ __forceinline__ void fill_rows(const EmbedBackParams &p, int64_t v0, int64_t rows)
+{
+    constexpr int E = ElemBytes<OUT>::value;
+    const int lane = threadIdx.x & 31;
+    const int64_t v1 = v0 + rows < p.vocab ? v0 + rows : p.vocab, K = p.K;
+    if (v0 >= v1)
+        return;
+    int64_t at = lower_bound(p, static_cast<uint32_t>(v0), 0);
+    for (int64_t v = v0; v < v1;) {
+        const uint32_t id = at + lane < p.tokens ? p.entries[at + lane].x : p.vocab;
+        const uint32_t next = __shfl_sync(0xFFFFFFFFu, id, 0);  // the next id that occurs
+        for (const int64_t end = next < v1 ? next : v1; v < end; ++v)
+            for (int64_t k = lane * kLaneVals; k < K; k += kWarpVals) {
+                Raw16<OUT> a;
+                a.load(p.add + (v * K + k) * E, p.add != nullptr);
+#pragma unroll
+                for (int l = 0; l < Raw16<OUT>::kParts; ++l)
+                    st_row32(p.dtable + (v * K + k) * E + 32 * l, a.r[l]);
+            }
+        ++v;  // past the id that occurs
+        const int same = __popc(__ballot_sync(0xFFFFFFFFu, id == next));
+        at = same < 32 ? at + same : lower_bound(p, next + 1, at + 32);
+    }
+}
+
+// The first `sum_blocks` blocks sum, RUN sorted rows a warp; the others write the rows
+// whose id does not occur, `rows` to a warp.
+template <int IN, int OUT, int RUN>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBackParams p, uint32_t sum_blocks, int64_t rows)
 {
     constexpr int E = ElemBytes<IN>::value;
-    constexpr int kAhead = IN == kBf16 ? 4 : 2;
+    constexpr int kAhead = IN == kBf16 || RUN == kShortRun ? 4 : 2;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t K = p.K;
     if (blockIdx.x >= sum_blocks) {
-        const int64_t v0 = (static_cast<int64_t>(blockIdx.x - sum_blocks) * kWarps + (threadIdx.x >> 5)) * fill_rows;
-        const int64_t v1 = v0 + fill_rows < p.vocab ? v0 + fill_rows : p.vocab;
-        for (int64_t v = v0; v < v1; ++v) {
-            if ((p.marks[v >> 5] >> (v & 31)) & 1)
-                continue;
-            const int64_t row = v * K;
-            for (int64_t k = lane * kLaneVals; k < K; k += kWarpVals) {
-                Raw16<OUT> a;
-                a.load(p.add + (row + k) * ElemBytes<OUT>::value, p.add != nullptr);
-#pragma unroll
-                for (int l = 0; l < Raw16<OUT>::kParts; ++l)
-                    st_row32(p.dtable + (row + k) * ElemBytes<OUT>::value + 32 * l, a.r[l]);
-            }
-        }
+        const int64_t warp = static_cast<int64_t>(blockIdx.x - sum_blocks) * kWarps + (threadIdx.x >> 5);
+        fill_rows<OUT>(p, warp * rows, rows);
         return;
     }
     const uint32_t slices = static_cast<uint32_t>((K + kWarpVals - 1) / kWarpVals);
     const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), run = unit / slices;
-    const int64_t c0 = static_cast<int64_t>(run) * kRun, k = (unit - run * slices) * kWarpVals + lane * kLaneVals;
+    const int64_t c0 = static_cast<int64_t>(run) * RUN, k = (unit - run * slices) * kWarpVals + lane * kLaneVals;
     if (c0 >= p.tokens)
         return;
     const bool inside = k < K;
     const uint2 none = make_uint2(p.vocab, 0);
-    const uint2 e = c0 + lane < p.tokens ? p.entries[c0 + lane] : none;
+    const uint2 e = lane < RUN && c0 + lane < p.tokens ? p.entries[c0 + lane] : none;
     const uint32_t before = c0 > 0 ? p.entries[c0 - 1].x : 0xFFFFFFFFu;
-    const uint32_t after = c0 + kRun < p.tokens ? p.entries[c0 + kRun].x : 0xFFFFFFFFu;
+    const uint32_t after = c0 + RUN < p.tokens ? p.entries[c0 + RUN].x : 0xFFFFFFFFu;
     const int n = __popc(__ballot_sync(0xFFFFFFFFu, e.x < p.vocab));  // ids outside the table come last
     bool open = __shfl_sync(0xFFFFFFFFu, e.x, 0) == before;           // the current run began before these rows
     float sum[kLaneVals];
@@ -276,8 +369,8 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBackPara
             for (int l = 0; l < kLaneVals; ++l)
                 sum[l] += x[j].at(l);
             const uint32_t id = __shfl_sync(0xFFFFFFFFu, e.x, i);
-            const uint32_t next = i == kRun - 1 ? after : __shfl_sync(0xFFFFFFFFu, e.x, (i + 1) & 31);
-            if (i < kRun - 1 && next == id)
+            const uint32_t next = i == RUN - 1 ? after : __shfl_sync(0xFFFFFFFFu, e.x, (i + 1) & 31);
+            if (i < RUN - 1 && next == id)
                 continue;
             const bool goes_on = next == id;
             if (inside) {
@@ -296,13 +389,13 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBackPara
     }
 }
 
-// Runs over more than one warp's rows: a warp looks at the run that leaves its 32 rows
+// Runs over more than one warp's rows: a warp looks at the run that leaves RUN rows
 // and began in them, and adds its partial sums in order.  Long ones (more than kLong
 // parts) are added by all warps of the block, each every kJoinWarps-th part.
 constexpr int kJoinWarps = 8;
-constexpr int kLong = 32;
+constexpr int kLong = 8;
 
-template <int OUT>
+template <int OUT, int RUN>
 __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const EmbedBackParams p)
 {
     __shared__ float sums[kJoinWarps][kWarpVals];
@@ -327,7 +420,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
     for (int i = 0; i < kLaneVals; ++i)
         sum[i] = 0.0f;
     {
-        const int64_t run = run0 + warp, c0 = run * kRun, end = c0 + kRun;
+        const int64_t run = run0 + warp, c0 = run * RUN, end = c0 + RUN;
         int parts = 0;
         uint32_t id = p.vocab;
         if (end < p.tokens) {
@@ -335,7 +428,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
             const bool here = c0 == 0 || p.entries[c0 - 1].x != id;  // where the last id began
             if (id < p.vocab && here && p.entries[end].x == id) {
                 parts = 1;
-                for (int64_t c = end + static_cast<int64_t>(lane) * kRun;; c += 32 * kRun) {
+                for (int64_t c = end + static_cast<int64_t>(lane) * RUN;; c += 32 * RUN) {
                     const uint32_t same = __ballot_sync(0xFFFFFFFFu, c < p.tokens && p.entries[c].x == id);
                     parts += __popc(same);  // ids are sorted: a prefix of the lanes
                     if (same != 0xFFFFFFFFu)
@@ -348,7 +441,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
             id_of[warp] = id;
         }
         if (parts > 0 && parts <= kLong) {
-#pragma unroll 4
+#pragma unroll 2
             for (int j = 0; j < parts; ++j)
                 add_part(sum, run, j);
             if (inside)
@@ -409,7 +502,12 @@ int key_bits(int64_t vocab)
 cudaError_t launch_sort(const EmbedSortParams &p, int tiles, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1], both[2];
-    const size_t smem = static_cast<size_t>(kSortWarps) * sizeof(int) << p.bits;
+    if (p.passes == 0) {
+        const cudaLaunchConfig_t cfg =
+            row_launch(static_cast<unsigned>((p.tokens + kRankEntries - 1) / kRankEntries), kRankThreads, 0, s, attr);
+        return cudaLaunchKernelEx(&cfg, embed_rank_kernel, p);
+    }
+    const size_t smem = static_cast<size_t>(kHistStep) * sizeof(int) << p.bits;
     cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(tiles), kSortThreads, smem, s, attr);
     both[0] = attr[0];
     both[1].id = cudaLaunchAttributeClusterDimension;
@@ -421,24 +519,33 @@ cudaError_t launch_sort(const EmbedSortParams &p, int tiles, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, embed_sort_kernel, p);
 }
 
-template <int IN, int OUT>
-cudaError_t launch_sums(const EmbedBackParams &p, cudaStream_t s)
+template <int IN, int OUT, int RUN>
+cudaError_t launch_runs(const EmbedBackParams &p, bool fill, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const int64_t slices = (p.K + kWarpVals - 1) / kWarpVals, runs = (p.tokens + kRun - 1) / kRun;
+    const int64_t slices = (p.K + kWarpVals - 1) / kWarpVals, runs = (p.tokens + RUN - 1) / RUN;
     const unsigned sum_blocks = warp_blocks(runs * slices);
-    unsigned blocks = sum_blocks;
-    const int64_t row = p.K * ElemBytes<OUT>::value;
-    const int fill_rows = row >= 16384 ? 1 : static_cast<int>(16384 / row);
-    if (p.marks)
-        blocks += warp_blocks((p.vocab + fill_rows - 1) / fill_rows);
-    cudaLaunchConfig_t cfg = row_launch(blocks, kThreads, 0, s, attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sum_kernel<IN, OUT>, p, sum_blocks, fill_rows);
+    const int64_t row = p.K * ElemBytes<OUT>::value, rows = row >= 16384 ? 1 : 16384 / row;  // of a warp that fills
+    const unsigned fill_blocks = fill ? warp_blocks((p.vocab + rows - 1) / rows) : 0;
+    cudaLaunchConfig_t cfg = row_launch(sum_blocks + fill_blocks, kThreads, 0, s, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sum_kernel<IN, OUT, RUN>, p, sum_blocks, rows);
     if (e != cudaSuccess || runs == 1)
         return e;
     cfg = row_launch(static_cast<unsigned>((runs + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, s, attr);
     cfg.gridDim.y = static_cast<unsigned>(slices);
-    return cudaLaunchKernelEx(&cfg, embed_join_kernel<OUT>, p);
+    return cudaLaunchKernelEx(&cfg, embed_join_kernel<OUT, RUN>, p);
+}
+
+bool short_runs(int64_t tokens, int64_t K)
+{
+    return tokens / kRun * ((K + kWarpVals - 1) / kWarpVals) < kShortRunWarps;
+}
+
+template <int IN, int OUT>
+cudaError_t launch_sums(const EmbedBackParams &p, bool fill, cudaStream_t s)
+{
+    return short_runs(p.tokens, p.K) ? launch_runs<IN, OUT, kShortRun>(p, fill, s)
+                                     : launch_runs<IN, OUT, kRun>(p, fill, s);
 }
 
 int64_t round_up(int64_t n) { return (n + 31) / 32 * 32; }
@@ -448,7 +555,7 @@ int64_t round_up(int64_t n) { return (n + 31) / 32 * 32; }
 cudaError_t prepare_embed()
 {
     const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSortWarps * kMaxDigits * static_cast<int>(sizeof(int)));
+                                               kHistStep * kMaxDigits * static_cast<int>(sizeof(int)));
     return e == cudaSuccess ? cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
                             : e;
 }
@@ -460,15 +567,14 @@ cudaError_t launch_embed(const EmbedParams &p, int in_dtype, int out_dtype, int 
     return out_dtype == kBf16 ? launch_lookup<kF32, kBf16>(p, num_sms, s) : launch_lookup<kF32, kF32>(p, num_sms, s);
 }
 
-// Two buffers of entries, the marks of the ids that occur, two rows of partial sums for every 32 tokens.
-EmbedWorkspace embed_workspace(int64_t tokens, int64_t vocab, int64_t K)
+// Two buffers of entries, and two rows of partial sums for every run.
+EmbedWorkspace embed_workspace(int64_t tokens, int64_t K)
 {
     EmbedWorkspace w;
     w.entries[0] = 0;
     w.entries[1] = round_up(tokens * static_cast<int64_t>(sizeof(uint2)));
-    w.marks = 2 * w.entries[1];
-    w.partial = w.marks + round_up((vocab + 31) / 32 * 4);
-    const int64_t runs = (tokens + kRun - 1) / kRun;
+    w.partial = 2 * w.entries[1];
+    const int64_t run = short_runs(tokens, K) ? kShortRun : kRun, runs = (tokens + run - 1) / run;
     w.bytes = static_cast<size_t>(w.partial + (runs > 1 ? runs * 2 * K * 4 : 0));
     return w;
 }
@@ -476,15 +582,16 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t vocab, int64_t K)
 cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64, char *workspace, int in_dtype,
                                   int out_dtype, cudaStream_t s)
 {
-    const EmbedWorkspace w = embed_workspace(p.tokens, p.vocab, p.K);
+    const EmbedWorkspace w = embed_workspace(p.tokens, p.K);
     EmbedSortParams o;
     o.ids = ids;
     o.ids64 = ids64;
     o.tokens = p.tokens;
     o.vocab = p.vocab;
     const int bits = key_bits(p.vocab);
-    o.passes = (bits + kEmbedDigitBits - 1) / kEmbedDigitBits;
-    o.bits = (bits + o.passes - 1) / o.passes;
+    // 0: by counting
+    o.passes = p.tokens <= kRankTokens && p.vocab < kRankVocab ? 0 : (bits + kEmbedDigitBits - 1) / kEmbedDigitBits;
+    o.bits = o.passes > 0 ? (bits + o.passes - 1) / o.passes : 0;
     int tiles = 1;
     while (tiles < kEmbedSortTiles && static_cast<int64_t>(tiles) * kSortThreads < p.tokens)
         tiles *= 2;
@@ -492,19 +599,15 @@ cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64
     o.run = ((p.tokens + warps - 1) / warps + 31) / 32 * 32;
     o.entries0 = reinterpret_cast<uint2 *>(workspace + w.entries[0]);
     o.entries1 = reinterpret_cast<uint2 *>(workspace + w.entries[1]);
-    // where the gradient is added to the table's own rows, no other row is touched
-    const bool fill = p.add != p.dtable;
-    o.marks = fill ? reinterpret_cast<uint32_t *>(workspace + w.marks) : nullptr;
-    o.mark_words = fill ? (static_cast<int64_t>(p.vocab) + 31) / 32 : 0;
     const cudaError_t e = launch_sort(o, tiles, s);
     if (e != cudaSuccess)
         return e;
-    p.entries = o.passes & 1 ? o.entries0 : o.entries1;
-    p.marks = o.marks;
+    p.entries = o.passes > 0 && o.passes % 2 == 0 ? o.entries1 : o.entries0;
+    const bool fill = p.add != p.dtable;  // where the gradient is added in place, no other row is touched
     p.partial = reinterpret_cast<float *>(workspace + w.partial);
     if (in_dtype == kBf16)
-        return out_dtype == kBf16 ? launch_sums<kBf16, kBf16>(p, s) : launch_sums<kBf16, kF32>(p, s);
-    return out_dtype == kBf16 ? launch_sums<kF32, kBf16>(p, s) : launch_sums<kF32, kF32>(p, s);
+        return out_dtype == kBf16 ? launch_sums<kBf16, kBf16>(p, fill, s) : launch_sums<kBf16, kF32>(p, fill, s);
+    return out_dtype == kBf16 ? launch_sums<kF32, kBf16>(p, fill, s) : launch_sums<kF32, kF32>(p, fill, s);
 }
 
 }  // namespace mxg

@@ -7,9 +7,8 @@
 // R turns the first `rotary` values of a head in pairs (a, b) -> (a cos - b sin, b cos + a sin),
 // which are i and i + rotary/2, or 2i and 2i + 1.  A lane holds sixteen values of a
 // head in which every pair is whole (two runs of eight), and their eight angles are
-// the same eight consecutive ones in both orders: nothing but the two sums crosses
-// lanes.  A head takes a team of 4 to 32 lanes, a warp walks over the heads of a
-// token and keeps the token's angles in registers.
+// the same eight consecutive ones in both orders: nothing but a sum crosses lanes.  A
+// head takes a team of 1 to 32 lanes.
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -52,11 +51,19 @@ struct Raw8 {
         else
             return __uint_as_float(r[i]);
     }
+    // values 2i and 2i + 1, and the other way round
+    __device__ __forceinline__ F2 pair(int i) const { return f2(at(2 * i), at(2 * i + 1)); }
+    __device__ __forceinline__ F2 swapped(int i) const { return f2(at(2 * i + 1), at(2 * i)); }
 };
 
+// Four pairs as eight values of type DT.
 template <int DT>
-__device__ __forceinline__ void store8(char *p, const float *v)
+__device__ __forceinline__ void store8(char *p, const F2 *pairs)
 {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f2_split(pairs[i], v[2 * i], v[2 * i + 1]);
     if constexpr (DT == kBf16) {
         *reinterpret_cast<uint4 *>(p) =
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
@@ -102,43 +109,6 @@ __device__ __forceinline__ float team_sum(float v, int team)
     return v;
 }
 
-// v = runs a (0..7) and b (8..15); turned by the angles' cosines and sines (inverse: by minus the angles).
-template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(float (&v)[16], const float (&cs)[8], const float (&sn)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int p = INTERLEAVED ? 2 * i : i, q = INTERLEAVED ? 2 * i + 1 : i + 8;
-        const float x = v[p], y = v[q];
-        v[p] = x * cs[i] - y * sn[i];
-        v[q] = y * cs[i] + x * sn[i];
-    }
-}
-
-// The angles of a token: false where its position is outside the table.
-__device__ __forceinline__ bool load_angles(const HeadsCommon &p, const Place &at, int64_t token, float (&cs)[8],
-                                            float (&sn)[8], bool inverse)
-{
-    bool real = true;
-    int64_t position = 0;
-    if (p.rope) {
-        position = p.positions64 ? static_cast<const int64_t *>(p.positions)[token]
-                                 : static_cast<const int32_t *>(p.positions)[token];
-        real = position >= 0 && position < p.rope_rows;
-    }
-    const bool take = p.rope && real && at.turned;
-    const char *row = reinterpret_cast<const char *>(p.rope + position * p.rotary + at.angle);
-    Raw8<kF32> c, s;
-    c.load(row, take);
-    s.load(row + p.rotary / 2 * 4, take);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        cs[i] = take ? c.at(i) : 1.0f;
-        sn[i] = take ? (inverse ? -s.at(i) : s.at(i)) : 0.0f;
-    }
-    return real;
-}
-
 // Which weight a head takes (one past the last head: any that there is).
 __device__ __forceinline__ bool is_query(const HeadsCommon &p, int h)
 {
@@ -148,191 +118,438 @@ __device__ __forceinline__ bool is_query(const HeadsCommon &p, int h)
 // Type of the weights of heads that are only rotated.
 constexpr int kNoWeight = 0;
 
+// A lane's sixteen weights, as pairs.
 template <int WT>
-__device__ __forceinline__ void load_weight(float (&w)[16], const HeadsCommon &p, const Place &at, bool query)
+struct Weights {
+    F2 v[WT == kNoWeight ? 1 : 8];
+
+    __device__ __forceinline__ void load(const HeadsCommon &p, const Place &at, bool query)
+    {
+        if constexpr (WT != kNoWeight) {
+            constexpr int E = ElemBytes<WT>::value;
+            const char *from = query ? p.q_weight : p.k_weight;
+            Raw8<WT> a, b;
+            a.load(from + at.a * E, at.inside);
+            b.load(from + at.b * E, at.inside);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a.pair(i);
+                v[4 + i] = b.pair(i);
+            }
+        }
+    }
+};
+
+// A warp's walk over its share of the work: all steps (a group of neighbouring heads of
+// a token, a head to each team) in order, split evenly over the warps of the grid.  What
+// the steps ahead need is copied to the warp's own ring in shared memory (cp.async): the
+// values of TENSORS tensors, rstd (TENSORS 2), and at a token's first step its angles,
+// whose address waits for the token's position.  A warp that loads a token's heads into
+// registers instead pays for that chain of latencies at every token.
+constexpr int kDepth = 4;  // a power of two
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
-    if constexpr (WT != kNoWeight) {
-        constexpr int E = ElemBytes<WT>::value;
-        const char *from = query ? p.q_weight : p.k_weight;
-        Raw8<WT> a, b;
-        a.load(from + at.a * E, at.inside);
-        b.load(from + at.b * E, at.inside);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void lds16(uint32_t from, uint32_t *r)
+{
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(from)
+                 : "memory");
+}
+
+template <int IN, int TENSORS>
+struct Ring {
+    static constexpr int E = ElemBytes<IN>::value;
+    static constexpr int kPieces = E / 2;       // 16-byte pieces of a run of eight
+    static constexpr int kPlane = 32 * 16;      // a piece of all lanes
+    static constexpr int kStage = 2 * TENSORS * kPieces * kPlane + (TENSORS == 2 ? 32 * 4 : 0);
+    // stages and angles (16 floats a member, a slot for every token under way) of a warp
+    static __device__ __host__ __forceinline__ int bytes(int team) { return kDepth * (kStage + team * 64); }
+
+    const HeadsCommon &p;
+    const Place at;
+    const int team, member, mine, side;        // mine: the team's head of a group
+    const int to_b;                            // bytes from a lane's first run to its second
+    const uint32_t own, angles;                // this lane's place in stage 0; the angle slots
+    const uint32_t own_rstd;                   // its team's rstd in stage 0
+    const char *const other;                   // TENSORS 2: dy
+    const int64_t other_token, other_head;
+    const float *const rstd;
+    int left;                                  // steps to finish
+    int64_t token;                             // of the current step
+    int head, stage, slot;                     // head: the team's
+    // the copying side: the next step's token, head and where its values are
+    int64_t f_token, f_position;
+    int f_head, f_stage, f_slot;
+    const char *f_x, *f_other;
+    const float *f_rstd;
+    uint32_t real;                             // bit d: the token of angle slot d has a position of the table
+
+    __device__ __forceinline__ int64_t position_of(int64_t t) const
+    {
+        if (!p.rope || t >= p.tokens)
+            return 0;
+        return p.positions64 ? static_cast<const int64_t *>(p.positions)[t] : static_cast<const int32_t *>(p.positions)[t];
+    }
+
+    __device__ __forceinline__ Ring(const HeadsCommon &params, const Place &place, int team_size, uint32_t smem,
+                                    const char *other_p, int64_t other_t, int64_t other_h, const float *rstd_p)
+        : p(params), at(place), team(team_size), member(threadIdx.x & (team_size - 1)),
+          mine((threadIdx.x & 31) / team_size), side(32 / team_size), to_b((place.b - place.a) * E),
+          own(smem + (threadIdx.x >> 5) * bytes(team_size) + (threadIdx.x & 31) * 16),
+          angles(smem + (threadIdx.x >> 5) * bytes(team_size) + kDepth * kStage),
+          own_rstd(smem + (threadIdx.x >> 5) * bytes(team_size) + 2 * TENSORS * kPieces * kPlane + mine * 4),
+          other(other_p), other_token(other_t), other_head(other_h), rstd(rstd_p)
+    {
+        const int64_t groups = (p.heads + side - 1) / side, all = p.tokens * groups;
+        const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+        const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+        const int64_t each = all / warps, more = all % warps;  // the first `more` warps have one step more
+        const int64_t u0 = w * each + (w < more ? w : more);
+        left = static_cast<int>(each) + (w < more ? 1 : 0);
+        token = f_token = u0 / groups;
+        head = f_head = static_cast<int>(u0 - token * groups) * side + mine;
+        stage = slot = f_stage = f_slot = 0;
+        real = 0;
+        f_position = left > 0 ? position_of(f_token) : 0;
+        if (mine == 0 && !(p.rope && at.turned))  // angle 0 where nothing is copied
+            for (int d = 0; d < kDepth; ++d)
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(angle_at(d, i >> 2) + (i & 3) * 4),
+                                 "f"(i < 8 ? 1.0f : 0.0f)
+                                 : "memory");
+        if (left > 0)
+            new_token();
+#pragma unroll
+        for (int d = 0; d < kDepth - 1; ++d)
+            fetch(d < left);
+    }
+
+    // a 16-byte piece of this member's angles; the members' pieces lie side by side, which their banks need
+    __device__ __forceinline__ uint32_t angle_at(int d, int piece) const
+    {
+        return angles + ((d * 4 + piece) * team + member) * 16;
+    }
+
+    __device__ __forceinline__ void copy(uint32_t to, const char *from)  // this lane's two runs of a head
+    {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            cp_async16(to + i * kPlane, from + 16 * i);
+            cp_async16(to + (kPieces + i) * kPlane, from + to_b + 16 * i);
+        }
+    }
+
+    // The copying side comes to a token: its angles, and where its heads are.
+    __device__ __forceinline__ void new_token()
+    {
+        const int64_t position = f_position;
+        const bool good = !p.rope || (position >= 0 && position < p.rope_rows);
+        real = (real & ~(1u << f_slot)) | (static_cast<uint32_t>(good) << f_slot);
+        if (p.rope && good && at.turned && mine == 0) {
+            const float *row = p.rope + position * p.rotary + at.angle;
+            cp_async16(angle_at(f_slot, 0), row);
+            cp_async16(angle_at(f_slot, 1), row + 4);
+            cp_async16(angle_at(f_slot, 2), row + p.rotary / 2);
+            cp_async16(angle_at(f_slot, 3), row + p.rotary / 2 + 4);
+        }
+        f_position = position_of(f_token + 1);
+        f_slot = (f_slot + 1) & (kDepth - 1);
+        f_x = p.x + f_token * p.x_token + f_head * p.x_head + at.a * E;
+        if constexpr (TENSORS == 2) {
+            f_other = other + f_token * other_token + f_head * other_head + at.a * E;
+            f_rstd = rstd + f_token * p.heads + f_head;
+        }
+    }
+
+    __device__ __forceinline__ void fetch(bool any)
+    {
+        if (any) {
+            if (f_head - mine >= p.heads) {  // warp-uniform
+                f_head = mine;
+                ++f_token;
+                new_token();
+            }
+            if (at.inside && f_head < p.heads) {
+                copy(own + f_stage * kStage, f_x);
+                if constexpr (TENSORS == 2) {
+                    copy(own + f_stage * kStage + 2 * kPieces * kPlane, f_other);
+                    if (member == 0)
+                        cp_async4(own_rstd + f_stage * kStage, f_rstd);
+                }
+            }
+            f_head += side;
+            f_x += side * p.x_head;
+            if constexpr (TENSORS == 2) {
+                f_other += side * other_head;
+                f_rstd += side;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        f_stage = (f_stage + 1) & (kDepth - 1);
+    }
+
+    // Makes the current step's copies visible and starts those of a later one; false: no step is left.
+    __device__ __forceinline__ bool ready(bool &good)
+    {
+        if (left == 0)
+            return false;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        __syncwarp();  // the others' copies have landed too, and nobody reads the stage that is refilled now
+        good = (real >> slot) & 1;
+        fetch(left >= kDepth);
+        return true;
+    }
+    __device__ __forceinline__ bool live() const { return at.inside && head < p.heads; }
+    // The current step's two runs of a tensor (whatever the memory holds where there are none).
+    __device__ __forceinline__ void take(Raw8<IN> &a, Raw8<IN> &b, int tensor) const
+    {
+        const uint32_t from = own + stage * kStage + tensor * 2 * kPieces * kPlane;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            lds16(from + i * kPlane, a.r + 4 * i);
+            lds16(from + (kPieces + i) * kPlane, b.r + 4 * i);
+        }
+    }
+    __device__ __forceinline__ float take_rstd() const
+    {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(own_rstd + stage * kStage) : "memory");
+        return v;
+    }
+    // cosines (0..7) and sines (8..15) of this lane's angles
+    __device__ __forceinline__ void take_angles(float (&c)[16]) const
+    {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            lds16(angle_at(slot, i), r + 4 * i);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            c[i] = __uint_as_float(r[i]);
+    }
+    // On to the next step; true: it is another token's.
+    __device__ __forceinline__ bool step()
+    {
+        --left;
+        head += side;
+        stage = (stage + 1) & (kDepth - 1);
+        if (head - mine < p.heads)
+            return false;
+        head = mine;
+        ++token;
+        slot = (slot + 1) & (kDepth - 1);
+        return true;
+    }
+};
+
+// Pairs (a, b) -> (a cos - b sin, b cos + a sin), of the runs v[0..3] and v[4..7]; INVERSE: by minus the angles.
+template <bool INTERLEAVED, bool INVERSE>
+__device__ __forceinline__ void turn(F2 (&v)[8], const float (&c)[16])
+{
+    if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = a.at(i);
-            w[8 + i] = b.at(i);
+            float lo, hi;
+            f2_split(v[i], lo, hi);
+            const float sn = c[8 + i];
+            v[i] = f2_fma(f2(hi, lo), INVERSE ? f2(sn, -sn) : f2(-sn, sn), f2_mul(v[i], f2(c[i], c[i])));
+        }
+    } else {
+        const F2 minus = f2(-1.0f, -1.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 cs = f2(c[2 * i], c[2 * i + 1]), sn = f2(c[8 + 2 * i], c[9 + 2 * i]), neg = f2_mul(sn, minus);
+            const F2 a = v[i], b = v[4 + i];
+            v[i] = f2_fma(b, INVERSE ? sn : neg, f2_mul(a, cs));
+            v[4 + i] = f2_fma(a, INVERSE ? neg : sn, f2_mul(b, cs));
         }
     }
 }
 
 // ------------------------------------------------------------------ forward --
-// (and, without weights and by minus the angles, the gradient of the rotation alone)
-// A warp takes `steps` groups of neighbouring heads of a token; the next group is
-// loaded before the current one is finished.
-template <int IN, int WT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsParams p, int team, int steps, uint32_t per_token)
+// (and, INVERSE and without weights, the gradient of the rotation alone)
+template <int IN, int WT, bool INTERLEAVED, bool INVERSE>
+__global__ void __launch_bounds__(kThreads, IN == kBf16 ? 5 : 4) heads_kernel(const HeadsParams p, int team)
 {
     constexpr int E = ElemBytes<IN>::value;
+    extern __shared__ __align__(16) char heads_smem[];
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), token = unit / per_token;
-    if (token >= p.tokens)
-        return;
-    const int lane = threadIdx.x & 31, member = lane & (team - 1), side = 32 / team;
-    const Place at(member, p.D, p.rotary, INTERLEAVED);
-    const int first = static_cast<int>(unit - token * per_token) * steps * side + lane / team;
-    const int last = first + steps * side;  // heads first, first + side, ..
-    const char *x = p.x + token * p.x_token;
-    Raw8<IN> a, b;
-    a.load(x + first * p.x_head + at.a * E, at.inside && first < p.heads);
-    b.load(x + first * p.x_head + at.b * E, at.inside && first < p.heads);
-    float cs[8], sn[8], w[16];
-    const bool real = load_angles(p, at, token, cs, sn, p.inverse);
-    bool query = is_query(p, first);
-    load_weight<WT>(w, p, at, query);
+    const Place at((threadIdx.x & 31) & (team - 1), p.D, p.rotary, INTERLEAVED);
+    Ring<IN, 1> ring(p, at, team, smem_addr(heads_smem), nullptr, 0, 0, nullptr);
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    for (int h = first; h - lane / team < p.heads && h < last; h += side) {
-        float v[16];
+    const bool leads = ring.member == 0 && p.rstd != nullptr;
+    bool query = is_query(p, ring.head);
+    Weights<WT> w;
+    w.load(p, at, query);
+    char *y = p.y + ring.token * p.y_token + ring.head * p.y_head + at.a * E;
+    const int64_t y_step = ring.side * p.y_head;
+    for (bool good; ring.ready(good);) {
+        const int h = ring.head;
+        Raw8<IN> a, b;
+        ring.take(a, b, 0);
+        F2 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = a.at(i);
-            v[8 + i] = b.at(i);
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a.pair(i);
+            v[4 + i] = b.pair(i);
         }
-        const int next = h + side;
-        const bool more = at.inside && next < p.heads && next < last;
-        a.load(x + next * p.x_head + at.a * E, more);
-        b.load(x + next * p.x_head + at.b * E, more);
-        const bool live = h < p.heads;
         if constexpr (WT != kNoWeight) {
-            float ss = 0.0f;
+            F2 ss2 = f2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                ss = fmaf(v[i], v[i], ss);
-            ss = team_sum(ss, team);
-            const float rstd = __frsqrt_rn(ss * inv_d + p.eps);
-            if (member == 0 && p.rstd && live)
-                p.rstd[token * static_cast<int64_t>(p.heads) + h] = real ? rstd : 0.0f;
+            for (int i = 0; i < 8; ++i)
+                ss2 = f2_fma(v[i], v[i], ss2);
+            float lo, hi;
+            f2_split(ss2, lo, hi);
+            const float rstd = rsqrtf(team_sum(at.inside ? lo + hi : 0.0f, team) * inv_d + p.eps);
+            if (leads && h < p.heads)
+                p.rstd[ring.token * p.heads + h] = good ? rstd : 0.0f;
             if (query != is_query(p, h)) {
-                query = false;
-                load_weight<WT>(w, p, at, false);
+                query = is_query(p, h);
+                w.load(p, at, query);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[i] = v[i] * rstd * w[i];
+            for (int i = 0; i < 8; ++i)
+                v[i] = f2_mul(f2_mul(v[i], f2(rstd, rstd)), w.v[i]);
         }
-        turn<INTERLEAVED>(v, cs, sn);
-        if (!real)
+        if (at.turned) {  // values that are not turned have no partner
+            float c[16];
+            ring.take_angles(c);
+            turn<INTERLEAVED, INVERSE>(v, c);
+        }
+        if (!good)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[i] = 0.0f;
-        if (at.inside && live) {
-            char *y = p.y + token * p.y_token + h * p.y_head;
-            store8<IN>(y + at.a * E, v);
-            store8<IN>(y + at.b * E, v + 8);
+            for (int i = 0; i < 8; ++i)
+                v[i] = f2(0.0f, 0.0f);
+        if (ring.live()) {
+            store8<IN>(y, v);
+            store8<IN>(y + ring.to_b, v + 4);
         }
+        y += y_step;
+        if (ring.step())
+            y = p.y + ring.token * p.y_token + ring.head * p.y_head + at.a * E;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ----------------------------------------------------------------- backward --
-// Blocks stride over (token, group of heads) and keep the sums for both weights in
-// registers; each leaves its sums in partial[block][query, key][D].
+// The same walk with dy, x and rstd.  A warp keeps the sums for both weights in
+// registers; a block leaves its sums in partial[block][query, key][D].
 template <int IN, int WT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 3) heads_backward_kernel(const HeadsBackParams p, int team)
+__global__ void __launch_bounds__(kThreads, kHeadsBackPerSm) heads_backward_kernel(const HeadsBackParams p, int team)
 {
     constexpr int E = ElemBytes<IN>::value;
-    extern __shared__ float sums[];  // [kWarps][2][D]
+    extern __shared__ __align__(16) char heads_smem[];
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, member = lane & (team - 1), side = 32 / team;
-    const Place at(member, p.D, p.rotary, INTERLEAVED);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Place at(lane & (team - 1), p.D, p.rotary, INTERLEAVED);
+    Ring<IN, 2> ring(p, at, team, smem_addr(heads_smem), p.dy, p.dy_token, p.dy_head, p.rstd);
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    float dq[16], dk[16], w[16];
+    F2 dq[8], dk[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        dq[i] = dk[i] = 0.0f;
-    bool query = is_query(p, 0);
-    load_weight<WT>(w, p, at, is_query(p, 0));
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t token = static_cast<int64_t>(blockIdx.x) * kWarps + warp; token < p.tokens; token += step) {
-        float cs[8], sn[8];
-        const char *x = p.x + token * p.x_token, *dy = p.dy + token * p.dy_token;
-        const int first = lane / team;
+    for (int i = 0; i < 8; ++i)
+        dq[i] = dk[i] = f2(0.0f, 0.0f);
+    bool query = is_query(p, ring.head);
+    Weights<WT> w;
+    w.load(p, at, query);
+    char *dx = p.dx + ring.token * p.dx_token + ring.head * p.dx_head + at.a * E;
+    const int64_t dx_step = ring.side * p.dx_head;
+    for (bool good; ring.ready(good);) {
+        const int h = ring.head;
         Raw8<IN> xa, xb, ga, gb;
-        float rstd;
-        auto fetch = [&](int h) {
-            const bool take = at.inside && h < p.heads;
-            xa.load(x + h * p.x_head + at.a * E, take);
-            xb.load(x + h * p.x_head + at.b * E, take);
-            ga.load(dy + h * p.dy_head + at.a * E, take);
-            gb.load(dy + h * p.dy_head + at.b * E, take);
-            rstd = h < p.heads ? p.rstd[token * p.heads + h] : 0.0f;
-        };
-        fetch(first);
-        const bool real = load_angles(p, at, token, cs, sn, true);
-        for (int h = first; h - first < p.heads; h += side) {
-            float n[16], g[16];
+        ring.take(xa, xb, 0);
+        ring.take(ga, gb, 1);
+        float rstd = ring.take_rstd();
+        F2 g[8], n[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                n[i] = xa.at(i) * rstd;
-                n[8 + i] = xb.at(i) * rstd;
-                g[i] = ga.at(i);
-                g[8 + i] = gb.at(i);
-            }
-            const float r = rstd;
-            fetch(h + side);
-            const bool q = is_query(p, h);
-            if (q != query) {
-                query = q;
-                load_weight<WT>(w, p, at, q);
-            }
-            turn<INTERLEAVED>(g, cs, sn);
-            if (!real)  // nothing of such a token counts, whatever its memory holds
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    n[i] = g[i] = 0.0f;
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                dot = fmaf(g[i] * w[i], n[i], dot);
-            dot = team_sum(dot, team) * inv_d;
-            if (q) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    dq[i] = fmaf(g[i], n[i], dq[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    dk[i] = fmaf(g[i], n[i], dk[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                g[i] = (g[i] * w[i] - n[i] * dot) * r;
-            if (!real)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    g[i] = 0.0f;
-            if (at.inside && h < p.heads) {
-                char *dx = p.dx + token * p.dx_token + h * p.dx_head;
-                store8<IN>(dx + at.a * E, g);
-                store8<IN>(dx + at.b * E, g + 8);
-            }
+        for (int i = 0; i < 4; ++i) {
+            g[i] = ga.pair(i);
+            g[4 + i] = gb.pair(i);
+            n[i] = f2_mul(xa.pair(i), f2(rstd, rstd));
+            n[4 + i] = f2_mul(xb.pair(i), f2(rstd, rstd));
         }
+        if (at.turned) {  // values that are not turned have no partner
+            float c[16];
+            ring.take_angles(c);
+            turn<INTERLEAVED, true>(g, c);
+        }
+        if (__any_sync(0xFFFFFFFFu, !good || !ring.live()))  // what is not there counts nothing, whatever the memory holds
+            if (!good || !ring.live()) {
+                rstd = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    g[i] = n[i] = f2(0.0f, 0.0f);
+            }
+        if (query != is_query(p, h)) {
+            query = is_query(p, h);
+            w.load(p, at, query);
+        }
+        F2 gw[8], dot2 = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            gw[i] = f2_mul(g[i], w.v[i]);
+            dot2 = f2_fma(gw[i], n[i], dot2);
+        }
+        float lo, hi;
+        f2_split(dot2, lo, hi);
+        const float dot = team_sum(lo + hi, team) * -inv_d;
+        if (query) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dq[i] = f2_fma(g[i], n[i], dq[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dk[i] = f2_fma(g[i], n[i], dk[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            gw[i] = f2_mul(f2_fma(n[i], f2(dot, dot), gw[i]), f2(rstd, rstd));
+        if (!good)  // (a weight may be infinite)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                gw[i] = f2(0.0f, 0.0f);
+        if (ring.live()) {
+            store8<IN>(dx, gw);
+            store8<IN>(dx + ring.to_b, gw + 4);
+        }
+        dx += dx_step;
+        if (ring.step())
+            dx = p.dx + ring.token * p.dx_token + ring.head * p.dx_head + at.a * E;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rings are done with: the sums take their place
+    float *const sums = reinterpret_cast<float *>(heads_smem);  // [kWarps][2][D]
     // over the teams of the warp, then over the warps in order
+    float q_sum[16], k_sum[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f2_split(dq[i], q_sum[2 * i], q_sum[2 * i + 1]);
+        f2_split(dk[i], k_sum[2 * i], k_sum[2 * i + 1]);
+    }
     for (int o = team; o < 32; o <<= 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            dq[i] += __shfl_xor_sync(0xFFFFFFFFu, dq[i], o);
-            dk[i] += __shfl_xor_sync(0xFFFFFFFFu, dk[i], o);
+            q_sum[i] += __shfl_xor_sync(0xFFFFFFFFu, q_sum[i], o);
+            k_sum[i] += __shfl_xor_sync(0xFFFFFFFFu, k_sum[i], o);
         }
     if (lane < team && at.inside) {
-        float *mine = sums + warp * 2 * p.D;
+        float *out = sums + warp * 2 * p.D;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            mine[at.a + i] = dq[i];
-            mine[at.b + i] = dq[8 + i];
-            mine[p.D + at.a + i] = dk[i];
-            mine[p.D + at.b + i] = dk[8 + i];
+            out[at.a + i] = q_sum[i];
+            out[at.b + i] = q_sum[8 + i];
+            out[p.D + at.a + i] = k_sum[i];
+            out[p.D + at.b + i] = k_sum[8 + i];
         }
     }
     __syncthreads();
@@ -379,34 +596,65 @@ int team_of(int D)
     return team;
 }
 
+// Blocks that the work fills, at most those that are on the multiprocessors at once.
+int64_t blocks_of(int64_t tokens, int heads, int D, int64_t resident)
+{
+    const int side = 32 / team_of(D);
+    const int64_t steps = tokens * ((heads + side - 1) / side), blocks = (steps + kWarps - 1) / kWarps;
+    return blocks < resident ? blocks : resident;
+}
+
+constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM's rings
+
+template <int IN, int WT>
+cudaError_t prepare_kernels()
+{
+    constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    constexpr int kForward = kWarps * kDepth * (Ring<IN, 1>::kStage + 32 * 64);
+    cudaError_t e = cudaFuncSetAttribute(heads_kernel<IN, WT, false, false>, kAttr, kForward);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(heads_kernel<IN, WT, true, false>, kAttr, kForward);
+    if constexpr (WT == kNoWeight) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(heads_kernel<IN, WT, false, true>, kAttr, kForward);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(heads_kernel<IN, WT, true, true>, kAttr, kForward);
+    } else {
+        constexpr int kBackward = kWarps * kDepth * (Ring<IN, 2>::kStage + 32 * 64);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(heads_backward_kernel<IN, WT, false>, kAttr, kBackward);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(heads_backward_kernel<IN, WT, true>, kAttr, kBackward);
+    }
+    return e;
+}
+
 template <int IN, int WT>
 cudaError_t launch_forward(const HeadsParams &p, bool interleaved, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const int team = team_of(p.D), side = 32 / team, groups = (p.heads + side - 1) / side;
-    // all heads of a token to a warp where that leaves every multiprocessor sixteen warps; else fewer, down to one group
-    int parts = 1;
-    while (parts < groups && p.tokens * parts < 16ll * num_sms)
-        ++parts;
-    const int steps = (groups + parts - 1) / parts;
-    const uint32_t per_token = static_cast<uint32_t>((groups + steps - 1) / steps);
-    const int64_t warps = p.tokens * per_token;
+    const int team = team_of(p.D), smem = kWarps * Ring<IN, 1>::bytes(team), fit = kRingBytes / smem;
+    constexpr int kPerSm = IN == kBf16 ? 5 : 4;
+    const int64_t blocks = blocks_of(p.tokens, p.heads, p.D, static_cast<int64_t>(num_sms) * (fit < kPerSm ? fit : kPerSm));
     const cudaLaunchConfig_t cfg =
-        row_launch(static_cast<unsigned>((warps + kWarps - 1) / kWarps), kThreads, 0, s, attr);
-    return interleaved ? cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, true>, p, team, steps, per_token)
-                       : cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, false>, p, team, steps, per_token);
+        row_launch(static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(smem), s, attr);
+    if constexpr (WT == kNoWeight)
+        if (p.inverse)
+            return interleaved ? cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, true, true>, p, team)
+                               : cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, false, true>, p, team);
+    return interleaved ? cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, true, false>, p, team)
+                       : cudaLaunchKernelEx(&cfg, heads_kernel<IN, WT, false, false>, p, team);
 }
 
 template <int IN, int WT>
 cudaError_t launch_backward(const HeadsBackParams &p, bool interleaved, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    int64_t blocks = heads_back_blocks(p.tokens);
-    const int64_t most = static_cast<int64_t>(num_sms) * kHeadsBackPerSm;
-    blocks = blocks < most ? blocks : most;
-    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kThreads,
-                                        static_cast<size_t>(kWarps) * 2 * p.D * sizeof(float), s, attr);
-    const int team = team_of(p.D);
+    const int team = team_of(p.D), smem = kWarps * Ring<IN, 2>::bytes(team);  // more than the sums need: 8 D a warp
+    const int sms = num_sms < kHeadsBackSms ? num_sms : kHeadsBackSms, fit = kRingBytes / smem;
+    const int64_t blocks = blocks_of(p.tokens, p.heads, p.D,
+                                     static_cast<int64_t>(sms) * (fit < kHeadsBackPerSm ? fit : kHeadsBackPerSm));
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(smem), s, attr);
     const cudaError_t e = interleaved ? cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, true>, p, team)
                                       : cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, false>, p, team);
     if (e != cudaSuccess)
@@ -418,10 +666,23 @@ cudaError_t launch_backward(const HeadsBackParams &p, bool interleaved, int num_
 
 }  // namespace
 
-int64_t heads_back_blocks(int64_t tokens)
+cudaError_t prepare_heads()
 {
-    const int64_t blocks = (tokens + kWarps - 1) / kWarps, most = static_cast<int64_t>(kHeadsBackSms) * kHeadsBackPerSm;
-    return blocks < most ? blocks : most;
+    cudaError_t e = prepare_kernels<kBf16, kNoWeight>();
+    if (e == cudaSuccess)
+        e = prepare_kernels<kBf16, kBf16>();
+    if (e == cudaSuccess)
+        e = prepare_kernels<kBf16, kF32>();
+    if (e == cudaSuccess)
+        e = prepare_kernels<kF32, kNoWeight>();
+    if (e == cudaSuccess)
+        e = prepare_kernels<kF32, kBf16>();
+    return e == cudaSuccess ? prepare_kernels<kF32, kF32>() : e;
+}
+
+int64_t heads_back_blocks(int64_t tokens, int heads, int D)
+{
+    return blocks_of(tokens, heads, D, static_cast<int64_t>(kHeadsBackSms) * kHeadsBackPerSm);
 }
 
 cudaError_t launch_heads(const HeadsParams &p, int in_dtype, int weight_dtype, bool interleaved, int num_sms,

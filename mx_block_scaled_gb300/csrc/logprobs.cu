@@ -18,11 +18,11 @@
 namespace mxg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a block at most
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMargin = 3.0f;
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 1024, kChunkList = 512;
 constexpr int kKeptMaxima = 32;  // maxima that a thread keeps, of one or more chunks each
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
@@ -51,42 +51,59 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
-// Largest of a chunk's sixteen values; NaN if one is.
-template <int IN>
-__device__ __forceinline__ float chunk_max(const Raw16<IN> &x)
-{
-    if constexpr (IN == kBf16) {
-        uint32_t m = x.r[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.r[0][i]));
-        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
-    } else {
-        float m = x.at(0);
-#pragma unroll
-        for (int i = 1; i + 1 < kLaneVals; i += 2)
-            asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x.at(i)), "f"(x.at(i + 1)));
-        return max_nan(m, x.at(kLaneVals - 1));
-    }
-}
+// 32 bytes of a row: sixteen BF16 or eight FP32 values.
+template <int DT>
+struct Chunk {
+    static constexpr int kVals = 32 / ElemBytes<DT>::value;
+    uint32_t r[8];
 
-// A chunk with its values raised to `low`.
-template <int IN>
-__device__ __forceinline__ Raw16<IN> raised(const Raw16<IN> &x, float low)
-{
-    Raw16<IN> y;
-    if constexpr (IN == kBf16) {
-        const uint32_t l = pack_bf16(low, low);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y.r[0][i]) : "r"(x.r[0][i]), "r"(l));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-            y.r[i >> 3][i & 7] = __float_as_uint(max_nan(x.at(i), low));
+    __device__ __forceinline__ void load(const char *p) { ld_row32(p, r); }
+    __device__ __forceinline__ float at(int i) const
+    {
+        if constexpr (DT == kBf16)
+            return __uint_as_float((i & 1) ? (r[i >> 1] & 0xFFFF0000u) : (r[i >> 1] << 16));
+        else
+            return __uint_as_float(r[i]);
     }
-    return y;
-}
+    __device__ __forceinline__ F2 pair(int i) const
+    {
+        if constexpr (DT == kBf16)
+            return f2_bf16(r[i]);
+        else
+            return f2(at(2 * i), at(2 * i + 1));
+    }
+    // the largest value; NaN if one is
+    __device__ __forceinline__ float max() const
+    {
+        if constexpr (DT == kBf16) {
+            uint32_t m = r[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(r[i]));
+            return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        } else {
+            float m = at(0);
+#pragma unroll
+            for (int i = 1; i < 7; i += 2)
+                asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(at(i)), "f"(at(i + 1)));
+            return max_nan(m, at(7));
+        }
+    }
+    // the values, raised to `low`
+    __device__ __forceinline__ Chunk raised(float low) const
+    {
+        Chunk y;
+        const uint32_t l = DT == kBf16 ? pack_bf16(low, low) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (DT == kBf16)
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y.r[i]) : "r"(r[i]), "r"(l));
+            else
+                y.r[i] = __float_as_uint(max_nan(at(i), low));
+        }
+        return y;
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ float load_one(const char *p)
@@ -125,12 +142,12 @@ struct Sums {
 
 // The chunk's part of the sums; `low` = floor_of(ref).
 template <int IN, bool ENT>
-__device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Raw16<IN> &x, float ref, float low, float c)
+__device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Chunk<IN> &x, float ref, float low, float c)
 {
     const F2 minus = f2(-ref, -ref), cc = f2(c, c);
     if (ENT && low == neg_inf()) {
 #pragma unroll
-        for (int i = 0; i < kLaneVals / 2; ++i) {
+        for (int i = 0; i < Chunk<IN>::kVals / 2; ++i) {
             float a, b;
             f2_split(f2_mul(f2_add(x.pair(i), minus), cc), a, b);
             const float ea = exp2_fast(a), eb = exp2_fast(b);
@@ -139,11 +156,11 @@ __device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Raw16<IN> &x, fl
         }
         return;
     }
-    Raw16<IN> y = x;
+    Chunk<IN> y = x;
     if constexpr (ENT)
-        y = raised(x, low);
+        y = x.raised(low);
 #pragma unroll
-    for (int i = 0; i < kLaneVals / 2; ++i) {
+    for (int i = 0; i < Chunk<IN>::kVals / 2; ++i) {
         const F2 z = f2_mul(f2_add(y.pair(i), minus), cc);
         float a, b;
         f2_split(z, a, b);
@@ -167,6 +184,9 @@ __device__ __forceinline__ float key_value(unsigned long long key)
     u ^= (u >> 31) ? 0x80000000u : 0xFFFFFFFFu;
     return __uint_as_float(u);
 }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) { return map_to_cta(smem_addr(p), rank); }
 __device__ __forceinline__ float ld_f32(uint32_t a)
@@ -196,9 +216,9 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-// A row as a block sees it: whole chunks of sixteen values from a 32-byte boundary on,
-// which the blocks of the cluster share, and up to 15 values before and after, one to a
-// thread of the first block.
+// A row as a block sees it: whole chunks from a 32-byte boundary on, which the blocks of
+// the cluster share, and up to 15 values before and after, one to a thread of the first
+// block.
 template <int IN>
 struct Row {
     static constexpr int E = ElemBytes<IN>::value;
@@ -212,65 +232,56 @@ struct Row {
     {
         head = ((32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31) / E;
         head = head < V ? head : V;
-        chunks = (V - head) / kLaneVals;
+        chunks = (V - head) / Chunk<IN>::kVals;
         const int64_t per = (chunks + blocks - 1) / blocks;
         from = rank * per < chunks ? rank * per : chunks;
         to = from + per < chunks ? from + per : chunks;
-        extras = rank == 0 ? static_cast<int>(V - chunks * kLaneVals) : 0;
+        extras = rank == 0 ? static_cast<int>(V - chunks * Chunk<IN>::kVals) : 0;
     }
-    __device__ __forceinline__ int64_t first_of(int64_t chunk) const { return head + chunk * kLaneVals; }
-    __device__ __forceinline__ int64_t extra(int i) const { return i < head ? i : i + chunks * kLaneVals; }
-    __device__ __forceinline__ void load(Raw16<IN> &r, int64_t chunk) const { r.load(x + first_of(chunk) * E, true); }
+    __device__ __forceinline__ int64_t first_of(int64_t chunk) const { return head + chunk * Chunk<IN>::kVals; }
+    __device__ __forceinline__ int64_t extra(int i) const { return i < head ? i : i + chunks * Chunk<IN>::kVals; }
+    __device__ __forceinline__ void load(Chunk<IN> &r, int64_t chunk) const { r.load(x + first_of(chunk) * E); }
     __device__ __forceinline__ float one(int64_t v) const { return load_one<IN>(x + v * E); }
 };
 
 // TOP: every thread keeps the maxima of its chunks, `group` of them in one.
 template <int IN, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel(const LogprobsParams p, uint32_t blocks, int64_t group)
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams p, uint32_t blocks, int64_t group)
 {
-    extern __shared__ float maxima[];  // [kept][kThreads], TOP only
+    extern __shared__ float maxima[];  // [kept][threads], TOP only
     __shared__ float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps], warp_bound[kWarps];
     __shared__ float block_m, block_s, block_w, block_bound;
     __shared__ unsigned long long candidates[TOP ? kCandidates : 1];
     __shared__ unsigned long long warp_best[kWarps], list[32];
-    __shared__ uint32_t count;
+    __shared__ uint32_t count, chunks_found, chunk_list[TOP ? kChunkList : 1];
     griddep_launch_dependents();
     griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const uint32_t rank = blockIdx.x % blocks;
     const int64_t row = blockIdx.x / blocks;
     const Row<IN> r(p.x + row * p.stride, p.V, rank, blocks);
     const float c = p.scale * kLog2E, step_up = kMargin / c;
-    float target_x = 0.0f;
-    bool real = false;
-    if (rank == 0 && tid == 0) {
-        count = 0;
-        if (p.targets) {
-            const int64_t t = p.targets64 ? static_cast<const int64_t *>(p.targets)[row]
-                                          : static_cast<const int32_t *>(p.targets)[row];
-            real = t >= 0 && t < p.V;
-            if (real)
-                target_x = r.one(t);
-        }
-    }
+    if (tid == 0)
+        count = chunks_found = 0;
 
     // ---- the pass over the row
     Sums a = {neg_inf(), 0.0f, 0.0f};
     float low = neg_inf(), own_max = neg_inf();
     F2 s2 = f2(0.0f, 0.0f), w2 = f2(0.0f, 0.0f);
-    bool nan = false;
-    const int64_t mine = (r.to - r.from - tid + kThreads - 1) / kThreads;  // this thread's chunks (0 or less: none)
+    bool nan = false, real = false;
+    float target_x = 0.0f;  // thread 0's
+    const int64_t mine = (r.to - r.from - tid + threads - 1) / threads;  // this thread's chunks (0 or less: none)
     float kept = neg_inf();
     int64_t in_group = 0;
     float *keep = maxima + tid;
-    auto take = [&](const Raw16<IN> &x) {
-        float m = chunk_max<IN>(x);
+    auto take = [&](const Chunk<IN> &x) {
+        float m = x.max();
         if (!(m <= a.ref + step_up)) {  // (also where the reference is still missing, and for a NaN)
             if (m != m) {
                 nan = true;
                 m = neg_inf();
 #pragma unroll
-                for (int i = 0; i < kLaneVals; ++i)
+                for (int i = 0; i < Chunk<IN>::kVals; ++i)
                     m = fmaxf(m, x.at(i));
             }
             if (m > a.ref) {
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
             kept = fmaxf(kept, m);
             if (++in_group == group) {
                 *keep = kept;
-                keep += kThreads;
+                keep += threads;
                 kept = neg_inf();
                 in_group = 0;
             }
@@ -299,24 +310,31 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
             add_chunk<IN, ENT>(s2, w2, x, a.ref, low, c);
     };
     {
-        Raw16<IN> x[2];
+        Chunk<IN> x[2];
         int64_t at = r.from + tid;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (j < mine)
-                r.load(x[j], at + j * kThreads);
+                r.load(x[j], at + j * threads);
+        if (rank == 0 && tid == 0 && p.targets) {
+            const int64_t t = p.targets64 ? static_cast<const int64_t *>(p.targets)[row]
+                                          : static_cast<const int32_t *>(p.targets)[row];
+            real = t >= 0 && t < p.V;
+            if (real)
+                target_x = r.one(t);
+        }
         // the first reference: the largest value of the warp's first chunks
-        float m = mine > 0 ? chunk_max<IN>(x[0]) : neg_inf();
+        float m = mine > 0 ? x[0].max() : neg_inf();
         a.ref = warp_max(m == m ? m : neg_inf());
         low = floor_of(a.ref, c);
-        for (int64_t i = 0; i < mine; i += 2, at += 2 * kThreads) {
+        for (int64_t i = 0; i < mine; i += 2, at += 2 * threads) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (i + j >= mine)
                     break;
-                const Raw16<IN> now = x[j];
+                const Chunk<IN> now = x[j];
                 if (i + j + 2 < mine)
-                    r.load(x[j], at + (j + 2) * kThreads);
+                    r.load(x[j], at + (j + 2) * threads);
                 take(now);
             }
         }
@@ -351,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
     a.w = warp_sum(a.w);
     // at least `each` threads of every warp reach the warp's bound, and `of` warps the block's
     const int need = TOP ? (p.top + static_cast<int>(blocks) - 1) / static_cast<int>(blocks) : 1;
-    const int each = (need + kWarps - 1) / kWarps, of = (need + each - 1) / each;
+    const int each = (need + warps - 1) / warps, of = (need + each - 1) / each;
     float bound = neg_inf();
     if constexpr (TOP) {
         float left = own_max;
@@ -371,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
     __syncthreads();
     if (warp == 0) {
         Sums b = {neg_inf(), 0.0f, 0.0f};
-        if (lane < kWarps)
+        if (lane < warps)
             b = {warp_m[lane], warp_s[lane], warp_w[lane]};
         const float m = warp_max(b.ref);
         if (m != neg_inf())
@@ -384,13 +402,13 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
             block_w = b.w;
         }
         if constexpr (TOP) {
-            const float v = lane < kWarps ? warp_bound[lane] : neg_inf();
+            const float v = lane < warps ? warp_bound[lane] : neg_inf();
             int larger = 0;
-            for (int i = 0; i < kWarps; ++i) {
+            for (int i = 0; i < warps; ++i) {
                 const float o = __shfl_sync(0xFFFFFFFFu, v, i);
                 larger += o > v || (o == v && i < lane);
             }
-            if (lane < kWarps && larger == of - 1)
+            if (lane < warps && larger == of - 1)
                 block_bound = v;
         }
     }
@@ -452,22 +470,39 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
         if (at < kCandidates)
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
     };
-    if (own_max >= least && own_max != neg_inf()) {
-        for (int64_t i = 0; i < mine; i += group) {
-            if (!(maxima[i / group * kThreads + tid] >= least))
-                continue;
-            for (int64_t j = i; j < i + group && j < mine; ++j) {
-                const int64_t chunk = r.from + tid + j * kThreads;
-                Raw16<IN> x;
-                r.load(x, chunk);
-#pragma unroll
-                for (int n = 0; n < kLaneVals; ++n)
-                    offer(x.at(n), r.first_of(chunk) + n);
+    // the chunks whose maximum reaches it, thread by thread of a warp, all its maxima at once
+    {
+        const int kept_n = mine > 0 ? static_cast<int>((mine + group - 1) / group) : 0;
+        for (uint32_t has = __ballot_sync(0xFFFFFFFFu, own_max >= least && own_max != neg_inf()); has; has &= has - 1) {
+            const int from = __ffs(has) - 1, thread = warp * 32 + from;
+            const bool hit = lane < __shfl_sync(0xFFFFFFFFu, kept_n, from) && maxima[lane * threads + thread] >= least;
+            const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
+            uint32_t at = 0;
+            if (lane == 0)
+                at = atomicAdd(&chunks_found, __popc(hits) * static_cast<uint32_t>(group));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(hits & ((1u << lane) - 1u)) * static_cast<uint32_t>(group);
+            if (hit)
+                for (int64_t j = 0; j < group && at + j < kChunkList; ++j)
+                    chunk_list[at + j] = static_cast<uint32_t>(thread + (lane * group + j) * threads);
+        }
+    }
+    __syncthreads();
+    // their values, one to a thread at a time
+    if (chunks_found > kChunkList) {
+        if (tid == 0)  // too many for the list: so will the candidates be
+            asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to_count), "r"(kCandidates + 1) : "memory");
+    } else {
+        const int64_t own_chunks = r.to - r.from;
+        for (uint32_t i = tid; i < chunks_found * Chunk<IN>::kVals; i += threads) {
+            const uint32_t chunk = chunk_list[i / Chunk<IN>::kVals];
+            if (chunk < own_chunks) {
+                const int64_t index = r.first_of(r.from + chunk) + i % Chunk<IN>::kVals;
+                offer(r.one(index), index);
             }
         }
-        if (tid < r.extras)
-            offer(r.one(r.extra(tid)), r.extra(tid));
     }
+    if (tid < r.extras)
+        offer(r.one(r.extra(tid)), r.extra(tid));
     if (blocks > 1)
         cluster_sync();
     else
@@ -484,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
                 if (v > neg_inf() && key < last && key > best)
                     best = key;
             };
-            for (int64_t chunk = r.from + tid; chunk < r.to; chunk += kThreads) {
-                Raw16<IN> x;
+            for (int64_t chunk = r.from + tid; chunk < r.to; chunk += threads) {
+                Chunk<IN> x;
                 r.load(x, chunk);
 #pragma unroll
-                for (int i = 0; i < kLaneVals; ++i)
+                for (int i = 0; i < Chunk<IN>::kVals; ++i)
                     look(x.at(i), r.first_of(chunk) + i);
             }
             if (tid < r.extras)
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
             if (lane == 0)
                 warp_best[warp] = best;
             __syncthreads();
-            for (int w = 0; w < kWarps; ++w)
+            for (int w = 0; w < warps; ++w)
                 best = warp_best[w] > best ? warp_best[w] : best;
             if (tid == 0)
                 list[k] = best;  // 0: there are no more
@@ -512,15 +547,18 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
             cluster_sync();
         n = static_cast<uint32_t>(p.top) * blocks;
         if (rank == 0)
-            for (uint32_t i = tid; i < n; i += kThreads)
+            for (uint32_t i = tid; i < n; i += threads)
                 candidates[i] = ld_u64(in_block(list, i / p.top) + i % p.top * 8);
         __syncthreads();
     }
+    __syncwarp();
+    if (blocks > 1)
+        cluster_arrive();  // this block reads no other's memory any more
     if (rank == 0) {
         const float m = warp_m[0], ls = warp_s[0];
         int64_t *ids = p.top_ids + row * p.top;
         float *values = p.top_logprobs + row * p.top;
-        for (uint32_t i = tid; i < n; i += kThreads) {
+        for (uint32_t i = tid; i < n; i += threads) {
             const unsigned long long key = candidates[i];
             if (key == 0)
                 continue;
@@ -537,20 +575,22 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 4 : 2) logprobs_kernel
         for (uint32_t j = lane; j < n; j += 32)
             found += candidates[j] != 0;
         found = __reduce_add_sync(0xFFFFFFFFu, found);
-        for (uint32_t i = found + tid; i < static_cast<uint32_t>(p.top); i += kThreads) {
+        for (uint32_t i = found + tid; i < static_cast<uint32_t>(p.top); i += threads) {
             ids[i] = -1;
             values[i] = neg_inf();
         }
     }
+    __syncwarp();
     if (blocks > 1)
-        cluster_sync();  // no block leaves while another may still read its memory
+        cluster_wait();  // no block leaves while another may still read its memory
 }
 
 // ----------------------------------------------------------------- backward --
 // A block takes kBackChunks chunks a thread of a row.  VECTOR: the row and its gradient
 // start alike against 32-byte boundaries; else one value a thread at a time.
 constexpr int kBackChunks = 2;
-constexpr int64_t kBackVals = static_cast<int64_t>(kThreads) * kBackChunks * kLaneVals;
+template <int IN>
+constexpr int64_t kBackVals = static_cast<int64_t>(kThreads) * kBackChunks * Chunk<IN>::kVals;
 
 struct RowGrad {
     float m, c, shift;   // ln p = ln2 * t, t = (x - m) * c - shift
@@ -577,13 +617,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
     const char *x = p.x + row * p.stride;
     char *d = p.dlogits + row * V * E;
     const int64_t head = VECTOR ? min(static_cast<int64_t>(((32 - (reinterpret_cast<uintptr_t>(x) & 31)) & 31) / E), V) : 0;
-    const int64_t chunks = VECTOR ? (V - head) / kLaneVals : 0;
+    const int64_t chunks = VECTOR ? (V - head) / Chunk<IN>::kVals : 0;
     const int64_t c0 = static_cast<int64_t>(part) * kThreads * kBackChunks + tid;
-    Raw16<IN> v[kBackChunks];
+    Chunk<IN> v[kBackChunks];
     if constexpr (VECTOR)
 #pragma unroll
         for (int j = 0; j < kBackChunks; ++j)
-            v[j].load(x + (head + (c0 + j * kThreads) * kLaneVals) * E, c0 + j * kThreads < chunks);
+            if (c0 + j * kThreads < chunks)
+                v[j].load(x + (head + (c0 + j * kThreads) * Chunk<IN>::kVals) * E);
     const int64_t target = p.targets == nullptr ? -1
                            : p.targets64        ? static_cast<const int64_t *>(p.targets)[row]
                                                 : static_cast<const int32_t *>(p.targets)[row];
@@ -604,7 +645,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
         store_one<IN>(d + i * E, r.at(load_one<IN>(x + i * E)) + (i == target ? peak : 0.0f));
     };
     if constexpr (!VECTOR) {
-        for (int64_t i = part * kBackVals + tid; i < V && i < (part + 1) * kBackVals; i += kThreads)
+        for (int64_t i = part * kBackVals<IN> + tid; i < V && i < (part + 1) * kBackVals<IN>; i += kThreads)
             single(i);
         return;
     }
@@ -614,16 +655,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
     for (int j = 0; j < kBackChunks; ++j) {
         if (c0 + j * kThreads >= chunks)
             break;
-        const int64_t k = head + (c0 + j * kThreads) * kLaneVals;
-        float o[kLaneVals];
+        const int64_t k = head + (c0 + j * kThreads) * Chunk<IN>::kVals;
+        float o[Chunk<IN>::kVals];
         if (r.none || r.low == neg_inf()) {
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
+            for (int i = 0; i < Chunk<IN>::kVals; ++i)
                 o[i] = r.at(v[j].at(i));
         } else {
-            const Raw16<IN> y = ENT ? raised(v[j], r.low) : v[j];
+            const Chunk<IN> y = ENT ? v[j].raised(r.low) : v[j];
 #pragma unroll
-            for (int i = 0; i < kLaneVals / 2; ++i) {
+            for (int i = 0; i < Chunk<IN>::kVals / 2; ++i) {
                 const F2 t = f2_fma(f2_add(y.pair(i), minus), cc, shift);
                 float lo, hi;
                 f2_split(t, lo, hi);
@@ -631,27 +672,32 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
                 f2_split(f2_mul(e, ENT ? f2_fma(b2, t, a2) : a2), o[2 * i], o[2 * i + 1]);
             }
         }
-        if (target >= k && target < k + kLaneVals)
+        if (target >= k && target < k + Chunk<IN>::kVals)
 #pragma unroll
-            for (int i = 0; i < kLaneVals; ++i)
+            for (int i = 0; i < Chunk<IN>::kVals; ++i)
                 if (target == k + i)
                     o[i] += peak;
-        store16<IN>(d + k * E, o);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = IN == kBf16 ? pack_bf16(o[2 * i % Chunk<IN>::kVals], o[(2 * i + 1) % Chunk<IN>::kVals])
+                               : __float_as_uint(o[i]);
+        st_row32(d + k * E, w);
     }
-    const int64_t extras = V - chunks * kLaneVals;
+    const int64_t extras = V - chunks * Chunk<IN>::kVals;
     if (part == 0 && tid < extras)
-        single(tid < head ? tid : tid + chunks * kLaneVals);
+        single(tid < head ? tid : tid + chunks * Chunk<IN>::kVals);
 }
 
 template <int IN, bool ENT, bool TOP>
-cudaError_t launch_rows(const LogprobsParams &p, unsigned blocks, cudaStream_t s)
+cudaError_t launch_rows(const LogprobsParams &p, unsigned blocks, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1], both[2];
     // chunks of a thread at most (a row that starts off a 32-byte boundary may have one less)
-    const int64_t chunks = (p.V / kLaneVals + blocks - 1) / blocks, mine = (chunks + kThreads - 1) / kThreads;
+    const int64_t chunks = (p.V / Chunk<IN>::kVals + blocks - 1) / blocks, mine = (chunks + threads - 1) / threads;
     const int64_t group = mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1;
-    const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * kThreads * sizeof(float) : 0;
-    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), kThreads, smem, s, attr);
+    const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * threads * sizeof(float) : 0;
+    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), threads, smem, s, attr);
     if (blocks > 1) {
         both[0] = attr[0];
         both[1].id = cudaLaunchAttributeClusterDimension;
@@ -668,13 +714,21 @@ template <int IN>
 cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
 {
     // few rows: blocks of a cluster share one, while each has at least two chunks a thread
+    const int64_t chunks = p.V / Chunk<IN>::kVals;
     unsigned blocks = 1;
-    while (blocks < kLogprobsCluster && p.rows * blocks < 2ll * num_sms &&
-           p.V >= static_cast<int64_t>(blocks) * 4 * kThreads * kLaneVals)
+    while (blocks < kLogprobsCluster && p.rows * blocks < 2ll * num_sms && chunks >= blocks * 4ll * kThreads)
         blocks *= 2;
+    // short rows: fewer threads, down to a warp; with many rows a thread takes more chunks, so that a block's reductions
+    // are fewer
+    const int64_t least = p.rows >= 16ll * num_sms ? 8 : 2;
+    int threads = 32;
+    while (threads < kThreads && chunks >= blocks * 2 * least * threads)
+        threads *= 2;
     if (p.top > 0)
-        return p.entropy ? launch_rows<IN, true, true>(p, blocks, s) : launch_rows<IN, false, true>(p, blocks, s);
-    return p.entropy ? launch_rows<IN, true, false>(p, blocks, s) : launch_rows<IN, false, false>(p, blocks, s);
+        return p.entropy ? launch_rows<IN, true, true>(p, blocks, threads, s)
+                         : launch_rows<IN, false, true>(p, blocks, threads, s);
+    return p.entropy ? launch_rows<IN, true, false>(p, blocks, threads, s)
+                     : launch_rows<IN, false, false>(p, blocks, threads, s);
 }
 
 template <int IN, bool ENT>
@@ -685,7 +739,7 @@ cudaError_t launch_backward(const LogprobsBackParams &p, cudaStream_t s)
     // every row and its gradient start alike where the first do and the rows' steps are alike
     const uintptr_t off = reinterpret_cast<uintptr_t>(p.x) - reinterpret_cast<uintptr_t>(p.dlogits);
     const bool vector = (off & 31) == 0 && (p.rows == 1 || ((p.stride - p.V * E) & 31) == 0);
-    const uint32_t per_row = static_cast<uint32_t>((p.V + kBackVals - 1) / kBackVals);
+    const uint32_t per_row = static_cast<uint32_t>((p.V + kBackVals<IN> - 1) / kBackVals<IN>);
     const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * per_row), kThreads, 0, s, attr);
     return vector ? cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, true>, p, per_row)
                   : cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, false>, p, per_row);
@@ -695,7 +749,7 @@ cudaError_t launch_backward(const LogprobsBackParams &p, cudaStream_t s)
 
 bool logprobs_fits(int64_t rows, int64_t V)
 {
-    return rows * ((V + kBackVals - 1) / kBackVals) < (1ll << 31) && rows * kLogprobsCluster < (1ll << 31);
+    return rows * ((V + kBackVals<kF32> - 1) / kBackVals<kF32>) < (1ll << 31) && rows * kLogprobsCluster < (1ll << 31);
 }
 
 cudaError_t launch_logprobs(const LogprobsParams &p, int in_dtype, int num_sms, cudaStream_t s)

@@ -166,11 +166,9 @@ struct EmbedSortParams {
     bool ids64;
     int64_t tokens;
     uint32_t vocab;
-    int bits, passes;
+    int bits, passes;              // passes 0: few tokens, sorted by counting
     int64_t run;                   // entries of a warp, a multiple of 32
     uint2 *entries0, *entries1;    // (id, token): the first pass writes entries0, the second entries1, and so on
-    uint32_t *marks;               // a bit for every id that occurs, or NULL
-    int64_t mark_words;
 };
 
 struct EmbedBackParams {
@@ -181,15 +179,14 @@ struct EmbedBackParams {
     float scale;
     const char *add;               // dense rows of the gradient's type, or NULL; dtable itself: only rows that occur
     char *dtable;                  // dense rows
-    const uint2 *entries;          // (id, token) sorted; these three are the launcher's
-    const uint32_t *marks;
+    const uint2 *entries;          // (id, token) sorted; this and the sums of parts are the launcher's
     float *partial;
 };
 struct EmbedWorkspace {
-    int64_t entries[2], marks, partial;  // bytes from the workspace's start
+    int64_t entries[2], partial;   // bytes from the workspace's start
     size_t bytes;
 };
-EmbedWorkspace embed_workspace(int64_t tokens, int64_t vocab, int64_t K);
+EmbedWorkspace embed_workspace(int64_t tokens, int64_t K);
 // Set the sort's shared-memory and cluster opt-in on the current device.
 cudaError_t prepare_embed();
 cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64, char *workspace, int in_dtype,
@@ -230,8 +227,10 @@ struct HeadsBackParams : HeadsCommon {
 };
 // Blocks that leave partial sums, at most, on a part of at most kHeadsBackSms multiprocessors.
 constexpr int kHeadsBackSms = 152;
-constexpr int kHeadsBackPerSm = 4;
-int64_t heads_back_blocks(int64_t tokens);
+constexpr int kHeadsBackPerSm = 3;
+int64_t heads_back_blocks(int64_t tokens, int heads, int D);
+// Set the kernels' shared-memory opt-in on the current device.
+cudaError_t prepare_heads();
 cudaError_t launch_heads_backward(const HeadsBackParams &p, int in_dtype, int weight_dtype, bool interleaved,
                                   int num_sms, cudaStream_t s);
 

@@ -249,14 +249,15 @@ static bool embed_back_shape_ok(int64_t tokens, int64_t vocab, int64_t K)
 static bool embed_back_fits(int64_t tokens, int64_t vocab, int64_t K)
 {
     const int64_t slices = (K + kWarpVals - 1) / kWarpVals;
-    return slices < (1 << 16) && (tokens + 31) / 32 * slices < (1ll << 31) - (1ll << 30) && vocab < (1ll << 30);
+    // warps of the sums; their blocks and, a row a warp at most, those that fill are below 2^31
+    return slices < (1 << 16) && (tokens + 7) / 8 * slices < (1ll << 31);
 }
 
 size_t mxgemm_embed_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t K)
 {
     if (!embed_back_shape_ok(tokens, vocab, K) || !embed_back_fits(tokens, vocab, K))
         return 0;
-    return embed_workspace(tokens, vocab, K).bytes;
+    return embed_workspace(tokens, K).bytes;
 }
 
 int mxgemm_embed_backward(int in_dtype, const void *dy, int64_t dy_stride, const void *ids, int id_bytes,
@@ -274,7 +275,7 @@ int mxgemm_embed_backward(int in_dtype, const void *dy, int64_t dy_stride, const
         return MXGEMM_ERR_ALIGN;
     if (!embed_back_fits(tokens, vocab, K))
         return MXGEMM_ERR_UNSUPPORTED;
-    const size_t need = embed_workspace(tokens, vocab, K).bytes;
+    const size_t need = embed_workspace(tokens, K).bytes;
     if (!workspace || ws_bytes < need)
         return MXGEMM_ERR_WORKSPACE;
     if (!outputs_apart({{dense(dtable, vocab, row), 0b1}, {flat(workspace, static_cast<int64_t>(need))}},
@@ -344,11 +345,13 @@ int mxgemm_qk_norm_rope(int in_dtype, const void *x, int64_t x_token_stride, int
                                   static_cast<cudaStream_t>(stream)));
 }
 
-size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t D)
+size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t heads, int64_t D)
 {
-    if (tokens < 1 || tokens > kMaxRows || D < 16 || D % 16 != 0 || D > kHeadsMaxDim)
+    if (tokens < 1 || tokens > kMaxRows || heads < 1 || heads > kMaxRows / tokens || D < 16 || D % 16 != 0 ||
+        D > kHeadsMaxDim)
         return 0;
-    return static_cast<size_t>(heads_back_blocks(tokens) * 2 * D) * sizeof(float);
+    return static_cast<size_t>(heads_back_blocks(tokens, static_cast<int>(heads), static_cast<int>(D)) * 2 * D) *
+           sizeof(float);
 }
 
 int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_stride, int64_t dy_head_stride,
@@ -377,7 +380,7 @@ int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_
         !heads_align_ok(in, tokens, heads, e) || !aligned(q_weight, 32) || !aligned(k_weight, 32) ||
         !aligned(rstd, 4) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(workspace, 32))
         return MXGEMM_ERR_ALIGN;
-    const size_t need = norm ? mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, D) : 0;
+    const size_t need = norm ? mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, heads, D) : 0;
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
     const int64_t w = norm ? D * elem_bytes(weight_dtype) : 0;

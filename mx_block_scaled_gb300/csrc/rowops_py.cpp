@@ -72,7 +72,7 @@ const at::Tensor *tensor(PyObject *o, const char *what)
 {
     if (o == Py_None)
         return nullptr;
-    if (!THPVariable_Check(o))
+    if (!THPVariable_CheckExact(o) && !THPVariable_Check(o))
         throw BadTensor(std::string(what) + " must be a tensor");
     return &THPVariable_Unpack(o);
 }
@@ -723,7 +723,7 @@ PyObject *qk_norm_rope_backward(Args a)
     const HeadsTensor to = heads_output(dx, a[9], s, "dx");
     output(dq, a[10], t.q != nullptr, {s.cols}, at::kFloat, s, "dq_weight");
     output(dk, a[11], t.k != nullptr, {s.cols}, at::kFloat, s, "dk_weight");
-    const Workspace ws(a[12], t.norm() ? g_entry.qk_norm_rope_backward_workspace_bytes(s.rows, s.cols) : 0, s);
+    const Workspace ws(a[12], t.norm() ? g_entry.qk_norm_rope_backward_workspace_bytes(s.rows, s.stride, s.cols) : 0, s);
     const auto call = [&] {
         return g_entry.qk_norm_rope_backward(
             s.in_dtype, dy.ptr, dy.token, dy.head, x.ptr, x.token, x.head, static_cast<const float *>(rstd.ptr), s.rows,
@@ -796,11 +796,13 @@ struct Grads {
         ptr.reserve(count);
         n.reserve(count);
         dtype.reserve(count);
+        const c10::DeviceIndex device = c10::cuda::current_device();
         for (Py_ssize_t i = 0; i < count; ++i) {
             const at::Tensor *t = tensor(PySequence_Fast_GET_ITEM(list, i), what);
             if (!t)
                 throw BadTensor(std::string(what) + ": an entry is None");
-            check_device(*t, what);
+            if (!t->is_cuda() || t->get_device() != device)
+                throw BadTensor(std::string(what) + " must be on the current CUDA device");
             if (!t->is_non_overlapping_and_dense())
                 throw BadTensor(std::string(what) + " must be dense tensors");
             if (like) {
