@@ -22,8 +22,8 @@ constexpr int kThreads = 256;  // of a block at most
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMargin = 3.0f;
-constexpr int kCandidates = 1024, kChunkList = 512;
-constexpr int kKeptMaxima = 32;  // maxima that a thread keeps, of one or more chunks each
+constexpr int kCandidates = 512, kChunkList = 384;
+constexpr int kKeptMaxima = 32;  // maxima that a thread keeps, of one or more chunks each; a bit of a word for every one
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
@@ -172,7 +172,7 @@ __device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Chunk<IN> &x, fl
 }
 
 // Order of logits: by value, equal ones by index; a larger key comes first.
-__device__ __forceinline__ unsigned long long key_of(float v, int64_t index)
+__device__ __forceinline__ unsigned long long key_of(float v, int index)
 {
     uint32_t u = __float_as_uint(v + 0.0f);  // -0 equals 0
     u ^= (u >> 31) ? 0xFFFFFFFFu : 0x80000000u;
@@ -223,30 +223,29 @@ template <int IN>
 struct Row {
     static constexpr int E = ElemBytes<IN>::value;
     const char *x;
-    int64_t head, chunks, V;
-    int64_t from, to;  // this block's chunks
+    int head, chunks;
+    int from, to;  // this block's chunks
     int extras;
 
-    __device__ __forceinline__ Row(const char *row, int64_t vocab, uint32_t rank, uint32_t blocks)
-        : x(row), V(vocab)
+    __device__ __forceinline__ Row(const char *row, int V, int rank, int log_blocks) : x(row)
     {
-        head = ((32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31) / E;
+        head = static_cast<int>((32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31) / E;
         head = head < V ? head : V;
         chunks = (V - head) / Chunk<IN>::kVals;
-        const int64_t per = (chunks + blocks - 1) / blocks;
+        const int per = (chunks + (1 << log_blocks) - 1) >> log_blocks;
         from = rank * per < chunks ? rank * per : chunks;
         to = from + per < chunks ? from + per : chunks;
-        extras = rank == 0 ? static_cast<int>(V - chunks * Chunk<IN>::kVals) : 0;
+        extras = rank == 0 ? V - chunks * Chunk<IN>::kVals : 0;
     }
-    __device__ __forceinline__ int64_t first_of(int64_t chunk) const { return head + chunk * Chunk<IN>::kVals; }
-    __device__ __forceinline__ int64_t extra(int i) const { return i < head ? i : i + chunks * Chunk<IN>::kVals; }
-    __device__ __forceinline__ void load(Chunk<IN> &r, int64_t chunk) const { r.load(x + first_of(chunk) * E); }
-    __device__ __forceinline__ float one(int64_t v) const { return load_one<IN>(x + v * E); }
+    __device__ __forceinline__ int first_of(int chunk) const { return head + chunk * Chunk<IN>::kVals; }
+    __device__ __forceinline__ int extra(int i) const { return i < head ? i : i + chunks * Chunk<IN>::kVals; }
+    __device__ __forceinline__ const char *at(int v) const { return x + static_cast<int64_t>(v) * E; }
+    __device__ __forceinline__ float one(int v) const { return load_one<IN>(at(v)); }
 };
 
 // TOP: every thread keeps the maxima of its chunks, `group` of them in one.
 template <int IN, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams p, uint32_t blocks, int64_t group)
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int group)
 {
     extern __shared__ float maxima[];  // [kept][threads], TOP only
     __shared__ float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps], warp_bound[kWarps];
@@ -257,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
-    const uint32_t rank = blockIdx.x % blocks;
-    const int64_t row = blockIdx.x / blocks;
-    const Row<IN> r(p.x + row * p.stride, p.V, rank, blocks);
+    const int blocks = 1 << log_blocks, rank = static_cast<int>(blockIdx.x) & (blocks - 1);
+    const int64_t row = blockIdx.x >> log_blocks;
+    const Row<IN> r(p.x + row * p.stride, static_cast<int>(p.V), rank, log_blocks);
     const float c = p.scale * kLog2E, step_up = kMargin / c;
     if (tid == 0)
         count = chunks_found = 0;
@@ -270,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     F2 s2 = f2(0.0f, 0.0f), w2 = f2(0.0f, 0.0f);
     bool nan = false, real = false;
     float target_x = 0.0f;  // thread 0's
-    const int64_t mine = (r.to - r.from - tid + threads - 1) / threads;  // this thread's chunks (0 or less: none)
+    // this thread's chunks
+    const int mine = r.to - r.from > tid ? (r.to - r.from - tid + threads - 1) / threads : 0;
     float kept = neg_inf();
-    int64_t in_group = 0;
-    float *keep = maxima + tid;
+    int in_group = 0, keep = tid;
     auto take = [&](const Chunk<IN> &x) {
         float m = x.max();
         if (!(m <= a.ref + step_up)) {  // (also where the reference is still missing, and for a NaN)
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         if constexpr (TOP) {
             kept = fmaxf(kept, m);
             if (++in_group == group) {
-                *keep = kept;
+                maxima[keep] = kept;
                 keep += threads;
                 kept = neg_inf();
                 in_group = 0;
@@ -311,35 +310,37 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     };
     {
         Chunk<IN> x[2];
-        int64_t at = r.from + tid;
+        const char *from = r.at(r.first_of(r.from + tid));
+        const int64_t step = threads * 32;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (j < mine)
-                r.load(x[j], at + j * threads);
+                x[j].load(from + j * step);
         if (rank == 0 && tid == 0 && p.targets) {
             const int64_t t = p.targets64 ? static_cast<const int64_t *>(p.targets)[row]
                                           : static_cast<const int32_t *>(p.targets)[row];
             real = t >= 0 && t < p.V;
             if (real)
-                target_x = r.one(t);
+                target_x = r.one(static_cast<int>(t));
         }
         // the first reference: the largest value of the warp's first chunks
         float m = mine > 0 ? x[0].max() : neg_inf();
         a.ref = warp_max(m == m ? m : neg_inf());
         low = floor_of(a.ref, c);
-        for (int64_t i = 0; i < mine; i += 2, at += 2 * threads) {
+        for (int i = 0; i < mine; i += 2) {
+            from += 2 * step;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (i + j >= mine)
                     break;
                 const Chunk<IN> now = x[j];
                 if (i + j + 2 < mine)
-                    r.load(x[j], at + (j + 2) * threads);
+                    x[j].load(from + j * step);
                 take(now);
             }
         }
         if (TOP && in_group > 0)
-            *keep = kept;
+            maxima[keep] = kept;
         float lo, hi;
         f2_split(s2, lo, hi);
         a.s = lo + hi;
@@ -368,16 +369,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     a.s = warp_sum(a.s);
     a.w = warp_sum(a.w);
     // at least `each` threads of every warp reach the warp's bound, and `of` warps the block's
-    const int need = TOP ? (p.top + static_cast<int>(blocks) - 1) / static_cast<int>(blocks) : 1;
+    const int need = TOP ? (p.top + blocks - 1) / blocks : 1;
     const int each = (need + warps - 1) / warps, of = (need + each - 1) / each;
     float bound = neg_inf();
     if constexpr (TOP) {
-        float left = own_max;
-        for (int i = 0; i < each; ++i) {
-            bound = warp_max(left);
-            const uint32_t has = __ballot_sync(0xFFFFFFFFu, left == bound);
-            if (lane == __ffs(has) - 1)
-                left = neg_inf();
+        if (each == 1) {
+            bound = m_warp;
+        } else {  // the lane that `each` - 1 others come before
+            int larger = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float o = __shfl_sync(0xFFFFFFFFu, own_max, i);
+                larger += o > own_max || (o == own_max && i < lane);
+            }
+            bound = __shfl_sync(0xFFFFFFFFu, own_max, __ffs(__ballot_sync(0xFFFFFFFFu, larger == each - 1)) - 1);
         }
     }
     if (lane == 0) {
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     float log_s = 0.0f, row_m = neg_inf();
     if (rank == 0 && warp == 0) {
         Sums b = {neg_inf(), 0.0f, 0.0f};
-        if (static_cast<uint32_t>(lane) < blocks) {
+        if (lane < blocks) {
             b.ref = ld_f32(in_block(&block_m, lane));
             b.s = ld_f32(in_block(&block_s, lane));
             b.w = ld_f32(in_block(&block_w, lane));
@@ -459,10 +464,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
 
     // ---- the most probable tokens
     float least = block_bound;
-    for (uint32_t b = 0; b < blocks && blocks > 1; ++b)
+    for (int b = 0; b < blocks && blocks > 1; ++b)
         least = fminf(least, ld_f32(in_block(&block_bound, b)));
     const uint32_t to_count = in_block(&count, 0), to_list = in_block(candidates, 0);
-    auto offer = [&](float v, int64_t index) {
+    auto offer = [&](float v, int index) {
         if (!(v >= least) || v == neg_inf())
             return;
         uint32_t at;
@@ -470,35 +475,62 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         if (at < kCandidates)
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
     };
-    // the chunks whose maximum reaches it, thread by thread of a warp, all its maxima at once
-    {
-        const int kept_n = mine > 0 ? static_cast<int>((mine + group - 1) / group) : 0;
-        for (uint32_t has = __ballot_sync(0xFFFFFFFFu, own_max >= least && own_max != neg_inf()); has; has &= has - 1) {
-            const int from = __ffs(has) - 1, thread = warp * 32 + from;
-            const bool hit = lane < __shfl_sync(0xFFFFFFFFu, kept_n, from) && maxima[lane * threads + thread] >= least;
-            const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
-            uint32_t at = 0;
-            if (lane == 0)
-                at = atomicAdd(&chunks_found, __popc(hits) * static_cast<uint32_t>(group));
-            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(hits & ((1u << lane) - 1u)) * static_cast<uint32_t>(group);
-            if (hit)
-                for (int64_t j = 0; j < group && at + j < kChunkList; ++j)
-                    chunk_list[at + j] = static_cast<uint32_t>(thread + (lane * group + j) * threads);
+    // the chunks whose maximum reaches it
+    if (__any_sync(0xFFFFFFFFu, own_max >= least && own_max != neg_inf())) {
+        uint32_t hits = 0;
+        const int kept_n = own_max != neg_inf() ? (mine + group - 1) / group : 0;
+#pragma unroll 8
+        for (int i = 0; i < kept_n; ++i)
+            hits |= static_cast<uint32_t>(maxima[i * threads + tid] >= least) << i;
+        uint32_t at = __popc(hits) * group;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+            at += lane >= o ? v : 0;
         }
+        uint32_t start = 0;
+        if (lane == 31)
+            start = atomicAdd(&chunks_found, at);
+        at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits) * group;
+        for (; hits; hits &= hits - 1)
+            for (int j = 0; j < group; ++j, ++at)
+                if (at < kChunkList)
+                    chunk_list[at] = tid + ((__ffs(hits) - 1) * group + j) * threads;
     }
     __syncthreads();
-    // their values, one to a thread at a time
+    // their values
     if (chunks_found > kChunkList) {
         if (tid == 0)  // too many for the list: so will the candidates be
             asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to_count), "r"(kCandidates + 1) : "memory");
     } else {
-        const int64_t own_chunks = r.to - r.from;
-        for (uint32_t i = tid; i < chunks_found * Chunk<IN>::kVals; i += threads) {
-            const uint32_t chunk = chunk_list[i / Chunk<IN>::kVals];
-            if (chunk < own_chunks) {
-                const int64_t index = r.first_of(r.from + chunk) + i % Chunk<IN>::kVals;
-                offer(r.one(index), index);
+        // eight bytes a thread, two at a time
+        constexpr int kPart = Chunk<IN>::kVals / 4;
+        for (uint32_t i0 = tid; i0 < chunks_found * 4; i0 += 2 * threads) {
+            uint2 v[2];
+            int index[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t i = i0 + j * threads;
+                const uint32_t chunk = i < chunks_found * 4 ? chunk_list[i >> 2] : 0xFFFFFFFFu;
+                index[j] = -1;
+                if (chunk < static_cast<uint32_t>(r.to - r.from)) {
+                    index[j] = r.first_of(r.from + chunk) + (i & 3) * kPart;
+                    v[j] = *reinterpret_cast<const uint2 *>(r.at(index[j]));
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (index[j] >= 0) {
+                    if constexpr (IN == kBf16) {
+                        offer(__uint_as_float(v[j].x << 16), index[j]);
+                        offer(__uint_as_float(v[j].x & 0xFFFF0000u), index[j] + 1);
+                        offer(__uint_as_float(v[j].y << 16), index[j] + 2);
+                        offer(__uint_as_float(v[j].y & 0xFFFF0000u), index[j] + 3);
+                    } else {
+                        offer(__uint_as_float(v[j].x), index[j]);
+                        offer(__uint_as_float(v[j].y), index[j] + 1);
+                    }
+                }
         }
     }
     if (tid < r.extras)
@@ -514,14 +546,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         unsigned long long last = ~0ull;
         for (int k = 0; k < p.top; ++k) {
             unsigned long long best = 0;
-            auto look = [&](float v, int64_t index) {
+            auto look = [&](float v, int index) {
                 const unsigned long long key = key_of(v, index);
                 if (v > neg_inf() && key < last && key > best)
                     best = key;
             };
-            for (int64_t chunk = r.from + tid; chunk < r.to; chunk += threads) {
+            for (int chunk = r.from + tid; chunk < r.to; chunk += threads) {
                 Chunk<IN> x;
-                r.load(x, chunk);
+                x.load(r.at(r.first_of(chunk)));
 #pragma unroll
                 for (int i = 0; i < Chunk<IN>::kVals; ++i)
                     look(x.at(i), r.first_of(chunk) + i);
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         }
         if (blocks > 1)
             cluster_sync();
-        n = static_cast<uint32_t>(p.top) * blocks;
+        n = static_cast<uint32_t>(p.top * blocks);
         if (rank == 0)
             for (uint32_t i = tid; i < n; i += threads)
                 candidates[i] = ld_u64(in_block(list, i / p.top) + i % p.top * 8);
@@ -690,12 +722,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
 }
 
 template <int IN, bool ENT, bool TOP>
-cudaError_t launch_rows(const LogprobsParams &p, unsigned blocks, int threads, cudaStream_t s)
+cudaError_t launch_rows(const LogprobsParams &p, int log_blocks, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1], both[2];
+    const unsigned blocks = 1u << log_blocks;
     // chunks of a thread at most (a row that starts off a 32-byte boundary may have one less)
     const int64_t chunks = (p.V / Chunk<IN>::kVals + blocks - 1) / blocks, mine = (chunks + threads - 1) / threads;
-    const int64_t group = mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1;
+    const int group = static_cast<int>(mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1);
     const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * threads * sizeof(float) : 0;
     cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), threads, smem, s, attr);
     if (blocks > 1) {
@@ -707,7 +740,7 @@ cudaError_t launch_rows(const LogprobsParams &p, unsigned blocks, int threads, c
         cfg.attrs = both;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP>, p, blocks, group);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP>, p, log_blocks, group);
 }
 
 template <int IN>
@@ -715,20 +748,21 @@ cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
 {
     // few rows: blocks of a cluster share one, while each has at least two chunks a thread
     const int64_t chunks = p.V / Chunk<IN>::kVals;
-    unsigned blocks = 1;
-    while (blocks < kLogprobsCluster && p.rows * blocks < 2ll * num_sms && chunks >= blocks * 4ll * kThreads)
-        blocks *= 2;
+    int log_blocks = 0;
+    while ((1 << log_blocks) < kLogprobsCluster && p.rows << log_blocks < 2ll * num_sms &&
+           chunks >= 4ll * kThreads << log_blocks)
+        ++log_blocks;
     // short rows: fewer threads, down to a warp; with many rows a thread takes more chunks, so that a block's reductions
     // are fewer
     const int64_t least = p.rows >= 16ll * num_sms ? 8 : 2;
     int threads = 32;
-    while (threads < kThreads && chunks >= blocks * 2 * least * threads)
+    while (threads < kThreads && chunks >= 2 * least * threads << log_blocks)
         threads *= 2;
     if (p.top > 0)
-        return p.entropy ? launch_rows<IN, true, true>(p, blocks, threads, s)
-                         : launch_rows<IN, false, true>(p, blocks, threads, s);
-    return p.entropy ? launch_rows<IN, true, false>(p, blocks, threads, s)
-                     : launch_rows<IN, false, false>(p, blocks, threads, s);
+        return p.entropy ? launch_rows<IN, true, true>(p, log_blocks, threads, s)
+                         : launch_rows<IN, false, true>(p, log_blocks, threads, s);
+    return p.entropy ? launch_rows<IN, true, false>(p, log_blocks, threads, s)
+                     : launch_rows<IN, false, false>(p, log_blocks, threads, s);
 }
 
 template <int IN, bool ENT>
