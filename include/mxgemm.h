@@ -626,7 +626,8 @@ MXGEMM_API int mxgemm_embed(int in_dtype, const void *table, int64_t table_strid
  * Sums are FP32, of an id's rows in the order of its tokens (in parts of 8 or 32
  * sorted rows), rounded once.  Ids outside the table add nothing, whatever their rows of dy
  * hold.  workspace: mxgemm_embed_backward_workspace_bytes(tokens, vocab, K) bytes (0
- * for sizes that the call refuses), 32-byte aligned, holding nothing between calls:
+ * for up to 64 tokens, and for sizes that the call refuses), 32-byte aligned, holding
+ * nothing between calls:
  * 16 bytes a token and 8 K bytes for every 32 tokens, or every 8 of a small batch.
  * vocab below 2^30.
  */
@@ -672,7 +673,8 @@ MXGEMM_API int mxgemm_qk_norm_rope(int in_dtype, const void *x, int64_t x_token_
  * rstd and the weights' gradients) and dx is dy rotated back.  Tokens whose position is
  * outside the table have a gradient of zero and add nothing to the weights'.
  * workspace: mxgemm_qk_norm_rope_backward_workspace_bytes(tokens, q_heads + k_heads,
- * D) bytes (none without weights), 32-byte aligned, holding nothing between calls.
+ * D) bytes (0 for few tokens, and none without weights), 32-byte aligned, holding
+ * nothing between calls.
  */
 MXGEMM_API size_t mxgemm_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t heads, int64_t D);
 MXGEMM_API int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_stride,

@@ -19,14 +19,23 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kChunk = static_cast<int64_t>(kThreads) * kLaneVals;
+// A block reads a contiguous part, so more of them are more places of HBM that are read at once: 872 M BF16 values
+// summed in 302 us with two a multiprocessor, 255 with three, 248 with four, 415 with six.
 constexpr int kBlocksPerSm = 4;
+
+constexpr int kMostBlocks = kGradSms * kBlocksPerSm;
 
 template <int N>
 struct Table {
     GradTensor t[N];
-    uint32_t end[N];  // chunks up to and with tensor i
-    int n;
+    uint32_t end[N];                      // chunks up to and with tensor i
+    uint16_t start[kMostBlocks + 1];      // the tensor of a block's first chunk, and of the last chunk
     uint32_t chunks;
+
+    __device__ __forceinline__ uint32_t chunk_of(uint32_t block) const  // a block's first chunk
+    {
+        return static_cast<uint32_t>(static_cast<uint64_t>(chunks) * block / gridDim.x);
+    }
 };
 
 // A thread's values of a tensor come eight at a time, a block's next to each other: a
@@ -38,29 +47,34 @@ static_assert(kSteps == 2, "a thread takes two runs of eight values of a chunk")
 
 // Part of a tensor that is a block's: chunks [from, to) counted in the tensor.
 struct Part {
-    int i;
-    int64_t from, to;
+    int i = 0;
+    int64_t from = 0, to = 0;
 };
 
-// A block's walk over the tensors of its chunks [c0, c1), forwards or backwards.
+// A tensor of the table.
+struct Tensor {
+    const void *src;
+    void *dst;
+    int64_t n;
+    uint32_t flags;
+
+    __device__ __forceinline__ explicit Tensor(const GradTensor &t)
+        : src(t.src), dst(t.dst), n(t.n_flags >> kGradFlagBits), flags(static_cast<uint32_t>(t.n_flags) & ((1u << kGradFlagBits) - 1))
+    {
+    }
+};
+
+// A block's walk over the tensors of its chunks [c0, c1), forwards or backwards (from the tensor of the next block's
+// first chunk on).
 template <int N, bool BACKWARDS>
 struct Walk {
     const Table<N> &table;
     uint32_t c0, c1;
     int i;
 
-    __device__ __forceinline__ Walk(const Table<N> &t, uint32_t from, uint32_t to) : table(t), c0(from), c1(to)
+    __device__ __forceinline__ explicit Walk(const Table<N> &t)
+        : table(t), c0(t.chunk_of(blockIdx.x)), c1(t.chunk_of(blockIdx.x + 1)), i(t.start[blockIdx.x + BACKWARDS])
     {
-        const uint32_t chunk = BACKWARDS ? to - 1 : from;
-        int lo = 0, hi = t.n - 1;  // the first tensor that ends past the chunk
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (t.end[mid] > chunk)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        i = lo;
     }
     __device__ __forceinline__ bool next(Part &p)
     {
@@ -84,37 +98,37 @@ struct Walk {
     }
 };
 
-// Eight values as they are in memory; zeros past the tensor's end.
+// Eight values as they are in memory.
+template <bool BF16>
 struct Values {
-    uint32_t r[8];
+    static constexpr int kWords = BF16 ? 4 : 8;
+    uint32_t r[kWords];
 
-    template <bool BF16>
-    __device__ __forceinline__ void load(const GradTensor &t, int64_t at)
+    __device__ __forceinline__ void load(const void *p)
     {
-        const int64_t left = t.n - at;
-        if (left >= kVals && (t.flags & kGradSrcVector)) {
-            if constexpr (BF16)
-                asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                             : "l"(static_cast<const char *>(t.src) + at * 2)
-                             : "memory");
-            else
-                ld_row32(static_cast<const char *>(t.src) + at * 4, r);
-            return;
-        }
+        if constexpr (BF16)
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                         : "l"(p)
+                         : "memory");
+        else
+            ld_row32(p, r);
+    }
+    // the first `left` of them (any number), one by one; zeros after
+    __device__ __forceinline__ void load_some(const void *p, int64_t left)
+    {
 #pragma unroll
-        for (int i = 0; i < (BF16 ? 4 : 8); ++i)
+        for (int i = 0; i < kWords; ++i)
             r[i] = 0;
 #pragma unroll
         for (int i = 0; i < kVals; ++i)
             if (i < left) {
                 if constexpr (BF16)
-                    r[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(t.src)[at + i]) << (16 * (i & 1));
+                    r[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
                 else
-                    r[i] = static_cast<const uint32_t *>(t.src)[at + i];
+                    r[i] = static_cast<const uint32_t *>(p)[i];
             }
     }
-    template <bool BF16>
     __device__ __forceinline__ F2 pair(int i) const
     {
         if constexpr (BF16)
@@ -124,30 +138,32 @@ struct Values {
     }
 };
 
+// Eight FP32 values as eight of the output's, and the first `left` of them.
 template <bool BF16>
-__device__ __forceinline__ void store_values(const GradTensor &t, int64_t at, const float (&v)[kVals])
+__device__ __forceinline__ void store_values(void *p, const float (&v)[kVals])
 {
-    const int64_t left = t.n - at;
-    if (left >= kVals && (t.flags & kGradDstVector)) {
-        if constexpr (BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<char *>(t.dst) + at * 2) = make_uint4(
-                pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-        } else {
-            uint32_t w[8];
+    if constexpr (BF16) {
+        *static_cast<uint4 *>(p) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+        uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < kVals; ++i)
-                w[i] = __float_as_uint(v[i]);
-            st_row32(static_cast<char *>(t.dst) + at * 4, w);
-        }
-        return;
+        for (int i = 0; i < kVals; ++i)
+            w[i] = __float_as_uint(v[i]);
+        st_row32(p, w);
     }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_some(void *p, int64_t left, const float (&v)[kVals])
+{
 #pragma unroll
     for (int i = 0; i < kVals; ++i)
         if (i < left) {
             if constexpr (BF16)
-                static_cast<__nv_bfloat16 *>(t.dst)[at + i] = __float2bfloat16_rn(v[i]);
+                static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v[i]);
             else
-                static_cast<float *>(t.dst)[at + i] = v[i];
+                static_cast<float *>(p)[i] = v[i];
         }
 }
 
@@ -180,54 +196,70 @@ constexpr float kSumLeast = 7.7e-34f, kSumMost = 1.2e30f;  // about 2^-110 and 2
 template <bool BF16>
 constexpr int kAhead = BF16 ? 4 : 2;
 
-// The sum of the squares of a block's part of a tensor, added to this thread's.
-template <bool BF16>
-__device__ __forceinline__ void sum_part(const GradTensor &t, const Part &p, double &sum)
+// The sum of the squares of U runs, added to this thread's.
+template <bool BF16, int U>
+__device__ __forceinline__ void add_squares(const Values<BF16> (&v)[U], double &sum)
 {
-    constexpr int U = kAhead<BF16>;
-    const int64_t last = p.to * kSteps;
-    int64_t step = p.from * kSteps;  // runs of a thread, counted in the tensor
-    Values next[U];
+    F2 s2 = f2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        next[u].template load<BF16>(t, step + u < last ? ((step + u) * kThreads + threadIdx.x) * kVals : t.n);
-    for (; step < last; step += U) {
-        Values v[U];
+#pragma unroll
+        for (int i = 0; i < kVals / 2; ++i)
+            s2 = f2_fma(v[u].pair(i), v[u].pair(i), s2);
+    float a, b;
+    f2_split(s2, a, b);
+    const float s = a + b;
+    if (s > kSumLeast && s < kSumMost) {
+        sum += s;
+        return;
+    }
+    uint32_t any = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < Values<BF16>::kWords; ++i)
+            any |= v[u].r[i] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+    if (any != 0)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = next[u];
-        if (step + U < last)
+#pragma unroll
+            for (int i = 0; i < kVals / 2; ++i) {
+                f2_split(v[u].pair(i), a, b);
+                sum += static_cast<double>(a) * a + static_cast<double>(b) * b;
+            }
+}
+
+// The squares of a block's part of a tensor.
+template <bool BF16>
+__device__ __forceinline__ void sum_part(const Tensor &t, const Part &p, double &sum)
+{
+    constexpr int E = BF16 ? 2 : 4, U = kAhead<BF16>;
+    constexpr int kRun = kThreads * kVals * E;  // bytes from a thread's run to its next
+    int64_t steps = (p.to - p.from) * kSteps;
+    const int64_t first = p.from * kChunk + threadIdx.x * kVals;
+    const char *from = static_cast<const char *>(t.src) + first * E;
+    if ((t.flags & kGradSrcVector) && p.to * kChunk <= t.n) {
+        for (; steps >= U; steps -= U, from += U * kRun) {
+            Values<BF16> v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                next[u].template load<BF16>(t, step + U + u < last ? ((step + U + u) * kThreads + threadIdx.x) * kVals
-                                                                   : t.n);
-        F2 s2 = f2(0.0f, 0.0f);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < kVals / 2; ++i)
-                s2 = f2_fma(v[u].template pair<BF16>(i), v[u].template pair<BF16>(i), s2);
-        float a, b;
-        f2_split(s2, a, b);
-        const float s = a + b;
-        if (s > kSumLeast && s < kSumMost) {
-            sum += s;
-        } else {
-            uint32_t any = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < (BF16 ? 4 : 8); ++i)
-                    any |= v[u].r[i] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
-            if (any != 0)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < kVals / 2; ++i) {
-                        f2_split(v[u].template pair<BF16>(i), a, b);
-                        sum += static_cast<double>(a) * a + static_cast<double>(b) * b;
-                    }
+                v[u].load(from + u * kRun);
+            add_squares<BF16, U>(v, sum);
         }
+        for (; steps > 0; --steps, from += kRun) {
+            Values<BF16> v[1];
+            v[0].load(from);
+            add_squares<BF16, 1>(v, sum);
+        }
+        return;
+    }
+    for (int64_t left = t.n - first; steps > 0; --steps, from += kRun, left -= kThreads * kVals) {
+        Values<BF16> v[1];
+        if ((t.flags & kGradSrcVector) && left >= kVals)
+            v[0].load(from);
+        else
+            v[0].load_some(from, left);
+        add_squares<BF16, 1>(v, sum);
     }
 }
 
@@ -238,17 +270,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __shared__ double part[kWarps];
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * blockIdx.x / gridDim.x);
-    const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * (blockIdx.x + 1) / gridDim.x);
     double sum = 0.0;
-    if (c0 < c1) {
-        Walk<N, false> walk(table, c0, c1);
-        for (Part p; walk.next(p);) {
-            if (table.t[p.i].flags & kGradSrcBf16)
-                sum_part<true>(table.t[p.i], p, sum);
-            else
-                sum_part<false>(table.t[p.i], p, sum);
-        }
+    Walk<N, false> walk(table);
+    for (Part p; walk.next(p);) {
+        const Tensor t(table.t[p.i]);
+        if (t.flags & kGradSrcBf16)
+            sum_part<true>(t, p, sum);
+        else
+            sum_part<false>(t, p, sum);
     }
     sum = block_sum64(sum, part);
     if (threadIdx.x == 0)
@@ -292,38 +321,54 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
         *norm = norm_of(total);
 }
 
+template <bool SRC, bool DST>
+__device__ __forceinline__ void scale(const Values<SRC> &v, F2 f, float (&o)[kVals])
+{
+#pragma unroll
+    for (int i = 0; i < kVals / 2; ++i)
+        f2_split(f2_mul(v.pair(i), f), o[2 * i], o[2 * i + 1]);
+}
+
 // A block's part of a tensor times the factor, from its end to its start.
 template <bool SRC, bool DST>
-__device__ __forceinline__ void clip_part(const GradTensor &t, const Part &p, float factor)
+__device__ __forceinline__ void clip_part(const Tensor &t, const Part &p, float factor)
 {
-    constexpr int U = kAhead<SRC>;
-    const int64_t first = p.from * kSteps;
-    int64_t step = p.to * kSteps;  // one past the run that is next
-    auto at = [&](int64_t run) { return (run * kThreads + threadIdx.x) * kVals; };
-    Values next[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        next[u].template load<SRC>(t, step - 1 - u >= first ? at(step - 1 - u) : t.n);
+    constexpr int ES = SRC ? 2 : 4, ED = DST ? 2 : 4, U = kAhead<SRC>;
+    constexpr int64_t kRun = kThreads * kVals;
     const F2 f = f2(factor, factor);
-    for (; step > first; step -= U) {
-        Values v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = next[u];
-        if (step - U > first)
+    int64_t steps = (p.to - p.from) * kSteps;
+    const int64_t last = p.to * kChunk - kRun + threadIdx.x * kVals;  // this thread's last run
+    const char *from = static_cast<const char *>(t.src) + last * ES;
+    char *to = static_cast<char *>(t.dst) + last * ED;
+    constexpr uint32_t kBoth = kGradSrcVector | kGradDstVector;
+    const bool vector = (t.flags & kBoth) == kBoth;
+    if (vector && p.to * kChunk <= t.n) {
+        for (; steps >= U; steps -= U, from -= U * kRun * ES, to -= U * kRun * ED) {
+            Values<SRC> v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                next[u].template load<SRC>(t, step - U - 1 - u >= first ? at(step - U - 1 - u) : t.n);
+                v[u].load(from - u * kRun * ES);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (step - 1 - u < first)
-                break;
-            float o[kVals];
-#pragma unroll
-            for (int i = 0; i < kVals / 2; ++i)
-                f2_split(f2_mul(v[u].template pair<SRC>(i), f), o[2 * i], o[2 * i + 1]);
-            store_values<DST>(t, at(step - 1 - u), o);
+            for (int u = 0; u < U; ++u) {
+                float o[kVals];
+                scale<SRC, DST>(v[u], f, o);
+                store_values<DST>(to - u * kRun * ED, o);
+            }
         }
+    }
+    for (int64_t left = t.n - (last - (p.to - p.from) * kChunk + steps * kRun); steps > 0;
+         --steps, from -= kRun * ES, to -= kRun * ED, left += kRun) {
+        Values<SRC> v;
+        if (vector && left >= kVals)
+            v.load(from);
+        else
+            v.load_some(from, left);
+        float o[kVals];
+        scale<SRC, DST>(v, f, o);
+        if (vector && left >= kVals)
+            store_values<DST>(to, o);
+        else
+            store_some<DST>(to, left, o);
     }
 }
 
@@ -334,9 +379,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __shared__ double part[kWarps];
     __shared__ float block_factor;
     griddep_launch_dependents();
+    Walk<N, true> walk(table);  // what does not depend on the norm comes before the wait for it
+    Part p;
+    bool any = walk.next(p);
+    Tensor t(table.t[p.i]);
     griddep_wait();
-    const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * blockIdx.x / gridDim.x);
-    const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(table.chunks) * (blockIdx.x + 1) / gridDim.x);
     const double total = total_of(partial, n, part);
     if (threadIdx.x == 0) {
         block_factor = factor_of(total, max_norm);
@@ -345,78 +392,117 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     __syncthreads();
     const float factor = block_factor;
-    if (c0 >= c1)
-        return;
-    Walk<N, true> walk(table, c0, c1);
-    for (Part p; walk.next(p);) {
-        const GradTensor &t = table.t[p.i];
-        if (factor == 1.0f && t.src == t.dst)
-            continue;  // what stays as it is need not be written
-        if (t.flags & kGradSrcBf16) {
-            if (t.flags & kGradDstBf16)
-                clip_part<true, true>(t, p, factor);
-            else
-                clip_part<true, false>(t, p, factor);
-        } else {
-            if (t.flags & kGradDstBf16)
-                clip_part<false, true>(t, p, factor);
-            else
-                clip_part<false, false>(t, p, factor);
+    while (any) {
+        if (factor != 1.0f || t.src != t.dst) {  // what stays as it is need not be written
+            if (t.flags & kGradSrcBf16) {
+                if (t.flags & kGradDstBf16)
+                    clip_part<true, true>(t, p, factor);
+                else
+                    clip_part<true, false>(t, p, factor);
+            } else {
+                if (t.flags & kGradDstBf16)
+                    clip_part<false, true>(t, p, factor);
+                else
+                    clip_part<false, false>(t, p, factor);
+            }
         }
+        any = walk.next(p);
+        t = Tensor(table.t[p.i]);
     }
 }
 
+// One launch's table, and the number of its blocks.
 template <int N>
-cudaError_t launch_tables(const GradTensor *tensors, int64_t n, int num_sms, bool clip, double *partial, int parts,
-                          float max_norm, float *norm, cudaStream_t s)
+unsigned fill_table(Table<N> &table, const GradTensor *tensors, int n, int num_sms)
+{
+    uint32_t chunks = 0;
+    for (int i = 0; i < n; ++i) {
+        table.t[i] = tensors[i];
+        chunks += static_cast<uint32_t>(((tensors[i].n_flags >> kGradFlagBits) + kChunk - 1) / kChunk);
+        table.end[i] = chunks;
+    }
+    table.chunks = chunks;
+    const unsigned most = static_cast<unsigned>((num_sms < kGradSms ? num_sms : kGradSms) * kBlocksPerSm);
+    // four chunks to a block where that still fills the multiprocessors: a block's start and sum cost as much as those
+    const unsigned wanted = chunks / 4 > most / kBlocksPerSm ? chunks / 4 : chunks < most / kBlocksPerSm ? chunks : most / kBlocksPerSm;
+    const unsigned blocks = wanted < 1 ? 1 : wanted < most ? wanted : most;
+    int i = 0;
+    for (unsigned b = 0; b <= blocks; ++b) {
+        const uint32_t chunk = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * b / blocks);
+        while (i + 1 < n && table.end[i] <= chunk)
+            ++i;
+        table.start[b] = static_cast<uint16_t>(i);
+    }
+    return blocks;
+}
+
+template <int N>
+cudaError_t launch_tables(const GradTensor *tensors, int64_t n, bool clip, double *partial, float max_norm, float *norm,
+                          int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
+    Table<N> table;
+    int parts = 0;
+    unsigned blocks = 0;
     for (int64_t at = 0; at < n; at += N) {
-        Table<N> table;
-        table.n = static_cast<int>(n - at < N ? n - at : N);
-        uint32_t chunks = 0;
-        for (int i = 0; i < table.n; ++i) {
-            table.t[i] = tensors[at + i];
-            chunks += static_cast<uint32_t>((tensors[at + i].n + kChunk - 1) / kChunk);
-            table.end[i] = chunks;
-        }
-        table.chunks = chunks;
-        const unsigned blocks = grad_blocks(num_sms);
+        blocks = fill_table(table, tensors + at, static_cast<int>(n - at < N ? n - at : N), num_sms);
         const cudaLaunchConfig_t cfg = row_launch(blocks, kThreads, 0, s, attr);
-        const cudaError_t e =
-            clip ? cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, table, static_cast<const double *>(partial), parts,
-                                      max_norm, at == 0 ? norm : nullptr)
-                 : cudaLaunchKernelEx(&cfg, grad_norm_kernel<N>, table, partial + at / N * blocks);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_norm_kernel<N>, table, partial + parts);
+        if (e != cudaSuccess)
+            return e;
+        parts += static_cast<int>(blocks);
+    }
+    if (!clip) {
+        const cudaLaunchConfig_t cfg = row_launch(1, kThreads, 0, s, attr);
+        return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const double *>(partial), parts, norm);
+    }
+    for (int64_t at = 0; at < n; at += N) {
+        if (n > N)
+            blocks = fill_table(table, tensors + at, static_cast<int>(n - at < N ? n - at : N), num_sms);
+        const cudaLaunchConfig_t cfg = row_launch(blocks, kThreads, 0, s, attr);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, table, static_cast<const double *>(partial),
+                                                 parts, max_norm, at == 0 ? norm : nullptr);
         if (e != cudaSuccess)
             return e;
     }
     return cudaSuccess;
 }
 
-// Few tensors take a short table: a launch copies its parameters.
-constexpr int kTables[3] = {32, 256, 896};
+// Few tensors take a short table: a launch copies its parameters (32 KB at most).
+constexpr int kTables[5] = {32, 128, 320, 640, 1024};
 
-int table_size(int64_t n) { return n <= kTables[0] ? kTables[0] : n <= kTables[1] ? kTables[1] : kTables[2]; }
-
-cudaError_t launch_any(const GradTensor *tensors, int64_t n, int num_sms, bool clip, double *partial, int parts,
-                       float max_norm, float *norm, cudaStream_t s)
+int table_size(int64_t n)
 {
-    const int size = table_size(n);
-    return size == kTables[0]   ? launch_tables<kTables[0]>(tensors, n, num_sms, clip, partial, parts, max_norm, norm, s)
-           : size == kTables[1] ? launch_tables<kTables[1]>(tensors, n, num_sms, clip, partial, parts, max_norm, norm, s)
-                                : launch_tables<kTables[2]>(tensors, n, num_sms, clip, partial, parts, max_norm, norm, s);
+    for (const int size : kTables)
+        if (n <= size)
+            return size;
+    return kTables[4];
 }
 
-int launches(int64_t n) { return static_cast<int>((n + table_size(n) - 1) / table_size(n)); }  // none for n = 0
+cudaError_t launch_any(const GradTensor *tensors, int64_t n, bool clip, double *partial, float max_norm, float *norm,
+                       int num_sms, cudaStream_t s)
+{
+    switch (table_size(n)) {
+    case kTables[0]:
+        return launch_tables<kTables[0]>(tensors, n, clip, partial, max_norm, norm, num_sms, s);
+    case kTables[1]:
+        return launch_tables<kTables[1]>(tensors, n, clip, partial, max_norm, norm, num_sms, s);
+    case kTables[2]:
+        return launch_tables<kTables[2]>(tensors, n, clip, partial, max_norm, norm, num_sms, s);
+    case kTables[3]:
+        return launch_tables<kTables[3]>(tensors, n, clip, partial, max_norm, norm, num_sms, s);
+    default:
+        return launch_tables<kTables[4]>(tensors, n, clip, partial, max_norm, norm, num_sms, s);
+    }
+}
 
 }  // namespace
 
-unsigned grad_blocks(int num_sms)
+size_t grad_workspace(int64_t n)
 {
-    return static_cast<unsigned>((num_sms < kGradSms ? num_sms : kGradSms) * kBlocksPerSm);
+    const int64_t launches = (n + table_size(n) - 1) / table_size(n);
+    return static_cast<size_t>(launches) * kMostBlocks * sizeof(double);
 }
-
-size_t grad_workspace(int64_t n) { return static_cast<size_t>(launches(n)) * grad_blocks(kGradSms) * sizeof(double); }
 
 // Chunks of 4096 values of a launch are numbered in 32 bits.
 bool grads_fit(const GradTensor *tensors, int64_t n)
@@ -424,7 +510,7 @@ bool grads_fit(const GradTensor *tensors, int64_t n)
     const int size = n > 0 ? table_size(n) : 1;
     int64_t chunks = 0;
     for (int64_t i = 0; i < n; ++i) {
-        chunks = (i % size == 0 ? 0 : chunks) + (tensors[i].n + kChunk - 1) / kChunk;
+        chunks = (i % size == 0 ? 0 : chunks) + ((tensors[i].n_flags >> kGradFlagBits) + kChunk - 1) / kChunk;
         if (chunks > 0x7FFFFFFF)
             return false;
     }
@@ -434,24 +520,13 @@ bool grads_fit(const GradTensor *tensors, int64_t n)
 cudaError_t launch_grad_norm(const GradTensor *tensors, int64_t n, double *partial, float *norm, int num_sms,
                              cudaStream_t s)
 {
-    cudaError_t e = launch_any(tensors, n, num_sms, false, partial, 0, 0.0f, nullptr, s);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(1, kThreads, 0, s, attr);
-    return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const double *>(partial),
-                              launches(n) * static_cast<int>(grad_blocks(num_sms)), norm);
+    return launch_any(tensors, n, false, partial, 0.0f, norm, num_sms, s);
 }
 
 cudaError_t launch_clip_grads(const GradTensor *tensors, int64_t n, double *partial, float max_norm, float *norm,
                               int num_sms, cudaStream_t s)
 {
-    if (n == 0)
-        return launch_grad_norm(tensors, n, partial, norm, num_sms, s);
-    const cudaError_t e = launch_any(tensors, n, num_sms, false, partial, 0, 0.0f, nullptr, s);
-    return e != cudaSuccess ? e
-                            : launch_any(tensors, n, num_sms, true, partial,
-                                         launches(n) * static_cast<int>(grad_blocks(num_sms)), max_norm, norm, s);
+    return launch_any(tensors, n, n > 0, partial, max_norm, norm, num_sms, s);  // no tensors: the norm alone
 }
 
 }  // namespace mxg

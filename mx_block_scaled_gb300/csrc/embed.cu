@@ -294,13 +294,26 @@ __device__ __forceinline__ int64_t lower_bound(const EmbedBackParams &p, uint32_
     return from;
 }
 
+// Row v as it is without the tokens.
+template <int OUT>
+__device__ __forceinline__ void fill_row(const EmbedBackParams &p, int64_t v)
+{
+    constexpr int E = ElemBytes<OUT>::value;
+    for (int64_t k = (threadIdx.x & 31) * kLaneVals; k < p.K; k += kWarpVals) {
+        Raw16<OUT> a;
+        a.load(p.add + (v * p.K + k) * E, p.add != nullptr);
+#pragma unroll
+        for (int l = 0; l < Raw16<OUT>::kParts; ++l)
+            st_row32(p.dtable + (v * p.K + k) * E + 32 * l, a.r[l]);
+    }
+}
+
 // The warp writes those of the rows v0 .. v0 + rows - 1 whose id does not occur.
 template <int OUT>
 __device__ __forceinline__ void fill_rows(const EmbedBackParams &p, int64_t v0, int64_t rows)
 {
-    constexpr int E = ElemBytes<OUT>::value;
     const int lane = threadIdx.x & 31;
-    const int64_t v1 = v0 + rows < p.vocab ? v0 + rows : p.vocab, K = p.K;
+    const int64_t v1 = v0 + rows < p.vocab ? v0 + rows : p.vocab;
     if (v0 >= v1)
         return;
     int64_t at = lower_bound(p, static_cast<uint32_t>(v0), 0);
@@ -308,13 +321,7 @@ __device__ __forceinline__ void fill_rows(const EmbedBackParams &p, int64_t v0, 
         const uint32_t id = at + lane < p.tokens ? p.entries[at + lane].x : p.vocab;
         const uint32_t next = __shfl_sync(0xFFFFFFFFu, id, 0);  // the next id that occurs
         for (const int64_t end = next < v1 ? next : v1; v < end; ++v)
-            for (int64_t k = lane * kLaneVals; k < K; k += kWarpVals) {
-                Raw16<OUT> a;
-                a.load(p.add + (v * K + k) * E, p.add != nullptr);
-#pragma unroll
-                for (int l = 0; l < Raw16<OUT>::kParts; ++l)
-                    st_row32(p.dtable + (v * K + k) * E + 32 * l, a.r[l]);
-            }
+            fill_row<OUT>(p, v);
         ++v;  // past the id that occurs
         const int same = __popc(__ballot_sync(0xFFFFFFFFu, id == next));
         at = same < 32 ? at + same : lower_bound(p, next + 1, at + 32);
@@ -475,6 +482,72 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
     }
 }
 
+// A handful of tokens: no sort.  Every warp reads all ids, two a lane; the warp of an id's
+// first token adds its rows, in token order, and the others of that id nothing.  One
+// launch instead of three: the host's part of a call is 3.5 us instead of 8.
+constexpr int64_t kFewTokens = 64;
+
+template <int IN, int OUT>
+__global__ void __launch_bounds__(kThreads)
+    embed_few_kernel(const EmbedBackParams p, const void *ids, bool ids64, uint32_t sum_blocks, int64_t rows)
+{
+    constexpr int E = ElemBytes<IN>::value;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t K = p.K;
+    uint32_t id[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        id[i] = lane + 32 * i < p.tokens ? key_of(ids, ids64, lane + 32 * i, p.vocab) : p.vocab;
+    if (blockIdx.x >= sum_blocks) {  // `rows`, 32 at most, to a warp: a bit for every one that occurs
+        const int64_t v0 = (static_cast<int64_t>(blockIdx.x - sum_blocks) * kWarps + warp) * rows;
+        uint32_t occurs = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (id[i] >= v0 && id[i] < v0 + rows)
+                occurs |= 1u << (id[i] - v0);
+        occurs = __reduce_or_sync(0xFFFFFFFFu, occurs);
+        for (int64_t v = v0; v < v0 + rows && v < p.vocab; ++v)
+            if (!((occurs >> (v - v0)) & 1))
+                fill_row<OUT>(p, v);
+        return;
+    }
+    const uint32_t slices = static_cast<uint32_t>((K + kWarpVals - 1) / kWarpVals);
+    const uint32_t unit = blockIdx.x * kWarps + warp, token = unit / slices;
+    if (token >= p.tokens)
+        return;
+    const int64_t k = (unit - token * slices) * kWarpVals + lane * kLaneVals;
+    const uint32_t lo = __shfl_sync(0xFFFFFFFFu, id[0], token & 31), hi = __shfl_sync(0xFFFFFFFFu, id[1], token & 31);
+    const uint32_t mine = token < 32 ? lo : hi;
+    unsigned long long same = __ballot_sync(0xFFFFFFFFu, id[0] == mine) |
+                              static_cast<unsigned long long>(__ballot_sync(0xFFFFFFFFu, id[1] == mine)) << 32;
+    if (mine >= p.vocab || __ffsll(same) - 1 != static_cast<int>(token) || k >= K)
+        return;
+    float sum[kLaneVals];
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i)
+        sum[i] = 0.0f;
+    while (same) {
+        Raw16<IN> x[4];
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t t = __ffsll(same) - 1;
+            x[j].load(p.dy + t * p.dy_stride + k * E, same != 0);
+            n += same != 0;
+            same &= same - 1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n)
+#pragma unroll
+                for (int i = 0; i < kLaneVals; ++i)
+                    sum[i] += x[j].at(i);
+    }
+    finish_row<OUT>(p, mine, k, sum);
+}
+
 unsigned warp_blocks(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
 
 template <int IN, int OUT>
@@ -542,6 +615,17 @@ bool short_runs(int64_t tokens, int64_t K)
 }
 
 template <int IN, int OUT>
+cudaError_t launch_few(const EmbedBackParams &p, const void *ids, bool ids64, bool fill, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const unsigned sum_blocks = warp_blocks(p.tokens * ((p.K + kWarpVals - 1) / kWarpVals));
+    const int64_t row = p.K * ElemBytes<OUT>::value, wanted = row >= 16384 ? 1 : 16384 / row, rows = wanted < 32 ? wanted : 32;
+    const unsigned fill_blocks = fill ? warp_blocks((p.vocab + rows - 1) / rows) : 0;
+    const cudaLaunchConfig_t cfg = row_launch(sum_blocks + fill_blocks, kThreads, 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, embed_few_kernel<IN, OUT>, p, ids, ids64, sum_blocks, rows);
+}
+
+template <int IN, int OUT>
 cudaError_t launch_sums(const EmbedBackParams &p, bool fill, cudaStream_t s)
 {
     return short_runs(p.tokens, p.K) ? launch_runs<IN, OUT, kShortRun>(p, fill, s)
@@ -570,7 +654,9 @@ cudaError_t launch_embed(const EmbedParams &p, int in_dtype, int out_dtype, int 
 // Two buffers of entries, and two rows of partial sums for every run.
 EmbedWorkspace embed_workspace(int64_t tokens, int64_t K)
 {
-    EmbedWorkspace w;
+    EmbedWorkspace w = {};
+    if (tokens <= kFewTokens)
+        return w;
     w.entries[0] = 0;
     w.entries[1] = round_up(tokens * static_cast<int64_t>(sizeof(uint2)));
     w.partial = 2 * w.entries[1];
@@ -582,6 +668,14 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t K)
 cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64, char *workspace, int in_dtype,
                                   int out_dtype, cudaStream_t s)
 {
+    const bool fill = p.add != p.dtable;  // where the gradient is added in place, no other row is touched
+    if (p.tokens <= kFewTokens) {
+        if (in_dtype == kBf16)
+            return out_dtype == kBf16 ? launch_few<kBf16, kBf16>(p, ids, ids64, fill, s)
+                                      : launch_few<kBf16, kF32>(p, ids, ids64, fill, s);
+        return out_dtype == kBf16 ? launch_few<kF32, kBf16>(p, ids, ids64, fill, s)
+                                  : launch_few<kF32, kF32>(p, ids, ids64, fill, s);
+    }
     const EmbedWorkspace w = embed_workspace(p.tokens, p.K);
     EmbedSortParams o;
     o.ids = ids;
@@ -603,7 +697,6 @@ cudaError_t launch_embed_backward(EmbedBackParams p, const void *ids, bool ids64
     if (e != cudaSuccess)
         return e;
     p.entries = o.passes > 0 && o.passes % 2 == 0 ? o.entries1 : o.entries0;
-    const bool fill = p.add != p.dtable;  // where the gradient is added in place, no other row is touched
     p.partial = reinterpret_cast<float *>(workspace + w.partial);
     if (in_dtype == kBf16)
         return out_dtype == kBf16 ? launch_sums<kBf16, kBf16>(p, fill, s) : launch_sums<kBf16, kF32>(p, fill, s);

@@ -95,8 +95,8 @@ struct Place {
             a = 8 * lane;
             b = rotary / 2 + 8 * lane;
         } else {
-            a = 16 * lane;
-            b = 16 * lane + 8;
+            a = inside ? 16 * lane : 0;
+            b = a + 8;
         }
     }
 };
@@ -146,7 +146,6 @@ struct Weights {
 // values of TENSORS tensors, rstd (TENSORS 2), and at a token's first step its angles,
 // whose address waits for the token's position.  A warp that loads a token's heads into
 // registers instead pays for that chain of latencies at every token.
-constexpr int kDepth = 4;  // a power of two
 
 __device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
@@ -167,18 +166,26 @@ __device__ __forceinline__ void lds16(uint32_t from, uint32_t *r)
 template <int IN, int TENSORS>
 struct Ring {
     static constexpr int E = ElemBytes<IN>::value;
-    static constexpr int kPieces = E / 2;       // 16-byte pieces of a run of eight
-    static constexpr int kPlane = 32 * 16;      // a piece of all lanes
-    static constexpr int kStage = 2 * TENSORS * kPieces * kPlane + (TENSORS == 2 ? 32 * 4 : 0);
+    static constexpr int kPieces = E / 2;             // 16-byte pieces of a run of eight
+    static constexpr int kDepth = IN == kBf16 ? 4 : 2;  // stages, a power of two: more bytes a stage, fewer of them
+    // heads of a group as they are in memory, then their rstd
+    static __device__ __host__ __forceinline__ int stage_bytes(int team, int D)
+    {
+        return TENSORS * (32 / team) * D * E + (TENSORS == 2 ? 32 * 4 : 0);
+    }
     // stages and angles (16 floats a member, a slot for every token under way) of a warp
-    static __device__ __host__ __forceinline__ int bytes(int team) { return kDepth * (kStage + team * 64); }
+    static __device__ __host__ __forceinline__ int bytes(int team, int D)
+    {
+        return kDepth * (stage_bytes(team, D) + team * 64);
+    }
 
     const HeadsCommon &p;
     const Place at;
     const int team, member, mine, side;        // mine: the team's head of a group
     const int to_b;                            // bytes from a lane's first run to its second
-    const uint32_t own, angles;                // this lane's place in stage 0; the angle slots
-    const uint32_t own_rstd;                   // its team's rstd in stage 0
+    const int stage_size, tensor_size;         // bytes of a stage, of one tensor in it
+    const uint32_t own, angles;                // this team's head in stage 0; the angle slots
+    const uint32_t own_rstd;                   // its rstd in stage 0
     const char *const other;                   // TENSORS 2: dy
     const int64_t other_token, other_head;
     const float *const rstd;
@@ -203,9 +210,10 @@ struct Ring {
                                     const char *other_p, int64_t other_t, int64_t other_h, const float *rstd_p)
         : p(params), at(place), team(team_size), member(threadIdx.x & (team_size - 1)),
           mine((threadIdx.x & 31) / team_size), side(32 / team_size), to_b((place.b - place.a) * E),
-          own(smem + (threadIdx.x >> 5) * bytes(team_size) + (threadIdx.x & 31) * 16),
-          angles(smem + (threadIdx.x >> 5) * bytes(team_size) + kDepth * kStage),
-          own_rstd(smem + (threadIdx.x >> 5) * bytes(team_size) + 2 * TENSORS * kPieces * kPlane + mine * 4),
+          stage_size(stage_bytes(team_size, p.D)), tensor_size(side * p.D * E),
+          own(smem + (threadIdx.x >> 5) * bytes(team_size, p.D) + mine * p.D * E),
+          angles(smem + (threadIdx.x >> 5) * bytes(team_size, p.D) + kDepth * stage_size),
+          own_rstd(smem + (threadIdx.x >> 5) * bytes(team_size, p.D) + TENSORS * tensor_size + mine * 4),
           other(other_p), other_token(other_t), other_head(other_h), rstd(rstd_p)
     {
         const int64_t groups = (p.heads + side - 1) / side, all = p.tokens * groups;
@@ -238,13 +246,13 @@ struct Ring {
         return angles + ((d * 4 + piece) * team + member) * 16;
     }
 
-    __device__ __forceinline__ void copy(uint32_t to, const char *from)  // this lane's two runs of a head
+    // a head by its team's lanes, neighbouring pieces by neighbouring lanes; `from`: this lane's first
+    __device__ __forceinline__ void copy(uint32_t to, const char *from) const
     {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            cp_async16(to + i * kPlane, from + 16 * i);
-            cp_async16(to + (kPieces + i) * kPlane, from + to_b + 16 * i);
-        }
+        for (int i = 0; i < E; ++i)
+            if ((i * team + member) * 16 < p.D * E)
+                cp_async16(to + (i * team + member) * 16, from + i * team * 16);
     }
 
     // The copying side comes to a token: its angles, and where its heads are.
@@ -262,9 +270,9 @@ struct Ring {
         }
         f_position = position_of(f_token + 1);
         f_slot = (f_slot + 1) & (kDepth - 1);
-        f_x = p.x + f_token * p.x_token + f_head * p.x_head + at.a * E;
+        f_x = p.x + f_token * p.x_token + f_head * p.x_head + member * 16;
         if constexpr (TENSORS == 2) {
-            f_other = other + f_token * other_token + f_head * other_head + at.a * E;
+            f_other = other + f_token * other_token + f_head * other_head + member * 16;
             f_rstd = rstd + f_token * p.heads + f_head;
         }
     }
@@ -277,12 +285,12 @@ struct Ring {
                 ++f_token;
                 new_token();
             }
-            if (at.inside && f_head < p.heads) {
-                copy(own + f_stage * kStage, f_x);
+            if (f_head < p.heads) {
+                copy(own + f_stage * stage_size, f_x);
                 if constexpr (TENSORS == 2) {
-                    copy(own + f_stage * kStage + 2 * kPieces * kPlane, f_other);
+                    copy(own + f_stage * stage_size + tensor_size, f_other);
                     if (member == 0)
-                        cp_async4(own_rstd + f_stage * kStage, f_rstd);
+                        cp_async4(own_rstd + f_stage * stage_size, f_rstd);
                 }
             }
             f_head += side;
@@ -311,17 +319,17 @@ struct Ring {
     // The current step's two runs of a tensor (whatever the memory holds where there are none).
     __device__ __forceinline__ void take(Raw8<IN> &a, Raw8<IN> &b, int tensor) const
     {
-        const uint32_t from = own + stage * kStage + tensor * 2 * kPieces * kPlane;
+        const uint32_t from = own + stage * stage_size + tensor * tensor_size + at.a * E;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            lds16(from + i * kPlane, a.r + 4 * i);
-            lds16(from + (kPieces + i) * kPlane, b.r + 4 * i);
+            lds16(from + 16 * i, a.r + 4 * i);
+            lds16(from + to_b + 16 * i, b.r + 4 * i);
         }
     }
     __device__ __forceinline__ float take_rstd() const
     {
         float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(own_rstd + stage * kStage) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(own_rstd + stage * stage_size) : "memory");
         return v;
     }
     // cosines (0..7) and sines (8..15) of this lane's angles
@@ -375,9 +383,11 @@ __device__ __forceinline__ void turn(F2 (&v)[8], const float (&c)[16])
 }
 
 // ------------------------------------------------------------------ forward --
+constexpr int kForwardPerSm = 5;
+
 // (and, INVERSE and without weights, the gradient of the rotation alone)
 template <int IN, int WT, bool INTERLEAVED, bool INVERSE>
-__global__ void __launch_bounds__(kThreads, IN == kBf16 ? 5 : 4) heads_kernel(const HeadsParams p, int team)
+__global__ void __launch_bounds__(kThreads, kForwardPerSm) heads_kernel(const HeadsParams p, int team)
 {
     constexpr int E = ElemBytes<IN>::value;
     extern __shared__ __align__(16) char heads_smem[];
@@ -442,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, IN == kBf16 ? 5 : 4) heads_kernel(co
 
 // ----------------------------------------------------------------- backward --
 // The same walk with dy, x and rstd.  A warp keeps the sums for both weights in
-// registers; a block leaves its sums in partial[block][query, key][D].
+// registers; a block leaves its sums in partial[block][query, key][D], or, `joined`, for
+// its cluster's first block.
 template <int IN, int WT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, kHeadsBackPerSm) heads_backward_kernel(const HeadsBackParams p, int team)
+__global__ void __launch_bounds__(kThreads, kHeadsBackPerSm) heads_backward_kernel(const HeadsBackParams p, int team, bool joined)
 {
     constexpr int E = ElemBytes<IN>::value;
     extern __shared__ __align__(16) char heads_smem[];
@@ -558,8 +569,30 @@ __global__ void __launch_bounds__(kThreads, kHeadsBackPerSm) heads_backward_kern
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             v += sums[w * 2 * p.D + i];
-        p.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.D + i] = v;
+        if (joined)
+            sums[i] = v;  // its own place
+        else
+            p.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.D + i] = v;
     }
+    if (!joined)
+        return;
+    cluster_sync();  // the grid is one cluster: its first block adds the others' sums
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
+            float v = 0.0f;
+            for (uint32_t b = 0; b < gridDim.x; ++b) {
+                float o;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(o)
+                             : "r"(map_to_cta(smem_addr(sums + i), b))
+                             : "memory");
+                v += o;
+            }
+            float *out = i < p.D ? p.dq_weight : p.dk_weight;
+            if (out)
+                out[i < p.D ? i : i - p.D] = v;
+        }
+    cluster_sync();  // no block leaves before its sums are read
 }
 
 // The blocks' sums in a fixed order: 32 slices of blocks a column, then the slices.
@@ -596,21 +629,36 @@ int team_of(int D)
     return team;
 }
 
+int64_t steps_of(int64_t tokens, int heads, int D)
+{
+    const int side = 32 / team_of(D);
+    return tokens * ((heads + side - 1) / side);
+}
+
 // Blocks that the work fills, at most those that are on the multiprocessors at once.
 int64_t blocks_of(int64_t tokens, int heads, int D, int64_t resident)
 {
-    const int side = 32 / team_of(D);
-    const int64_t steps = tokens * ((heads + side - 1) / side), blocks = (steps + kWarps - 1) / kWarps;
+    const int64_t blocks = (steps_of(tokens, heads, D) + kWarps - 1) / kWarps;
     return blocks < resident ? blocks : resident;
 }
 
+// Blocks of a gradient that is one cluster, 0 where it is not: up to two steps a warp (with four, 108 steps take 7.2 us
+// and two launches 4.9, but the host 3 us more for the second).
+int64_t joined_blocks(int64_t tokens, int heads, int D)
+{
+    constexpr int64_t kCluster = 8, kSteps = 2 * kWarps;
+    const int64_t steps = steps_of(tokens, heads, D);
+    return steps <= kCluster * kSteps ? (steps + kSteps - 1) / kSteps : 0;
+}
+
 constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM's rings
+constexpr int kMostSmem = 96 * 1024;    // of a block; D = 512 in BF16, the largest, takes 66 KB
 
 template <int IN, int WT>
 cudaError_t prepare_kernels()
 {
     constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    constexpr int kForward = kWarps * kDepth * (Ring<IN, 1>::kStage + 32 * 64);
+    constexpr int kForward = kMostSmem, kBackward = kMostSmem;
     cudaError_t e = cudaFuncSetAttribute(heads_kernel<IN, WT, false, false>, kAttr, kForward);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(heads_kernel<IN, WT, true, false>, kAttr, kForward);
@@ -620,7 +668,6 @@ cudaError_t prepare_kernels()
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(heads_kernel<IN, WT, true, true>, kAttr, kForward);
     } else {
-        constexpr int kBackward = kWarps * kDepth * (Ring<IN, 2>::kStage + 32 * 64);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(heads_backward_kernel<IN, WT, false>, kAttr, kBackward);
         if (e == cudaSuccess)
@@ -633,9 +680,8 @@ template <int IN, int WT>
 cudaError_t launch_forward(const HeadsParams &p, bool interleaved, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const int team = team_of(p.D), smem = kWarps * Ring<IN, 1>::bytes(team), fit = kRingBytes / smem;
-    constexpr int kPerSm = IN == kBf16 ? 5 : 4;
-    const int64_t blocks = blocks_of(p.tokens, p.heads, p.D, static_cast<int64_t>(num_sms) * (fit < kPerSm ? fit : kPerSm));
+    const int team = team_of(p.D), smem = kWarps * Ring<IN, 1>::bytes(team, p.D), fit = kRingBytes / smem;
+    const int64_t blocks = blocks_of(p.tokens, p.heads, p.D, static_cast<int64_t>(num_sms) * (fit < kForwardPerSm ? fit : kForwardPerSm));
     const cudaLaunchConfig_t cfg =
         row_launch(static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(smem), s, attr);
     if constexpr (WT == kNoWeight)
@@ -650,13 +696,28 @@ template <int IN, int WT>
 cudaError_t launch_backward(const HeadsBackParams &p, bool interleaved, int num_sms, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    const int team = team_of(p.D), smem = kWarps * Ring<IN, 2>::bytes(team);  // more than the sums need: 8 D a warp
+    const int team = team_of(p.D), smem = kWarps * Ring<IN, 2>::bytes(team, p.D);  // more than the sums need: 8 D a warp
+    const int64_t joined = joined_blocks(p.tokens, p.heads, p.D);
+    cudaLaunchConfig_t cfg;
+    if (joined > 0) {
+        cudaLaunchAttribute both[2];
+        cfg = row_launch(static_cast<unsigned>(joined), kThreads, static_cast<size_t>(smem), s, attr);
+        both[0] = attr[0];
+        both[1].id = cudaLaunchAttributeClusterDimension;
+        both[1].val.clusterDim.x = static_cast<unsigned>(joined);
+        both[1].val.clusterDim.y = 1;
+        both[1].val.clusterDim.z = 1;
+        cfg.attrs = both;
+        cfg.numAttrs = 2;
+        return interleaved ? cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, true>, p, team, true)
+                           : cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, false>, p, team, true);
+    }
     const int sms = num_sms < kHeadsBackSms ? num_sms : kHeadsBackSms, fit = kRingBytes / smem;
     const int64_t blocks = blocks_of(p.tokens, p.heads, p.D,
                                      static_cast<int64_t>(sms) * (fit < kHeadsBackPerSm ? fit : kHeadsBackPerSm));
-    cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(smem), s, attr);
-    const cudaError_t e = interleaved ? cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, true>, p, team)
-                                      : cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, false>, p, team);
+    cfg = row_launch(static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(smem), s, attr);
+    const cudaError_t e = interleaved ? cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, true>, p, team, false)
+                                      : cudaLaunchKernelEx(&cfg, heads_backward_kernel<IN, WT, false>, p, team, false);
     if (e != cudaSuccess)
         return e;
     cfg = row_launch(static_cast<unsigned>(p.D / 16), 32 * kSlices, 0, s, attr);
@@ -682,7 +743,9 @@ cudaError_t prepare_heads()
 
 int64_t heads_back_blocks(int64_t tokens, int heads, int D)
 {
-    return blocks_of(tokens, heads, D, static_cast<int64_t>(kHeadsBackSms) * kHeadsBackPerSm);
+    return joined_blocks(tokens, heads, D) > 0
+               ? 0
+               : blocks_of(tokens, heads, D, static_cast<int64_t>(kHeadsBackSms) * kHeadsBackPerSm);
 }
 
 cudaError_t launch_heads(const HeadsParams &p, int in_dtype, int weight_dtype, bool interleaved, int num_sms,

@@ -225,7 +225,7 @@ struct HeadsBackParams : HeadsCommon {
     float *dq_weight, *dk_weight;  // either may be NULL
     float *partial;                // [blocks][2][D]
 };
-// Blocks that leave partial sums, at most, on a part of at most kHeadsBackSms multiprocessors.
+// Blocks that leave partial sums, at most, on a part of at most kHeadsBackSms multiprocessors (none for few tokens).
 constexpr int kHeadsBackSms = 152;
 constexpr int kHeadsBackPerSm = 3;
 int64_t heads_back_blocks(int64_t tokens, int heads, int D);
@@ -263,16 +263,16 @@ struct LogprobsBackParams {
 };
 cudaError_t launch_logprobs_backward(const LogprobsBackParams &p, int in_dtype, cudaStream_t s);
 
+// Vector: the tensor starts on a 32-byte boundary.
 constexpr uint32_t kGradSrcBf16 = 1, kGradDstBf16 = 2, kGradSrcVector = 4, kGradDstVector = 8;
+constexpr int kGradFlagBits = 4;
 struct GradTensor {
     const void *src;
     void *dst;
-    int64_t n;
-    uint32_t flags;                // kGrad*; Vector: starts on a 32-byte boundary
+    int64_t n_flags;               // elements << kGradFlagBits, and the flags above
 };
-// Blocks of a launch (each leaves one partial sum), on at most kGradSms multiprocessors.
+// Blocks of a launch (each leaves one partial sum) are on at most kGradSms multiprocessors.
 constexpr int kGradSms = 152;
-unsigned grad_blocks(int num_sms);
 size_t grad_workspace(int64_t n);
 bool grads_fit(const GradTensor *tensors, int64_t n);
 cudaError_t launch_grad_norm(const GradTensor *tensors, int64_t n, double *partial, float *norm, int num_sms,

@@ -111,18 +111,20 @@ int read_grads(std::vector<GradTensor> &t, int64_t n, const void *const *grads, 
     for (int64_t i = 0; i < n; ++i) {
         GradTensor &g = t[i];
         const int to = out ? out_dtypes[i] : dtypes[i];
+        const int64_t count = sizes[i];
         g.src = grads[i];
         g.dst = out ? out[i] : const_cast<void *>(grads[i]);
-        g.n = sizes[i];
-        if (g.n < 0 || g.n > (1ll << 40))
+        if (count < 0 || count > (1ll << 40))
             return MXGEMM_ERR_SHAPE;
-        if (!known_dtype(dtypes[i]) || !known_dtype(to) || (g.n > 0 && (!g.src || !g.dst)))
+        if (!known_dtype(dtypes[i]) || !known_dtype(to) || (count > 0 && (!g.src || !g.dst)))
             return MXGEMM_ERR_ARG;
         if (!aligned(g.src, static_cast<unsigned>(elem_bytes(dtypes[i]))) ||
             !aligned(g.dst, static_cast<unsigned>(elem_bytes(to))))
             return MXGEMM_ERR_ALIGN;
-        g.flags = (dtypes[i] == MXGEMM_IN_BF16 ? kGradSrcBf16 : 0) | (to == MXGEMM_IN_BF16 ? kGradDstBf16 : 0) |
-                  (aligned(g.src, 32) ? kGradSrcVector : 0) | (aligned(g.dst, 32) ? kGradDstVector : 0);
+        const uint32_t flags = (dtypes[i] == MXGEMM_IN_BF16 ? kGradSrcBf16 : 0) |
+                               (to == MXGEMM_IN_BF16 ? kGradDstBf16 : 0) | (aligned(g.src, 32) ? kGradSrcVector : 0) |
+                               (aligned(g.dst, 32) ? kGradDstVector : 0);
+        g.n_flags = count << kGradFlagBits | flags;
     }
     return grads_fit(t.data(), n) ? MXGEMM_OK : MXGEMM_ERR_UNSUPPORTED;
 }
@@ -131,6 +133,25 @@ struct Bytes {
     uintptr_t from, to;
     bool operator<(const Bytes &o) const { return from < o.from; }
 };
+
+// In the order of their addresses: an allocator leaves a few ascending runs, which are merged.
+void sort_bytes(std::vector<Bytes> &v)
+{
+    constexpr size_t kRuns = 16;
+    size_t run[kRuns + 1] = {0}, runs = 0;  // run[i] .. run[i + 1]: ascending
+    for (size_t i = 1; i <= v.size(); ++i)
+        if (i == v.size() || v[i] < v[i - 1]) {
+            if (runs == kRuns) {
+                std::sort(v.begin(), v.end());
+                return;
+            }
+            run[++runs] = i;
+        }
+    for (size_t width = 1; width < runs; width *= 2)
+        for (size_t i = 0; i + width < runs; i += 2 * width)
+            std::inplace_merge(v.begin() + run[i], v.begin() + run[i + width],
+                               v.begin() + run[std::min(i + 2 * width, runs)]);
+}
 
 // No output touches another, nor an input other than its own, nor the norm or the
 // workspace, which no input touches either: both lists in the order of their addresses,
@@ -141,21 +162,21 @@ bool grads_apart(const std::vector<GradTensor> &t, const Bytes &norm, const Byte
     in.reserve(t.size());
     out.reserve(t.size() + 2);
     for (const GradTensor &g : t) {
-        if (g.n == 0)
+        const uintptr_t n = static_cast<uintptr_t>(g.n_flags >> kGradFlagBits);
+        if (n == 0)
             continue;
         const uintptr_t src = reinterpret_cast<uintptr_t>(g.src), dst = reinterpret_cast<uintptr_t>(g.dst);
-        const bool own = g.src == g.dst && !(g.flags & kGradSrcBf16) == !(g.flags & kGradDstBf16);
-        if (!(writes && own))  // an input that is its own output is one list's alone
-            in.push_back({src, src + static_cast<uintptr_t>(g.n) * ((g.flags & kGradSrcBf16) ? 2 : 4)});
+        const bool src16 = (g.n_flags & kGradSrcBf16) != 0, dst16 = (g.n_flags & kGradDstBf16) != 0;
+        if (!(writes && src == dst && src16 == dst16))  // an input that is its own output is one list's alone
+            in.push_back({src, src + n * (src16 ? 2 : 4)});
         if (writes)
-            out.push_back({dst, dst + static_cast<uintptr_t>(g.n) * ((g.flags & kGradDstBf16) ? 2 : 4)});
+            out.push_back({dst, dst + n * (dst16 ? 2 : 4)});
     }
     for (const Bytes &b : {norm, workspace})
         if (b.from != b.to)
             out.push_back(b);
-    for (std::vector<Bytes> *v : {&in, &out})
-        if (!std::is_sorted(v->begin(), v->end()))
-            std::sort(v->begin(), v->end());
+    sort_bytes(in);
+    sort_bytes(out);
     for (size_t i = 1; i < out.size(); ++i)
         if (out[i].from < out[i - 1].to)
             return false;
@@ -276,9 +297,10 @@ int mxgemm_embed_backward(int in_dtype, const void *dy, int64_t dy_stride, const
     if (!embed_back_fits(tokens, vocab, K))
         return MXGEMM_ERR_UNSUPPORTED;
     const size_t need = embed_workspace(tokens, K).bytes;
-    if (!workspace || ws_bytes < need)
+    if (need > 0 && (!workspace || ws_bytes < need))
         return MXGEMM_ERR_WORKSPACE;
-    if (!outputs_apart({{dense(dtable, vocab, row), 0b1}, {flat(workspace, static_cast<int64_t>(need))}},
+    if (!outputs_apart({{dense(dtable, vocab, row), 0b1},
+                        {flat(need > 0 ? workspace : nullptr, static_cast<int64_t>(need))}},
                        {dense(add, vocab, row),
                         {dy, tokens, dy_stride * e, K * e},
                         flat(ids, id_bytes * tokens)}))

@@ -89,14 +89,14 @@ def test_lookup_reads_named_rows_only():
     assert _np(got).tolist() == [[1.0] * 64, [0.0] * 64, [0.0] * 64, [1.0] * 64]
 
 
-# the counting sort takes up to 8192 ids of tables below 2^19 - 1 rows, the radix sort the rest: one pass up to 1023 rows,
+# up to 64 tokens take no sort; the counting sort takes up to 8192 ids of tables below 2^19 - 1 rows, the radix sort the rest: one pass up to 1023 rows,
 # two up to 2^20 - 1, three beyond
 @pytest.mark.parametrize("tokens,vocab,K,how", [
     (1, 1, 32, "even"), (1, 50, 160, "none"), (7, 3, 96, "skewed"), (8, 9, 512, "one"), (9, 9, 512, "one"),
-    (31, 40, 544, "skewed"), (64, 64, 64, "even"), (65, 5, 1056, "skewed"), (1000, 300, 96, "skewed"),
+    (31, 40, 544, "skewed"), (64, 64, 64, "even"), (33, 5, 64, "even"), (64, 3, 4096, "one"), (64, 100, 1056, "skewed"), (65, 5, 1056, "skewed"), (1000, 300, 96, "skewed"),
     (1000, 1000, 4096, "even"), (3000, 2, 64, "one"), (8192, 5000, 64, "skewed"), (8192, 60, 32, "none"),
     (8193, 900, 64, "skewed"), (9000, 70000, 32, "even"), (20000, 5000, 96, "skewed"), (20000, 50, 32, "one"),
-    (300, 600_000, 32, "even"), (40000, 1_100_000, 32, "skewed"), (33, 524_287, 32, "even"), (33, 524_286, 32, "even"),
+    (300, 600_000, 32, "even"), (33, 600_000, 32, "even"), (40000, 1_100_000, 32, "skewed"), (133, 524_287, 32, "even"), (133, 524_286, 32, "even"),
     (9000, 1023, 4096, "skewed"), (9000, 1024, 32, "skewed"), (70001, 128, 512, "skewed"),
 ])
 @pytest.mark.parametrize("dtype,out,form", [("bf16", "f32", "plain"), ("f32", "bf16", "add"), ("f32", "f32", "in place"),
@@ -192,6 +192,6 @@ def test_refusals():
     with pytest.raises((ValueError, b.MxGemmError)):
         b.embed_backward(table[:4], ids, 0)
     with pytest.raises(b.MxGemmError):
-        b.embed_backward(table[:4], ids, 8, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        b.embed_backward(table.repeat(20, 1), ids.repeat(40), 8, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         b.embed_backward(table[:4], ids, 9, add=table)

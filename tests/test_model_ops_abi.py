@@ -18,7 +18,7 @@ F32, BF16 = 1, 2
 CALLS = dict(
     mxgemm_embed=dict(in_dtype=BF16, table=1 * MB, table_stride=256, vocab=100, K=256, ids=2 * MB, id_bytes=8, tokens=9,
                       scale=1.5, out_dtype=F32, out=3 * MB, stream=None),
-    mxgemm_embed_backward=dict(in_dtype=BF16, dy=1 * MB, dy_stride=256, ids=2 * MB, id_bytes=4, tokens=9, vocab=100,
+    mxgemm_embed_backward=dict(in_dtype=BF16, dy=1 * MB, dy_stride=256, ids=2 * MB, id_bytes=4, tokens=99, vocab=100,
                                K=256, scale=1.0, add=3 * MB, out_dtype=F32, dtable=4 * MB, workspace=5 * MB,
                                ws_bytes=MB, stream=None),
     mxgemm_qk_norm_rope=dict(in_dtype=BF16, x=1 * MB, x_token=512, x_head=64, tokens=9, q_heads=4, k_heads=2, D=64,
@@ -26,7 +26,7 @@ CALLS = dict(
                              rotary=32, positions=5 * MB, position_bytes=8, flags=1, y=6 * MB, y_token=384, y_head=64,
                              rstd=7 * MB, stream=None),
     mxgemm_qk_norm_rope_backward=dict(in_dtype=F32, dy=1 * MB, dy_token=384, dy_head=64, x=2 * MB, x_token=384,
-                                      x_head=64, rstd=3 * MB, tokens=9, q_heads=4, k_heads=2, D=64, q_weight=4 * MB,
+                                      x_head=64, rstd=3 * MB, tokens=300, q_heads=4, k_heads=2, D=64, q_weight=4 * MB,
                                       k_weight=5 * MB, weight_dtype=BF16, rope=6 * MB, rope_rows=50, rotary=64,
                                       positions=7 * MB, position_bytes=4, flags=0, dx=8 * MB, dx_token=384, dx_head=64,
                                       dq_weight=9 * MB, dk_weight=10 * MB, workspace=11 * MB, ws_bytes=MB, stream=None),
@@ -209,10 +209,10 @@ def test_workspaces():
     from mx_block_scaled_gb300 import binding as lib
     f = lib.mxgemm_embed_backward_workspace_bytes
     assert f(0, 100, 64) == f(9, 0, 64) == f(9, 100, 40) == f(9, 1 << 30, 64) == 0
-    assert 0 < f(1, 100, 64) <= 128 and f(1 << 15, 128256, 4096) <= (1 << 19) + (1 << 10) * 2 * 4096 * 4 + 64
+    assert f(1, 100, 64) == f(64, 100, 64) == 0 and 0 < f(65, 100, 64) <= 1 << 14 and f(1 << 15, 128256, 4096) <= (1 << 19) + (1 << 10) * 2 * 4096 * 4 + 64
     g = lib.mxgemm_qk_norm_rope_backward_workspace_bytes
     assert g(0, 4, 64) == g(4, 0, 64) == g(4, 4, 24) == g(4, 4, 528) == g(1 << 30, 1 << 20, 64) == 0
-    assert 0 < g(1, 1, 16) <= 128 and g(1 << 20, 40, 128) <= 1 << 20
+    assert g(1, 1, 16) == 0 and 0 < g(1000, 40, 128) <= g(1 << 20, 40, 128) <= 1 << 20
     assert lib.mxgemm_grad_workspace_bytes(0) == 0 and 0 < lib.mxgemm_grad_workspace_bytes(1) <= 1 << 13
     assert lib.mxgemm_grad_workspace_bytes(2000) <= 1 << 15
 
