@@ -712,14 +712,16 @@ MXGEMM_API int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride,
  *   dlogits_v = scale * (dlogprob * ([v = target] - p_v) - dentropy * p_v * (ln p_v + entropy))
  *   stats and entropy as the forward left them; targets and dlogprob are both given or
  *   both NULL, and so is entropy where dentropy is (NULL: 0).
- *   dlogits: [rows, V] dense, of type in_dtype; may be logits itself.
+ *   dlogits: [rows, V] of type in_dtype, with its own stride; may be logits itself, with
+ *            its stride.  Rows that start alike against 32-byte boundaries in both (the
+ *            same matrix, two of one stride) go 32 bytes at a time, others value by value.
  * A target outside 0..V-1 leaves only the entropy's part; a row without a value above
  * -infinity has a gradient of zero.
  */
 MXGEMM_API int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, int64_t rows, int64_t V,
                                         float scale, const void *targets, int id_bytes, const float *stats,
                                         const float *dlogprob, const float *entropy, const float *dentropy,
-                                        void *dlogits, void *stream);
+                                        void *dlogits, int64_t dlogits_stride, void *stream);
 
 /*
  * The norm of n gradients together, and the gradients clipped to it:

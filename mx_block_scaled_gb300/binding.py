@@ -115,7 +115,7 @@ SIGNATURES = [
     ("mxgemm_logprobs", ctypes.c_int,
      [_I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, _P, _I64, _P, _P, _P]),
     ("mxgemm_logprobs_backward", ctypes.c_int,
-     [_I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P]),
+     [_I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _I64, _P]),
     ("mxgemm_grad_workspace_bytes", ctypes.c_size_t, [_I64]),
     ("mxgemm_grad_norm", ctypes.c_int, [_I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("mxgemm_clip_grads", ctypes.c_int,
@@ -744,7 +744,7 @@ def logprobs(logits, targets=None, scale: float = 1.0, top: int = 0, logprob=Non
 @_on_stream
 def logprobs_backward(logits, targets, stats, dlogprob=None, entropy=None, dentropy=None, scale: float = 1.0,
                       dlogits=None):
-    """Gradient of :func:`logprobs`: dlogits [rows, V], which may be ``logits`` itself.
+    """Gradient of :func:`logprobs`: dlogits [rows, V] (any row stride), which may be ``logits`` itself.
 
     From ``dlogprob`` [rows] with ``targets``, from ``dentropy`` [rows] with the forward's
     ``entropy``, or from both.

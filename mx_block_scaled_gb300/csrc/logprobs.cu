@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         const int kept_n = own_max != neg_inf() ? (mine + group - 1) / group : 0;
 #pragma unroll 8
         for (int i = 0; i < kept_n; ++i)
-            hits |= static_cast<uint32_t>(maxima[i * threads + tid] >= least) << i;
+            hits |= static_cast<uint32_t>(maxima[i * threads + tid] >= least && maxima[i * threads + tid] != neg_inf()) << i;
         uint32_t at = __popc(hits) * group;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -622,7 +622,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
 // start alike against 32-byte boundaries; else one value a thread at a time.
 constexpr int kBackChunks = 2;
 template <int IN>
-constexpr int64_t kBackVals = static_cast<int64_t>(kThreads) * kBackChunks * Chunk<IN>::kVals;
+__device__ __host__ __forceinline__ int64_t back_values(int threads)  // of a block
+{
+    return static_cast<int64_t>(threads) * kBackChunks * Chunk<IN>::kVals;
+}
 
 struct RowGrad {
     float m, c, shift;   // ln p = ln2 * t, t = (x - m) * c - shift
@@ -643,20 +646,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
     constexpr int E = ElemBytes<IN>::value;
     griddep_launch_dependents();
     griddep_wait();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, threads = blockDim.x;
     const uint32_t part = blockIdx.x % per_row;
     const int64_t row = blockIdx.x / per_row, V = p.V;
     const char *x = p.x + row * p.stride;
-    char *d = p.dlogits + row * V * E;
+    char *d = p.dlogits + row * p.dlogits_stride;
     const int64_t head = VECTOR ? min(static_cast<int64_t>(((32 - (reinterpret_cast<uintptr_t>(x) & 31)) & 31) / E), V) : 0;
     const int64_t chunks = VECTOR ? (V - head) / Chunk<IN>::kVals : 0;
-    const int64_t c0 = static_cast<int64_t>(part) * kThreads * kBackChunks + tid;
+    const int64_t c0 = static_cast<int64_t>(part) * threads * kBackChunks + tid;
     Chunk<IN> v[kBackChunks];
     if constexpr (VECTOR)
 #pragma unroll
         for (int j = 0; j < kBackChunks; ++j)
-            if (c0 + j * kThreads < chunks)
-                v[j].load(x + (head + (c0 + j * kThreads) * Chunk<IN>::kVals) * E);
+            if (c0 + j * threads < chunks)
+                v[j].load(x + (head + (c0 + j * threads) * Chunk<IN>::kVals) * E);
     const int64_t target = p.targets == nullptr ? -1
                            : p.targets64        ? static_cast<const int64_t *>(p.targets)[row]
                                                 : static_cast<const int32_t *>(p.targets)[row];
@@ -677,17 +680,27 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
         store_one<IN>(d + i * E, r.at(load_one<IN>(x + i * E)) + (i == target ? peak : 0.0f));
     };
     if constexpr (!VECTOR) {
-        for (int64_t i = part * kBackVals<IN> + tid; i < V && i < (part + 1) * kBackVals<IN>; i += kThreads)
-            single(i);
+        constexpr int kAhead = 8;  // values a thread has in flight
+        const int64_t end = min(V, (part + 1) * back_values<IN>(threads));
+        for (int64_t i = part * back_values<IN>(threads) + tid; i < end; i += kAhead * threads) {
+            float one[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                one[j] = i + j * threads < end ? load_one<IN>(x + (i + j * threads) * E) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i + j * threads < end)
+                    store_one<IN>(d + (i + j * threads) * E, r.at(one[j]) + (i + j * threads == target ? peak : 0.0f));
+        }
         return;
     }
     const F2 minus = f2(-r.m, -r.m), cc = f2(r.c, r.c), shift = f2(-r.shift, -r.shift), a2 = f2(r.a, r.a),
              b2 = f2(r.b, r.b);
 #pragma unroll
     for (int j = 0; j < kBackChunks; ++j) {
-        if (c0 + j * kThreads >= chunks)
+        if (c0 + j * threads >= chunks)
             break;
-        const int64_t k = head + (c0 + j * kThreads) * Chunk<IN>::kVals;
+        const int64_t k = head + (c0 + j * threads) * Chunk<IN>::kVals;
         float o[Chunk<IN>::kVals];
         if (r.none || r.low == neg_inf()) {
 #pragma unroll
@@ -752,12 +765,14 @@ cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
     while ((1 << log_blocks) < kLogprobsCluster && p.rows << log_blocks < 2ll * num_sms &&
            chunks >= 4ll * kThreads << log_blocks)
         ++log_blocks;
-    // short rows: fewer threads, down to a warp; with many rows a thread takes more chunks, so that a block's reductions
-    // are fewer
-    const int64_t least = p.rows >= 16ll * num_sms ? 8 : 2;
-    int threads = 32;
-    while (threads < kThreads && chunks >= 2 * least * threads << log_blocks)
-        threads *= 2;
+    // short rows: fewer threads, down to a warp, of two chunks each; and where more rows are to be done than fit at once,
+    // fewer still, up to sixteen chunks each, since a block's reductions are latency that other blocks have to cover
+    // (8192 x 4096 BF16 15 us, 24 with two; 1446 x 10721 FP32 with the 20 most probable 21 us, 29)
+    int threads = kThreads;
+    while (threads > 32 && chunks < 2ll * threads << log_blocks)
+        threads /= 2;
+    while (threads > 32 && chunks < 16ll * threads << log_blocks && p.rows * threads / 2 >= 1024ll * num_sms)
+        threads /= 2;
     if (p.top > 0)
         return p.entropy ? launch_rows<IN, true, true>(p, log_blocks, threads, s)
                          : launch_rows<IN, false, true>(p, log_blocks, threads, s);
@@ -769,12 +784,14 @@ template <int IN, bool ENT>
 cudaError_t launch_backward(const LogprobsBackParams &p, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
-    constexpr int E = ElemBytes<IN>::value;
     // every row and its gradient start alike where the first do and the rows' steps are alike
     const uintptr_t off = reinterpret_cast<uintptr_t>(p.x) - reinterpret_cast<uintptr_t>(p.dlogits);
-    const bool vector = (off & 31) == 0 && (p.rows == 1 || ((p.stride - p.V * E) & 31) == 0);
-    const uint32_t per_row = static_cast<uint32_t>((p.V + kBackVals<IN> - 1) / kBackVals<IN>);
-    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * per_row), kThreads, 0, s, attr);
+    const bool vector = (off & 31) == 0 && (p.rows == 1 || ((p.stride - p.dlogits_stride) & 31) == 0);
+    int threads = kThreads;
+    while (threads > 64 && p.V <= back_values<IN>(threads / 2))  // short rows
+        threads /= 2;
+    const uint32_t per_row = static_cast<uint32_t>((p.V + back_values<IN>(threads) - 1) / back_values<IN>(threads));
+    const cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * per_row), threads, 0, s, attr);
     return vector ? cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, true>, p, per_row)
                   : cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<IN, ENT, false>, p, per_row);
 }
@@ -783,7 +800,7 @@ cudaError_t launch_backward(const LogprobsBackParams &p, cudaStream_t s)
 
 bool logprobs_fits(int64_t rows, int64_t V)
 {
-    return rows * ((V + kBackVals<kF32> - 1) / kBackVals<kF32>) < (1ll << 31) && rows * kLogprobsCluster < (1ll << 31);
+    return rows * ((V + back_values<kF32>(kThreads) - 1) / back_values<kF32>(kThreads)) < (1ll << 31) && rows * kLogprobsCluster < (1ll << 31);
 }
 
 cudaError_t launch_logprobs(const LogprobsParams &p, int in_dtype, int num_sms, cudaStream_t s)

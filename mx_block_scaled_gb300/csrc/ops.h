@@ -259,7 +259,8 @@ struct LogprobsBackParams {
     const void *targets;
     bool targets64;
     const float *stats, *dlogprob, *entropy, *dentropy;  // dlogprob, or entropy and dentropy, may be NULL
-    char *dlogits;                 // dense rows
+    char *dlogits;
+    int64_t dlogits_stride;        // bytes
 };
 cudaError_t launch_logprobs_backward(const LogprobsBackParams &p, int in_dtype, cudaStream_t s);
 

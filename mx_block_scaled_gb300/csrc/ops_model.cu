@@ -502,13 +502,15 @@ int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride, int64_t ro
 
 int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, int64_t rows, int64_t V, float scale,
                              const void *targets, int id_bytes, const float *stats, const float *dlogprob,
-                             const float *entropy, const float *dentropy, void *dlogits, void *stream)
+                             const float *entropy, const float *dentropy, void *dlogits, int64_t dlogits_stride,
+                             void *stream)
 {
     if (!logits || !stats || !dlogits || !known_dtype(in_dtype) || !(scale > 0.0f) || !std::isfinite(scale) ||
         (targets != nullptr) != (dlogprob != nullptr) || (targets && !known_ids(id_bytes)) ||
         (dentropy && !entropy) || (!dlogprob && !dentropy))
         return MXGEMM_ERR_ARG;
-    if (rows < 1 || rows > kMaxRows || V < 1 || V > kMaxCols || !logits_shape_ok(stride, rows, V))
+    if (rows < 1 || rows > kMaxRows || V < 1 || V > kMaxCols || !logits_shape_ok(stride, rows, V) ||
+        !logits_shape_ok(dlogits_stride, rows, V))
         return MXGEMM_ERR_SHAPE;
     const int64_t e = elem_bytes(in_dtype);
     if (!aligned(logits, static_cast<unsigned>(e)) || (targets && !aligned(targets, static_cast<unsigned>(id_bytes))) ||
@@ -517,8 +519,9 @@ int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, i
         return MXGEMM_ERR_ALIGN;
     if (!logprobs_fits(rows, V))
         return MXGEMM_ERR_UNSUPPORTED;
-    if (!outputs_apart({{dense(dlogits, rows, V * e), 0b1}},
-                       {{logits, rows, stride * e, V * e},
+    const bool same = dlogits == logits && (rows == 1 || dlogits_stride == stride);
+    if (!outputs_apart({{{dlogits, rows, dlogits_stride * e, V * e}}},
+                       {same ? Span{} : Span{logits, rows, stride * e, V * e},
                         flat(targets, id_bytes * rows),
                         flat(stats, 8 * rows),
                         flat(dlogprob, 4 * rows),
@@ -542,6 +545,7 @@ int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, i
     p.entropy = entropy;
     p.dentropy = dentropy;
     p.dlogits = static_cast<char *>(dlogits);
+    p.dlogits_stride = dlogits_stride * e;
     return status_of(launch_logprobs_backward(p, in_dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -769,11 +769,20 @@ PyObject *logprobs_backward(Args a)
     const float scale = number(a[6]);
     Out stats, dlogits;
     output(stats, a[2], false, {s.rows, 2}, at::kFloat, s, "stats");
-    output(dlogits, a[7], true, {s.rows, s.cols}, s.dtype, s, "dlogits");
+    int64_t stride = s.cols;
+    if (a[7] != Py_None) {  // the caller's, with its own stride
+        const Rows r = in_rows(a[7], s, s.rows, s.cols, "dlogits");
+        stride = r.stride;
+        dlogits.ptr = const_cast<void *>(r.ptr);
+        Py_INCREF(a[7]);
+        dlogits.object = a[7];
+    } else {
+        output(dlogits, a[7], true, {s.rows, s.cols}, s.dtype, s, "dlogits");
+    }
     const auto call = [&] {
         return g_entry.logprobs_backward(s.in_dtype, s.ptr, s.stride, s.rows, s.cols, scale, targets.ptr,
                                          targets.bytes, static_cast<const float *>(stats.ptr), g, entropy, h,
-                                         dlogits.ptr, current_stream(s));
+                                         dlogits.ptr, stride, current_stream(s));
     };
     return result(call, dlogits);
 }

@@ -210,6 +210,24 @@ def test_gradient_of_shapes_of_rows(how, dtype):
     _backward(x, x64, got, t, t64, 1.0, rng, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_of_a_padded_vocabulary(dtype):
+    """Logits whose rows have columns past the vocabulary: their gradient in place, beside, and dense."""
+    import torch
+    b, rng = lib(), np.random.default_rng(12)
+    wide, _ = _logits(rng, 9, 1024, dtype)
+    keep = wide.clone()
+    x = wide[:, :999]
+    x64 = _np(x)
+    got, t, t64, _ = _check(x, x64, rng, top=4)
+    dense = b.logprobs_backward(x, t, got.stats, torch.ones(9, device="cuda"))
+    beside = torch.full_like(wide, 3.0)
+    assert b.logprobs_backward(x, t, got.stats, torch.ones(9, device="cuda"), dlogits=beside[:, :999]).data_ptr() == beside.data_ptr()
+    assert torch.equal(beside[:, :999], dense) and (beside[:, 999:] == 3).all()
+    _backward(x, x64, got, t, t64, 1.0, rng, dtype, over=True)
+    assert torch.equal(wide[:, 999:], keep[:, 999:])
+
+
 def test_gradient_into_other_alignment():
     """Logits off a 32-byte boundary, their gradient on one: value by value."""
     import torch

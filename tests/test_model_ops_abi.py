@@ -35,7 +35,7 @@ CALLS = dict(
                          stream=None),
     mxgemm_logprobs_backward=dict(in_dtype=BF16, logits=1 * MB, stride=100, rows=9, V=100, scale=2.0, targets=2 * MB,
                                   id_bytes=4, stats=3 * MB, dlogprob=4 * MB, entropy=5 * MB, dentropy=6 * MB,
-                                  dlogits=7 * MB, stream=None),
+                                  dlogits=7 * MB, dlogits_stride=100, stream=None),
 )
 NO_NORM = dict(q_weight=None, k_weight=None, rstd=None)
 NO_NORM_BACK = dict(NO_NORM, x=None, dq_weight=None, dk_weight=None, workspace=None, ws_bytes=0)
@@ -108,7 +108,7 @@ REFUSED = [
         (dict(targets=None, dlogprob=None, dentropy=None), ARG),
         (dict(rows=0), SHAPE), (dict(V=0), SHAPE), (dict(stride=50), SHAPE),
         (dict(logits=MB + 1), ALIGN), (dict(dlogits=7 * MB + 1), ALIGN), (dict(stats=3 * MB + 4), ALIGN),
-        (dict(dlogits=MB + 2), ARG), (dict(dlogits=MB, stride=128), ARG), (dict(dlogits=2 * MB), ARG),
+        (dict(dlogits_stride=99), SHAPE), (dict(dlogits=MB + 2), ARG), (dict(dlogits=MB, stride=128), ARG), (dict(dlogits=2 * MB), ARG),
         (dict(dlogits=3 * MB), ARG), (dict(dlogits=4 * MB), ARG), (dict(dlogits=5 * MB), ARG), (dict(dlogits=6 * MB), ARG)]),
 ]
 SERVED = [(name, {}) for name in CALLS] + [
@@ -126,7 +126,8 @@ SERVED = [(name, {}) for name in CALLS] + [
     ("mxgemm_logprobs", dict(targets=None, logprob=None)), ("mxgemm_logprobs", dict(top=0, top_ids=None, top_logprobs=None)),
     ("mxgemm_logprobs", dict(entropy=None, stats=None)), ("mxgemm_logprobs", dict(logits=MB + 4)),
     ("mxgemm_logprobs", dict(top=32, V=3)),
-    ("mxgemm_logprobs_backward", dict(dlogits=MB)), ("mxgemm_logprobs_backward", dict(entropy=None, dentropy=None)),
+    ("mxgemm_logprobs_backward", dict(dlogits=MB)), ("mxgemm_logprobs_backward", dict(dlogits=MB, stride=128, dlogits_stride=128)),
+    ("mxgemm_logprobs_backward", dict(stride=128, dlogits_stride=104)), ("mxgemm_logprobs_backward", dict(entropy=None, dentropy=None)),
     ("mxgemm_logprobs_backward", dict(targets=None, dlogprob=None)),
 ]
 
