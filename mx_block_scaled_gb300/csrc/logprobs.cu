@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     __shared__ float block_m, block_s, block_w, block_bound;
     __shared__ unsigned long long candidates[TOP ? kCandidates : 1];
     __shared__ unsigned long long warp_best[kWarps], list[32];
+    __shared__ int warp_equal[kWarps];
     __shared__ uint32_t count, chunks_found, chunk_list[TOP ? kChunkList : 1];
     griddep_launch_dependents();
     griddep_wait();
@@ -468,81 +469,129 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         least = fminf(least, ld_f32(in_block(&block_bound, b)));
     const uint32_t to_count = in_block(&count, 0), to_list = in_block(candidates, 0);
     auto offer = [&](float v, int index) {
-        if (!(v >= least) || v == neg_inf())
-            return;
         uint32_t at;
         asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(to_count) : "memory");
         if (at < kCandidates)
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
     };
-    // the chunks whose maximum reaches it
-    if (__any_sync(0xFFFFFFFFu, own_max >= least && own_max != neg_inf())) {
-        uint32_t hits = 0;
-        const int kept_n = own_max != neg_inf() ? (mine + group - 1) / group : 0;
+    // Offers the logits that reach `least`, or, `over`, those above it.
+    auto collect = [&](bool over) {
+        auto counts = [&](float v) { return (over ? v > least : v >= least) && v != neg_inf(); };
+        // the chunks whose maximum counts
+        if (__any_sync(0xFFFFFFFFu, counts(own_max))) {
+            uint32_t hits = 0;
+            const int kept_n = (mine + group - 1) / group;
 #pragma unroll 8
-        for (int i = 0; i < kept_n; ++i)
-            hits |= static_cast<uint32_t>(maxima[i * threads + tid] >= least && maxima[i * threads + tid] != neg_inf()) << i;
-        uint32_t at = __popc(hits) * group;
+            for (int i = 0; i < kept_n; ++i)
+                hits |= static_cast<uint32_t>(counts(maxima[i * threads + tid])) << i;
+            uint32_t at = __popc(hits) * group;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
-            at += lane >= o ? v : 0;
-        }
-        uint32_t start = 0;
-        if (lane == 31)
-            start = atomicAdd(&chunks_found, at);
-        at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits) * group;
-        for (; hits; hits &= hits - 1)
-            for (int j = 0; j < group; ++j, ++at)
-                if (at < kChunkList)
-                    chunk_list[at] = tid + ((__ffs(hits) - 1) * group + j) * threads;
-    }
-    __syncthreads();
-    // their values
-    if (chunks_found > kChunkList) {
-        if (tid == 0)  // too many for the list: so will the candidates be
-            asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to_count), "r"(kCandidates + 1) : "memory");
-    } else {
-        // eight bytes a thread, two at a time
-        constexpr int kPart = Chunk<IN>::kVals / 4;
-        for (uint32_t i0 = tid; i0 < chunks_found * 4; i0 += 2 * threads) {
-            uint2 v[2];
-            int index[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t i = i0 + j * threads;
-                const uint32_t chunk = i < chunks_found * 4 ? chunk_list[i >> 2] : 0xFFFFFFFFu;
-                index[j] = -1;
-                if (chunk < static_cast<uint32_t>(r.to - r.from)) {
-                    index[j] = r.first_of(r.from + chunk) + (i & 3) * kPart;
-                    v[j] = *reinterpret_cast<const uint2 *>(r.at(index[j]));
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                at += lane >= o ? v : 0;
             }
+            uint32_t start = 0;
+            if (lane == 31)
+                start = atomicAdd(&chunks_found, at);
+            at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits) * group;
+            for (; hits; hits &= hits - 1)
+                for (int j = 0; j < group; ++j, ++at)
+                    if (at < kChunkList)
+                        chunk_list[at] = tid + ((__ffs(hits) - 1) * group + j) * threads;
+        }
+        __syncthreads();
+        // their values: eight bytes a thread, two at a time
+        if (chunks_found > kChunkList) {
+            if (tid == 0)  // too many for the list: so will the candidates be
+                asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to_count), "r"(kCandidates + 1) : "memory");
+        } else {
+            constexpr int kPart = Chunk<IN>::kVals / 4;
+            for (uint32_t i0 = tid; i0 < chunks_found * 4; i0 += 2 * threads) {
+                uint2 v[2];
+                int index[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (index[j] >= 0) {
-                    if constexpr (IN == kBf16) {
-                        offer(__uint_as_float(v[j].x << 16), index[j]);
-                        offer(__uint_as_float(v[j].x & 0xFFFF0000u), index[j] + 1);
-                        offer(__uint_as_float(v[j].y << 16), index[j] + 2);
-                        offer(__uint_as_float(v[j].y & 0xFFFF0000u), index[j] + 3);
-                    } else {
-                        offer(__uint_as_float(v[j].x), index[j]);
-                        offer(__uint_as_float(v[j].y), index[j] + 1);
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t i = i0 + j * threads;
+                    const uint32_t chunk = i < chunks_found * 4 ? chunk_list[i >> 2] : 0xFFFFFFFFu;
+                    index[j] = -1;
+                    if (chunk < static_cast<uint32_t>(r.to - r.from)) {
+                        index[j] = r.first_of(r.from + chunk) + (i & 3) * kPart;
+                        v[j] = *reinterpret_cast<const uint2 *>(r.at(index[j]));
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (index[j] >= 0) {
+                        const uint32_t w[2] = {v[j].x, v[j].y};
+#pragma unroll
+                        for (int n = 0; n < kPart; ++n) {
+                            const float f = IN == kBf16 ? __uint_as_float((n & 1) ? (w[n >> 1] & 0xFFFF0000u) : (w[n >> 1] << 16))
+                                                        : __uint_as_float(w[n & 1]);
+                            if (counts(f))
+                                offer(f, index[j] + n);
+                        }
+                    }
+            }
         }
-    }
-    if (tid < r.extras)
-        offer(r.one(r.extra(tid)), r.extra(tid));
-    if (blocks > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    uint32_t n = blocks > 1 ? ld_u32(to_count) : count;
+        if (tid < r.extras && counts(r.one(r.extra(tid))))
+            offer(r.one(r.extra(tid)), r.extra(tid));
+    };
+    auto everybody = [&]() {
+        if (blocks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    collect(false);
+    everybody();
+    uint32_t n = ld_u32(to_count);
     if (n > kCandidates) {
-        // More logits reach the bound than fit (long runs of equal ones, or the largest in few threads' chunks): every
-        // block finds its own best ones, one at a time, and the first block ranks those.
+        // Many equal logits (a mask of the type's lowest value): those above the bound, and each block's first ones of
+        // those that equal it.
+        everybody();
+        if (tid == 0)
+            count = chunks_found = 0;
+        everybody();
+        collect(true);
+        if (tid < r.extras && r.one(r.extra(tid)) == least && least != neg_inf())
+            offer(least, r.extra(tid));
+        int found = 0;  // equal ones before this tile of chunks
+        for (int i = 0; i * threads < r.to - r.from && found < p.top && least != neg_inf(); ++i) {
+            const bool here = i < mine && maxima[i / group * threads + tid] >= least;
+            if (!__syncthreads_or(here))
+                continue;
+            uint32_t equal = 0;
+            if (here) {
+                Chunk<IN> x;
+                x.load(r.at(r.first_of(r.from + i * threads + tid)));
+#pragma unroll
+                for (int j = 0; j < Chunk<IN>::kVals; ++j)
+                    equal |= static_cast<uint32_t>(x.at(j) == least) << j;
+            }
+            int before = __popc(equal);  // and in the chunks before this one
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+                before += lane >= o ? v : 0;
+            }
+            if (lane == 31)
+                warp_equal[warp] = before;
+            __syncthreads();
+            before += found - __popc(equal);
+            for (int w = 0; w < warps; ++w) {
+                before += w < warp ? warp_equal[w] : 0;
+                found += warp_equal[w];
+            }
+            for (; equal && before < p.top; equal &= equal - 1, ++before)
+                offer(least, r.first_of(r.from + i * threads + tid) + __ffs(equal) - 1);
+            __syncthreads();
+        }
+        everybody();
+        n = ld_u32(to_count);
+    }
+    if (n > kCandidates) {
+        // Too many are above it (the largest of the row in few threads' chunks): every block finds its own best ones, one
+        // at a time, and the first block ranks those.
         unsigned long long last = ~0ull;
         for (int k = 0; k < p.top; ++k) {
             unsigned long long best = 0;
