@@ -124,9 +124,8 @@ __global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const EmbedSor
 
 // More tokens: a stable radix sort in one cluster.  Every block owns a contiguous part
 // of the entries and every warp of it a contiguous run.  A pass counts its run's digits
-// by warp (lanes with the same digit find each other with match.any), scans the counts
-// over the warps, adds the other blocks' counts from their shared memory, and walks the
-// run again to write the entries in order.
+// by warp, scans the counts over the warps, adds the other blocks' counts from their
+// shared memory, and walks the run again to write the entries in order.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 4;
@@ -183,12 +182,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
             for (int i = 0; i < kSortAhead; ++i) {
                 if (b + 32 * i >= s1)
                     break;  // warp-uniform
-                const bool live = b + 32 * i + lane < s1;
-                const int d = live ? digit(e[i]) : -1;
-                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
-                if (live && lane == __ffs(peers) - 1)
-                    mine[d * kHistStep] += __popc(peers);
-                __syncwarp();
+                if (b + 32 * i + lane < s1)
+                    atomicAdd(&mine[digit(e[i]) * kHistStep], 1);  // counts only: the order does not matter
             }
         }
         __syncthreads();
@@ -241,8 +236,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
                 if (b + 32 * i >= s1)
                     break;  // warp-uniform
                 const bool live = b + 32 * i + lane < s1;
-                const int d = live ? digit(e[i]) : -1;
-                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+                const int d = digit(e[i]);
+                // the lanes with the same digit, a bit of it at a time (match.any takes its turns value by value)
+                uint32_t peers = __ballot_sync(0xFFFFFFFFu, live);
+                for (int bit = 0; bit < p.bits; ++bit) {
+                    const uint32_t ones = __ballot_sync(0xFFFFFFFFu, (d >> bit) & 1);
+                    peers &= (d >> bit) & 1 ? ones : ~ones;
+                }
                 const int at = live ? mine[d * kHistStep] : 0;
                 __syncwarp();
                 if (live) {
