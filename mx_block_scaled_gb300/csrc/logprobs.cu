@@ -11,6 +11,12 @@
 // maximum at the end.  The most probable tokens: the threads' own maxima give a value
 // that at least `top` logits reach; the few logits that reach it are collected from
 // the chunks whose maximum does, and ranked against each other.
+//
+// Bound by HBM for long rows: 4096 x 128256 BF16 155 us (6.8 TB/s), with entropy 159 (a
+// value costs one 2^t and eight packed or paired instructions), with the 20 most
+// probable 195 (a row's last steps, 3 us, are covered by the three other blocks of its
+// multiprocessor); 16 such rows on clusters of eight blocks 3.9, 4.5 and 8.2 us, latency:
+// two memory accesses, two cluster barriers, with the most probable ones four and four.
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -667,6 +673,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
 }
 
 // ----------------------------------------------------------------- backward --
+// Bound by HBM: 4096 x 128256 BF16 295 us (7.1 TB/s with what stays in L2), with entropy or
+// without; 8192 x 1000 FP32 9.8 us; where logits and gradient start differently, 1000 x
+// 50257 FP32 80 us instead of 60, BF16 81 instead of 32.
 // A block takes kBackChunks chunks a thread of a row.  VECTOR: the row and its gradient
 // start alike against 32-byte boundaries; else one value a thread at a time.
 constexpr int kBackChunks = 2;
