@@ -14,8 +14,8 @@
 //
 // Bound by HBM for long rows: 4096 x 128256 BF16 155 us (6.8 TB/s), with entropy 159 (a
 // value costs one 2^t and eight packed or paired instructions), with the 20 most
-// probable 195 (a row's last steps, 3 us, are covered by the three other blocks of its
-// multiprocessor); 16 such rows on clusters of eight blocks 3.9, 4.5 and 8.2 us, latency:
+// probable 193 (a row's last steps, 3 us, are covered by the three other blocks of its
+// multiprocessor); 16 such rows on clusters of eight blocks 4.0, 4.4 and 7.8 us, latency:
 // two memory accesses, two cluster barriers, with the most probable ones four and four.
 #include "mx_block.cuh"
 #include "ops.h"
@@ -249,9 +249,12 @@ struct Row {
     __device__ __forceinline__ float one(int v) const { return load_one<IN>(at(v)); }
 };
 
-// TOP: every thread keeps the maxima of its chunks, `group` of them in one.
-template <int IN, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int group)
+// TOP: every thread keeps the maxima of its chunks, `group` of them in one.  SPLIT: a
+// cluster of 2^log_blocks blocks shares a row; there are few rows then, so more chunks in
+// flight count for more than more blocks on a multiprocessor (64 x 128256 with the 20 most
+// probable: 9.9 us with four chunks and two blocks, 12.4 with two and four).
+template <int IN, bool ENT, bool TOP, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int group)
 {
     extern __shared__ float maxima[];  // [kept][threads], TOP only
     __shared__ float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps], warp_bound[kWarps];
@@ -263,9 +266,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
-    const int blocks = 1 << log_blocks, rank = static_cast<int>(blockIdx.x) & (blocks - 1);
-    const int64_t row = blockIdx.x >> log_blocks;
-    const Row<IN> r(p.x + row * p.stride, static_cast<int>(p.V), rank, log_blocks);
+    constexpr int kAhead = SPLIT ? 4 : 2;  // chunks of a thread in flight
+    const int blocks = SPLIT ? 1 << log_blocks : 1, rank = SPLIT ? static_cast<int>(blockIdx.x) & (blocks - 1) : 0;
+    const int64_t row = SPLIT ? blockIdx.x >> log_blocks : blockIdx.x;
+    auto everybody = [&]() {
+        if constexpr (SPLIT)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    const Row<IN> r(p.x + row * p.stride, static_cast<int>(p.V), rank, SPLIT ? log_blocks : 0);
     const float c = p.scale * kLog2E, step_up = kMargin / c;
     if (tid == 0)
         count = chunks_found = 0;
@@ -316,11 +326,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
             add_chunk<IN, ENT>(s2, w2, x, a.ref, low, c);
     };
     {
-        Chunk<IN> x[2];
+        Chunk<IN> x[kAhead];
         const char *from = r.at(r.first_of(r.from + tid));
         const int64_t step = threads * 32;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kAhead; ++j)
             if (j < mine)
                 x[j].load(from + j * step);
         if (rank == 0 && tid == 0 && p.targets) {
@@ -334,14 +344,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         float m = mine > 0 ? x[0].max() : neg_inf();
         a.ref = warp_max(m == m ? m : neg_inf());
         low = floor_of(a.ref, c);
-        for (int i = 0; i < mine; i += 2) {
-            from += 2 * step;
+        for (int i = 0; i < mine; i += kAhead) {
+            from += kAhead * step;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < kAhead; ++j) {
                 if (i + j >= mine)
                     break;
                 const Chunk<IN> now = x[j];
-                if (i + j + 2 < mine)
+                if (i + j + kAhead < mine)
                     x[j].load(from + j * step);
                 take(now);
             }
@@ -424,10 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
                 block_bound = v;
         }
     }
-    if (blocks > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    everybody();
 
     // ---- the row's sums
     float log_s = 0.0f, row_m = neg_inf();
@@ -464,21 +471,32 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         }
     }
     if constexpr (!TOP) {
-        if (blocks > 1)
+        if constexpr (SPLIT)
             cluster_sync();  // no block leaves while the first may still read its sums
         return;
     }
 
     // ---- the most probable tokens
     float least = block_bound;
-    for (int b = 0; b < blocks && blocks > 1; ++b)
-        least = fminf(least, ld_f32(in_block(&block_bound, b)));
+    if constexpr (SPLIT) {
+        least = ld_f32(in_block(&block_bound, lane & (blocks - 1)));  // a block a lane: one latency for all of them
+#pragma unroll
+        for (int o = kLogprobsCluster / 2; o > 0; o >>= 1)
+            least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+    }
+    // the row's candidates, in the first block, in any order: they are ranked by their keys
     const uint32_t to_count = in_block(&count, 0), to_list = in_block(candidates, 0);
     auto offer = [&](float v, int index) {
-        uint32_t at;
-        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(to_count) : "memory");
-        if (at < kCandidates)
-            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
+        if constexpr (SPLIT) {
+            uint32_t at;
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(to_count) : "memory");
+            if (at < kCandidates)
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
+        } else {
+            const uint32_t at = atomicAdd(&count, 1);
+            if (at < kCandidates)
+                candidates[at] = key_of(v, index);
+        }
     };
     // Offers the logits that reach `least`, or, `over`, those above it.
     auto collect = [&](bool over) {
@@ -542,15 +560,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         if (tid < r.extras && counts(r.one(r.extra(tid))))
             offer(r.one(r.extra(tid)), r.extra(tid));
     };
-    auto everybody = [&]() {
-        if (blocks > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-    };
     collect(false);
     everybody();
-    uint32_t n = ld_u32(to_count);
+    uint32_t n = SPLIT ? ld_u32(to_count) : count;
     if (n > kCandidates) {
         // Many equal logits (a mask of the type's lowest value): those above the bound, and each block's first ones of
         // those that equal it.
@@ -593,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
             __syncthreads();
         }
         everybody();
-        n = ld_u32(to_count);
+        n = SPLIT ? ld_u32(to_count) : count;
     }
     if (n > kCandidates) {
         // Too many are above it (the largest of the row in few threads' chunks): every block finds its own best ones, one
@@ -630,8 +642,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
             last = best;
             __syncthreads();
         }
-        if (blocks > 1)
-            cluster_sync();
+        everybody();
         n = static_cast<uint32_t>(p.top * blocks);
         if (rank == 0)
             for (uint32_t i = tid; i < n; i += threads)
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         __syncthreads();
     }
     __syncwarp();
-    if (blocks > 1)
+    if constexpr (SPLIT)
         cluster_arrive();  // this block reads no other's memory any more
     if (rank == 0) {
         const float m = warp_m[0], ls = warp_s[0];
@@ -650,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
             if (key == 0)
                 continue;
             uint32_t larger = 0;
+#pragma unroll 8
             for (uint32_t j = 0; j < n; ++j)
                 larger += candidates[j] > key;
             if (larger < static_cast<uint32_t>(p.top)) {
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsPar
         }
     }
     __syncwarp();
-    if (blocks > 1)
+    if constexpr (SPLIT)
         cluster_wait();  // no block leaves while another may still read its memory
 }
 
@@ -802,30 +814,32 @@ cudaError_t launch_rows(const LogprobsParams &p, int log_blocks, int threads, cu
     const int group = static_cast<int>(mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1);
     const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * threads * sizeof(float) : 0;
     cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), threads, smem, s, attr);
-    if (blocks > 1) {
-        both[0] = attr[0];
-        both[1].id = cudaLaunchAttributeClusterDimension;
-        both[1].val.clusterDim.x = blocks;
-        both[1].val.clusterDim.y = 1;
-        both[1].val.clusterDim.z = 1;
-        cfg.attrs = both;
-        cfg.numAttrs = 2;
-    }
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP>, p, log_blocks, group);
+    if (blocks == 1)
+        return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, false>, p, 0, group);
+    both[0] = attr[0];
+    both[1].id = cudaLaunchAttributeClusterDimension;
+    both[1].val.clusterDim.x = blocks;
+    both[1].val.clusterDim.y = 1;
+    both[1].val.clusterDim.z = 1;
+    cfg.attrs = both;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, true>, p, log_blocks, group);
 }
 
 template <int IN>
 cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
 {
-    // few rows: blocks of a cluster share one, while each has at least two chunks a thread
+    // few rows: blocks of a cluster share one, while each has at least two chunks a thread and all of them are resident
+    // at once, two to a multiprocessor (100 x 128256 with the 20 most probable: 13.7 us on two blocks a row, 16.6 where
+    // a second wave is left)
     const int64_t chunks = p.V / Chunk<IN>::kVals;
     int log_blocks = 0;
-    while ((1 << log_blocks) < kLogprobsCluster && p.rows << log_blocks < 2ll * num_sms &&
+    while ((1 << log_blocks) < kLogprobsCluster && p.rows << (log_blocks + 1) <= 2ll * num_sms &&
            chunks >= 4ll * kThreads << log_blocks)
         ++log_blocks;
     // short rows: fewer threads, down to a warp, of two chunks each; and where more rows are to be done than fit at once,
     // fewer still, up to sixteen chunks each, since a block's reductions are latency that other blocks have to cover
-    // (8192 x 4096 BF16 15 us, 24 with two; 1446 x 10721 FP32 with the 20 most probable 21 us, 29)
+    // (8192 x 4096 BF16 15 us, 24 with two; 1446 x 10721 FP32 with the 20 most probable 18 us, 29)
     int threads = kThreads;
     while (threads > 32 && chunks < 2ll * threads << log_blocks)
         threads /= 2;
