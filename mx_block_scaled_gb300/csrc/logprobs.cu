@@ -17,6 +17,8 @@
 // probable 193 (a row's last steps, 3 us, are covered by the three other blocks of its
 // multiprocessor); 16 such rows on clusters of eight blocks 4.0, 4.4 and 7.8 us, latency:
 // two memory accesses, two cluster barriers, with the most probable ones four and four.
+#include <cfloat>
+
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -216,10 +218,21 @@ __device__ __forceinline__ unsigned long long ld_u64(uint32_t a)
 
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// The k-th largest of the lanes' values.
+__device__ __forceinline__ float warp_kth(float v, int k)
+{
+    float m = warp_max(v);
+    for (int n = __popc(__ballot_sync(0xFFFFFFFFu, v == m)); n < k && m != neg_inf();
+         n += __popc(__ballot_sync(0xFFFFFFFFu, v == m))) {
+        v = v == m ? neg_inf() : v;
+        m = warp_max(v);
+    }
+    return m;
 }
 
 // A row as a block sees it: whole chunks from a 32-byte boundary on, which the blocks of
@@ -384,24 +397,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     if (m_warp != neg_inf())
         a.rebase(m_warp, c);
     a.s = warp_sum(a.s);
-    a.w = warp_sum(a.w);
+    if constexpr (ENT)
+        a.w = warp_sum(a.w);
     // at least `each` threads of every warp reach the warp's bound, and `of` warps the block's
     const int need = TOP ? (p.top + blocks - 1) / blocks : 1;
     const int each = (need + warps - 1) / warps, of = (need + each - 1) / each;
-    float bound = neg_inf();
-    if constexpr (TOP) {
-        if (each == 1) {
-            bound = m_warp;
-        } else {  // the lane that `each` - 1 others come before
-            int larger = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float o = __shfl_sync(0xFFFFFFFFu, own_max, i);
-                larger += o > own_max || (o == own_max && i < lane);
-            }
-            bound = __shfl_sync(0xFFFFFFFFu, own_max, __ffs(__ballot_sync(0xFFFFFFFFu, larger == each - 1)) - 1);
-        }
-    }
+    const float bound = TOP && each > 1 ? warp_kth(own_max, each) : m_warp;
     if (lane == 0) {
         warp_m[warp] = m_warp;
         warp_s[warp] = a.s;
@@ -409,17 +410,23 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
         warp_bound[warp] = bound;
     }
     __syncthreads();
-    if (warp == 0) {
-        Sums b = {neg_inf(), 0.0f, 0.0f};
-        if (lane < warps)
-            b = {warp_m[lane], warp_s[lane], warp_w[lane]};
+    // the largest and the sums of as many parts as there are lanes, for all of them
+    auto join = [&](Sums &b) {
         const float m = warp_max(b.ref);
         if (m != neg_inf())
             b.rebase(m, c);
         b.s = warp_sum(b.s);
-        b.w = warp_sum(b.w);
-        if (lane == 0) {
-            block_m = m;
+        if constexpr (ENT)
+            b.w = warp_sum(b.w);
+        b.ref = m;
+    };
+    Sums b = {neg_inf(), 0.0f, 0.0f};
+    if (warp == 0) {
+        if (lane < warps)
+            b = {warp_m[lane], warp_s[lane], warp_w[lane]};
+        join(b);
+        if (SPLIT && lane == 0) {
+            block_m = b.ref;
             block_s = b.s;
             block_w = b.w;
         }
@@ -439,17 +446,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     // ---- the row's sums
     float log_s = 0.0f, row_m = neg_inf();
     if (rank == 0 && warp == 0) {
-        Sums b = {neg_inf(), 0.0f, 0.0f};
-        if (lane < blocks) {
-            b.ref = ld_f32(in_block(&block_m, lane));
-            b.s = ld_f32(in_block(&block_s, lane));
-            b.w = ld_f32(in_block(&block_w, lane));
+        if constexpr (SPLIT) {
+            b = {neg_inf(), 0.0f, 0.0f};
+            if (lane < blocks) {
+                b.ref = ld_f32(in_block(&block_m, lane));
+                b.s = ld_f32(in_block(&block_s, lane));
+                b.w = ld_f32(in_block(&block_w, lane));
+            }
+            join(b);
         }
-        row_m = warp_max(b.ref);
-        if (row_m != neg_inf())
-            b.rebase(row_m, c);
-        b.s = warp_sum(b.s);
-        b.w = warp_sum(b.w);
+        row_m = b.ref;
         log_s = logf(b.s);
         if (lane == 0) {
             // a row without a finite value: no token has a probability, and nothing is uncertain
@@ -486,21 +492,37 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     }
     // the row's candidates, in the first block, in any order: they are ranked by their keys
     const uint32_t to_count = in_block(&count, 0), to_list = in_block(candidates, 0);
-    auto offer = [&](float v, int index) {
+    auto places = [&](uint32_t n) {
         if constexpr (SPLIT) {
             uint32_t at;
-            asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(to_count) : "memory");
-            if (at < kCandidates)
-                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(to_count), "r"(n) : "memory");
+            return at;
         } else {
-            const uint32_t at = atomicAdd(&count, 1);
-            if (at < kCandidates)
-                candidates[at] = key_of(v, index);
+            return atomicAdd(&count, n);
         }
     };
+    auto put = [&](uint32_t at, float v, int index) {
+        if (at >= kCandidates)
+            return;
+        if constexpr (SPLIT)
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_list + at * 8), "l"(key_of(v, index)) : "memory");
+        else
+            candidates[at] = key_of(v, index);
+    };
+    auto offer = [&](float v, int index) { put(places(1), v, index); };
     // Offers the logits that reach `least`, or, `over`, those above it.
     auto collect = [&](bool over) {
-        auto counts = [&](float v) { return (over ? v > least : v >= least) && v != neg_inf(); };
+        const float reach = fmaxf(least, -FLT_MAX);
+        auto counts = [&](float v) { return over ? v > least : v >= reach; };  // -inf never does
+        // the sum of the lanes' up to this one
+        auto up_to_lane = [&](uint32_t n) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, n, o);
+                n += lane >= o ? v : 0;
+            }
+            return n;
+        };
         // the chunks whose maximum counts
         if (__any_sync(0xFFFFFFFFu, counts(own_max))) {
             uint32_t hits = 0;
@@ -508,13 +530,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
 #pragma unroll 8
             for (int i = 0; i < kept_n; ++i)
                 hits |= static_cast<uint32_t>(counts(maxima[i * threads + tid])) << i;
-            uint32_t at = __popc(hits) * group;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
-                at += lane >= o ? v : 0;
-            }
-            uint32_t start = 0;
+            uint32_t at = up_to_lane(__popc(hits) * group), start = 0;
             if (lane == 31)
                 start = atomicAdd(&chunks_found, at);
             at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits) * group;
@@ -527,34 +543,41 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
         // their values: eight bytes a thread, two at a time
         if (chunks_found > kChunkList) {
             if (tid == 0)  // too many for the list: so will the candidates be
-                asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to_count), "r"(kCandidates + 1) : "memory");
+                places(kCandidates + 1);
         } else {
             constexpr int kPart = Chunk<IN>::kVals / 4;
-            for (uint32_t i0 = tid; i0 < chunks_found * 4; i0 += 2 * threads) {
-                uint2 v[2];
+            for (uint32_t first = warp * 32; first < chunks_found * 4; first += 2 * threads) {
+                uint32_t w[4], hits = 0;
                 int index[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t i = i0 + j * threads;
+                    const uint32_t i = first + lane + j * threads;
                     const uint32_t chunk = i < chunks_found * 4 ? chunk_list[i >> 2] : 0xFFFFFFFFu;
                     index[j] = -1;
                     if (chunk < static_cast<uint32_t>(r.to - r.from)) {
                         index[j] = r.first_of(r.from + chunk) + (i & 3) * kPart;
-                        v[j] = *reinterpret_cast<const uint2 *>(r.at(index[j]));
+                        const uint2 v = *reinterpret_cast<const uint2 *>(r.at(index[j]));
+                        w[2 * j] = v.x;
+                        w[2 * j + 1] = v.y;
                     }
                 }
+                auto value = [&](uint32_t word, int n) {
+                    return __uint_as_float(IN == kF32 ? word : (n & 1) ? (word & 0xFFFF0000u) : (word << 16));
+                };
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (index[j] >= 0) {
-                        const uint32_t w[2] = {v[j].x, v[j].y};
-#pragma unroll
-                        for (int n = 0; n < kPart; ++n) {
-                            const float f = IN == kBf16 ? __uint_as_float((n & 1) ? (w[n >> 1] & 0xFFFF0000u) : (w[n >> 1] << 16))
-                                                        : __uint_as_float(w[n & 1]);
-                            if (counts(f))
-                                offer(f, index[j] + n);
-                        }
-                    }
+                for (int n = 0; n < 2 * kPart; ++n)
+                    if (index[n / kPart] >= 0 && counts(value(w[n * 2 / kPart], n)))
+                        hits |= 1u << n;
+                if (!__any_sync(0xFFFFFFFFu, hits))
+                    continue;
+                uint32_t at = up_to_lane(__popc(hits)), start = 0;  // one addition for the warp's
+                if (lane == 31)
+                    start = places(at);
+                at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits);
+                for (; hits; hits &= hits - 1, ++at) {
+                    const int n = __ffs(hits) - 1, k = n * 2 / kPart;
+                    put(at, value(k < 2 ? (k ? w[1] : w[0]) : (k == 2 ? w[2] : w[3]), n), (n < kPart ? index[0] : index[1]) + n % kPart);
+                }
             }
         }
         if (tid < r.extras && counts(r.one(r.extra(tid))))
@@ -830,7 +853,7 @@ template <int IN>
 cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
 {
     // few rows: blocks of a cluster share one, while each has at least two chunks a thread and all of them are resident
-    // at once, two to a multiprocessor (100 x 128256 with the 20 most probable: 13.7 us on two blocks a row, 16.6 where
+    // at once, two to a multiprocessor (100 x 128256 with the 20 most probable: 13.7 us on two blocks a row, 17.5 on four, where
     // a second wave is left)
     const int64_t chunks = p.V / Chunk<IN>::kVals;
     int log_blocks = 0;
