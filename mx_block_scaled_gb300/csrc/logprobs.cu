@@ -194,9 +194,6 @@ __device__ __forceinline__ float key_value(unsigned long long key)
     return __uint_as_float(u);
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) { return map_to_cta(smem_addr(p), rank); }
 __device__ __forceinline__ float ld_f32(uint32_t a)
 {

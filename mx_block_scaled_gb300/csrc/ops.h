@@ -169,6 +169,7 @@ struct EmbedSortParams {
     int bits, passes;              // passes 0: few tokens, sorted by counting
     int64_t run;                   // entries of a warp, a multiple of 32
     uint2 *entries0, *entries1;    // (id, token): the first pass writes entries0, the second entries1, and so on
+    int *counts;                   // [blocks][2^kEmbedDigitBits]
 };
 
 struct EmbedBackParams {
