@@ -12,11 +12,11 @@
 // that at least `top` logits reach; the few logits that reach it are collected from
 // the chunks whose maximum does, and ranked against each other.
 //
-// Bound by HBM for long rows: 4096 x 128256 BF16 155 us (6.8 TB/s), with entropy 159 (a
+// Bound by HBM for long rows: 4096 x 128256 BF16 153 us (6.9 TB/s), with entropy 157 (a
 // value costs one 2^t and eight packed or paired instructions), with the 20 most
-// probable 193 (a row's last steps, 3 us, are covered by the three other blocks of its
-// multiprocessor); 16 such rows on clusters of eight blocks 4.0, 4.4 and 7.8 us, latency:
-// two memory accesses, two cluster barriers, with the most probable ones four and four.
+// probable 183 (a row's last steps, 3 us, are covered by the three other blocks of its
+// multiprocessor); 16 such rows on clusters of eight blocks 3.7, 4.2 and 7.4 us, latency:
+// two memory accesses, two cluster barriers, with the most probable ones four and three.
 #include <cfloat>
 
 #include "mx_block.cuh"
@@ -178,6 +178,13 @@ __device__ __forceinline__ void add_chunk(F2 &s2, F2 &w2, const Chunk<IN> &x, fl
         if constexpr (ENT)
             w2 = f2_fma(e, z, w2);
     }
+}
+
+// The next larger value; -inf gives the lowest finite one, inf none (a NaN).
+__device__ __forceinline__ float next_above(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return __uint_as_float((u >> 31) ? u - 1 : u + 1);
 }
 
 // Order of logits: by value, equal ones by index; a larger key comes first.
@@ -525,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     auto offer = [&](float v, int index) { put(places(1), v, index); };
     // Offers the logits that reach `least`, or, `over`, those above it.
     auto collect = [&](bool over) {
-        const float reach = fmaxf(least, -FLT_MAX);
-        auto counts = [&](float v) { return over ? v > least : v >= reach; };  // -inf never does
+        const float reach = over ? next_above(least) : fmaxf(least, -FLT_MAX);
+        auto counts = [&](float v) { return v >= reach; };  // -inf never does
         // the sum of the lanes' up to this one
         auto up_to_lane = [&](uint32_t n) {
 #pragma unroll
@@ -596,17 +603,43 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
         if (tid < r.extras && counts(r.one(r.extra(tid))))
             offer(r.one(r.extra(tid)), r.extra(tid));
     };
-    collect(false);
-    everybody();
-    uint32_t n = SPLIT ? ld_u32(to_count) : count;
-    if (n > kCandidates) {
-        // Many equal logits (a mask of the type's lowest value): those above the bound, and each block's first ones of
-        // those that equal it.
+    bool over = false;
+    uint32_t n = 0;
+    for (int tries = 0;; ++tries) {
+        collect(over);
+        if (over)
+            break;
+        everybody();
+        n = SPLIT ? ld_u32(to_count) : count;
+        if (n <= kCandidates)
+            break;
         everybody();
         if (tid == 0)
             count = chunks_found = 0;
+        // The largest logits are next to each other (tokens of one range, the others masked), so that few warps hold
+        // them: the `top`-th largest maximum of a block's threads is reached often enough by itself.
+        over = true;
+        if (tries == 0) {
+            float *const all = reinterpret_cast<float *>(chunk_list);
+            all[tid] = own_max;
+            __syncthreads();
+            int larger = 0;
+            for (int i = 0; i < threads; ++i)
+                larger += all[i] > own_max || (all[i] == own_max && i < tid);
+            if (larger == p.top - 1)
+                block_bound = own_max;
+            everybody();
+            float bound = block_bound;
+            if constexpr (SPLIT)
+                bound = warp_max(ld_f32(in_block(&block_bound, lane & (blocks - 1))));
+            over = bound <= least;
+            least = fmaxf(least, bound);
+        }
         everybody();
-        collect(true);
+    }
+    if (over) {
+        // Many equal logits (a mask of the type's lowest value): those above the bound, and each block's first ones of
+        // those that equal it.
         if (tid < r.extras && r.one(r.extra(tid)) == least && least != neg_inf())
             offer(least, r.extra(tid));
         int found = 0;  // equal ones before this tile of chunks

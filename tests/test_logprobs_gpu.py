@@ -106,6 +106,33 @@ def test_shapes_of_rows(rows, V, top, how, dtype):
     _check(x, x64, rng, top=top)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("outside", ["-inf", "lower", "steps"])
+@pytest.mark.parametrize("rows,V,first,n", [(3, 128256, 40000, 1000), (2, 128256, 127000, 1256), (160, 60000, 4096, 2048),
+                                            (160, 60001, 0, 700), (700, 5000, 513, 900), (5, 1_000_003, 500_000, 40_000)])
+def test_one_range_of_tokens(rows, V, first, n, outside, dtype):
+    """The largest logits are a range's, which few threads hold; then in steps, many of them equal."""
+    rng = np.random.default_rng([rows, first])
+    x, _ = _logits(rng, rows, V, dtype, "steps" if outside == "steps" else "model")
+    x[:, first:first + n] += 40
+    if outside == "-inf":
+        x[:, :first] = x[:, first + n:] = -float("inf")
+    for top in (1, 20, 32):
+        _check(x, _np(x), rng, top=top)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2, 160])
+def test_most_probable_tokens_of_two_threads(rows, dtype):
+    """More of them than are ranked at once, at the places of two threads of a block of 256."""
+    rng = np.random.default_rng(rows)
+    V, values = 65536 * (2 if rows > 100 else 8), 16 if dtype == "bf16" else 8
+    x, _ = _logits(rng, rows, V, dtype)
+    x[:, (np.arange(V) // values % 256 == 9) | (np.arange(V) // values % 256 == 201)] += 40
+    for top in (5, 20):
+        _check(x, _np(x), rng, top=top)
+
+
 @pytest.mark.parametrize("rows,V,threads", [(2500, 500, 32), (2500, 5000, 32), (2600, 20000, 128), (400, 9000, 256)])
 def test_many_rows(rows, V, threads):
     """Enough rows for every rule on a block's size."""
