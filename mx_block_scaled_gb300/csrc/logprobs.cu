@@ -17,7 +17,9 @@
 // probable 183 (a row's last steps, 3 us, are covered by the three other blocks of its
 // multiprocessor); 16 such rows on clusters of eight blocks 3.7, 4.2 and 7.4 us, latency:
 // two memory accesses, two cluster barriers, with the most probable ones four and three.
+#include <algorithm>
 #include <cfloat>
+#include <cstdint>
 
 #include "mx_block.cuh"
 #include "ops.h"
@@ -873,18 +875,44 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
         single(tid < head ? tid : tid + chunks * Chunk<IN>::kVals);
 }
 
+// Threads of a block for long rows, such that as little of the machine idles as can be: 700 x 50257 FP32 with the 20 most
+// probable 30 us in one wave of blocks of 192, 38 in a wave of 256 and a seventh of one; 1216 rows are two waves of 256
+// alike.  In tenths of a row's time on a full multiprocessor: the full waves' rows, those of the last one, which takes no
+// less than six tenths of a full one, and every wave's last steps.  After three waves blocks no longer end together
+// (4096 x 128256 BF16 on blocks of 96: 188 us, 176 on those of 256).
+int wave_threads(int64_t rows, int num_sms, int resident)
+{
+    int64_t least = INT64_MAX;
+    int threads = kThreads;
+    for (const int t : {256, 192, 160, 128, 96}) {
+        const int64_t fit = resident / t, wave = fit * num_sms, full = rows / wave, rest = rows % wave;
+        const int64_t last = rest == 0 ? 0 : std::max(10 * rest / num_sms, 6 * fit);
+        const int64_t cost = 10 * fit * full + last + 5 * (full + (rest > 0));
+        if (cost < least) {
+            least = cost;
+            threads = t;
+        }
+    }
+    return threads;
+}
+
 template <int IN, bool ENT, bool TOP>
 cudaError_t launch_rows(const LogprobsParams &p, int num_sms, int log_blocks, int threads, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1], both[2];
     const unsigned blocks = 1u << log_blocks;
+    constexpr int resident = IN == kF32 && !ENT && !TOP ? 1280 : 1024;  // threads on a multiprocessor (46, up to 64 registers)
+    if (log_blocks == 0 && threads == kThreads && p.rows <= 12ll * num_sms)
+        threads = wave_threads(p.rows, num_sms, resident);
     // chunks of a thread at most (a row that starts off a 32-byte boundary may have one less)
     const int64_t chunks = (p.V / Chunk<IN>::kVals + blocks - 1) / blocks, mine = (chunks + threads - 1) / threads;
-    const int group = static_cast<int>(mine > kKeptMaxima ? (mine + kKeptMaxima - 1) / kKeptMaxima : 1);
+    // (smaller blocks, of which there are more on a multiprocessor, keep fewer: shared memory is L1's)
+    const int most = threads >= kThreads ? kKeptMaxima : std::max(kKeptMaxima * threads / kThreads, kKeptMaxima / 2);
+    const int group = static_cast<int>(mine > most ? (mine + most - 1) / most : 1);
     const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * threads * sizeof(float) : 0;
     cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), threads, smem, s, attr);
     if (blocks == 1)
-        return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, false>, p, 0, group, num_sms * (4 * kThreads / threads));
+        return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, false>, p, 0, group, num_sms * (resident / threads));
     both[0] = attr[0];
     both[1].id = cudaLaunchAttributeClusterDimension;
     both[1].val.clusterDim.x = blocks;

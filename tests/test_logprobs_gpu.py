@@ -106,6 +106,16 @@ def test_shapes_of_rows(rows, V, top, how, dtype):
     _check(x, x64, rng, top=top)
 
 
+@pytest.mark.parametrize("rows,V,dtype,top,how", [(700, 9000, "bf16", 20, "model"), (900, 9001, "f32", 32, "masked"),
+                                                  (900, 9000, "f32", 0, "model"), (1100, 9000, "bf16", 7, "steps"),
+                                                  (1250, 33000, "f32", 20, "model")])
+def test_rows_of_a_part_of_a_wave(rows, V, dtype, top, how):
+    """Blocks of 192, 160, 128 and 96 threads."""
+    rng = np.random.default_rng(rows + top)
+    x, x64 = _logits(rng, rows, V, dtype, how)
+    _check(x, x64, rng, top=top)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("outside", ["-inf", "lower", "steps"])
 @pytest.mark.parametrize("rows,V,first,n", [(3, 128256, 40000, 1000), (2, 128256, 127000, 1256), (160, 60000, 4096, 2048),
