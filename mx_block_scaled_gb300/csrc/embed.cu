@@ -74,12 +74,13 @@ __device__ __forceinline__ uint32_t key_of(const void *ids, bool wide, int64_t t
 // Few tokens: every entry's place is the number of entries before it, counted by
 // comparing it with all of them.  Id and token make one 32-bit number (the sizes below
 // see to that), so a comparison is two instructions, and the blocks, of 64 entries each,
-// have nothing to tell each other: 8192 tokens are 67 million comparisons, half a
-// million a multiprocessor, and no barrier between blocks (1023 ids 4 us; by digits 12).
+// have nothing to tell each other: no barrier between blocks (with the kernels that follow
+// and find nothing to add, 1024 ids 5.1 us, by digits 10.3; 2048 7.2 and 10.8, 3000 12.4
+// and 10.8, 8192 23.7 and 11.6).
 constexpr int kRankThreads = 256;
 constexpr int kRankEntries = 64;  // of a block: 16 lanes with four each
 constexpr int kRankParts = kRankThreads / (kRankEntries / 4);
-constexpr int kRankTokenBits = 13;
+constexpr int kRankTokenBits = 11;
 constexpr int64_t kRankTokens = 1 << kRankTokenBits;
 constexpr int64_t kRankVocab = (1ll << (32 - kRankTokenBits)) - 1;
 

@@ -89,7 +89,7 @@ def test_lookup_reads_named_rows_only():
     assert _np(got).tolist() == [[1.0] * 64, [0.0] * 64, [0.0] * 64, [1.0] * 64]
 
 
-# up to 64 tokens take no sort; the counting sort takes up to 8192 ids of tables below 2^19 - 1 rows, the radix sort the rest: one pass up to 1023 rows,
+# up to 64 tokens take no sort; the counting sort takes up to 2048 ids of tables below 2^21 - 1 rows, the radix sort the rest: one pass up to 1023 rows,
 # two up to 2^20 - 1, three beyond
 @pytest.mark.parametrize("tokens,vocab,K,how", [
     (1, 1, 32, "even"), (1, 50, 160, "none"), (7, 3, 96, "skewed"), (8, 9, 512, "one"), (9, 9, 512, "one"),
@@ -121,6 +121,28 @@ def test_gradient(tokens, vocab, K, how, dtype, out, form):
     else:
         again = b.embed_backward(dy, ids_dev, vocab, scale=0.75, dtype=_dt(out), add=add)
         assert torch.equal(again, got)                     # the same sums in every run
+
+
+@pytest.mark.parametrize("tokens,vocab,how", [(2047, 5000, "skewed"), (2048, 60, "none"), (2048, 2048, "even"), (2049, 900, "skewed"),
+                                              (2049, 128256, "even"), (4100, 3, "one"), (700, 2_097_150, "skewed"),
+                                              (700, 2_097_151, "skewed"), (65, 3_000_000, "even"), (2049, 3_000_000, "skewed")])
+def test_gradient_around_the_rules_of_the_sort(tokens, vocab, how):
+    import torch
+    b, rng = lib(), np.random.default_rng([tokens, vocab])
+    ids = _ids(rng, tokens, vocab, how)
+    ids[tokens // 2:tokens // 2 + 2] = vocab - 1           # the last row, and ids outside the table
+    ids[:2] = [vocab, -1]
+    real = (ids >= 0) & (ids < vocab)
+    dy, d64 = _make(rng, (tokens, 32), "f32")
+    d64[~real] = 0
+    # the rows that occur, and those next to them
+    rows = np.unique(np.clip(np.concatenate([ids[real], ids[real] + 1, ids[real] - 1, [0, vocab - 1]]), 0, vocab - 1))
+    place = np.full(tokens, -1)
+    place[real] = np.searchsorted(rows, ids[real])
+    got = b.embed_backward(dy, _dev(ids, tokens % 2 == 0), vocab, dtype=torch.float32)
+    want, err = ref.embed_backward(d64, place, len(rows), 1.0, None)
+    assert_near(_np(got[torch.from_numpy(rows).cuda()]), want, err, False, "dtable")
+    assert int(got.any(1).sum()) == len(np.unique(ids[real]))
 
 
 def test_gradient_strides_guards_stream_and_graph():
