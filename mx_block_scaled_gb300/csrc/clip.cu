@@ -10,9 +10,11 @@
 // one partial sum, and every block of the second kernel adds those in the same order.
 // That kernel walks its part backwards: what the first read last is still in L2.
 //
-// Bound by HBM: 872 M BF16 values summed in 247 us (7.1 TB/s), scaled into FP32 in 869 more
-// (6.0 TB/s); 42 M FP32 values of 448 tensors 31 and 52 us.  Two million values take 8.5 us,
-// two launches' latency.
+// Bound by HBM: 872 M BF16 values summed in 247 us (7.1 TB/s), scaled into FP32 in 854 more
+// (6.1 TB/s); 42 M FP32 values of 448 tensors 30 and 51 us.  Four million BF16 values take
+// 8.0 us, one million 5.6, two launches' latency.
+#include <algorithm>
+
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -179,17 +181,19 @@ __device__ __forceinline__ double warp_sum64(double v)
     return v;
 }
 
-__device__ __forceinline__ double block_sum64(double v, double *part)
+// The sum over the block, in its first warp's lanes.  An FP64 addition holds a multiprocessor's pipe for 16 cycles a
+// warp, so one warp adds the threads' sums, 13 additions (43 where every warp adds its own first).
+__device__ __forceinline__ double block_sum64(double v, double *all)
 {
-    v = warp_sum64(v);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = v;
+    all[threadIdx.x] = v;
     __syncthreads();
-    double s = 0.0;
+    if (threadIdx.x < 32) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        s += part[w];
-    return s;
+        for (int w = 1; w < kWarps; ++w)
+            v += all[w * 32 + threadIdx.x];
+        v = warp_sum64(v);
+    }
+    return v;
 }
 
 // Sums of squares between these keep FP32's precision: none overflowed, and what
@@ -271,7 +275,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_norm_kernel(const __grid_constant__ Table<N> table, double *partial)
 {
-    __shared__ double part[kWarps];
+    __shared__ double part[kThreads];
     griddep_launch_dependents();
     griddep_wait();
     double sum = 0.0;
@@ -291,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // The sum of all squares from the blocks' sums.
 __device__ __forceinline__ double total_of(const double *partial, int n, double *part)
 {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads)
+    double s = static_cast<int>(threadIdx.x) < n ? __ldcg(partial + threadIdx.x) : 0.0;
+    for (int i = threadIdx.x + kThreads; i < n; i += kThreads)
         s += __ldcg(partial + i);
     return block_sum64(s, part);
 }
@@ -317,7 +321,7 @@ __device__ __forceinline__ float factor_of(double total, float max_norm)
 
 __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double *partial, int n, float *norm)
 {
-    __shared__ double part[kWarps];
+    __shared__ double part[kThreads];
     griddep_launch_dependents();
     griddep_wait();
     const double total = total_of(partial, n, part);
@@ -380,7 +384,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_clip_kernel(const __grid_constant__ Table<N> table, const double *partial, int n, float max_norm, float *norm)
 {
-    __shared__ double part[kWarps];
+    __shared__ double part[kThreads];
     __shared__ float block_factor;
     griddep_launch_dependents();
     Walk<N, true> walk(table);  // what does not depend on the norm comes before the wait for it
@@ -427,9 +431,11 @@ unsigned fill_table(Table<N> &table, const GradTensor *tensors, int n, int num_s
     }
     table.chunks = chunks;
     const unsigned most = static_cast<unsigned>((num_sms < kGradSms ? num_sms : kGradSms) * kBlocksPerSm);
-    // four chunks to a block where that still fills the multiprocessors: a block's start and sum cost as much as those
-    const unsigned wanted = chunks / 4 > most / kBlocksPerSm ? chunks / 4 : chunks < most / kBlocksPerSm ? chunks : most / kBlocksPerSm;
-    const unsigned blocks = wanted < 1 ? 1 : wanted < most ? wanted : most;
+    // As many chunks to a block as the largest share is anyway, two at least where that still fills the multiprocessors: a
+    // block's start and sum cost as much as those (4 M BF16 values 8 us with two chunks a block, 10 with four; 8 M 11.5
+    // with 512 blocks of four, 12.2 with 608 of three or four).
+    const unsigned share = std::max(2u, (chunks + most - 1) / most), sms = most / kBlocksPerSm;
+    const unsigned blocks = std::max({1u, std::min(chunks, sms), (chunks + share - 1) / share});
     int i = 0;
     for (unsigned b = 0; b <= blocks; ++b) {
         const uint32_t chunk = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * b / blocks);
