@@ -452,16 +452,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
             block_s = b.s;
             block_w = b.w;
         }
-        if constexpr (TOP) {
-            const float v = lane < warps ? warp_bound[lane] : neg_inf();
-            int larger = 0;
-            for (int i = 0; i < warps; ++i) {
-                const float o = __shfl_sync(0xFFFFFFFFu, v, i);
-                larger += o > v || (o == v && i < lane);
-            }
-            if (lane < warps && larger == of - 1)
-                block_bound = v;
-        }
+    }
+    if (TOP && warp == warps - 1) {  // beside the first warp where there is another
+        const float v = warp_kth(lane < warps ? warp_bound[lane] : neg_inf(), of);
+        if (lane == 0)
+            block_bound = v;
     }
     everybody();
 
