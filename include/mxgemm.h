@@ -710,6 +710,7 @@ MXGEMM_API int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride,
 /*
  * The logits' gradient from those of logprob and of entropy:
  *   dlogits_v = scale * (dlogprob * ([v = target] - p_v) - dentropy * p_v * (ln p_v + entropy))
+ *   scale is the forward's, which stats do not hold.
  *   stats and entropy as the forward left them; targets and dlogprob are both given or
  *   both NULL, and so is entropy where dentropy is (NULL: 0).
  *   dlogits: [rows, V] of type in_dtype, with its own stride; may be logits itself, with

@@ -691,7 +691,7 @@ def embed(ids, table, scale: float = 1.0, dtype=None, out=None):
 def embed_backward(dy, ids, vocab: int, scale: float = 1.0, dtype=None, add=None, dtable=None, workspace=None):
     """Gradient of :func:`embed`: dtable[v] = add[v] + scale * sum of dy[t] over ids[t] = v.
 
-    ``dtype`` (float32) is dtable's [vocab, K] and ``add``'s, the gradient so far.  With
+    ``scale`` is the forward's.  ``dtype`` (float32) is dtable's [vocab, K] and ``add``'s, the gradient so far.  With
     ``dtable`` the same tensor as ``add`` only the rows whose id occurs are touched.
     """
     return _done(_rowops.embed_backward(dy, ids, vocab, scale, dtype, add, dtable, workspace),
@@ -720,8 +720,8 @@ def qk_norm_rope_backward(dy, x, rstd, q_heads: int, q_weight=None, k_weight=Non
                           interleaved: bool = False, dx=None, dq_weight=None, dk_weight=None, workspace=None):
     """Gradients of :func:`qk_norm_rope`: (dx, dq_weight, dk_weight), the weights' [D] float32.
 
-    ``x`` and ``rstd`` as the forward had and left them; without weights both are None, and
-    so are the weights' gradients.  ``dx`` may be ``dy`` or ``x`` itself.
+    ``x`` and ``rstd`` as the forward had and left them, ``q_heads``, ``rope``, ``positions``
+    and ``interleaved`` its own; without weights x and rstd are None, and so are the weights' gradients.  ``dx`` may be ``dy`` or ``x`` itself.
     """
     return _done(_rowops.qk_norm_rope_backward(dy, x, rstd, q_heads, q_weight, k_weight, rope, positions, interleaved,
                                                dx, dq_weight, dk_weight, workspace), "mxgemm_qk_norm_rope_backward")
@@ -747,7 +747,7 @@ def logprobs_backward(logits, targets, stats, dlogprob=None, entropy=None, dentr
     """Gradient of :func:`logprobs`: dlogits [rows, V] (any row stride), which may be ``logits`` itself.
 
     From ``dlogprob`` [rows] with ``targets``, from ``dentropy`` [rows] with the forward's
-    ``entropy``, or from both.
+    ``entropy``, or from both.  ``scale`` is the forward's: ``stats`` do not hold it.
     """
     return _done(_rowops.logprobs_backward(logits, targets, stats, dlogprob, entropy, dentropy, scale, dlogits),
                  "mxgemm_logprobs_backward")[0]
