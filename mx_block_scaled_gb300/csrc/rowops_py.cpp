@@ -122,13 +122,20 @@ Sizes matrix(PyObject *o, const char *what)
     return s;
 }
 
+// The address of a tensor that is read, or of one that the call writes: data_ptr() first gives
+// a tensor that shares its memory copy-on-write a copy of its own.
+void *address(const at::Tensor &t, bool written)
+{
+    return written ? t.data_ptr() : const_cast<void *>(t.const_data_ptr());
+}
+
 struct Rows {
-    const void *ptr = nullptr;
+    void *ptr = nullptr;
     int64_t stride = 0;
 };
 
-// A further input matrix of s's type, or nothing.
-Rows in_rows(PyObject *o, const Sizes &s, int64_t rows, int64_t cols, const char *what)
+// A further matrix of s's type, or nothing.
+Rows in_rows(PyObject *o, const Sizes &s, int64_t rows, int64_t cols, const char *what, bool written = false)
 {
     Rows r;
     if (const at::Tensor *t = tensor(o, what)) {
@@ -136,7 +143,7 @@ Rows in_rows(PyObject *o, const Sizes &s, int64_t rows, int64_t cols, const char
             t->device() != s.device || t->stride(1) != 1)
             throw BadTensor(std::string(what) + " must be a " + shape_text({rows, cols}) +
                             " tensor of the same dtype and device, with contiguous rows");
-        r.ptr = t->const_data_ptr();
+        r.ptr = address(*t, written);
         r.stride = t->stride(0);
     }
     return r;
@@ -596,17 +603,17 @@ PyObject *embed_backward(Args a)
 
 // [tokens, heads, D] with contiguous values.
 struct HeadsTensor {
-    const void *ptr = nullptr;
+    void *ptr = nullptr;
     int64_t token = 0, head = 0;
 };
 
-HeadsTensor heads_of(const at::Tensor &t, const char *what)
+HeadsTensor heads_of(const at::Tensor &t, const char *what, bool written)
 {
     if (t.dim() != 3 || t.stride(2) != 1)
         throw BadTensor(std::string(what) + " must be a 3-D CUDA tensor [tokens, heads, D] with contiguous heads");
     check_device(t, what);
     HeadsTensor h;
-    h.ptr = t.const_data_ptr();
+    h.ptr = address(t, written);
     h.token = t.stride(0);
     h.head = t.stride(1);
     return h;
@@ -617,7 +624,7 @@ Sizes heads_sizes(PyObject *o, const char *what)
     const at::Tensor *t = tensor(o, what);
     if (!t)
         throw BadTensor(std::string(what) + " is missing");
-    heads_of(*t, what);
+    heads_of(*t, what, false);
     Sizes s{};
     s.rows = t->size(0);
     s.stride = t->size(1);  // heads
@@ -628,7 +635,7 @@ Sizes heads_sizes(PyObject *o, const char *what)
     return s;
 }
 
-HeadsTensor heads_like(PyObject *o, const Sizes &s, const char *what)
+HeadsTensor heads_like(PyObject *o, const Sizes &s, const char *what, bool written = false)
 {
     const at::Tensor *t = tensor(o, what);
     if (!t)
@@ -637,14 +644,14 @@ HeadsTensor heads_like(PyObject *o, const Sizes &s, const char *what)
         t->scalar_type() != s.dtype || t->device() != s.device)
         throw BadTensor(std::string(what) + " must be a " + shape_text({s.rows, s.stride, s.cols}) +
                         " tensor of the same dtype and device");
-    return heads_of(*t, what);
+    return heads_of(*t, what, written);
 }
 
 // The caller's strided heads, or new dense ones.
 HeadsTensor heads_output(Out &out, PyObject *o, const Sizes &s, const char *what)
 {
     if (o != Py_None) {
-        const HeadsTensor h = heads_like(o, s, what);
+        const HeadsTensor h = heads_like(o, s, what, true);
         Py_INCREF(o);
         out.object = o;
         return h;
@@ -706,7 +713,7 @@ PyObject *qk_norm_rope(Args a)
     const auto call = [&] {
         return g_entry.qk_norm_rope(s.in_dtype, x.ptr, x.token, x.head, s.rows, t.q_heads, t.k_heads, s.cols, t.q, t.k,
                                     t.weight_dtype, eps, t.rope, t.rope_rows, t.rotary, t.positions.ptr,
-                                    t.positions.bytes, t.flags, const_cast<void *>(to.ptr), to.token, to.head,
+                                    t.positions.bytes, t.flags, to.ptr, to.token, to.head,
                                     static_cast<float *>(rstd.ptr), current_stream(s));
     };
     return result(call, y, rstd);
@@ -728,7 +735,7 @@ PyObject *qk_norm_rope_backward(Args a)
         return g_entry.qk_norm_rope_backward(
             s.in_dtype, dy.ptr, dy.token, dy.head, x.ptr, x.token, x.head, static_cast<const float *>(rstd.ptr), s.rows,
             t.q_heads, t.k_heads, s.cols, t.q, t.k, t.weight_dtype, t.rope, t.rope_rows, t.rotary, t.positions.ptr,
-            t.positions.bytes, t.flags, const_cast<void *>(to.ptr), to.token, to.head, static_cast<float *>(dq.ptr),
+            t.positions.bytes, t.flags, to.ptr, to.token, to.head, static_cast<float *>(dq.ptr),
             static_cast<float *>(dk.ptr), ws.ptr, ws.bytes, current_stream(s));
     };
     return result(call, dx, dq, dk);
@@ -771,9 +778,9 @@ PyObject *logprobs_backward(Args a)
     output(stats, a[2], false, {s.rows, 2}, at::kFloat, s, "stats");
     int64_t stride = s.cols;
     if (a[7] != Py_None) {  // the caller's, with its own stride
-        const Rows r = in_rows(a[7], s, s.rows, s.cols, "dlogits");
+        const Rows r = in_rows(a[7], s, s.rows, s.cols, "dlogits", true);
         stride = r.stride;
-        dlogits.ptr = const_cast<void *>(r.ptr);
+        dlogits.ptr = r.ptr;
         Py_INCREF(a[7]);
         dlogits.object = a[7];
     } else {
@@ -789,13 +796,13 @@ PyObject *logprobs_backward(Args a)
 
 // A list or tuple of gradients as host arrays.
 struct Grads {
-    std::vector<const void *> ptr;
+    std::vector<void *> ptr;
     std::vector<int64_t> n;
     std::vector<int> dtype;
 
     Grads() = default;
     // `like`: another list, of the same shapes and strides.
-    Grads(PyObject *list, const char *what, PyObject *like)
+    Grads(PyObject *list, const char *what, bool written, PyObject *like = nullptr)
     {
         if (!PyList_Check(list) && !PyTuple_Check(list))
             throw BadTensor(std::string(what) + " must be a list or tuple of tensors");
@@ -819,7 +826,7 @@ struct Grads {
                 if (t->sizes() != g.sizes() || (t->strides() != g.strides() && !(t->is_contiguous() && g.is_contiguous())))
                     throw BadTensor(std::string(what) + " must have the gradients' shapes and strides");
             }
-            ptr.push_back(t->const_data_ptr());
+            ptr.push_back(address(*t, written));
             n.push_back(t->numel());
             dtype.push_back(in_dtype(t->scalar_type(), what));
         }
@@ -837,7 +844,7 @@ Sizes current_sizes()
 // (grads, norm, workspace)
 PyObject *grad_norm(Args a)
 {
-    const Grads g(a[0], "grads", nullptr);
+    const Grads g(a[0], "grads", false);
     const Sizes s = current_sizes();
     const int64_t n = static_cast<int64_t>(g.n.size());
     Out norm;
@@ -853,10 +860,10 @@ PyObject *grad_norm(Args a)
 // (grads, max_norm, out, norm, workspace)
 PyObject *clip_grads(Args a)
 {
-    const Grads g(a[0], "grads", nullptr);
-    const float max_norm = number(a[1]);
     const bool apart = a[2] != Py_None;
-    const Grads to = apart ? Grads(a[2], "out", a[0]) : Grads();
+    const Grads g(a[0], "grads", !apart);
+    const float max_norm = number(a[1]);
+    const Grads to = apart ? Grads(a[2], "out", true, a[0]) : Grads();
     const Sizes s = current_sizes();
     const int64_t n = static_cast<int64_t>(g.n.size());
     Out norm;
@@ -864,7 +871,7 @@ PyObject *clip_grads(Args a)
     const Workspace ws(a[4], g_entry.grad_workspace_bytes(n), s);
     const auto call = [&] {
         return g_entry.clip_grads(n, g.ptr.data(), g.n.data(), g.dtype.data(),
-                                  apart ? const_cast<void *const *>(to.ptr.data()) : nullptr,
+                                  apart ? to.ptr.data() : nullptr,
                                   apart ? to.dtype.data() : nullptr, max_norm, static_cast<float *>(norm.ptr), ws.ptr,
                                   ws.bytes, current_stream(s));
     };
