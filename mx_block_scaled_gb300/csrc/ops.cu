@@ -13,36 +13,42 @@ namespace {
 constexpr int kMaxDevices = 64;
 
 struct OpsDevice {
-    bool ready = false;
+    bool known = false;
     bool is_sm103 = false;
     int num_sms = 0;
+    bool prepared[mxg::kUnprepared] = {};
 };
 OpsDevice g_ops_dev[kMaxDevices];
 std::mutex g_ops_mutex;
 
 }  // namespace
 
-int mxg::ops_device(int *num_sms)
+int mxg::ops_device(int *num_sms, Family family)
 {
+    constexpr cudaError_t (*kPrepare[kUnprepared])() = {prepare_norm, prepare_embed, prepare_heads};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
         return MXGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_ops_mutex);
     OpsDevice &d = g_ops_dev[dev];
-    if (!d.ready) {
+    if (!d.known) {
         int major = 0, minor = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return MXGEMM_ERR_CUDA;
         d.is_sm103 = major == 10 && minor == 3;
-        if (d.is_sm103 && (mxg::prepare_norm() != cudaSuccess || mxg::prepare_embed() != cudaSuccess ||
-                           mxg::prepare_heads() != cudaSuccess))
+        d.known = true;
+    }
+    if (!d.is_sm103)
+        return MXGEMM_ERR_ARCH;
+    if (family != kUnprepared && !d.prepared[family]) {
+        if (kPrepare[family]() != cudaSuccess)
             return MXGEMM_ERR_CUDA;
-        d.ready = true;
+        d.prepared[family] = true;
     }
     *num_sms = d.num_sms;
-    return d.is_sm103 ? MXGEMM_OK : MXGEMM_ERR_ARCH;
+    return MXGEMM_OK;
 }
 
 namespace {
@@ -175,7 +181,7 @@ int mxgemm_rmsnorm_backward(int in_dtype, const void *dy, int64_t dy_stride, con
                         flat(weight, K * elem_bytes(weight_dtype))}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
-    const int st = ops_device(&sms);
+    const int st = ops_device(&sms, kNormGradient);
     if (st != MXGEMM_OK)
         return st;
     mxg::NormBackParams p;

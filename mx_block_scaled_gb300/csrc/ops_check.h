@@ -11,8 +11,12 @@
 
 namespace mxg {
 
-// The current device's SM count; prepares it on first use (ops.cu).
-int ops_device(int *num_sms);
+// Kernels that a device is prepared for (shared memory, cluster sizes) before their first launch.  Each family by itself:
+// a call prepares, and fails for, no other's.
+enum Family { kNormGradient, kEmbedGradient, kHeads, kUnprepared };
+
+// The current device's SM count, with the family's kernels prepared on it (ops.cu).
+int ops_device(int *num_sms, Family family = kUnprepared);
 
 inline int status_of(cudaError_t e) { return e == cudaSuccess ? MXGEMM_OK : MXGEMM_ERR_CUDA; }
 

@@ -306,7 +306,7 @@ int mxgemm_embed_backward(int in_dtype, const void *dy, int64_t dy_stride, const
                         flat(ids, id_bytes * tokens)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
-    const int st = ops_device(&sms);
+    const int st = ops_device(&sms, kEmbedGradient);
     if (st != MXGEMM_OK)
         return st;
     EmbedBackParams p = {};
@@ -352,7 +352,7 @@ int mxgemm_qk_norm_rope(int in_dtype, const void *x, int64_t x_token_stride, int
                         flat(positions, position_bytes * tokens)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
-    st = ops_device(&sms);
+    st = ops_device(&sms, kHeads);
     if (st != MXGEMM_OK)
         return st;
     HeadsParams p = {};
@@ -423,7 +423,7 @@ int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_
                         {heads_span(from, tokens, heads, D, e)})))
         return MXGEMM_ERR_ARG;
     int sms = 0;
-    st = ops_device(&sms);
+    st = ops_device(&sms, kHeads);
     if (st != MXGEMM_OK)
         return st;
     const bool interleaved = (flags & MXGEMM_ROPE_INTERLEAVED) != 0;
