@@ -37,8 +37,9 @@ bool heads_shape_ok(const Heads &h, int64_t tokens, int64_t heads, int64_t D)
         return true;
     if ((tokens > 1 && (h.token < D || h.token > kMost)) || (heads > 1 && (h.head < D || h.head > kMost)))
         return false;
-    return tokens == 1 || heads == 1 || h.token >= (heads - 1) * h.head + D || h.head / tokens >= h.token ||
-           h.head >= (tokens - 1) * h.token + D;
+    using Wide = __int128;  // 2^31 steps of 2^40 elements
+    return tokens == 1 || heads == 1 || h.token >= static_cast<Wide>(heads - 1) * h.head + D ||
+           h.head >= static_cast<Wide>(tokens - 1) * h.token + D;
 }
 
 bool heads_align_ok(const Heads &h, int64_t tokens, int64_t heads, int64_t elem)
