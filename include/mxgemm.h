@@ -696,7 +696,7 @@ MXGEMM_API int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_
  *   top_ids, top_logprobs: [rows, top], the `top` (0..32) largest logits' ids (int64) and
  *                 log probabilities, largest first, equal ones by id.
  *   logits: [rows, V], any V and any stride of at least V elements, rows aligned to
- *           their type only.   scale: above 0 (1 / temperature).
+ *           their type only.   scale: above 0 (1 / temperature), below 2.35e38.
  * A logit of -infinity has probability 0: its log probability is -infinity, it adds
  * nothing to the entropy, and it is not among the top ones; where fewer than `top` are
  * left, the others are id -1 and -infinity.  A row without another value has log
@@ -710,7 +710,8 @@ MXGEMM_API int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride,
 /*
  * The logits' gradient from those of logprob and of entropy:
  *   dlogits_v = scale * (dlogprob * ([v = target] - p_v) - dentropy * p_v * (ln p_v + entropy))
- *   scale is the forward's, which stats do not hold.
+ *   scale is the forward's, which stats do not hold; times dlogprob and dentropy * entropy it
+ *   is within FP32's range.
  *   stats and entropy as the forward left them; targets and dlogprob are both given or
  *   both NULL, and so is entropy where dentropy is (NULL: 0).
  *   dlogits: [rows, V] of type in_dtype, with its own stride; may be logits itself, with

@@ -17,6 +17,9 @@ using namespace mxg;
 
 bool known_ids(int id_bytes) { return id_bytes == 4 || id_bytes == 8; }
 
+// The kernels take exponents to base 2: scale * log2(e) is an FP32 number too.
+bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.4426950408889634f); }
+
 // Rows of logits start where their type allows.
 bool logits_shape_ok(int64_t stride, int64_t rows, int64_t V)
 {
@@ -459,7 +462,7 @@ int mxgemm_logprobs(int in_dtype, const void *logits, int64_t stride, int64_t ro
                     const void *targets, int id_bytes, float *logprob, float *entropy, float *stats, int64_t top,
                     int64_t *top_ids, float *top_logprobs, void *stream)
 {
-    if (!logits || !known_dtype(in_dtype) || !(scale > 0.0f) || !std::isfinite(scale) ||
+    if (!logits || !known_dtype(in_dtype) || !scale_ok(scale) ||
         (targets != nullptr) != (logprob != nullptr) || (targets && !known_ids(id_bytes)) ||
         (top != 0) != (top_ids != nullptr) || (top != 0) != (top_logprobs != nullptr) ||
         (!logprob && !entropy && !stats && top == 0))
@@ -506,7 +509,7 @@ int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_t stride, i
                              const float *entropy, const float *dentropy, void *dlogits, int64_t dlogits_stride,
                              void *stream)
 {
-    if (!logits || !stats || !dlogits || !known_dtype(in_dtype) || !(scale > 0.0f) || !std::isfinite(scale) ||
+    if (!logits || !stats || !dlogits || !known_dtype(in_dtype) || !scale_ok(scale) ||
         (targets != nullptr) != (dlogprob != nullptr) || (targets && !known_ids(id_bytes)) ||
         (dentropy && !entropy) || (!dlogprob && !dentropy))
         return MXGEMM_ERR_ARG;
