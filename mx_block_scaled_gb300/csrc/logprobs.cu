@@ -48,11 +48,11 @@ __device__ __forceinline__ float exp2_fast(float x)
 // Below this a logit's share of the sums is zero, relative to the reference r: its
 // exponent is -1000 or less.  Values are raised to it so that an infinite one gives 0
 // times a finite number.  At least a BF16 step below r; -inf where there is no such
-// number (the sums then guard every product).
-__device__ __forceinline__ float floor_of(float r, float c)
+// number, or its exponent times `factor` is not finite (the sums then guard every product).
+__device__ __forceinline__ float floor_of(float r, float c, float factor = 1.0f)
 {
-    const float f = fminf(r - 1000.0f / c, r - fabsf(r) * 0.0078125f);
-    return __bfloat162float(__float2bfloat16_rd(f));
+    const float f = fminf(r - 1000.0f / c, r - fabsf(r) * 0.0078125f), low = __bfloat162float(__float2bfloat16_rd(f));
+    return (r - low) * c * factor <= FLT_MAX ? low : neg_inf();
 }
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
     r.shift = stats.y * kLog2E;
     r.a = ENT ? -(g + h * p.entropy[row]) * p.scale : -g * p.scale;
     r.b = -h * kLn2 * p.scale;
-    r.low = floor_of(stats.x, r.c);
+    r.low = floor_of(stats.x, r.c, fmaxf(1.0f, fabsf(r.b)));
     r.none = stats.x == neg_inf();
     const float peak = r.none ? 0.0f : g * p.scale;
     auto single = [&](int64_t i) {
