@@ -734,7 +734,8 @@ MXGEMM_API int mxgemm_logprobs_backward(int in_dtype, const void *logits, int64_
  *       which type; both NULL: all in place (written only where the factor is not 1).
  *   norm: device, one FP32 value.
  * The sum is kept in FP64 and takes squares outside FP32's range; a norm of NaN makes
- * every output NaN, one of infinity zeros (NaN where the gradient is not finite).
+ * every output NaN, one of infinity zeros (NaN where the gradient is not finite, or
+ * max_norm is not).
  * An output touches no other output and no other tensor's input: a tensor that is given
  * twice can be summed, but not clipped in place.
  * workspace: mxgemm_grad_workspace_bytes(n) bytes, 16-byte aligned, holding nothing
