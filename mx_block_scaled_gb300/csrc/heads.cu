@@ -233,12 +233,6 @@ struct Ring {
         stage = slot = f_stage = f_slot = 0;
         real = 0;
         f_position = left > 0 ? position_of(f_token) : 0;
-        if (mine == 0 && !(p.rope && at.turned))  // angle 0 where nothing is copied
-            for (int d = 0; d < kDepth; ++d)
-                for (int i = 0; i < 16; ++i)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(angle_at(d, i >> 2) + (i & 3) * 4),
-                                 "f"(i < 8 ? 1.0f : 0.0f)
-                                 : "memory");
         if (left > 0)
             new_token();
 #pragma unroll
@@ -338,7 +332,8 @@ struct Ring {
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(own_rstd + stage * stage_size) : "memory");
         return v;
     }
-    // cosines (0..7) and sines (8..15) of this lane's angles
+    // cosines (0..7) and sines (8..15) of this lane's angles (a turned lane's; whatever the memory holds where the
+    // position is none of the table's)
     __device__ __forceinline__ void take_angles(float (&c)[16]) const
     {
         uint32_t r[16];
