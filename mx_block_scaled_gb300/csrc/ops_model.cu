@@ -420,11 +420,7 @@ int mxgemm_qk_norm_rope_backward(int in_dtype, const void *dy, int64_t dy_token_
                         flat(q_weight, w),
                         flat(k_weight, w),
                         flat(rope, 4 * rope_rows * rotary),
-                        flat(positions, position_bytes * tokens)}) ||
-        (same_heads(from, to, tokens, heads) &&  // dx over dy: the sums are still not among its bytes
-         !outputs_apart({{flat(dq_weight, 4 * D)}, {flat(dk_weight, 4 * D)},
-                         {flat(need > 0 ? workspace : nullptr, static_cast<int64_t>(need))}},
-                        {heads_span(from, tokens, heads, D, e)})))
+                        flat(positions, position_bytes * tokens)}))
         return MXGEMM_ERR_ARG;
     int sms = 0;
     st = ops_device(&sms, kHeads);
