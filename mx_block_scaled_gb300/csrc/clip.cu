@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
         *norm = norm_of(total);
 }
 
-template <bool SRC, bool DST>
+template <bool SRC>
 __device__ __forceinline__ void scale(const Values<SRC> &v, F2 f, float (&o)[kVals])
 {
 #pragma unroll
@@ -359,7 +359,7 @@ __device__ __forceinline__ void clip_part(const Tensor &t, const Part &p, float 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float o[kVals];
-                scale<SRC, DST>(v[u], f, o);
+                scale(v[u], f, o);
                 store_values<DST>(to - u * kRun * ED, o);
             }
         }
@@ -372,7 +372,7 @@ __device__ __forceinline__ void clip_part(const Tensor &t, const Part &p, float 
         else
             v.load_some(from, left);
         float o[kVals];
-        scale<SRC, DST>(v, f, o);
+        scale(v, f, o);
         if (vector && left >= kVals)
             store_values<DST>(to, o);
         else
