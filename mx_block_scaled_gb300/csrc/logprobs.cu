@@ -33,7 +33,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMargin = 3.0f;
 constexpr int kFetchAhead = 32768;  // bytes of a later row
-constexpr int kCandidates = 512, kChunkList = 384;
+constexpr int kCandidates = 512, kGroupList = 384;
 constexpr int kKeptMaxima = 32;  // maxima that a thread keeps, of one or more chunks each; a bit of a word for every one
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
@@ -280,12 +280,15 @@ __device__ __forceinline__ void fetch_ahead(const char *row, int64_t bytes)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row + skip), "r"(size) : "memory");
 }
 
-// TOP: every thread keeps the maxima of its chunks, `group` of them in one.  SPLIT: a
+// TOP: every thread keeps the maxima of its chunks, 2^log_group of them in one, and the
+// groups whose maximum counts are what is listed, so that a long row's list is no longer than a
+// short one's (1300 x 262144 FP32 with the 32 most probable 251 us; a list of their chunks
+// overflowed, and the pass a token below took 11 ms).  SPLIT: a
 // cluster of 2^log_blocks blocks shares a row; there are few rows then, so more chunks in
 // flight count for more than more blocks on a multiprocessor (64 x 128256 with the 20 most
 // probable: 9.9 us with four chunks and two blocks, 12.4 with two and four).
 template <int IN, bool ENT, bool TOP, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int group, int resident)
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int log_group, int resident)
 {
     extern __shared__ float maxima[];  // [kept][threads], TOP only
     __shared__ float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps], warp_bound[kWarps];
@@ -293,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     __shared__ unsigned long long candidates[TOP ? kCandidates : 1];
     __shared__ unsigned long long warp_best[kWarps], list[32];
     __shared__ int warp_equal[kWarps];
-    __shared__ uint32_t count, chunks_found, chunk_list[TOP ? kChunkList : 1];
+    __shared__ uint32_t count, groups_found, group_list[TOP ? kGroupList : 1];
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     constexpr int kAhead = SPLIT ? 4 : 2;  // chunks of a thread in flight
-    const int blocks = SPLIT ? 1 << log_blocks : 1, rank = SPLIT ? static_cast<int>(blockIdx.x) & (blocks - 1) : 0;
+    const int group = 1 << log_group, blocks = SPLIT ? 1 << log_blocks : 1, rank = SPLIT ? static_cast<int>(blockIdx.x) & (blocks - 1) : 0;
     const int64_t row = SPLIT ? blockIdx.x >> log_blocks : blockIdx.x;
     auto everybody = [&]() {
         if constexpr (SPLIT)
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
     const Row<IN> r(p.x + row * p.stride, static_cast<int>(p.V), rank, SPLIT ? log_blocks : 0);
     const float c = p.scale * kLog2E, step_up = kMargin / c;
     if (tid == 0)
-        count = chunks_found = 0;
+        count = groups_found = 0;
 
     // ---- the pass over the row
     Sums a = {neg_inf(), 0.0f, 0.0f};
@@ -540,36 +543,39 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
             }
             return n;
         };
-        // the chunks whose maximum counts
+        // the groups of chunks whose maximum counts
         if (__any_sync(0xFFFFFFFFu, counts(own_max))) {
             uint32_t hits = 0;
-            const int kept_n = (mine + group - 1) / group;
+            const int kept_n = (mine + group - 1) >> log_group;
 #pragma unroll 8
             for (int i = 0; i < kept_n; ++i)
                 hits |= static_cast<uint32_t>(counts(maxima[i * threads + tid])) << i;
-            uint32_t at = up_to_lane(__popc(hits) * group), start = 0;
+            uint32_t at = up_to_lane(__popc(hits)), start = 0;
             if (lane == 31)
-                start = atomicAdd(&chunks_found, at);
-            at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits) * group;
-            for (; hits; hits &= hits - 1)
-                for (int j = 0; j < group; ++j, ++at)
-                    if (at < kChunkList)
-                        chunk_list[at] = tid + ((__ffs(hits) - 1) * group + j) * threads;
+                start = atomicAdd(&groups_found, at);
+            at += __shfl_sync(0xFFFFFFFFu, start, 31) - __popc(hits);
+            for (; hits; hits &= hits - 1, ++at)
+                if (at < kGroupList)
+                    group_list[at] = tid + ((__ffs(hits) - 1) << log_group) * threads;  // its first chunk
         }
         __syncthreads();
         // their values: eight bytes a thread, two at a time
-        if (chunks_found > kChunkList) {
+        if (groups_found > kGroupList) {
             if (tid == 0)  // too many for the list: so will the candidates be
                 places(kCandidates + 1);
         } else {
             constexpr int kPart = Chunk<IN>::kVals / 4;
-            for (uint32_t first = warp * 32; first < chunks_found * 4; first += 2 * threads) {
+            const uint32_t parts = groups_found << (log_group + 2);
+            for (uint32_t first = warp * 32; first < parts; first += 2 * threads) {
                 uint32_t w[4], hits = 0;
                 int index[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t i = first + lane + j * threads;
-                    const uint32_t chunk = i < chunks_found * 4 ? chunk_list[i >> 2] : 0xFFFFFFFFu;
+                    uint32_t chunk = 0xFFFFFFFFu;
+                    if (i < parts)
+                        chunk = SPLIT && log_group == 0 ? group_list[i >> 2]
+                                                        : group_list[i >> (log_group + 2)] + ((i >> 2) & (group - 1)) * threads;
                     index[j] = -1;
                     if (chunk < static_cast<uint32_t>(r.to - r.from)) {
                         index[j] = r.first_of(r.from + chunk) + (i & 3) * kPart;
@@ -612,12 +618,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
             break;
         everybody();
         if (tid == 0)
-            count = chunks_found = 0;
+            count = groups_found = 0;
         // The largest logits are next to each other (tokens of one range, the others masked), so that few warps hold
         // them: the `top`-th largest maximum of a block's threads is reached often enough by itself.
         over = true;
         if (tries == 0) {
-            float *const all = reinterpret_cast<float *>(chunk_list);
+            float *const all = reinterpret_cast<float *>(group_list);
             all[tid] = own_max;
             __syncthreads();
             int larger = 0;
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const
             offer(least, r.extra(tid));
         int found = 0;  // equal ones before this tile of chunks
         for (int i = 0; i * threads < r.to - r.from && found < p.top && least != neg_inf(); ++i) {
-            const bool here = i < mine && maxima[i / group * threads + tid] >= least;
+            const bool here = i < mine && maxima[(i >> log_group) * threads + tid] >= least;
             if (!__syncthreads_or(here))
                 continue;
             uint32_t equal = 0;
@@ -903,11 +909,14 @@ cudaError_t launch_rows(const LogprobsParams &p, int num_sms, int log_blocks, in
     const int64_t chunks = (p.V / Chunk<IN>::kVals + blocks - 1) / blocks, mine = (chunks + threads - 1) / threads;
     // (smaller blocks, of which there are more on a multiprocessor, keep fewer: shared memory is L1's)
     const int most = threads >= kThreads ? kKeptMaxima : std::max(kKeptMaxima * threads / kThreads, kKeptMaxima / 2);
-    const int group = static_cast<int>(mine > most ? (mine + most - 1) / most : 1);
-    const size_t smem = TOP ? static_cast<size_t>((mine + group - 1) / group) * threads * sizeof(float) : 0;
+    int log_group = 0;
+    while (mine > static_cast<int64_t>(most) << log_group)
+        ++log_group;
+    const int64_t kept = (mine + (1ll << log_group) - 1) >> log_group;
+    const size_t smem = TOP ? static_cast<size_t>(kept) * threads * sizeof(float) : 0;
     cudaLaunchConfig_t cfg = row_launch(static_cast<unsigned>(p.rows * blocks), threads, smem, s, attr);
     if (blocks == 1)
-        return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, false>, p, 0, group, num_sms * (resident / threads));
+        return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, false>, p, 0, log_group, num_sms * (resident / threads));
     both[0] = attr[0];
     both[1].id = cudaLaunchAttributeClusterDimension;
     both[1].val.clusterDim.x = blocks;
@@ -915,7 +924,7 @@ cudaError_t launch_rows(const LogprobsParams &p, int num_sms, int log_blocks, in
     both[1].val.clusterDim.z = 1;
     cfg.attrs = both;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, true>, p, log_blocks, group, 0);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<IN, ENT, TOP, true>, p, log_blocks, log_group, 0);
 }
 
 template <int IN>
