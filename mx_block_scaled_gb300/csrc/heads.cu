@@ -233,11 +233,10 @@ struct Ring {
         stage = slot = f_stage = f_slot = 0;
         real = 0;
         f_position = left > 0 ? position_of(f_token) : 0;
-        if (left > 0)
-            new_token();
+        place_token();
 #pragma unroll
         for (int d = 0; d < kDepth - 1; ++d)
-            fetch(d < left);
+            fetch(d < left, d == 0);  // (the first heads are not to wait for their token's position)
     }
 
     // a 16-byte piece of this member's angles; the members' pieces lie side by side, which their banks need
@@ -255,8 +254,17 @@ struct Ring {
                 cp_async16(to + (i * team + member) * 16, from + i * team * 16);
     }
 
-    // The copying side comes to a token: its angles, and where its heads are.
-    __device__ __forceinline__ void new_token()
+    // The copying side comes to a token: where its heads are.
+    __device__ __forceinline__ void place_token()
+    {
+        f_x = p.x + f_token * p.x_token + f_head * p.x_head + member * 16;
+        if constexpr (TENSORS == 2) {
+            f_other = other + f_token * other_token + f_head * other_head + member * 16;
+            f_rstd = rstd + f_token * p.heads + f_head;
+        }
+    }
+    // And its angles.
+    __device__ __forceinline__ void turn_token()
     {
         const int64_t position = f_position;
         const bool good = !p.rope || (position >= 0 && position < p.rope_rows);
@@ -270,20 +278,16 @@ struct Ring {
         }
         f_position = position_of(f_token + 1);
         f_slot = (f_slot + 1) & (kDepth - 1);
-        f_x = p.x + f_token * p.x_token + f_head * p.x_head + member * 16;
-        if constexpr (TENSORS == 2) {
-            f_other = other + f_token * other_token + f_head * other_head + member * 16;
-            f_rstd = rstd + f_token * p.heads + f_head;
-        }
     }
 
-    __device__ __forceinline__ void fetch(bool any)
+    __device__ __forceinline__ void fetch(bool any, bool first = false)
     {
         if (any) {
-            if (f_head - mine >= p.heads) {  // warp-uniform
+            if (!first && f_head - mine >= p.heads) {  // warp-uniform
                 f_head = mine;
                 ++f_token;
-                new_token();
+                place_token();
+                turn_token();
             }
             if (f_head < p.heads) {
                 copy(own + f_stage * stage_size, f_x);
@@ -293,6 +297,8 @@ struct Ring {
                         cp_async4(own_rstd + f_stage * stage_size, f_rstd);
                 }
             }
+            if (first)
+                turn_token();
             f_head += side;
             f_x += side * p.x_head;
             if constexpr (TENSORS == 2) {
