@@ -182,7 +182,7 @@ __device__ __forceinline__ double warp_sum64(double v)
 }
 
 // The sum over the block, in its first warp's lanes.  An FP64 addition holds a multiprocessor's pipe for 16 cycles a
-// warp, so one warp adds the threads' sums, 13 additions (43 where every warp adds its own first).
+// warp, so one warp adds the threads' sums, 12 additions (43 where every warp adds its own first).
 __device__ __forceinline__ double block_sum64(double v, double *all)
 {
     all[threadIdx.x] = v;

@@ -25,7 +25,7 @@ __device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t t
 
 // ------------------------------------------------------------------- lookup --
 // A warp copies 512 values of a row, CHUNKS times: two where there are warps enough, so
-// that more bytes are in flight behind one id (16384 x 8192 BF16 61 us, 6.6 TB/s of the
+// that more bytes are in flight behind one id (16384 x 8192 BF16 60.4 us, 6.3 TB/s of the
 // rows written and the different rows read; bound by HBM), one for few tokens (8 x 8192:
 // 1.8 us, an id's latency and a row's).
 template <int IN, int OUT, int CHUNKS>

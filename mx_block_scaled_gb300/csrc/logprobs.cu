@@ -14,9 +14,10 @@
 //
 // Bound by HBM for long rows: 4096 x 128256 BF16 153 us (6.9 TB/s), with entropy 157 (a
 // value costs one 2^t and eight packed or paired instructions), with the 20 most
-// probable 183 (a row's last steps, 3 us, are covered by the three other blocks of its
-// multiprocessor); 16 such rows on clusters of eight blocks 3.7, 4.2 and 7.4 us, latency:
-// two memory accesses, two cluster barriers, with the most probable ones four and three.
+// probable 172, with both 183 (a row's last steps, 3 us, are covered by the three other
+// blocks of its multiprocessor); 16 such rows on clusters of eight blocks, from L2, 3.7, 4.1,
+// 6.7 and 7.0 us (the last from HBM 7.8), latency: two memory accesses, two cluster barriers,
+// with the most probable ones four and three.
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -271,7 +272,7 @@ struct Row {
 
 // The first bytes of a later row into L2: blocks that start together end together, and
 // HBM would idle through their last steps (4096 x 128256 BF16 with the 20 most probable
-// 176 us, 181 without; 16 and 64 KB 179 and 174, but with entropy 187 and 188, 186 here).
+// 174 us, 179 without; 16 and 64 KB 177 and 173; with entropy 184, without 186, and 184 and 185).
 __device__ __forceinline__ void fetch_ahead(const char *row, int64_t bytes)
 {
     const int skip = static_cast<int>(-reinterpret_cast<uintptr_t>(row) & 15);
@@ -285,8 +286,8 @@ __device__ __forceinline__ void fetch_ahead(const char *row, int64_t bytes)
 // short one's (1300 x 262144 FP32 with the 32 most probable 251 us; a list of their chunks
 // overflowed, and the pass a token below took 11 ms).  SPLIT: a
 // cluster of 2^log_blocks blocks shares a row; there are few rows then, so more chunks in
-// flight count for more than more blocks on a multiprocessor (64 x 128256 with the 20 most
-// probable: 9.9 us with four chunks and two blocks, 12.4 with two and four).
+// flight count for more than more blocks on a multiprocessor (64 x 128256 with entropy and the
+// 20 most probable: 9.4 us with four chunks and two blocks, 11.9 with two and four).
 template <int IN, bool ENT, bool TOP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 4) logprobs_kernel(const LogprobsParams p, int log_blocks, int log_group, int resident)
 {
@@ -877,10 +878,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const Logpr
 }
 
 // Threads of a block for long rows, such that as little of the machine idles as can be: 700 x 50257 FP32 with the 20 most
-// probable 30 us in one wave of blocks of 192, 38 in a wave of 256 and a seventh of one; 1216 rows are two waves of 256
-// alike.  In tenths of a row's time on a full multiprocessor: the full waves' rows, those of the last one, which takes no
+// probable 28.6 us in one wave of blocks of 192, 36.3 in a wave of 256 and a seventh of one.  In tenths of a row's time on a full multiprocessor: the full waves' rows, those of the last one, which takes no
 // less than six tenths of a full one, and every wave's last steps.  After three waves blocks no longer end together
-// (4096 x 128256 BF16 on blocks of 96: 188 us, 176 on those of 256).
+// (4096 x 128256 BF16 with the 20 most probable: on blocks of 96 192 us, 174 on those of 256).  Of 364 sizes (160 to 1824
+// rows of 9000 to 262144 values, both types, with the 20 most probable and without) blocks of 256 throughout take 0.90 to
+// 1.51 times this choice's time, 1.05 in the mean; the best of the five sizes 0.97 in the mean and 0.79 at the least.
 int wave_threads(int64_t rows, int num_sms, int resident)
 {
     int64_t least = INT64_MAX;
@@ -931,7 +933,7 @@ template <int IN>
 cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
 {
     // few rows: blocks of a cluster share one, while each has at least two chunks a thread and all of them are resident
-    // at once, two to a multiprocessor (100 x 128256 with the 20 most probable: 13.7 us on two blocks a row, 17.5 on four, where
+    // at once, two to a multiprocessor (100 x 128256 with the 20 most probable: 11.7 us on two blocks a row, 15.1 on four, where
     // a second wave is left)
     const int64_t chunks = p.V / Chunk<IN>::kVals;
     int log_blocks = 0;
@@ -940,7 +942,7 @@ cudaError_t launch_forward(const LogprobsParams &p, int num_sms, cudaStream_t s)
         ++log_blocks;
     // short rows: fewer threads, down to a warp, of two chunks each; and where more rows are to be done than fit at once,
     // fewer still, up to sixteen chunks each, since a block's reductions are latency that other blocks have to cover
-    // (8192 x 4096 BF16 15 us, 24 with two; 1446 x 10721 FP32 with the 20 most probable 18 us, 29)
+    // (8192 x 4096 BF16 12.6 us, 17.4 with two; 1446 x 10721 FP32 with the 20 most probable 15.0 us, 19.4 with six)
     int threads = kThreads;
     while (threads > 32 && chunks < 2ll * threads << log_blocks)
         threads /= 2;
