@@ -11,10 +11,10 @@
 // head takes a team of 1 to 32 lanes.
 //
 // One read and one write of the heads, two reads for the gradient.  16384 x 40 heads of
-// 128 BF16 60 us (5.8 TB/s), their gradient at 8192 tokens 47 us (5.5 TB/s, 4 of it the
+// 128 BF16 59 us (5.8 TB/s), their gradient at 8192 tokens 46 us (5.6 TB/s, 4 of it the
 // second launch): instructions (300 and 370 for a warp's 512 values, issued in 72% of the
-// cycles) nearly as much as HBM; FP32 10550 x 32 heads of 96 46 us, gradient of 4000 x 40
-// of 128 44 us (0.85 and 0.84 of a copy).
+// cycles) nearly as much as HBM; FP32 10550 x 32 heads of 96 45 us, gradient of 4000 x 40
+// of 128 43 us (0.87 and 0.85 of a copy).
 #include "mx_block.cuh"
 #include "ops.h"
 #include "ptx.cuh"
