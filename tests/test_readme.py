@@ -1,4 +1,4 @@
-"""The calls that README.md shows: names and arguments that the binding has, and every
+"""The calls that the usage text shows: names and arguments that the binding has, and every
 `_backward` call with the settings of the forward call before it (no GPU)."""
 import ast
 import inspect
